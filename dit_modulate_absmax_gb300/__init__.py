@@ -39,6 +39,12 @@ _SIGNATURES = {
                                             _STATUS),
     "h3fp4_diag_gemm_wait_timeout": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, ctypes.c_uint32, _P],
                                      _STATUS),
+    "h3fp4_rope_axes": ([_P, _I64, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P], _STATUS),
+    "h3fp4_kv_cache_write": ([_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _P], _STATUS),
+    "h3fp4_kv_cache_read": ([_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _P], _STATUS),
+    "h3fp4_kv_attention": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _I32, ctypes.c_float, _I32, _I32,
+                            _P, _I64, _P], _STATUS),
+    "h3fp4_kv_attention_workspace": ([_I64, _I32, _I32, _I32, _I32, _I32, _I32], _I64),
     "h3fp4_status_string": ([_STATUS], ctypes.c_char_p),
     "h3fp4_build_info": ([], ctypes.c_char_p),
 }
@@ -55,6 +61,28 @@ class H3FP4Error(RuntimeError):
 
 class GemmConfig(ctypes.Structure):
     _fields_ = [("n_group", _I32), ("stages", _I32), ("cta_pair", _I32), ("reserved", _I32)]
+
+
+ROPE_MAX_AXES = 4
+ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
+
+
+class RopeStruct(ctypes.Structure):
+    """h3fp4_rope."""
+    _fields_ = [("positions", _P), ("ld_positions", _I64), ("freqs", _P), ("axes", _I32),
+                ("dims", _I32 * ROPE_MAX_AXES), ("layout", _I32), ("inverse", _I32)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    """h3fp4_kv_cache."""
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I32),
+                ("page_size", _I32), ("heads", _I32), ("head_dim", _I32)]
+
+
+class KVBatchStruct(ctypes.Structure):
+    """h3fp4_kv_batch."""
+    _fields_ = [("page_table", _P), ("ld_table", _I64), ("len", _P), ("cu_tokens", _P), ("batch", _I32),
+                ("max_tokens", _I32)]
 
 
 _lib = None
@@ -164,6 +192,39 @@ def h3fp4_diag_producer_barrier_timeout(x, ldx, m, m_pad, d, tensor_scale, scrat
 def h3fp4_diag_gemm_wait_timeout(a_q, a_sf, a_ts, b_q, b_sf, b_ts, c, ldc, m, m_pad, n, k, limit_us, stream=0):
     """Failure-detection check: the default GEMM with its loads withheld; its waits give up after limit_us."""
     _call("h3fp4_diag_gemm_wait_timeout", a_q, a_sf, a_ts, b_q, b_sf, b_ts, c, ldc, m, m_pad, n, k, limit_us, stream)
+
+
+def h3fp4_rope_axes(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads, head_dim,
+                    rope: RopeStruct, stream=0):
+    _call("h3fp4_rope_axes", x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads,
+          head_dim, ctypes.byref(rope), stream)
+
+
+def h3fp4_kv_cache_write(cache: KVCacheStruct, batch: KVBatchStruct, k, k_token_stride, k_head_stride, v,
+                         v_token_stride, v_head_stride, tokens, rope: RopeStruct | None = None, stream=0):
+    _call("h3fp4_kv_cache_write", ctypes.byref(cache), ctypes.byref(batch), k, k_token_stride, k_head_stride, v,
+          v_token_stride, v_head_stride, tokens, ctypes.byref(rope) if rope is not None else None, stream)
+
+
+def h3fp4_kv_cache_read(cache: KVCacheStruct, batch: KVBatchStruct, k, k_token_stride, k_head_stride, v,
+                        v_token_stride, v_head_stride, tokens, stream=0):
+    _call("h3fp4_kv_cache_read", ctypes.byref(cache), ctypes.byref(batch), k, k_token_stride, k_head_stride, v,
+          v_token_stride, v_head_stride, tokens, stream)
+
+
+def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens, heads,
+                       cache: KVCacheStruct, batch: KVBatchStruct, max_kv, softmax_scale, causal, window, workspace,
+                       workspace_bytes, stream=0):
+    _call("h3fp4_kv_attention", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
+          heads, ctypes.byref(cache), ctypes.byref(batch), max_kv, softmax_scale, causal, window, workspace,
+          workspace_bytes, stream)
+
+
+def h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv) -> int:
+    n = lib().h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv)
+    if n < 0:
+        raise H3FP4Error("h3fp4_kv_attention_workspace", 3)
+    return n
 
 
 def h3fp4_build_info() -> str:
@@ -321,3 +382,179 @@ def swizzle_scales(sf_logical, *, out=None, stream=None):
         out = torch.empty(sf_rows(rows) * cols, dtype=torch.uint8, device=sf_logical.device)
     h3fp4_swizzle_scales(sf_logical.data_ptr(), rows, cols, sf_logical.stride(0), out.data_ptr(), _stream(stream))
     return out
+
+
+# ----------------------------------------------------------------------------
+# Rotary positions, the 8-bit key/value cache, and attention over it.  bf16
+# tensors are torch.bfloat16 or int16 patterns; outputs take their input's type.
+# ----------------------------------------------------------------------------
+def _need(ok, what):
+    """Raises ValueError with the text, or the result of the function, `what`."""
+    if not ok:
+        raise ValueError(what() if callable(what) else what)
+
+
+def _need_array(t, name, dtype, ndim):
+    """A device array of this element type whose last dimension is contiguous."""
+    _need_cuda(t)
+    _need(str(t.dtype) == "torch." + dtype and t.dim() == ndim and (t.shape[-1] <= 1 or t.stride(-1) == 1),
+          lambda: f"{name}: a {ndim}-D {dtype} tensor with a contiguous last dimension is wanted, "
+          f"got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
+
+
+def _need_tokens(t, name, shape=None):
+    """A [tokens, heads, head_dim] array of bf16 values or patterns."""
+    _need_cuda(t)
+    _need(str(t.dtype) in ("torch.bfloat16", "torch.int16") and t.dim() == 3 and t.stride(2) == 1,
+          lambda: f"{name}: a [tokens, heads, head_dim] tensor of bf16 values (bfloat16 or int16) with contiguous channels is "
+          f"wanted, got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
+    _need(shape is None or tuple(t.shape) == tuple(shape), lambda: f"{name}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+
+
+class Rope:
+    """Rotary positions of a call's tokens: ``positions`` [tokens, axes] float32,
+    ``freqs`` [sum(dims)/2] float64 in radians per unit of position (the pairs of
+    axis 0 first), ``dims`` the channels each axis turns, ``layout`` how a pair lies
+    in its axis' channels: "interleaved" (2j, 2j+1) or "halves" (j, j + dims/2)."""
+
+    def __init__(self, positions, freqs, dims, layout="interleaved"):
+        _need_array(positions, "positions", "float32", 2)
+        _need_array(freqs, "freqs", "float64", 1)
+        _need(1 <= len(dims) <= ROPE_MAX_AXES and positions.shape[1] >= len(dims),
+              lambda: f"rope: {len(dims)} axes for positions {tuple(positions.shape)}")
+        _need(2 * freqs.shape[0] >= sum(dims), lambda: f"rope: {freqs.shape[0]} frequencies for dims {tuple(dims)}")
+        _need(layout in ROPE_LAYOUTS, lambda: f"rope: layout {layout!r}, not one of {sorted(ROPE_LAYOUTS)}")
+        self.positions, self.freqs, self.dims, self.layout = positions, freqs, tuple(dims), layout
+
+    def struct(self, inverse=False) -> RopeStruct:
+        return RopeStruct(self.positions.data_ptr(), max(self.positions.stride(0), self.positions.shape[1]),
+                          self.freqs.data_ptr(), len(self.dims), self.dims, ROPE_LAYOUTS[self.layout], int(inverse))
+
+
+def rope_frequencies(dims, theta=10000.0, device="cuda"):
+    """theta^(-2j/d) for the pairs j of each axis' d channels: ``freqs`` of a Rope."""
+    import torch
+    return torch.cat([theta ** (-torch.arange(0, d, 2, dtype=torch.float64) / max(d, 1)) for d in dims]).to(device)
+
+
+def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
+    """x [tokens, heads, head_dim] turned by its tokens' positions; inverse=True turns
+    back (and is the gradient).  out=x works in place.  Returns out."""
+    import torch
+    _need_tokens(x, "x")
+    tokens, heads, dim = x.shape
+    _need(rope.positions.shape[0] >= tokens, lambda: f"rope: {rope.positions.shape[0]} positions for {tokens} tokens")
+    if out is None:
+        out = torch.empty(tokens, heads, dim, dtype=x.dtype, device=x.device)
+    _need_tokens(out, "out", x.shape)
+    h3fp4_rope_axes(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), tokens, heads,
+                    dim, rope.struct(inverse), _stream(stream))
+    return out
+
+
+class KVCache:
+    """Keys and values in E4M3 pages: codes [num_pages, heads, page_size, head_dim]
+    uint8 and scales [num_pages, heads] float32, for keys and values each."""
+
+    def __init__(self, k_codes, k_scale, v_codes, v_scale):
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _need_array(t, name, "uint8", 4)
+            _need(t.is_contiguous() and t.shape == k_codes.shape, lambda: f"{name}: contiguous, both alike")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need_array(t, name, "float32", 2)
+            _need(t.is_contiguous() and t.shape == k_codes.shape[:2], lambda: f"{name}: contiguous [num_pages, heads]")
+        self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
+        self.num_pages, self.heads, self.page_size, self.head_dim = k_codes.shape
+
+    @classmethod
+    def empty(cls, num_pages, page_size, heads, head_dim, device="cuda"):
+        """A cache of uninitialised pages (a page's first write sets its scales)."""
+        import torch
+        codes = [torch.empty(num_pages, heads, page_size, head_dim, dtype=torch.uint8, device=device) for _ in "kv"]
+        scale = [torch.ones(num_pages, heads, dtype=torch.float32, device=device) for _ in "kv"]
+        return cls(codes[0], scale[0], codes[1], scale[1])
+
+    def struct(self) -> KVCacheStruct:
+        return KVCacheStruct(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scale.data_ptr(),
+                             self.v_scale.data_ptr(), self.num_pages, self.page_size, self.heads, self.head_dim)
+
+
+def _kv_batch(page_table, length, cu_tokens, max_tokens) -> KVBatchStruct:
+    _need_array(page_table, "page_table", "int32", 2)
+    _need_array(cu_tokens, "cu_tokens", "int32", 1)
+    batch, pages = page_table.shape
+    _need(cu_tokens.shape[0] == batch + 1, lambda: f"cu_tokens: {batch + 1} entries are wanted, got {cu_tokens.shape[0]}")
+    if length is not None:
+        _need_array(length, "lengths", "int32", 1)
+        _need(length.shape[0] == batch, lambda: f"lengths: {batch} entries are wanted, got {length.shape[0]}")
+    _need(page_table.is_contiguous(), "page_table: contiguous rows are wanted")
+    return KVBatchStruct(page_table.data_ptr(), pages, length.data_ptr() if length is not None else None,
+                         cu_tokens.data_ptr(), batch, max_tokens)
+
+
+def kv_cache_write(cache: KVCache, k, v, page_table, held, cu_tokens, max_tokens, *, rope: Rope | None = None,
+                   stream=None):
+    """Quantises new keys and values [tokens, heads, head_dim] into the cache.  Sequence
+    b's tokens are rows cu_tokens[b] .. cu_tokens[b+1]-1 and go to positions held[b] on
+    (page_table [batch, pages], held [batch], cu_tokens [batch+1]: device int32);
+    max_tokens is the most new tokens of any sequence.  With ``rope`` the keys are
+    turned first.  The caller advances its lengths."""
+    _need_tokens(k, "k")
+    tokens = k.shape[0]
+    _need_tokens(k, "k", (tokens, cache.heads, cache.head_dim))
+    _need_tokens(v, "v", k.shape)
+    _need(rope is None or rope.positions.shape[0] >= tokens, "rope: fewer positions than tokens")
+    _need(held is not None, "held: lengths before the call are wanted")
+    h3fp4_kv_cache_write(cache.struct(), _kv_batch(page_table, held, cu_tokens, max_tokens), k.data_ptr(), k.stride(0),
+                         k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), tokens,
+                         rope.struct() if rope is not None else None, _stream(stream))
+
+
+def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_tokens, *, k=None, v=None, stream=None):
+    """The cache's keys and values as bf16: sequence b's positions start[b] on (start
+    None: from 0), into rows cu_tokens[b] .. cu_tokens[b+1]-1 of [tokens, heads,
+    head_dim] outputs.  Returns (k, v)."""
+    import torch
+    shape = (tokens, cache.heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+    _need_tokens(k, "k", shape)
+    _need_tokens(v, "v", shape)
+    h3fp4_kv_cache_read(cache.struct(), _kv_batch(page_table, start, cu_tokens, max_tokens), k.data_ptr(), k.stride(0),
+                        k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), tokens, _stream(stream))
+    return k, v
+
+
+def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, max_kv, *, scale=None, causal=False,
+                 window=0, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """Attention of q [tokens, heads, head_dim] over the cache.  kv_len[b] counts all keys
+    of sequence b, its new tokens' among them; query i of n stands at kv_len[b] - n + i and
+    sees the keys before kv_len[b] that are not after it (causal) and not window or more
+    before it (window > 0).  scale defaults to head_dim ** -0.5.  Returns (out, lse); lse
+    [tokens, heads] float32 is None unless asked for."""
+    import torch
+    _need_tokens(q, "q")
+    tokens, heads, dim = q.shape
+    _need(dim == cache.head_dim and heads % cache.heads == 0,
+          lambda: f"q: {heads} heads of {dim} for a cache of {cache.heads} heads of {cache.head_dim}")
+    _need(kv_len is not None, "kv_len: lengths are wanted")
+    if out is None:
+        out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=q.device)
+    _need_tokens(out, "out", q.shape)
+    if lse is None and return_lse:
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need_array(lse, "lse", "float32", 2)
+        _need(lse.is_contiguous() and tuple(lse.shape) == (tokens, heads), "lse: contiguous [tokens, heads]")
+    batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens)
+    need = h3fp4_kv_attention_workspace(tokens, heads, cache.heads, dim, batch.batch, max_tokens, max_kv)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    h3fp4_kv_attention(q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
+                       lse.data_ptr() if lse is not None else None, tokens, heads, cache.struct(), batch, max_kv,
+                       dim ** -0.5 if scale is None else scale, int(causal), window,
+                       workspace.data_ptr() if workspace is not None else None,
+                       workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream))
+    return out, lse

@@ -241,6 +241,229 @@ h3fp4_status h3fp4_gemm_gated_residual(const uint8_t *a_q, const uint8_t *a_sf, 
                               ldo, m, m_pad, n, k, c, &g, as_stream(stream));
 }
 
+namespace {
+
+// Token arrays [tokens, heads, dim] with element strides of tokens and heads.
+struct Strided {
+    const void *p;
+    int64_t token, head;
+};
+
+// Largest stride accepted: byte offsets (up to 2^31 tokens) stay within 63 bits.
+constexpr int64_t kMaxStride = int64_t(1) << 30;
+
+h3fp4_status check_strided(const Strided &a)
+{
+    if (a.p == nullptr)
+        return H3FP4_ERR_NULL;
+    if (a.token < 0 || a.head < 0 || a.token > kMaxStride || a.head > kMaxStride)
+        return H3FP4_ERR_SHAPE;
+    if (!aligned16(a.p) || a.token % 8 != 0 || a.head % 8 != 0)
+        return H3FP4_ERR_ALIGN;
+    return H3FP4_OK;
+}
+
+// An output's rows must be distinct: neither stride may fold two of them together.
+h3fp4_status check_strided_out(const Strided &a, int64_t tokens, int64_t heads, int64_t dim)
+{
+    const h3fp4_status s = check_strided(a);
+    if (s != H3FP4_OK)
+        return s;
+    const bool token_outer = a.token >= a.head;
+    const int64_t inner = token_outer ? a.head : a.token, outer = token_outer ? a.token : a.head;
+    const int64_t n_inner = token_outer ? heads : tokens, n_outer = token_outer ? tokens : heads;
+    if ((n_inner > 1 && inner < dim) || (n_outer > 1 && outer < (n_inner - 1) * inner + dim))
+        return H3FP4_ERR_SHAPE;
+    return H3FP4_OK;
+}
+
+bool ranges_overlap(const Strided &a, const Strided &b, int64_t tokens, int64_t heads, int64_t dim)
+{
+    const auto bytes = [&](const Strided &x) { return 2 * ((tokens - 1) * x.token + (heads - 1) * x.head + dim); };
+    const char *pa = static_cast<const char *>(a.p), *pb = static_cast<const char *>(b.p);
+    return pa < pb + bytes(b) && pb < pa + bytes(a);
+}
+
+h3fp4_status make_rope(const h3fp4_rope *r, int64_t dim, int64_t tokens, h3fp4::RopeArgs *out)
+{
+    if (r == nullptr)
+        return H3FP4_ERR_NULL;
+    if (r->axes < 1 || r->axes > H3FP4_ROPE_MAX_AXES || r->ld_positions < r->axes ||
+        r->ld_positions > (int64_t(1) << 30) || (r->inverse != 0 && r->inverse != 1))
+        return H3FP4_ERR_SHAPE;
+    int64_t total = 0;
+    for (int i = 0; i < H3FP4_ROPE_MAX_AXES; ++i) {
+        if (i < r->axes) {
+            if (r->dims[i] < 0 || r->dims[i] % 2 != 0 || r->dims[i] > dim - total)
+                return H3FP4_ERR_SHAPE;
+            total += r->dims[i];
+        }
+        out->end[i] = static_cast<int32_t>(total);
+    }
+    if (r->layout != 0 && r->layout != 1)
+        return H3FP4_ERR_UNSUPPORTED;
+    if ((r->positions == nullptr || r->freqs == nullptr) && total != 0 && tokens != 0)
+        return H3FP4_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(r->positions) & 3u) != 0 || (reinterpret_cast<uintptr_t>(r->freqs) & 7u) != 0)
+        return H3FP4_ERR_ALIGN;
+    out->positions = r->positions;
+    out->ld_positions = r->ld_positions;
+    out->freqs = r->freqs;
+    out->pairs = static_cast<int32_t>(total / 2);
+    out->layout = r->layout;
+    out->inverse = r->inverse;
+    return H3FP4_OK;
+}
+
+h3fp4_status check_cache(const h3fp4_kv_cache *c)
+{
+    if (c == nullptr)
+        return H3FP4_ERR_NULL;
+    if (c->num_pages < 0 || c->heads < 1 || c->heads > 65535)
+        return H3FP4_ERR_SHAPE;
+    if ((c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) ||
+        (c->head_dim != 64 && c->head_dim != 128))
+        return H3FP4_ERR_UNSUPPORTED;
+    if (c->num_pages > 0 && (c->k_codes == nullptr || c->v_codes == nullptr || c->k_scale == nullptr || c->v_scale == nullptr))
+        return H3FP4_ERR_NULL;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) != 0)
+        return H3FP4_ERR_ALIGN;
+    return H3FP4_OK;
+}
+
+h3fp4_status check_batch(const h3fp4_kv_batch *b, bool need_len, int64_t tokens)
+{
+    if (b == nullptr)
+        return H3FP4_ERR_NULL;
+    if (b->batch < 0 || b->batch > 65535 || b->max_tokens < 0 || b->max_tokens > 1000000 || b->ld_table < 0 ||
+        b->ld_table > INT32_MAX || tokens < 0 || tokens > INT32_MAX)
+        return H3FP4_ERR_SHAPE;
+    if (b->batch > 0 && tokens > 0) {
+        if (b->cu_tokens == nullptr || (need_len && b->len == nullptr) || (b->page_table == nullptr && b->ld_table > 0))
+            return H3FP4_ERR_NULL;
+        if (((reinterpret_cast<uintptr_t>(b->cu_tokens) | reinterpret_cast<uintptr_t>(b->len) |
+              reinterpret_cast<uintptr_t>(b->page_table)) & 3u) != 0)
+            return H3FP4_ERR_ALIGN;
+    }
+    return H3FP4_OK;
+}
+
+bool attention_sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch,
+                        int32_t max_tokens, int32_t max_kv)
+{
+    return tokens >= 0 && tokens <= INT32_MAX && heads >= 1 && heads <= 65535 && kv_heads >= 1 &&
+           heads % kv_heads == 0 && (head_dim == 64 || head_dim == 128) && batch >= 0 && batch <= 65535 &&
+           max_tokens >= 0 && max_tokens <= 1000000 && max_kv >= 0 && max_kv <= (1 << 30);
+}
+
+}  // namespace
+
+h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_stride, int64_t x_head_stride, void *out_bf16,
+                             int64_t out_token_stride, int64_t out_head_stride, int64_t tokens, int32_t heads,
+                             int32_t head_dim, const h3fp4_rope *rope, void *stream)
+{
+    if (tokens < 0 || tokens > INT32_MAX || heads < 0 || heads > 65535 || head_dim < 8 || head_dim > 256 ||
+        head_dim % 8 != 0)
+        return H3FP4_ERR_SHAPE;
+    h3fp4::RopeArgs r;
+    h3fp4_status s = make_rope(rope, head_dim, tokens, &r);
+    if (s != H3FP4_OK || tokens == 0 || heads == 0)
+        return s;
+    const Strided x{x_bf16, x_token_stride, x_head_stride}, out{out_bf16, out_token_stride, out_head_stride};
+    if ((s = check_strided(x)) != H3FP4_OK || (s = check_strided_out(out, tokens, heads, head_dim)) != H3FP4_OK)
+        return s;
+    const bool same = x.p == out.p && x.token == out.token && x.head == out.head;
+    if (!same && ranges_overlap(x, out, tokens, heads, head_dim))
+        return H3FP4_ERR_UNSUPPORTED;
+    return from_cuda(h3fp4::launch_rope(static_cast<const uint16_t *>(x_bf16), x.token, x.head,
+                                        static_cast<uint16_t *>(out_bf16), out.token, out.head, tokens, heads, head_dim,
+                                        r, as_stream(stream)));
+}
+
+h3fp4_status h3fp4_kv_cache_write(const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch, const void *k_bf16,
+                                  int64_t k_token_stride, int64_t k_head_stride, const void *v_bf16,
+                                  int64_t v_token_stride, int64_t v_head_stride, int64_t tokens,
+                                  const h3fp4_rope *rope, void *stream)
+{
+    h3fp4_status s = check_cache(cache);
+    if (s != H3FP4_OK || (s = check_batch(batch, true, tokens)) != H3FP4_OK)
+        return s;
+    h3fp4::RopeArgs r{};
+    if (rope != nullptr && (s = make_rope(rope, cache->head_dim, tokens, &r)) != H3FP4_OK)
+        return s;
+    if (batch->batch == 0 || tokens == 0 || batch->max_tokens == 0)
+        return H3FP4_OK;
+    const Strided k{k_bf16, k_token_stride, k_head_stride}, v{v_bf16, v_token_stride, v_head_stride};
+    if ((s = check_strided(k)) != H3FP4_OK || (s = check_strided(v)) != H3FP4_OK)
+        return s;
+    return from_cuda(h3fp4::launch_kv_write(*cache, *batch, static_cast<const uint16_t *>(k_bf16), k.token, k.head,
+                                            static_cast<const uint16_t *>(v_bf16), v.token, v.head, tokens, r,
+                                            as_stream(stream)));
+}
+
+h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch, void *k_bf16,
+                                 int64_t k_token_stride, int64_t k_head_stride, void *v_bf16, int64_t v_token_stride,
+                                 int64_t v_head_stride, int64_t tokens, void *stream)
+{
+    h3fp4_status s = check_cache(cache);
+    if (s != H3FP4_OK || (s = check_batch(batch, false, tokens)) != H3FP4_OK)
+        return s;
+    if (batch->batch == 0 || tokens == 0 || batch->max_tokens == 0)
+        return H3FP4_OK;
+    if (k_bf16 == nullptr && v_bf16 == nullptr)
+        return H3FP4_ERR_NULL;
+    const Strided k{k_bf16, k_token_stride, k_head_stride}, v{v_bf16, v_token_stride, v_head_stride};
+    if ((k.p != nullptr && (s = check_strided_out(k, tokens, cache->heads, cache->head_dim)) != H3FP4_OK) ||
+        (v.p != nullptr && (s = check_strided_out(v, tokens, cache->heads, cache->head_dim)) != H3FP4_OK))
+        return s;
+    return from_cuda(h3fp4::launch_kv_read(*cache, *batch, static_cast<uint16_t *>(k_bf16), k.token, k.head,
+                                           static_cast<uint16_t *>(v_bf16), v.token, v.head, tokens,
+                                           as_stream(stream)));
+}
+
+int64_t h3fp4_kv_attention_workspace(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t batch,
+                                     int32_t max_tokens, int32_t max_kv)
+{
+    if (!attention_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv))
+        return -1;
+    return h3fp4::attention_workspace(h3fp4::AttnShape{tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv});
+}
+
+h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, void *out_bf16,
+                                int64_t out_token_stride, int64_t out_head_stride, float *lse, int64_t tokens,
+                                int32_t heads, const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch,
+                                int32_t max_kv, float softmax_scale, int32_t causal, int32_t window, void *workspace,
+                                int64_t workspace_bytes, void *stream)
+{
+    h3fp4_status s = check_cache(cache);
+    if (s != H3FP4_OK || (s = check_batch(batch, true, tokens)) != H3FP4_OK)
+        return s;
+    if (!attention_sizes_ok(tokens, heads, cache->heads, cache->head_dim, batch->batch, batch->max_tokens, max_kv) ||
+        window < 0 || (causal != 0 && causal != 1) || !(softmax_scale - softmax_scale == 0.0f))
+        return H3FP4_ERR_SHAPE;
+    if (batch->batch == 0 || tokens == 0 || batch->max_tokens == 0)
+        return H3FP4_OK;
+    const Strided q{q_bf16, q_token_stride, q_head_stride}, out{out_bf16, out_token_stride, out_head_stride};
+    if ((s = check_strided(q)) != H3FP4_OK ||
+        (s = check_strided_out(out, tokens, heads, cache->head_dim)) != H3FP4_OK)
+        return s;
+    if (ranges_overlap(q, out, tokens, heads, cache->head_dim))
+        return H3FP4_ERR_UNSUPPORTED;
+    const int64_t need = h3fp4::attention_workspace(h3fp4::AttnShape{tokens, heads, cache->heads, cache->head_dim,
+                                                                     batch->batch, batch->max_tokens, max_kv});
+    if (need > 0 && workspace == nullptr)
+        return H3FP4_ERR_NULL;
+    if (workspace_bytes < need)
+        return H3FP4_ERR_SHAPE;
+    if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+        return H3FP4_ERR_ALIGN;
+    const h3fp4::AttnArgs a{static_cast<const uint16_t *>(q_bf16), q.token, q.head, static_cast<uint16_t *>(out_bf16),
+                            out.token, out.head, lse, tokens, heads, *cache, *batch, max_kv, softmax_scale, causal,
+                            window};
+    return from_cuda(h3fp4::launch_attention(a, workspace, as_stream(stream)));
+}
+
 h3fp4_status h3fp4_swizzle_scales(const uint8_t *sf_logical, int64_t rows, int64_t cols, int64_t ld,
                                   uint8_t *sf_out, void *stream)
 {
@@ -293,7 +516,14 @@ h3fp4_status h3fp4_device_error(uint32_t *code)
 {
     if (code == nullptr)
         return H3FP4_ERR_NULL;
-    return h3fp4::read_device_error(code);
+    uint32_t kv = 0, attn = 0;
+    const h3fp4_status s = h3fp4::read_device_error(code);
+    if (s != H3FP4_OK)
+        return s;
+    if (h3fp4::read_kvcache_error(&kv) != cudaSuccess || h3fp4::read_attention_error(&attn) != cudaSuccess)
+        return H3FP4_ERR_CUDA;
+    *code |= kv | attn;
+    return H3FP4_OK;
 }
 
 const char *h3fp4_status_string(h3fp4_status status)

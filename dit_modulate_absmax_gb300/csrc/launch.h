@@ -72,4 +72,55 @@ cudaError_t launch_quantize_pack_barrier_timeout(const uint16_t *x, int64_t ldx,
 
 h3fp4_status read_device_error(uint32_t *code);
 
+// ---------------------------------------------------------------------------
+// Rotary positions, the 8-bit cache and its attention: arguments by value.
+// ---------------------------------------------------------------------------
+struct RopeArgs {
+    const float *positions;
+    int64_t ld_positions;
+    const double *freqs;
+    int32_t end[H3FP4_ROPE_MAX_AXES];   // first channel past each axis (unused axes: the total)
+    int32_t pairs;                      // turned pairs; 0 = no rotation
+    int32_t layout, inverse;
+};
+
+using KvCache = h3fp4_kv_cache;
+using KvBatch = h3fp4_kv_batch;
+
+cudaError_t launch_rope(const uint16_t *x, int64_t xt, int64_t xh, uint16_t *out, int64_t ot, int64_t oh,
+                        int64_t tokens, int heads, int dim, const RopeArgs &r, cudaStream_t st);
+
+cudaError_t launch_kv_write(const KvCache &cache, const KvBatch &batch, const uint16_t *k, int64_t kt, int64_t kh,
+                            const uint16_t *v, int64_t vt, int64_t vh, int64_t tokens, const RopeArgs &rope,
+                            cudaStream_t st);
+
+cudaError_t launch_kv_read(const KvCache &cache, const KvBatch &batch, uint16_t *k, int64_t kt, int64_t kh,
+                           uint16_t *v, int64_t vt, int64_t vh, int64_t tokens, cudaStream_t st);
+
+struct AttnArgs {
+    const uint16_t *q;
+    int64_t qt, qh;        // strides of tokens and heads
+    uint16_t *out;
+    int64_t ot, oh;
+    float *lse;
+    int64_t tokens;
+    int32_t heads;
+    KvCache cache;
+    KvBatch batch;
+    int32_t max_kv;
+    float scale;
+    int32_t causal, window;
+};
+
+struct AttnShape {
+    int64_t tokens;
+    int32_t heads, kv_heads, head_dim, batch, max_tokens, max_kv;
+};
+
+int64_t attention_workspace(const AttnShape &s);
+cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st);
+
+cudaError_t read_kvcache_error(uint32_t *code);
+cudaError_t read_attention_error(uint32_t *code);
+
 }  // namespace h3fp4

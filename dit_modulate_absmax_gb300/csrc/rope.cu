@@ -1,0 +1,133 @@
+// rope.cu -- rotary positions with several axes (h3fp4_rope_axes).
+//
+// Reads and writes each value once: 4 bytes a channel, bound by HBM.  A CTA
+// takes 4 tokens and a range of heads.  It first computes the cosines and
+// sines of its tokens' pairs into shared memory (they serve every head), then
+// two warps walk each token's heads, a lane holding 8 channels (16 bytes) and
+// their coefficients in registers.
+#include <cuda_bf16.h>
+
+#include "rope.cuh"
+
+namespace h3fp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTokens = 4;                       // tokens per CTA
+constexpr int kWarpsPerToken = kThreads / 32 / kTokens;
+constexpr int kInFlight = 4;                     // head groups in flight per warp
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t bf_pack(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <int kLayout>
+__global__ void __launch_bounds__(kThreads)
+    rope_kernel(const uint16_t *x, int64_t xt, int64_t xh, uint16_t *out, int64_t ot, int64_t oh, int64_t tokens,
+                int heads, int dim, int heads_per_cta, RopeArgs r)
+{
+    __shared__ float2 cs[kTokens][kRopeMaxPairs];
+    // halves: a warp's channels, member e of each lane's eight side by side, so that partners are read
+    // without bank conflicts
+    __shared__ uint16_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 8][32];
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+    for (int i = threadIdx.x; i < kTokens * r.pairs; i += kThreads) {
+        const int tt = i / r.pairs, p = i - tt * r.pairs;
+        if (t0 + tt < tokens) {
+            const float pos = r.positions[(t0 + tt) * r.ld_positions + rope_axis(r, p)];
+            cs[tt][p] = rope_cos_sin(r.inverse ? -pos : pos, rope_turns(r, p));
+        }
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tt = warp % kTokens;
+    const int64_t t = t0 + tt;
+    if (t >= tokens)
+        return;
+    const int per_head = dim >> 3, per_warp = 32 / per_head;
+    const int sub = lane / per_head, c0 = (lane - sub * per_head) * 8;
+    const bool live = sub < per_warp;
+
+    float cosv[8], ss[8];
+    uint32_t turned = 0;      // channels that turn
+    int from[8];              // halves: where the partner stands in the warp's buffer
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const RopeChannel ch = rope_channel(r, c0 + e);
+        const float2 v = ch.pair >= 0 && live ? cs[tt][ch.pair] : make_float2(1.0f, 0.0f);
+        cosv[e] = v.x;
+        ss[e] = ch.first ? -v.y : v.y;
+        turned |= ch.pair >= 0 ? 1u << e : 0u;
+        from[e] = (ch.partner & 7) * 32 + sub * per_head + (ch.partner >> 3);
+    }
+    const int begin = blockIdx.y * heads_per_cta, end = min(heads, begin + heads_per_cta);
+    const int step = kWarpsPerToken * per_warp;
+    const uint16_t *xp = x + t * xt + c0;
+    uint16_t *op = out + t * ot + c0;
+    for (int h0 = begin + (warp / kTokens) * per_warp; h0 < end; h0 += kInFlight * step) {   // the same in the whole warp
+        uint4 raw[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int h = h0 + u * step + sub;
+            raw[u] = live && h < end ? *reinterpret_cast<const uint4 *>(xp + h * xh) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+            const int h = h0 + u * step + sub;
+            const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+            float v[8], partner[8], y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf_lo(w[i]);
+                v[2 * i + 1] = bf_hi(w[i]);
+            }
+            if constexpr (kLayout == 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    partner[e] = v[e ^ 1];
+            } else {
+                uint16_t *buf = &swap[warp][0][0];
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    buf[e * 32 + lane] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    partner[e] = __uint_as_float(static_cast<uint32_t>(live ? buf[from[e]] : 0) << 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                y[e] = (turned >> e) & 1u ? rope_mix(v[e], partner[e], cosv[e], ss[e]) : v[e];
+            if (live && h < end)
+                *reinterpret_cast<uint4 *>(op + h * oh) =
+                    make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const uint16_t *x, int64_t xt, int64_t xh, uint16_t *out, int64_t ot, int64_t oh,
+                        int64_t tokens, int heads, int dim, const RopeArgs &r, cudaStream_t st)
+{
+    const int64_t groups = (tokens + kTokens - 1) / kTokens;
+    // Few tokens: their heads are spread over several CTAs until every SM has one.
+    const int per_pass = kWarpsPerToken * (32 / (dim / 8));
+    int64_t split = (sm_count() + groups - 1) / groups;
+    const int64_t most = (heads + per_pass - 1) / per_pass;
+    split = split < 1 ? 1 : split > most ? most : split;
+    const int heads_per_cta = static_cast<int>(((heads + split - 1) / split + per_pass - 1) / per_pass) * per_pass;
+    const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>((heads + heads_per_cta - 1) / heads_per_cta));
+    if (r.layout == 0)
+        rope_kernel<0><<<grid, kThreads, 0, st>>>(x, xt, xh, out, ot, oh, tokens, heads, dim, heads_per_cta, r);
+    else
+        rope_kernel<1><<<grid, kThreads, 0, st>>>(x, xt, xh, out, ot, oh, tokens, heads, dim, heads_per_cta, r);
+    return cudaGetLastError();
+}
+
+}  // namespace h3fp4

@@ -260,6 +260,172 @@ H3FP4_API h3fp4_status h3fp4_gemm_gated_residual(
     int64_t k, const h3fp4_gemm_config *cfg, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Attention between the QKV and the attention-output projections: rotary
+ * positions with several axes, an 8-bit key/value cache in pages, and the
+ * attention that reads it.  No counterpart on the source pages, which stop at
+ * the linears; arithmetic and layouts are defined here.
+ * ---------------------------------------------------------------------------
+ *
+ * h3fp4_rope -- rotary positions along up to 4 axes (time, height, width, ...).
+ *
+ * The first dims[0] channels of a head turn with the position on axis 0, the
+ * next dims[1] with axis 1, and so on; channels past sum(dims) are copied.
+ * Pair j of axis a (j < dims[a]/2) takes the angle phi = position * frequency,
+ * with the frequency of that pair in radians per unit of position, and
+ *     a' = RN_bf16(a cos(phi) - b sin(phi)),  b' = RN_bf16(a sin(phi) + b cos(phi))
+ * in FP32 before the rounding.  The angle is reduced to a fraction of a turn
+ * without rounding error, so that the result keeps FP32 accuracy at any
+ * position a float holds exactly.  Non-finite positions or frequencies, or
+ * |position * frequency| >= 2^24 turns, are outside the definition: their
+ * results are unspecified.
+ * inverse = 1 turns by -phi: the inverse map and, the map being orthogonal,
+ * also the gradient of the forward one.
+ */
+#define H3FP4_ROPE_MAX_AXES 4
+typedef struct h3fp4_rope {
+    const float *positions;     /* device [tokens, axes], leading dimension ld_positions (>= axes) */
+    int64_t ld_positions;
+    const double *freqs;        /* device [sum(dims)/2]: the pairs of axis 0, then of axis 1, ... */
+    int32_t axes;               /* 1 .. H3FP4_ROPE_MAX_AXES */
+    int32_t dims[H3FP4_ROPE_MAX_AXES]; /* channels of each axis: even, >= 0, their sum <= the head's channels */
+    int32_t layout;             /* within an axis' channels, pair j is 0: (2j, 2j + 1); 1: (j, j + dims/2) */
+    int32_t inverse;            /* 0 or 1 */
+} h3fp4_rope;
+
+/*
+ * h3fp4_rope_axes -- out = x with every head of every token turned.
+ *
+ *   x_bf16, out_bf16  [tokens, heads, head_dim] bf16, the channels contiguous; strides of tokens and
+ *                     heads in elements (multiples of 8, not negative), 16-byte aligned.  out either is x
+ *                     (same pointer and strides: in place) or does not overlap it (the two address ranges
+ *                     from first to last element; else H3FP4_ERR_UNSUPPORTED).  Queries and keys in the
+ *                     rows of a QKV projection are one call with heads = 2 H.
+ *   head_dim          multiple of 8, 8 .. 256
+ */
+H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_stride, int64_t x_head_stride,
+                                       void *out_bf16, int64_t out_token_stride, int64_t out_head_stride,
+                                       int64_t tokens, int32_t heads, int32_t head_dim, const h3fp4_rope *rope,
+                                       void *stream);
+
+/*
+ * h3fp4_kv_cache -- keys and values in E4M3 (bias 7, max 448), in pages of
+ * page_size tokens, with one FP32 scale per page and head for the keys and
+ * one for the values: a value is code * scale.
+ *
+ *   codes   [num_pages, heads, page_size, head_dim] bytes, contiguous, 16-byte aligned
+ *   scales  [num_pages, heads] float, contiguous
+ *   page_size 16, 32, 64 or 128;  head_dim 64 or 128
+ *
+ * A page table names each sequence's pages: position p of sequence b is token
+ * p % page_size of page page_table[b * ld_table + p / page_size].  A page may
+ * appear in several tables as long as no call writes it for more than one.
+ */
+typedef struct h3fp4_kv_cache {
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int32_t num_pages, page_size, heads, head_dim;
+} h3fp4_kv_cache;
+
+/*
+ * h3fp4_kv_batch -- the sequences of a call.  Tokens of all sequences are
+ * packed: those of sequence b are rows cu_tokens[b] .. cu_tokens[b+1] - 1 of
+ * the call's token arrays, max_tokens the most that any sequence has.  The
+ * arrays are in DEVICE memory (they may change between replays of a captured
+ * call); what they hold is checked by the kernels: an entry that is out of
+ * range (a page outside the cache or past the table, rows outside the token
+ * arrays, more tokens than max_tokens) is not followed, and bit 512 is
+ * reported through h3fp4_device_error.  What such a sequence's outputs hold is
+ * then unspecified.
+ */
+typedef struct h3fp4_kv_batch {
+    const int32_t *page_table;  /* device [batch, ld_table] */
+    int64_t ld_table;           /* pages a sequence's row of the table has room for */
+    const int32_t *len;         /* device [batch]: meaning at each call */
+    const int32_t *cu_tokens;   /* device [batch + 1] */
+    int32_t batch;              /* 0 .. 65535 */
+    int32_t max_tokens;         /* 0 .. 1,000,000 */
+} h3fp4_kv_batch;
+
+/*
+ * h3fp4_kv_cache_write -- quantises new keys and values into the cache.
+ *
+ * len[b] is the number of tokens that sequence b holds before the call; its
+ * new tokens take the positions from len[b] on.  For each page and head with
+ * new tokens, for keys and values each:
+ *     e = ceil(log2(amax / 448)) held to [-40, 119] (amax = 0: -40), amax over the page's new values
+ *     scale = 2^e, or the page's scale so far if that is larger and the page holds earlier tokens
+ *     code = E4M3_RNE_sat(x / scale)
+ * Where the scale grows, the page's earlier codes are rounded to it (a shift
+ * by a power of two: exact but for codes that become subnormal).  Powers of
+ * two keep that repeated rounding harmless, and code * scale exact in bf16.  A
+ * NaN or infinite element is stored as the E4M3 NaN 0x7F and does not count
+ * for amax.  Pages' tokens past the new ones keep their bytes.
+ *
+ *   k_bf16, v_bf16  [tokens, heads, head_dim] bf16, strides as for h3fp4_rope_axes
+ *   rope            NULL, or positions of the new tokens: keys are turned first, with the bf16 result
+ *                   of h3fp4_rope_axes
+ */
+H3FP4_API h3fp4_status h3fp4_kv_cache_write(const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch,
+                                            const void *k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                                            const void *v_bf16, int64_t v_token_stride, int64_t v_head_stride,
+                                            int64_t tokens, const h3fp4_rope *rope, void *stream);
+
+/*
+ * h3fp4_kv_cache_read -- the cache's keys and values as bf16,
+ * RN_bf16(code * scale).
+ *
+ * len[b] is the first position of sequence b that is read (NULL: 0 for every
+ * sequence), its number of tokens cu_tokens[b+1] - cu_tokens[b].
+ *
+ *   k_bf16, v_bf16  [tokens, heads, head_dim] bf16 outputs, strides as for h3fp4_rope_axes; one of the
+ *                   two may be NULL
+ */
+H3FP4_API h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch, void *k_bf16,
+                                           int64_t k_token_stride, int64_t k_head_stride, void *v_bf16,
+                                           int64_t v_token_stride, int64_t v_head_stride, int64_t tokens,
+                                           void *stream);
+
+/*
+ * h3fp4_kv_attention -- attention of new queries over the cache.
+ *
+ * len[b] is the number of keys of sequence b, those of the new tokens
+ * included; query i of its n tokens stands at position len[b] - n + i.  A
+ * query sees the positions j < len[b] with
+ *     j <= its own position          if causal, and
+ *     j >  its own position - window if window > 0.
+ * For each query and head h (which reads cache head h / (heads / cache heads)):
+ *     s_j = softmax_scale * q . k_j,  out = RN_bf16(sum_j exp(s_j) v_j / sum_j exp(s_j)),
+ *     lse = log(sum_j exp(s_j))
+ * with sums, the softmax and its statistics in FP32.  The products take the
+ * stored codes exactly; q is scaled by a power of two per row and exact in
+ * FP16 but for channels below 2^-28 of the row's largest, and the weights
+ * exp(s_j - max) enter the second product rounded to FP16.  A query that sees
+ * nothing gets out = 0 and lse = -infinity.  Positions that a query does not
+ * see have no effect on it, whatever their codes hold.
+ *
+ *   q_bf16, out_bf16  [tokens, heads, head_dim] bf16, strides as for h3fp4_rope_axes, no overlap
+ *   lse               NULL, or [tokens, heads] float, contiguous
+ *   heads             a multiple of the cache's heads, at most 65535
+ *   max_kv            the most keys that any sequence has (sizes the launch; longer ones are
+ *                     reported as out of range); at most 2^30
+ *   softmax_scale     finite; scales of the cache's pages must be positive and finite
+ *   workspace         h3fp4_kv_attention_workspace bytes of device scratch, 16-byte aligned (contents on
+ *                     entry are ignored; two calls that overlap on the GPU must not share it); may be NULL
+ *                     where that is 0
+ */
+H3FP4_API h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                                          void *out_bf16, int64_t out_token_stride, int64_t out_head_stride,
+                                          float *lse, int64_t tokens, int32_t heads, const h3fp4_kv_cache *cache,
+                                          const h3fp4_kv_batch *batch, int32_t max_kv, float softmax_scale,
+                                          int32_t causal, int32_t window, void *workspace, int64_t workspace_bytes,
+                                          void *stream);
+
+/* Bytes of workspace that h3fp4_kv_attention wants for these sizes (host only; -1 for sizes it refuses). */
+H3FP4_API int64_t h3fp4_kv_attention_workspace(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                               int32_t batch, int32_t max_tokens, int32_t max_kv);
+
+/*
  * h3fp4_swizzle_scales -- helper for preparing weights: copies a LOGICAL
  * row-major E4M3 scale matrix [rows, cols] (leading dimension ld bytes) into
  * the scale layout above, padding rows up to a multiple of 128 with zeros.
@@ -309,7 +475,8 @@ H3FP4_API h3fp4_status h3fp4_swiglu_pack_noalloc(const void *gate_bf16, int64_t 
  * their time limit (2 s) record a nonzero code there instead of hanging, and
  * return.  Bits: GEMM waits 1 (a free stage), 2 (operands landed), 4 (a
  * finished accumulator), 8 (a drained accumulator), 16 (scale atoms landed);
- * 256 the cooperative producer's grid barrier.
+ * 256 the cooperative producer's grid barrier; 512 an entry of a page table
+ * or length array out of range (attention calls).
  * Returns H3FP4_OK and stores the word in *code (0 = no error).
  */
 H3FP4_API h3fp4_status h3fp4_device_error(uint32_t *code);
