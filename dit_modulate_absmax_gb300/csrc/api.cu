@@ -454,13 +454,13 @@ h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int6
                                                                      batch->batch, batch->max_tokens, max_kv});
     if (need > 0 && workspace == nullptr)
         return H3FP4_ERR_NULL;
-    if (workspace_bytes < need)
+    if (need < 0 || workspace_bytes < need)
         return H3FP4_ERR_SHAPE;
     if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
         return H3FP4_ERR_ALIGN;
     const h3fp4::AttnArgs a{static_cast<const uint16_t *>(q_bf16), q.token, q.head, static_cast<uint16_t *>(out_bf16),
                             out.token, out.head, lse, tokens, heads, *cache, *batch, max_kv, softmax_scale, causal,
-                            window};
+                            window > max_kv ? 0 : window};   // a window past every position hides nothing
     return from_cuda(h3fp4::launch_attention(a, workspace, as_stream(stream)));
 }
 

@@ -1,0 +1,110 @@
+// attention.cuh -- what the attention kernels share: the rows of a tile, what
+// they see, and the queries' conversion to FP16.
+//
+// All of a cache head's query heads are taken together: row r of sequence b
+// and cache head kh is query token r / group, head kh * group + r % group, so
+// that keys and values are read once for the group.
+//
+// Softmax in base 2 with the values' scales inside: a key j in page P has
+//     s'_j = S_j * (c * k_scale_P) + log2(v_scale_P),   S = q~ . k codes,
+// where q~ is the query row times a power of two that brings its largest
+// channel to [2^14, 2^15) (exact in FP16 but for channels below 2^-28 of it)
+// and c = |softmax_scale| * log2(e) / that power (the sign goes into q~).
+// The weight that meets the value codes is 2^(s'_j - m'), with m' the running
+// maximum of s': the largest CONTRIBUTION to the output, not the largest
+// probability, is 1, so FP16's range serves it whatever the pages' scales.
+// Dividing a page's weights by its scale gives the softmax's own sum.
+#pragma once
+
+#include "kvcache.cuh"
+
+namespace h3fp4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Positions [lo, hi) that query i of a sequence sees.
+struct Span {
+    int lo, hi;
+};
+
+__device__ __forceinline__ Span seen_by(const AttnArgs &a, const KvSequence &s, int i)
+{
+    const int pos = s.len - s.n + i;   // may be negative: nothing seen if causal
+    Span r{0, s.len};
+    if (a.causal)
+        r.hi = min(s.len, pos + 1);
+    if (a.window > 0)
+        r.lo = max(0, pos - a.window + 1);   // pos >= -2^20 and window <= 2^31 - 1: no wrap
+    if (r.hi <= r.lo)
+        r.hi = r.lo = max(0, min(r.lo, s.len));   // empty
+    return r;
+}
+
+// Power of two that brings a row whose largest magnitude is amax (a bf16
+// pattern) to [2^14, 2^15), and its inverse; 1 for zero and non-finite rows.
+__device__ __forceinline__ float2 row_power(uint32_t amax_bf16)
+{
+    const int e = static_cast<int>(amax_bf16 >> 7);   // biased exponent
+    if (amax_bf16 == 0 || e == 255)
+        return make_float2(1.0f, 1.0f);
+    const int s = min(14 - (e - 127), 126);           // tiny rows: as far as a float's power goes
+    return make_float2(__uint_as_float(static_cast<uint32_t>(s + 127) << 23),
+                       __uint_as_float(static_cast<uint32_t>(127 - s) << 23));
+}
+
+// Largest magnitude among the two bf16 of each word, as a pattern.
+__device__ __forceinline__ uint32_t bf16x2_absmax(uint32_t m2, uint32_t w) { return __vmaxu2(m2, w & 0x7FFF7FFFu); }
+
+// Two bf16 times a power of two, as FP16.
+__device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w, float f)
+{
+    return pack_half2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+
+// A page's table entry as the kernels keep it: id (< 0: out of range), the
+// keys' scale, log2 of the values' scale and its inverse.
+struct PageEntry {
+    int32_t id;
+    float ks, lv, inv_vs;
+};
+
+// Bit 7 of each byte that is an E4M3 NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
+{
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// A launch's split over the keys: `splits` parts of `chunk` tokens each.
+struct SplitPlan {
+    int32_t splits, chunk;
+};
+
+SplitPlan plan_rows(const AttnShape &s);
+cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
+cudaError_t launch_attention_join(const AttnArgs &a, const SplitPlan &plan, const float2 *stat, const float *part,
+                                  cudaStream_t st);
+cudaError_t read_attention_rows_error(uint32_t *code);
+
+}  // namespace h3fp4

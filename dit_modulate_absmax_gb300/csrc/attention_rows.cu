@@ -1,0 +1,537 @@
+// attention_rows.cu -- attention of few queries (decoding): a tile of 8 or 16
+// rows against a part of the keys, joined afterwards where there are several
+// parts.
+//
+// Reads every visible code once (2 * dim bytes a token and cache head) for at
+// most 16 rows, so it is bound by HBM.  What it takes to stay there:
+//  - The keys are split over CTAs until the SMs are covered; each of a CTA's 4
+//    warps runs its own online softmax over units of 32 tokens, fed by its own
+//    ring of asynchronous 16-byte copies, with no barrier in the loop.
+//  - Codes go from shared memory to registers as they lie and are converted to
+//    FP16 there (exact) for mma.sync m16n8k16 with FP32 accumulation.  The
+//    order of the contraction index is free, so a lane takes 4 adjacent
+//    channels where the instruction wants (2t, 2t+1, 2t+8, 2t+9): S = Q K^T
+//    reads each token's row in 16-byte pieces, and in O^T = V^T P^T a lane
+//    reads 16 channels of its 4 tokens and pairs up tokens with byte
+//    permutes.  S's accumulator layout is that product's B operand.
+//  - Shared-memory rows are XOR-swizzled in 16-byte pieces (dim 128: no bank
+//    conflicts; dim 64: two-way for the values).
+// The tensor work is small next to the memory's (24 instructions per 4 KB of
+// codes at dim 128 and 8 rows), so the older warp-level instruction serves; a
+// 128-row tcgen05 tile would be 8-16 times padding.
+#include "attention.cuh"
+
+namespace h3fp4 {
+namespace {
+
+__device__ uint32_t g_error;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 32;                 // tokens a warp takes at a time
+constexpr int kStages = 3;
+constexpr int kMaxEntries = 512;          // pages of one part
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int kLeft>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Byte offset of 16-byte piece c of row r of a [32][kDim] tile.
+template <int kDim>
+__device__ __forceinline__ uint32_t piece(int r, int c)
+{
+    const int l = r * (kDim / 16) + c, line = l >> 3;
+    return static_cast<uint32_t>((line << 7) | (((l & 7) ^ (line & 7)) << 4));
+}
+
+template <int kDim, int kRows>
+__global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan plan, int row_tiles, float2 *ws_stat,
+                                                        float *ws_out)
+{
+    constexpr int kSteps = kDim / 16;            // k16 steps of Q K^T = 16-channel tiles of O^T
+    constexpr int kHalf = kRows / 8;             // groups of 8 rows
+    constexpr int kTile = kUnit * kDim;          // bytes of a unit's keys
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ PageEntry entry[kMaxEntries];
+    __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int b = blockIdx.y, page = a.cache.page_size, group = a.heads / a.cache.heads;
+    const int tile = blockIdx.x % row_tiles, kh = blockIdx.x / row_tiles % a.cache.heads;
+    const int split = blockIdx.x / row_tiles / a.cache.heads;
+    const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+    if (!s.ok || s.len > a.max_kv || (s.len > 0 && (s.len - 1) / page >= a.batch.ld_table)) {
+        if (threadIdx.x == 0)
+            atomicOr(&g_error, ERR_KV_RANGE);
+        return;
+    }
+    const int rows = s.n * group, row0 = tile * kRows;   // n <= 2^20 and rows of this kernel are few: no overflow
+    if (row0 >= rows || (split > 0 && split * plan.chunk >= s.len))
+        return;
+    // what the tile's first and last rows see bounds what all of them see
+    const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, min(rows - 1, row0 + kRows - 1) / group);
+    const int begin = max(split * plan.chunk, min(first.lo, last.lo) & ~(kUnit - 1));
+    const int end = min(min((split + 1) * plan.chunk, s.len), max(first.hi, last.hi));
+
+    // Page entries of [begin, end), then the first copies, then the scales.
+    const int page0 = begin / page, pages = end > begin ? (end - 1) / page - page0 + 1 : 0;
+    for (int i = threadIdx.x; i < pages; i += kThreads) {
+        int32_t id = a.batch.page_table[b * a.batch.ld_table + page0 + i];
+        if (id < 0 || id >= a.cache.num_pages) {
+            atomicOr(&g_error, ERR_KV_RANGE);
+            id = -1;
+        }
+        entry[i].id = id;
+    }
+    __syncthreads();
+
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * (kStages * 2 * kTile);
+    const auto fetch = [&](int unit, int stage) {   // unit: first token
+        if (unit < end) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int c = lane + 32 * i, r = c / kSteps, tok = unit + r;
+                const int32_t id = tok < end ? entry[tok / page - page0].id : -1;
+                if (id >= 0) {
+                    const int64_t at =
+                        ((static_cast<int64_t>(id) * a.cache.heads + kh) * page + (tok & (page - 1))) * kDim + (c % kSteps) * 16;
+                    const uint32_t dst = ring + stage * (2 * kTile) + piece<kDim>(r, c % kSteps);
+                    copy16(dst, a.cache.k_codes + at);
+                    copy16(dst + kTile, a.cache.v_codes + at);
+                }
+            }
+        }
+        copy_commit();
+    };
+    const int unit0 = begin + warp * kUnit;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        fetch(unit0 + i * kWarps * kUnit, i);
+    for (int i = threadIdx.x; i < pages; i += kThreads) {
+        const int64_t bh = static_cast<int64_t>(max(entry[i].id, 0)) * a.cache.heads + kh;
+        const float vs = a.cache.v_scale[bh];
+        entry[i].ks = a.cache.k_scale[bh];
+        entry[i].lv = lg2(vs);
+        entry[i].inv_vs = __frcp_rn(vs);
+    }
+
+    // Q: rows g and g + 8; this lane's channels kDim/4 * t ...
+    uint32_t q[kSteps][4];
+    float c_row[kHalf];
+    Span see[kHalf];
+#pragma unroll
+    for (int hf = 0; hf < kHalf; ++hf) {
+        const int r = row0 + g + 8 * hf;
+        const bool live = r < rows;
+        const uint16_t *src = a.q + (s.row + (live ? r / group : 0)) * a.qt + (kh * group + (live ? r % group : 0)) * a.qh +
+                              (kDim / 4) * t;
+        uint32_t w[kDim / 8], m2 = 0;
+#pragma unroll
+        for (int i = 0; i < kDim / 32; ++i) {
+            const uint4 v = live ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i)
+            m2 = bf16x2_absmax(m2, w[i]);
+        uint32_t amax = max(m2 & 0xFFFFu, m2 >> 16);
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const float2 p = row_power(amax);
+        const float f = a.scale < 0.0f ? -p.x : p.x;
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            q[st][hf] = bf16x2_to_half2(w[2 * st], f);
+            q[st][hf + 2] = bf16x2_to_half2(w[2 * st + 1], f);
+            if (kHalf == 1)
+                q[st][1] = q[st][3] = 0u;
+        }
+        c_row[hf] = fabsf(a.scale) * kLog2e * p.y;
+        see[hf] = live ? seen_by(a, s, r / group) : Span{0, 0};
+    }
+    const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);   // seen by every row
+    const int out_lo = min(first.lo, last.lo), out_hi = max(first.hi, last.hi); // seen by any
+    __syncthreads();   // scales
+
+    float o[kHalf][kSteps][4];
+    float m[kHalf], l[kHalf];
+#pragma unroll
+    for (int hf = 0; hf < kHalf; ++hf) {
+        m[hf] = -INFINITY;
+        l[hf] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[hf][j][e] = 0.0f;
+    }
+
+    int stage = 0;
+    for (int unit = unit0; unit < end; unit += kWarps * kUnit) {
+        copy_wait<kStages - 2>();
+        __syncwarp();
+        const uint8_t *kt = dyn + warp * (kStages * 2 * kTile) + stage * (2 * kTile), *vt = kt + kTile;
+
+        float sc[4][4];   // S of the unit's four groups of 8 tokens
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            uint32_t w[kDim / 16];
+#pragma unroll
+            for (int i = 0; i < kDim / 64; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(kt + piece<kDim>(8 * n + g, (kDim / 64) * t + i));
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+            sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st)
+                mma_f16(sc[n], q[st], e4m3x2_to_f16x2(w[st] & 0xFFFFu), e4m3x2_to_f16x2(w[st] >> 16));
+        }
+
+        const bool edge = unit < in_lo || unit + kUnit > in_hi;
+        float top[kHalf];
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf)
+            top[hf] = -INFINITY;
+        const int e0 = unit / page - page0, e1 = min(pages - 1, (unit + 16) / page - page0);
+        const PageEntry pe[2] = {entry[e0], entry[e1]};
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int hf = 0; hf < kHalf; ++hf)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float &v = sc[n][2 * hf + e];
+                    v = fmaf(v, c_row[hf] * pe[n >> 1].ks, pe[n >> 1].lv);
+                    if (edge) {
+                        const int tok = unit + 8 * n + 2 * t + e;
+                        if (tok < see[hf].lo || tok >= see[hf].hi)
+                            v = -INFINITY;
+                    }
+                    top[hf] = fmaxf(top[hf], v);
+                }
+        bool grew = false;
+        float keep[kHalf], ref[kHalf];
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf) {
+            top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 1));
+            top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 2));
+            const float mm = fmaxf(m[hf], top[hf]);
+            ref[hf] = mm == -INFINITY ? 0.0f : mm;
+            keep[hf] = ex2(m[hf] - ref[hf]);
+            grew |= mm > m[hf];
+            m[hf] = mm;
+        }
+        if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+            for (int hf = 0; hf < kHalf; ++hf) {
+                l[hf] *= keep[hf];
+                // the accumulator holds rows 2t and 2t + 1, whose factors are in lanes 8t and 8t + 4
+                const float f0 = __shfl_sync(0xFFFFFFFFu, keep[hf], 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, keep[hf], 8 * t + 4);
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) {
+                    o[hf][j][0] *= f0;
+                    o[hf][j][1] *= f1;
+                    o[hf][j][2] *= f0;
+                    o[hf][j][3] *= f1;
+                }
+            }
+        }
+        uint32_t pb[kHalf][4];   // weights of the four token groups, FP16 pairs
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf) {
+#pragma unroll
+            for (int n2 = 0; n2 < 2; ++n2) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int n = 2 * n2; n < 2 * n2 + 2; ++n) {
+                    const float p0 = ex2(sc[n][2 * hf] - ref[hf]), p1 = ex2(sc[n][2 * hf + 1] - ref[hf]);
+                    sum += p0 + p1;
+                    pb[hf][n] = pack_half2(p0, p1);
+                }
+                l[hf] = fmaf(sum, pe[n2].inv_vs, l[hf]);
+            }
+        }
+
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {   // 16 tokens at a time
+            constexpr int kW = kDim / 32;  // words of 4 channels per token: this lane's kDim/8 channels
+            uint32_t w[4][kW];
+            uint32_t odd = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * hh + 2 * t + (i & 1) + 8 * (i >> 1);
+                if constexpr (kDim == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vt + piece<kDim>(r, g));
+                    w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(vt + piece<kDim>(r, g >> 1) + 8 * (g & 1));
+                    w[i][0] = v.x; w[i][1] = v.y;
+                }
+                if (edge) {   // codes that no row sees may be anything: zeros
+                    const int tok = unit + r;
+                    const uint32_t mask = tok >= out_lo && tok < out_hi ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+                    for (int x = 0; x < kW; ++x) {
+                        w[i][x] &= mask;
+                        odd |= nan_bytes(w[i][x]);
+                    }
+                }
+            }
+            // NaN among tokens that some rows see and others do not: a zero weight would not keep it out.  The NaN
+            // codes leave the product, and a product of two masks counts the NaNs that each row and channel sees.
+            const bool slow = edge && __any_sync(0xFFFFFFFFu, odd != 0);
+#pragma unroll
+            for (int x = 0; x < kW; ++x) {
+                // bytes of 4 tokens per channel: a 4 x 4 byte transpose
+                const uint32_t a01 = __byte_perm(w[0][x], w[1][x], 0x5140), b01 = __byte_perm(w[0][x], w[1][x], 0x7362);
+                const uint32_t a23 = __byte_perm(w[2][x], w[3][x], 0x5140), b23 = __byte_perm(w[2][x], w[3][x], 0x7362);
+                const uint32_t ch[4] = {__byte_perm(a01, a23, 0x5410), __byte_perm(a01, a23, 0x7632),
+                                        __byte_perm(b01, b23, 0x5410), __byte_perm(b01, b23, 0x7632)};
+#pragma unroll
+                for (int j2 = 0; j2 < 2; ++j2) {
+                    uint32_t c0 = ch[2 * j2], c1 = ch[2 * j2 + 1];
+                    const int j = 2 * x + j2;
+                    if (slow) {
+                        const uint32_t n0 = nan_bytes(c0) >> 7, n1 = nan_bytes(c1) >> 7;   // 1 in each NaN byte
+                        c0 &= ~(n0 * 0xFFu);
+                        c1 &= ~(n1 * 0xFFu);
+                        const auto ones = [](uint32_t n) { return ((n & 1u) | (n >> 8 & 1u) << 16) * 0x3C00u; };
+                        const uint32_t na[4] = {ones(n0), ones(n1), ones(n0 >> 16), ones(n1 >> 16)};
+#pragma unroll
+                        for (int hf = 0; hf < kHalf; ++hf) {
+                            uint32_t vis[2];
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                const int tok = unit + 16 * hh + 8 * n + 2 * t;
+                                vis[n] = (tok >= see[hf].lo && tok < see[hf].hi ? 0x3C00u : 0u) |
+                                         (tok + 1 >= see[hf].lo && tok + 1 < see[hf].hi ? 0x3C000000u : 0u);
+                            }
+                            float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma_f16(cnt, na, vis[0], vis[1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (cnt[e] > 0.0f)
+                                    o[hf][j][e] = __uint_as_float(0x7FC00000u);
+                        }
+                    }
+                    const uint32_t av[4] = {e4m3x2_to_f16x2(c0 & 0xFFFFu), e4m3x2_to_f16x2(c1 & 0xFFFFu),
+                                            e4m3x2_to_f16x2(c0 >> 16), e4m3x2_to_f16x2(c1 >> 16)};
+#pragma unroll
+                    for (int hf = 0; hf < kHalf; ++hf)
+                        mma_f16(o[hf][j], av, pb[hf][2 * hh], pb[hf][2 * hh + 1]);
+                }
+            }
+        }
+        __syncwarp();   // every lane has read the stage that the next copies overwrite
+        fetch(unit + (kStages - 1) * kWarps * kUnit, stage == 0 ? kStages - 1 : stage - 1);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+
+    // Join the warps: maxima and sums, then the outputs through shared memory (the rings are drained).
+#pragma unroll
+    for (int hf = 0; hf < kHalf; ++hf) {
+        l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 1);
+        l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 2);
+        if (t == 0) {
+            stat_m[warp][g + 8 * hf] = m[hf];
+            stat_l[warp][g + 8 * hf] = l[hf];
+        }
+    }
+    __syncthreads();
+    float *part = reinterpret_cast<float *>(dyn);   // [warp][row][kDim]
+#pragma unroll
+    for (int hf = 0; hf < kHalf; ++hf)
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)   // channels (kDim/8) g + 2j and + 1
+                *reinterpret_cast<float2 *>(part + (warp * kRows + 8 * hf + 2 * t + e) * kDim + (kDim / 8) * g + 2 * j) =
+                    make_float2(o[hf][j][e], o[hf][j][e + 2]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * (kDim / 4); i += kThreads) {
+        const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
+        if (row0 + r >= rows)
+            continue;
+        float mm = stat_m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w)
+            mm = fmaxf(mm, stat_m[w][r]);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(stat_m[w][r] - (mm == -INFINITY ? 0.0f : mm));
+            const float4 v = *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c);
+            sum.x = fmaf(v.x, f, sum.x);
+            sum.y = fmaf(v.y, f, sum.y);
+            sum.z = fmaf(v.z, f, sum.z);
+            sum.w = fmaf(v.w, f, sum.w);
+            ll = fmaf(stat_l[w][r], f, ll);
+        }
+        const int64_t row = s.row + (row0 + r) / group;
+        const int head = kh * group + (row0 + r) % group;
+        const int64_t at = row * a.heads + head;
+        if (plan.splits == 1) {
+            const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+            const __nv_bfloat162 x = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), y = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+            *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+            if (a.lse != nullptr && c == 0)
+                a.lse[at] = (mm + lg2(ll)) * kLn2;
+        } else {
+            *reinterpret_cast<float4 *>(ws_out + (at * plan.splits + split) * kDim + c) = sum;
+            if (c == 0)
+                ws_stat[at * plan.splits + split] = make_float2(mm, ll);
+        }
+    }
+}
+
+// Joins the parts of each row: one warp per query token and head.
+template <int kDim>
+__global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, SplitPlan plan, const float2 *ws_stat, const float *ws_out)
+{
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+    if (!s.ok || s.len > a.max_kv || w >= static_cast<int64_t>(s.n) * a.heads)
+        return;
+    const int64_t row = s.row + w / a.heads;
+    const int head = static_cast<int>(w % a.heads);
+    const int64_t at = row * a.heads + head;
+    const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
+    const float2 *stat = ws_stat + at * plan.splits;
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 32)
+        mm = fmaxf(mm, stat[i].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    constexpr int kPer = kDim / 32;
+    float sum[kPer], ll = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+        sum[c] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float2 st = stat[i];
+        const float f = ex2(st.x - ref);
+        ll = fmaf(st.y, f, ll);
+        const float *src = ws_out + (at * plan.splits + i) * kDim + lane * kPer;
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(src + c);
+            sum[c] = fmaf(v.x, f, sum[c]);
+            sum[c + 1] = fmaf(v.y, f, sum[c + 1]);
+        }
+    }
+    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+    uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(sum[c] * inv, sum[c + 1] * inv);
+        *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    if (a.lse != nullptr && lane == 0)
+        a.lse[at] = (mm + lg2(ll)) * kLn2;
+}
+
+}  // namespace
+
+// Parts of the keys: enough CTAs for kCtasPerSm on every SM, parts of 256
+// tokens at least (less leaves a warp fewer than two units) and at most what
+// kMaxEntries of the smallest pages hold.  Ragged batches launch as for their longest
+// sequence; the parts past a shorter one's end return at once.
+SplitPlan plan_rows(const AttnShape &s)
+{
+    constexpr int64_t kCtasPerSm = 4;
+    const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);
+    const int64_t tile = rows <= 8 ? 8 : 16;
+    const int64_t ctas = static_cast<int64_t>(s.batch) * s.kv_heads * ((rows + tile - 1) / tile);
+    const int64_t kv = s.max_kv < 1 ? 1 : s.max_kv;
+    int64_t splits = ctas > 0 ? (kCtasPerSm * sm_count() + ctas - 1) / ctas : 1;
+    const int64_t most = (kv + 255) / 256;
+    splits = splits > most ? most : splits;
+    int64_t chunk = (kv + splits - 1) / splits;
+    const int64_t round = kWarps * kUnit;
+    chunk = (chunk + round - 1) / round * round;
+    const int64_t cap = static_cast<int64_t>(kMaxEntries - 2) * 16 / round * round;
+    chunk = chunk > cap ? cap : chunk;
+    return SplitPlan{static_cast<int32_t>((kv + chunk - 1) / chunk), static_cast<int32_t>(chunk)};
+}
+
+namespace {
+
+template <int kDim, int kRows>
+cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+{
+    constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = kWarps * kRows * kDim * 4;
+    constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<kDim, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
+    const int64_t tiles = (rows + kRows - 1) / kRows;
+    const int64_t x = tiles * a.cache.heads * plan.splits;
+    if (x > INT32_MAX)
+        return cudaErrorInvalidValue;
+    rows_kernel<kDim, kRows><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(
+        a, plan, static_cast<int>(tiles), stat, part);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+{
+    const bool small = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads) <= 8;
+    if (a.cache.head_dim == 64)
+        return small ? run_rows<64, 8>(a, plan, stat, part, st) : run_rows<64, 16>(a, plan, stat, part, st);
+    return small ? run_rows<128, 8>(a, plan, stat, part, st) : run_rows<128, 16>(a, plan, stat, part, st);
+}
+
+cudaError_t launch_attention_join(const AttnArgs &a, const SplitPlan &plan, const float2 *stat, const float *part,
+                                  cudaStream_t st)
+{
+    const int64_t x = (static_cast<int64_t>(a.batch.max_tokens) * a.heads + kWarps - 1) / kWarps;
+    if (x > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(x), a.batch.batch);
+    if (a.cache.head_dim == 64)
+        join_kernel<64><<<grid, kThreads, 0, st>>>(a, plan, stat, part);
+    else
+        join_kernel<128><<<grid, kThreads, 0, st>>>(a, plan, stat, part);
+    return cudaGetLastError();
+}
+
+cudaError_t read_attention_rows_error(uint32_t *code)
+{
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_error, sizeof(v));
+    if (e != cudaSuccess)
+        return e;
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+    *code = v;
+    return e;
+}
+
+}  // namespace h3fp4
