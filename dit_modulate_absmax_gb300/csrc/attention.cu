@@ -7,7 +7,13 @@ namespace {
 
 constexpr int64_t kMostWorkspace = int64_t(1) << 50;
 
-SplitPlan plan_of(const AttnShape &s) { return plan_rows(s); }
+// Most rows (query tokens times query heads of a cache head) of a sequence
+// that the row kernel takes.
+constexpr int64_t kMostRows = 16;
+
+bool few_rows(const AttnShape &s) { return static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads) <= kMostRows; }
+
+SplitPlan plan_of(const AttnShape &s) { return few_rows(s) ? plan_rows(s) : plan_tile(s); }
 
 // Rows of parts that the workspace holds: an output and (maximum, sum) for each row and part.
 int64_t part_rows(const AttnShape &s, const SplitPlan &p)
@@ -37,12 +43,20 @@ cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st
     const SplitPlan plan = plan_of(s);
     float *part = static_cast<float *>(workspace);
     float2 *stat = reinterpret_cast<float2 *>(part + part_rows(s, plan) * s.head_dim);
-    cudaError_t e = launch_attention_rows(a, plan, stat, part, st);
+    cudaError_t e = few_rows(s) ? launch_attention_rows(a, plan, stat, part, st) : launch_attention_tile(a, plan, stat, part, st);
     if (e == cudaSuccess && plan.splits > 1)
         e = launch_attention_join(a, plan, stat, part, st);
     return e;
 }
 
-cudaError_t read_attention_error(uint32_t *code) { return read_attention_rows_error(code); }
+cudaError_t read_attention_error(uint32_t *code)
+{
+    uint32_t rows = 0, tile = 0;
+    cudaError_t e = read_attention_rows_error(&rows);
+    if (e == cudaSuccess)
+        e = read_attention_tile_error(&tile);
+    *code = rows | tile;
+    return e;
+}
 
 }  // namespace h3fp4

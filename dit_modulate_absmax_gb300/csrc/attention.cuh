@@ -105,6 +105,9 @@ SplitPlan plan_rows(const AttnShape &s);
 cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
 cudaError_t launch_attention_join(const AttnArgs &a, const SplitPlan &plan, const float2 *stat, const float *part,
                                   cudaStream_t st);
+SplitPlan plan_tile(const AttnShape &s);
+cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
+cudaError_t read_attention_tile_error(uint32_t *code);
 cudaError_t read_attention_rows_error(uint32_t *code);
 
 }  // namespace h3fp4

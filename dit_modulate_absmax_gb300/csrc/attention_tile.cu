@@ -1,0 +1,570 @@
+// attention_tile.cu -- attention of many queries: two tiles of 128 rows per
+// CTA against tiles of 128 keys, both products on the tcgen05 tensor cores.
+//
+// The work is 4 * dim FLOP a visible pair and row; the bound is the FP16
+// tensor rate (bf16's: 2.1 MFLOP-pairs, 512 SM cycles, a 128 x 128 x 128
+// product) next to the exponentials and shared memory.  The parts:
+//  - 8 softmax warps, a thread a row: S from TMEM (tcgen05.ld), one pass for
+//    the maximum and one for the weights, which go back to TMEM as FP16 over
+//    S's own columns, the A operand of the second product.  The two row tiles
+//    alternate, one in the tensor cores while the other is in the softmax.
+//    The output accumulator in TMEM is rescaled only when a row's maximum has
+//    grown by more than 2^8 since the reference it is kept against; FP16 and
+//    FP32 hold weights up to 2^8 as well as up to 1.
+//  - 4 conversion warps: codes straight from global memory to registers (they
+//    are in L2: every row tile of a head reads them), E4M3 -> FP16, which is
+//    exact, and into shared memory in the 128-byte-swizzled operand layout.
+//    Keys are the first product's K-major B operand; values have the same
+//    layout, read as the second product's MN-major B operand.
+//  - 1 warp issues the MMAs.
+// Shared memory at dim 128: queries 64 KB, two stages of keys and of values 32
+// KB each.
+#include <type_traits>
+
+#include "attention.cuh"
+#include "ptx.cuh"
+
+namespace h3fp4 {
+namespace {
+
+__device__ uint32_t g_error;
+constexpr uint32_t ERR_ATTN_WAIT = 1u << 10;   // a pipeline wait gave up
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+constexpr int kKeys = 128;                     // keys per step
+constexpr int kTiles = 2;                      // row tiles of 128 per CTA
+constexpr int kSoftmaxWarps = 4 * kTiles;
+constexpr int kConvertWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kStages = 2;
+constexpr int kEntrySlots = 4;
+constexpr float kLazy = 8.0f;                  // log2 of how far a maximum may pass its reference
+
+template <int kDim>
+struct __align__(1024) Smem {
+    uint8_t q[kTiles][128 * kDim * 2];
+    uint8_t k[kStages][kKeys * kDim * 2];
+    uint8_t v[kStages][kKeys * kDim * 2];
+    PageEntry entry[kEntrySlots][kKeys / 16];
+    uint16_t nan_mask[kStages][kKeys][kDim / 16];   // edge steps: NaN codes of each value row
+    uint16_t row_nan[kTiles * 128][kDim / 16];      // channels in which a row has met NaN in an edge step
+    int32_t nan_step[kStages];                      // 1 + the last edge step in which a NaN was found
+    uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles], o_full[kTiles];
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], entry_full[kEntrySlots];
+    uint64_t drained;
+    uint32_t tmem;
+};
+
+// Byte offset of 16-byte piece c (8 halves) of row r in the operand layout: blocks of 64 channels, rows of 128 bytes
+// swizzled in 16-byte pieces by the row's low three bits.
+__device__ __forceinline__ uint32_t operand_at(int r, int c)
+{
+    return static_cast<uint32_t>((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+constexpr uint32_t idesc_f16(int n, bool b_mn_major)   // M = 128, FP32 accumulator
+{
+    return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
+}
+
+__device__ __forceinline__ bool wait_for(const uint64_t &bar, uint32_t parity)
+{
+    if (mbar_wait_bounded(smem_u32(&bar), parity, kWaitNs))
+        return true;
+    atomicOr(&g_error, ERR_ATTN_WAIT);
+    return false;
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(AttnArgs a, SplitPlan plan, int row_tiles, float2 *ws_stat, float *ws_out)
+{
+    extern __shared__ uint8_t dyn[];
+    Smem<kDim> &sm = *reinterpret_cast<Smem<kDim> *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, page = a.cache.page_size, group = a.heads / a.cache.heads;
+    const int tile = blockIdx.x % row_tiles, kh = blockIdx.x / row_tiles % a.cache.heads;
+    const int split = blockIdx.x / row_tiles / a.cache.heads;
+    const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+    if (!s.ok || s.len > a.max_kv || (s.len > 0 && (s.len - 1) / page >= a.batch.ld_table)) {
+        if (threadIdx.x == 0)
+            atomicOr(&g_error, ERR_KV_RANGE);
+        return;
+    }
+    const int64_t rows = static_cast<int64_t>(s.n) * group;
+    const int64_t row0 = static_cast<int64_t>(a.causal ? row_tiles - 1 - tile : tile) * (kTiles * 128);   // causal: longest first
+    if (row0 >= rows || (split > 0 && split * plan.chunk >= s.len))
+        return;
+    const int64_t row_end = row0 + kTiles * 128 < rows ? row0 + kTiles * 128 : rows;
+    const Span first = seen_by(a, s, static_cast<int>(row0 / group)), last = seen_by(a, s, static_cast<int>((row_end - 1) / group));
+    const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);     // seen by every row
+    const int out_lo = min(first.lo, last.lo);                                    // seen by any
+    const int begin = max(split * plan.chunk, out_lo & ~(kKeys - 1));
+    const int end = min(min((split + 1) * plan.chunk, s.len), max(first.hi, last.hi));
+    const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
+    const int tiles = row_end - row0 > 128 ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(smem_u32(&sm.q_full[i]), 128);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), 128);
+            mbar_init(smem_u32(&sm.o_full[i]), 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), 32 * kConvertWarps);
+            mbar_init(smem_u32(&sm.v_full[i]), 32 * kConvertWarps);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            sm.nan_step[i] = 0;
+        }
+        for (int i = 0; i < kEntrySlots; ++i)
+            mbar_init(smem_u32(&sm.entry_full[i]), 1);
+        mbar_init(smem_u32(&sm.drained), 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        // One CTA per SM (the shared memory sees to that), so the whole TMEM is free.
+        tmem_alloc(smem_u32(&sm.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const auto s_col = [&](int t) { return tmem + 128u * t; };
+    const auto o_col = [&](int t) { return tmem + 256u + static_cast<uint32_t>(kDim) * t; };
+
+    if (warp < kSoftmaxWarps) {
+        const int t = warp >> 2, in_tile = (warp & 3) * 32 + lane;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int64_t r = row0 + 128 * t + in_tile;
+        const bool live = r < rows;
+        if (t < tiles) {
+            const int tok = live ? static_cast<int>(r / group) : 0, head = kh * group + (live ? static_cast<int>(r % group) : 0);
+            const Span see = live ? seen_by(a, s, tok) : Span{0, 0};
+            // what the tile's rows all see
+            const int64_t tr0 = row0 + 128 * t, tr1 = (tr0 + 128 < rows ? tr0 + 128 : rows) - 1;
+            const Span tf = seen_by(a, s, static_cast<int>(tr0 / group)), tl = seen_by(a, s, static_cast<int>(tr1 / group));
+            const int t_lo = max(tf.lo, tl.lo), t_hi = min(tf.hi, tl.hi);
+            float c_row;
+            {
+                const uint16_t *src = a.q + (s.row + tok) * a.qt + head * a.qh;
+                uint4 w[kDim / 8];
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int i = 0; i < kDim / 8; ++i) {
+                    w[i] = live ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+                    m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, w[i].x), w[i].y), w[i].z), w[i].w);
+                }
+                const float2 p = row_power(max(m2 & 0xFFFFu, m2 >> 16));
+                const float f = a.scale < 0.0f ? -p.x : p.x;
+                c_row = fabsf(a.scale) * kLog2e * p.y;
+#pragma unroll
+                for (int i = 0; i < kDim / 8; ++i)
+                    st_shared_v4(smem_u32(sm.q[t]) + operand_at(in_tile, i), bf16x2_to_half2(w[i].x, f), bf16x2_to_half2(w[i].y, f),
+                                 bf16x2_to_half2(w[i].z, f), bf16x2_to_half2(w[i].w, f));
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&sm.q_full[t]));
+            }
+            float ref = -INFINITY, l = 0.0f;
+            bool met_nan = false, ok = true;
+            const int shift = 31 - __clz(page);
+            const uint32_t sc = s_col(t) + lanes, oc = o_col(t) + lanes;
+            for (int j = 0; j < steps; ++j) {
+                const int k0 = begin + j * kKeys;
+                const bool edge = k0 < t_lo || k0 + kKeys > t_hi;
+                if (!wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) || !wait_for(sm.s_full[t], j & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const PageEntry *pe = sm.entry[j % kEntrySlots];
+                const int lo = see.lo - k0, hi = see.hi - k0;
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(sc + 32 * c, v);
+                    tmem_ld_wait_regs(v);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const PageEntry e = pe[(32 * c + 16 * h) >> shift];
+                        float g = -INFINITY;
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int x = 32 * c + 16 * h + i;
+                                g = fmaxf(g, x >= lo && x < hi ? __uint_as_float(v[16 * h + i]) : -INFINITY);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                g = fmaxf(g, __uint_as_float(v[16 * h + i]));
+                        }
+                        top = fmaxf(top, g == -INFINITY ? g : fmaf(g, c_row * e.ks, e.lv));
+                    }
+                }
+                const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, move)) {
+                    const float next = move ? top : ref;
+                    const float f = ref == -INFINITY ? 0.0f : ex2(ref - next);
+                    l *= f;
+                    ref = next;
+                    if (j > 0) {   // the accumulator's last product has completed: S of this step was issued after it
+#pragma unroll
+                        for (int c = 0; c < kDim / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(oc + 32 * c, v);
+                            tmem_ld_wait_regs(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            tmem_st_32x32b_x32(oc + 32 * c, v);
+                        }
+                    }
+                }
+                const float at = ref == -INFINITY ? 0.0f : ref;
+                // Ordinary steps take the exponent in one fused multiply-add.  Past 2^20 the reference's own rounding
+                // would show in it (and could reach FP16's limit): there, as in edge steps, the score is rounded first,
+                // so that the largest one meets its own copy in the reference.
+                const auto weights = [&](auto careful) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32], p[16];
+                        tmem_ld_32x32b_x32(sc + 32 * c, v);
+                        tmem_ld_wait_regs(v);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const PageEntry e = pe[(32 * c + 16 * h) >> shift];
+                            const float ck = c_row * e.ks, off = e.lv - at;
+                            float w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float x = __uint_as_float(v[16 * h + i]);
+                                if constexpr (decltype(careful)::value) {
+                                    const int col = 32 * c + 16 * h + i;
+                                    w[i] = col >= lo && col < hi ? ex2(fmaf(x, ck, e.lv) - at) : 0.0f;
+                                } else {
+                                    w[i] = ex2(fmaf(x, ck, off));
+                                }
+                            }
+                            float sum = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                sum += w[i] + w[i + 1];
+                                p[8 * h + i / 2] = pack_half2(w[i], w[i + 1]);
+                            }
+                            l = fmaf(sum, e.inv_vs, l);
+                        }
+                        tmem_st_32x32b_x16(sc + 16 * c, p);   // columns of S that are read already
+                    }
+                };
+                if (edge || __any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f))
+                    weights(std::true_type{});
+                else
+                    weights(std::false_type{});
+                tmem_st_wait();
+                tc_fence_before();
+                if (k0 < in_lo || k0 + kKeys > in_hi) {   // the conversion warps keep NaN out of such a step's values
+                    if (!wait_for(sm.v_full[j % kStages], (j / kStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (sm.nan_step[j % kStages] == j + 1) {
+                        uint16_t *mine = sm.row_nan[128 * t + in_tile];
+                        for (int c = 0; c < kDim / 16; ++c) {
+                            uint32_t m = met_nan ? mine[c] : 0u;
+                            for (int x = max(lo, 0); x < min(hi, kKeys); ++x)
+                                m |= sm.nan_mask[j % kStages][x][c];
+                            mine[c] = static_cast<uint16_t>(m);
+                        }
+                        met_nan = true;
+                    }
+                }
+                mbar_arrive(smem_u32(&sm.p_full[t]));
+            }
+            if (ok && steps > 0)
+                ok = wait_for(sm.o_full[t], (steps - 1) & 1);
+            if (ok) {
+                tc_fence_after();
+                const int64_t row = s.row + tok, at = row * a.heads + head;
+                const bool final = plan.splits == 1;
+                const float inv = !final ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                uint16_t *out = a.out + row * a.ot + head * a.oh;
+                float *part = ws_out + (at * plan.splits + split) * kDim;
+#pragma unroll
+                for (int c = 0; c < kDim / 32; ++c) {
+                    uint32_t v[32];
+                    if (steps > 0) {
+                        tmem_ld_32x32b_x32(oc + 32 * c, v);
+                        tmem_ld_wait_regs(v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = 0u;
+                    }
+                    float o[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __uint_as_float(v[i]) * inv;
+                    if (met_nan) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (sm.row_nan[128 * t + in_tile][2 * c + (i >> 4)] >> (i & 15) & 1)
+                                o[i] = __uint_as_float(0x7FC00000u);
+                    }
+                    if (live && final) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const __nv_bfloat162 y = __floats2bfloat162_rn(o[i + 2 * x], o[i + 2 * x + 1]);
+                                w[x] = *reinterpret_cast<const uint32_t *>(&y);
+                            }
+                            *reinterpret_cast<uint4 *>(out + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(part + 32 * c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                }
+                if (live && !final)
+                    ws_stat[at * plan.splits + split] = make_float2(ref, l);
+                else if (live && a.lse != nullptr)
+                    a.lse[at] = (ref + lg2(l)) * kLn2;
+                tc_fence_before();
+            }
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------------ conversion
+        constexpr int kPieces = kDim / 16;                        // 16-byte pieces of codes per token
+        constexpr int kRowStep = 32 * kConvertWarps / kPieces;    // tokens between a thread's pieces
+        constexpr int kPer = kKeys / kRowStep;
+        const int tid = threadIdx.x - 32 * kSoftmaxWarps, r0 = tid / kPieces, c = tid % kPieces;
+        const int64_t head_off = static_cast<int64_t>(kh) * page;
+        const auto id_of = [&](int tok) -> int32_t {              // page of a token that any row sees, else -1
+            if (tok < out_lo || tok >= end)
+                return -1;
+            const int32_t id = a.batch.page_table[b * a.batch.ld_table + tok / page];
+            if (id < 0 || id >= a.cache.num_pages) {
+                atomicOr(&g_error, ERR_KV_RANGE);
+                return -1;
+            }
+            return id;
+        };
+        const auto load = [&](const uint8_t *codes, int k0, const int32_t (&id)[kPer], uint4 (&w)[kPer]) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int tok = k0 + r0 + i * kRowStep;
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (id[i] >= 0)
+                    w[i] = *reinterpret_cast<const uint4 *>(
+                        codes + ((static_cast<int64_t>(id[i]) * a.cache.heads * page + head_off + (tok & (page - 1))) * kDim + 16 * c));
+            }
+        };
+        const auto store = [&](uint32_t dst, const uint4 &w, int r) {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[2 * i] = e4m3x2_to_f16x2(x[i] & 0xFFFFu);
+                h[2 * i + 1] = e4m3x2_to_f16x2(x[i] >> 16);
+            }
+            // the upper half of the pieces stores its second half first: the other banks
+            const int odd = (c >> 2) & 1;
+            if (odd == 0) {
+                st_shared_v4(dst + operand_at(r, 2 * c), h[0], h[1], h[2], h[3]);
+                st_shared_v4(dst + operand_at(r, 2 * c + 1), h[4], h[5], h[6], h[7]);
+            } else {
+                st_shared_v4(dst + operand_at(r, 2 * c + 1), h[4], h[5], h[6], h[7]);
+                st_shared_v4(dst + operand_at(r, 2 * c), h[0], h[1], h[2], h[3]);
+            }
+        };
+        int32_t id[kPer], id_next[kPer];
+        uint4 kw[kPer], vw[kPer];
+        const auto ids = [&](int j, int32_t (&x)[kPer]) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                x[i] = id_of(begin + j * kKeys + r0 + i * kRowStep);
+        };
+        if (steps > 0) {
+            ids(0, id);
+            load(a.cache.k_codes, begin, id, kw);
+            load(a.cache.v_codes, begin, id, vw);
+            ids(1, id_next);
+        }
+        for (int j = 0; j < steps; ++j) {
+            const int k0 = begin + j * kKeys, st = j % kStages;
+            const bool edge = k0 < in_lo || k0 + kKeys > in_hi;
+            if (!wait_for(sm.k_empty[st], ((j / kStages) & 1) ^ 1))
+                break;
+            if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
+                if (lane < kKeys / page) {
+                    const int32_t p = id_of(max(k0 + lane * page, out_lo));   // a page that a window cuts counts from there
+                    const bool any = k0 + lane * page < end && k0 + (lane + 1) * page > out_lo;
+                    const int64_t bh = static_cast<int64_t>(any && p >= 0 ? p : 0) * a.cache.heads + kh;
+                    PageEntry e{p, 1.0f, 0.0f, 1.0f};
+                    if (any && p >= 0) {
+                        const float vs = a.cache.v_scale[bh];
+                        e.ks = a.cache.k_scale[bh];
+                        e.lv = lg2(vs);
+                        e.inv_vs = __frcp_rn(vs);
+                    }
+                    sm.entry[j % kEntrySlots][lane] = e;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sm.entry_full[j % kEntrySlots]));
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                store(smem_u32(sm.k[st]), kw[i], r0 + i * kRowStep);
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sm.k_full[st]));
+            if (j + 1 < steps)
+                load(a.cache.k_codes, k0 + kKeys, id_next, kw);
+
+            if (!wait_for(sm.v_empty[st], ((j / kStages) & 1) ^ 1))
+                break;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = r0 + i * kRowStep;
+                if (edge) {   // NaN that only some rows see stays out of the product (a weight of zero would not stop it)
+                    uint32_t x[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w}, m = 0;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t n = nan_bytes(x[y]) >> 7;   // 1 in each NaN byte
+                        x[y] &= ~(n * 0xFFu);
+                        m |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * y);
+                    }
+                    vw[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                    sm.nan_mask[st][r][c] = static_cast<uint16_t>(m);
+                    if (m != 0)
+                        sm.nan_step[st] = j + 1;
+                }
+                store(smem_u32(sm.v[st]), vw[i], r);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sm.v_full[st]));
+            if (j + 1 < steps) {
+                load(a.cache.v_codes, k0 + kKeys, id_next, vw);
+                ids(j + 2, id_next);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------------ MMA issue
+        constexpr uint32_t kQk = idesc_f16(kKeys, false), kPv = idesc_f16(kDim, true);
+        const auto qk = [&](int t, int st) {
+            const uint32_t q = smem_u32(sm.q[t]), k = smem_u32(sm.k[st]);
+#pragma unroll
+            for (int x = 0; x < kDim / 16; ++x) {
+                const uint32_t off = (x >> 2) * (128 * 128) + (x & 3) * 32;
+                tc_mma_f16_elect(s_col(t), smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), kQk, x > 0);
+            }
+        };
+        const auto pv = [&](int t, int st, bool accumulate) {
+            const uint32_t v = smem_u32(sm.v[st]);
+#pragma unroll
+            for (int x = 0; x < kKeys / 16; ++x)   // values: 8-token groups 1024 bytes apart, 64-channel blocks 16 KB
+                tc_mma_f16_ts_elect(o_col(t), s_col(t) + 8 * x, smem_desc(v + x * 2048, 128 * 128, 1024, 2), kPv,
+                                    accumulate || x > 0);
+        };
+        bool ok = true;
+        for (int t = 0; ok && steps > 0 && t < tiles; ++t) {
+            ok = wait_for(sm.q_full[t], 0) && wait_for(sm.k_full[0], 0);
+            if (!ok)
+                break;
+            tc_fence_after();
+            qk(t, 0);
+            tc_commit_elect(smem_u32(&sm.s_full[t]));
+        }
+        if (ok && steps > 0)
+            tc_commit_elect(smem_u32(&sm.k_empty[0]));
+        for (int j = 0; ok && j < steps; ++j) {
+            const int st = j % kStages, nx = (j + 1) % kStages;
+            for (int t = 0; t < tiles; ++t) {
+                if (!(ok = wait_for(sm.v_full[st], (j / kStages) & 1) && wait_for(sm.p_full[t], j & 1)))
+                    break;
+                tc_fence_after();
+                pv(t, st, j > 0);
+                tc_commit_elect(smem_u32(&sm.o_full[t]));
+                if (t == tiles - 1)
+                    tc_commit_elect(smem_u32(&sm.v_empty[st]));
+                if (j + 1 < steps) {
+                    // the next S goes over the weights that this product reads: wait for it
+                    if (!(ok = wait_for(sm.k_full[nx], ((j + 1) / kStages) & 1) && wait_for(sm.o_full[t], j & 1)))
+                        break;
+                    tc_fence_after();
+                    qk(t, nx);
+                    tc_commit_elect(smem_u32(&sm.s_full[t]));
+                    if (t == tiles - 1)
+                        tc_commit_elect(smem_u32(&sm.k_empty[nx]));
+                }
+            }
+        }
+        tc_commit_elect(smem_u32(&sm.drained));   // nothing of this CTA is in the tensor cores when TMEM is freed
+        wait_for(sm.drained, 0);
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int kDim>
+cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+{
+    // More than half of an SM's shared memory even at dim 64: a second CTA on the SM would wait for the first one's TMEM.
+    constexpr int kNeed = sizeof(Smem<kDim>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
+    static_assert(kSmem <= 227 * 1024, "fits an SM");
+    const cudaError_t e = cudaFuncSetAttribute(tile_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
+    const int64_t tiles = (rows + kTiles * 128 - 1) / (kTiles * 128), x = tiles * a.cache.heads * plan.splits;
+    if (x > INT32_MAX)
+        return cudaErrorInvalidValue;
+    tile_kernel<kDim><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(a, plan, static_cast<int>(tiles),
+                                                                                           stat, part);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Parts of the keys: as many as give every SM a CTA, of 512 keys at least.
+SplitPlan plan_tile(const AttnShape &s)
+{
+    const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);
+    const int64_t ctas = static_cast<int64_t>(s.batch) * s.kv_heads * ((rows + kTiles * 128 - 1) / (kTiles * 128));
+    const int64_t kv = s.max_kv < 1 ? 1 : s.max_kv;
+    int64_t splits = ctas > 0 ? sm_count() / ctas : 1;
+    const int64_t most = (kv + 511) / 512;
+    splits = splits > most ? most : splits < 1 ? 1 : splits;
+    const int64_t chunk = ((kv + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
+    return SplitPlan{static_cast<int32_t>((kv + chunk - 1) / chunk), static_cast<int32_t>(chunk)};
+}
+
+cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+{
+    return a.cache.head_dim == 64 ? run_tile<64>(a, plan, stat, part, st) : run_tile<128>(a, plan, stat, part, st);
+}
+
+cudaError_t read_attention_tile_error(uint32_t *code)
+{
+    uint32_t v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_error, sizeof(v));
+    if (e != cudaSuccess)
+        return e;
+    const uint32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_error, &zero, sizeof(zero));
+    *code = v;
+    return e;
+}
+
+}  // namespace h3fp4
