@@ -11,7 +11,9 @@ an error status.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libh3fp4.so")
@@ -67,22 +69,10 @@ ROPE_MAX_AXES = 4
 ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
 
 
-class RopeStruct(ctypes.Structure):
-    """h3fp4_rope."""
-    _fields_ = [("positions", _P), ("ld_positions", _I64), ("freqs", _P), ("axes", _I32),
-                ("dims", _I32 * ROPE_MAX_AXES), ("layout", _I32), ("inverse", _I32)]
-
-
-class KVCacheStruct(ctypes.Structure):
-    """h3fp4_kv_cache."""
-    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I32),
-                ("page_size", _I32), ("heads", _I32), ("head_dim", _I32)]
-
-
-class KVBatchStruct(ctypes.Structure):
-    """h3fp4_kv_batch."""
-    _fields_ = [("page_table", _P), ("ld_table", _I64), ("len", _P), ("cu_tokens", _P), ("batch", _I32),
-                ("max_tokens", _I32)]
+# h3fp4_rope, h3fp4_kv_cache and h3fp4_kv_batch in the platform's C layout.
+_ROPE = struct.Struct("@PqPi4iii4x")
+_KV_CACHE = struct.Struct("@PPPPiiii")
+_KV_BATCH = struct.Struct("@PqPPii")
 
 
 _lib = None
@@ -195,31 +185,31 @@ def h3fp4_diag_gemm_wait_timeout(a_q, a_sf, a_ts, b_q, b_sf, b_ts, c, ldc, m, m_
 
 
 def h3fp4_rope_axes(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads, head_dim,
-                    rope: RopeStruct, stream=0):
+                    rope, stream=0):
+    """`rope` (and `cache`, `batch` below): the structure's bytes, or None where the C entry takes NULL."""
     _call("h3fp4_rope_axes", x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads,
-          head_dim, ctypes.byref(rope), stream)
+          head_dim, rope, stream)
 
 
-def h3fp4_kv_cache_write(cache: KVCacheStruct, batch: KVBatchStruct, k, k_token_stride, k_head_stride, v,
-                         v_token_stride, v_head_stride, tokens, rope: RopeStruct | None = None, stream=0):
-    _call("h3fp4_kv_cache_write", ctypes.byref(cache), ctypes.byref(batch), k, k_token_stride, k_head_stride, v,
-          v_token_stride, v_head_stride, tokens, ctypes.byref(rope) if rope is not None else None, stream)
+def h3fp4_kv_cache_write(cache, batch, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, tokens,
+                         rope=None, stream=0):
+    _call("h3fp4_kv_cache_write", cache, batch, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
+          tokens, rope, stream)
 
 
-def h3fp4_kv_cache_read(cache: KVCacheStruct, batch: KVBatchStruct, k, k_token_stride, k_head_stride, v,
-                        v_token_stride, v_head_stride, tokens, stream=0):
-    _call("h3fp4_kv_cache_read", ctypes.byref(cache), ctypes.byref(batch), k, k_token_stride, k_head_stride, v,
-          v_token_stride, v_head_stride, tokens, stream)
+def h3fp4_kv_cache_read(cache, batch, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, tokens,
+                        stream=0):
+    _call("h3fp4_kv_cache_read", cache, batch, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
+          tokens, stream)
 
 
 def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens, heads,
-                       cache: KVCacheStruct, batch: KVBatchStruct, max_kv, softmax_scale, causal, window, workspace,
-                       workspace_bytes, stream=0):
+                       cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream=0):
     _call("h3fp4_kv_attention", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
-          heads, ctypes.byref(cache), ctypes.byref(batch), max_kv, softmax_scale, causal, window, workspace,
-          workspace_bytes, stream)
+          heads, cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream)
 
 
+@functools.lru_cache(maxsize=256)          # a function of the sizes alone
 def h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv) -> int:
     n = lib().h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv)
     if n < 0:
@@ -387,28 +377,49 @@ def swizzle_scales(sf_logical, *, out=None, stream=None):
 # ----------------------------------------------------------------------------
 # Rotary positions, the 8-bit key/value cache, and attention over it.  bf16
 # tensors are torch.bfloat16 or int16 patterns; outputs take their input's type.
+# The checks stand between a caller's tensors and raw pointers, so each call
+# makes all of them; they are written to cost little (a decoding step's calls
+# take longer on the host than on the GPU).
 # ----------------------------------------------------------------------------
-def _need(ok, what):
-    """Raises ValueError with the text, or the result of the function, `what`."""
-    if not ok:
-        raise ValueError(what() if callable(what) else what)
+_types = None
+
+
+def _dtypes():
+    global _types
+    if _types is None:
+        import torch
+        _types = {"bf16": (torch.bfloat16, torch.int16), "i32": torch.int32, "f32": torch.float32, "f64": torch.float64,
+                  "u8": torch.uint8}
+    return _types
 
 
 def _need_array(t, name, dtype, ndim):
-    """A device array of this element type whose last dimension is contiguous."""
-    _need_cuda(t)
-    _need(str(t.dtype) == "torch." + dtype and t.dim() == ndim and (t.shape[-1] <= 1 or t.stride(-1) == 1),
-          lambda: f"{name}: a {ndim}-D {dtype} tensor with a contiguous last dimension is wanted, "
-          f"got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
+    """A contiguous device array of this element type; returns its address."""
+    if not (t.is_cuda and t.dtype is _dtypes()[dtype] and t.dim() == ndim and t.is_contiguous()):
+        _refuse(t, name, f"a contiguous {ndim}-D {_dtypes()[dtype]} tensor")
+    return t.data_ptr()
 
 
 def _need_tokens(t, name, shape=None):
-    """A [tokens, heads, head_dim] array of bf16 values or patterns."""
-    _need_cuda(t)
-    _need(str(t.dtype) in ("torch.bfloat16", "torch.int16") and t.dim() == 3 and t.stride(2) == 1,
-          lambda: f"{name}: a [tokens, heads, head_dim] tensor of bf16 values (bfloat16 or int16) with contiguous channels is "
-          f"wanted, got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
-    _need(shape is None or tuple(t.shape) == tuple(shape), lambda: f"{name}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+    """A [tokens, heads, head_dim] array of bf16 values or patterns; returns its address and strides."""
+    s = t.stride()
+    if not (t.is_cuda and t.dtype in _dtypes()["bf16"] and len(s) == 3 and (s[2] == 1 or t.shape[2] == 1)
+            and (shape is None or t.shape == shape)):
+        _refuse(t, name, f"a [tokens, heads, head_dim] tensor {'' if shape is None else tuple(shape)} of bf16 values "
+                         "(bfloat16 or int16) with contiguous channels")
+    return t.data_ptr(), s[0], s[1]
+
+
+def _refuse(t, name, what):
+    raise ValueError(f"{name}: {what} on a CUDA device is wanted, got {tuple(t.shape)} {t.dtype} strides {t.stride()} on "
+                     f"{t.device}")
+
+
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 class Rope:
@@ -417,18 +428,19 @@ class Rope:
     axis 0 first), ``dims`` the channels each axis turns, ``layout`` how a pair lies
     in its axis' channels: "interleaved" (2j, 2j+1) or "halves" (j, j + dims/2)."""
 
-    def __init__(self, positions, freqs, dims, layout="interleaved"):
-        _need_array(positions, "positions", "float32", 2)
-        _need_array(freqs, "freqs", "float64", 1)
-        _need(1 <= len(dims) <= ROPE_MAX_AXES and positions.shape[1] >= len(dims),
-              lambda: f"rope: {len(dims)} axes for positions {tuple(positions.shape)}")
-        _need(2 * freqs.shape[0] >= sum(dims), lambda: f"rope: {freqs.shape[0]} frequencies for dims {tuple(dims)}")
-        _need(layout in ROPE_LAYOUTS, lambda: f"rope: layout {layout!r}, not one of {sorted(ROPE_LAYOUTS)}")
-        self.positions, self.freqs, self.dims, self.layout = positions, freqs, tuple(dims), layout
+    __slots__ = ("positions", "freqs", "dims", "layout", "_struct")
 
-    def struct(self, inverse=False) -> RopeStruct:
-        return RopeStruct(self.positions.data_ptr(), max(self.positions.stride(0), self.positions.shape[1]),
-                          self.freqs.data_ptr(), len(self.dims), self.dims, ROPE_LAYOUTS[self.layout], int(inverse))
+    def __init__(self, positions, freqs, dims, layout="interleaved"):
+        p, f, n = _need_array(positions, "positions", "f32", 2), _need_array(freqs, "freqs", "f64", 1), len(dims)
+        if not 1 <= n <= ROPE_MAX_AXES or positions.shape[1] < n or 2 * freqs.shape[0] < sum(dims) or layout not in ROPE_LAYOUTS:
+            raise ValueError(f"rope: dims {tuple(dims)}, layout {layout!r} (one of {sorted(ROPE_LAYOUTS)}) with positions "
+                             f"{tuple(positions.shape)} and {freqs.shape[0]} frequencies")
+        self.positions, self.freqs, self.dims, self.layout = positions, freqs, tuple(dims), layout
+        self._struct = _ROPE.pack(p, positions.shape[1], f, n, *self.dims, *(0,) * (ROPE_MAX_AXES - n),
+                                  ROPE_LAYOUTS[layout], 0)
+
+    def struct(self, inverse=False) -> bytes:
+        return self._struct[:-8] + struct.pack("@i4x", 1) if inverse else self._struct
 
 
 def rope_frequencies(dims, theta=10000.0, device="cuda"):
@@ -437,18 +449,20 @@ def rope_frequencies(dims, theta=10000.0, device="cuda"):
     return torch.cat([theta ** (-torch.arange(0, d, 2, dtype=torch.float64) / max(d, 1)) for d in dims]).to(device)
 
 
+def _positions_for(rope, tokens):
+    if rope.positions.shape[0] < tokens:
+        raise ValueError(f"rope: {rope.positions.shape[0]} positions for {tokens} tokens")
+
+
 def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
     """x [tokens, heads, head_dim] turned by its tokens' positions; inverse=True turns
     back (and is the gradient).  out=x works in place.  Returns out."""
     import torch
-    _need_tokens(x, "x")
-    tokens, heads, dim = x.shape
-    _need(rope.positions.shape[0] >= tokens, lambda: f"rope: {rope.positions.shape[0]} positions for {tokens} tokens")
+    xs, shape = _need_tokens(x, "x"), x.shape
+    _positions_for(rope, shape[0])
     if out is None:
-        out = torch.empty(tokens, heads, dim, dtype=x.dtype, device=x.device)
-    _need_tokens(out, "out", x.shape)
-    h3fp4_rope_axes(x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), tokens, heads,
-                    dim, rope.struct(inverse), _stream(stream))
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    h3fp4_rope_axes(*xs, *_need_tokens(out, "out", shape), *shape, rope.struct(inverse), _raw_stream(stream, x))
     return out
 
 
@@ -456,15 +470,18 @@ class KVCache:
     """Keys and values in E4M3 pages: codes [num_pages, heads, page_size, head_dim]
     uint8 and scales [num_pages, heads] float32, for keys and values each."""
 
+    __slots__ = ("k_codes", "k_scale", "v_codes", "v_scale", "num_pages", "heads", "page_size", "head_dim", "_struct")
+
     def __init__(self, k_codes, k_scale, v_codes, v_scale):
-        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-            _need_array(t, name, "uint8", 4)
-            _need(t.is_contiguous() and t.shape == k_codes.shape, lambda: f"{name}: contiguous, both alike")
-        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need_array(t, name, "float32", 2)
-            _need(t.is_contiguous() and t.shape == k_codes.shape[:2], lambda: f"{name}: contiguous [num_pages, heads]")
+        kc, vc = _need_array(k_codes, "k_codes", "u8", 4), _need_array(v_codes, "v_codes", "u8", 4)
+        ks, vs = _need_array(k_scale, "k_scale", "f32", 2), _need_array(v_scale, "v_scale", "f32", 2)
+        shape = k_codes.shape
+        if v_codes.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+            raise ValueError(f"cache: codes {tuple(shape)} and {tuple(v_codes.shape)} with scales {tuple(k_scale.shape)} and "
+                             f"{tuple(v_scale.shape)}")
         self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
-        self.num_pages, self.heads, self.page_size, self.head_dim = k_codes.shape
+        self.num_pages, self.heads, self.page_size, self.head_dim = shape
+        self._struct = _KV_CACHE.pack(kc, vc, ks, vs, shape[0], shape[2], shape[1], shape[3])
 
     @classmethod
     def empty(cls, num_pages, page_size, heads, head_dim, device="cuda"):
@@ -474,22 +491,20 @@ class KVCache:
         scale = [torch.ones(num_pages, heads, dtype=torch.float32, device=device) for _ in "kv"]
         return cls(codes[0], scale[0], codes[1], scale[1])
 
-    def struct(self) -> KVCacheStruct:
-        return KVCacheStruct(self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scale.data_ptr(),
-                             self.v_scale.data_ptr(), self.num_pages, self.page_size, self.heads, self.head_dim)
+    def struct(self) -> bytes:
+        return self._struct
 
 
-def _kv_batch(page_table, length, cu_tokens, max_tokens) -> KVBatchStruct:
-    _need_array(page_table, "page_table", "int32", 2)
-    _need_array(cu_tokens, "cu_tokens", "int32", 1)
+def _kv_batch(page_table, length, cu_tokens, max_tokens) -> bytes:
+    table, cu = _need_array(page_table, "page_table", "i32", 2), _need_array(cu_tokens, "cu_tokens", "i32", 1)
     batch, pages = page_table.shape
-    _need(cu_tokens.shape[0] == batch + 1, lambda: f"cu_tokens: {batch + 1} entries are wanted, got {cu_tokens.shape[0]}")
+    n = 0
     if length is not None:
-        _need_array(length, "lengths", "int32", 1)
-        _need(length.shape[0] == batch, lambda: f"lengths: {batch} entries are wanted, got {length.shape[0]}")
-    _need(page_table.is_contiguous(), "page_table: contiguous rows are wanted")
-    return KVBatchStruct(page_table.data_ptr(), pages, length.data_ptr() if length is not None else None,
-                         cu_tokens.data_ptr(), batch, max_tokens)
+        n = _need_array(length, "lengths", "i32", 1)
+    if cu_tokens.shape[0] != batch + 1 or (length is not None and length.shape[0] != batch):
+        raise ValueError(f"page_table has {batch} sequences: cu_tokens of {batch + 1} and lengths of {batch} are wanted, got "
+                         f"{cu_tokens.shape[0]} and {None if length is None else length.shape[0]}")
+    return _KV_BATCH.pack(table, pages, n, cu, batch, max_tokens)
 
 
 def kv_cache_write(cache: KVCache, k, v, page_table, held, cu_tokens, max_tokens, *, rope: Rope | None = None,
@@ -499,15 +514,14 @@ def kv_cache_write(cache: KVCache, k, v, page_table, held, cu_tokens, max_tokens
     (page_table [batch, pages], held [batch], cu_tokens [batch+1]: device int32);
     max_tokens is the most new tokens of any sequence.  With ``rope`` the keys are
     turned first.  The caller advances its lengths."""
-    _need_tokens(k, "k")
-    tokens = k.shape[0]
-    _need_tokens(k, "k", (tokens, cache.heads, cache.head_dim))
-    _need_tokens(v, "v", k.shape)
-    _need(rope is None or rope.positions.shape[0] >= tokens, "rope: fewer positions than tokens")
-    _need(held is not None, "held: lengths before the call are wanted")
-    h3fp4_kv_cache_write(cache.struct(), _kv_batch(page_table, held, cu_tokens, max_tokens), k.data_ptr(), k.stride(0),
-                         k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), tokens,
-                         rope.struct() if rope is not None else None, _stream(stream))
+    shape = (k.shape[0], cache.heads, cache.head_dim)
+    ks, vs = _need_tokens(k, "k", shape), _need_tokens(v, "v", shape)
+    if held is None:
+        raise ValueError("held: lengths before the call are wanted")
+    if rope is not None:
+        _positions_for(rope, shape[0])
+    h3fp4_kv_cache_write(cache._struct, _kv_batch(page_table, held, cu_tokens, max_tokens), *ks, *vs, shape[0],
+                         rope._struct if rope is not None else None, _raw_stream(stream, k))
 
 
 def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_tokens, *, k=None, v=None, stream=None):
@@ -520,10 +534,8 @@ def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_toke
         k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
     if v is None:
         v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
-    _need_tokens(k, "k", shape)
-    _need_tokens(v, "v", shape)
-    h3fp4_kv_cache_read(cache.struct(), _kv_batch(page_table, start, cu_tokens, max_tokens), k.data_ptr(), k.stride(0),
-                        k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), tokens, _stream(stream))
+    h3fp4_kv_cache_read(cache._struct, _kv_batch(page_table, start, cu_tokens, max_tokens), *_need_tokens(k, "k", shape),
+                        *_need_tokens(v, "v", shape), tokens, _raw_stream(stream, k))
     return k, v
 
 
@@ -535,26 +547,29 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
     before it (window > 0).  scale defaults to head_dim ** -0.5.  Returns (out, lse); lse
     [tokens, heads] float32 is None unless asked for."""
     import torch
-    _need_tokens(q, "q")
-    tokens, heads, dim = q.shape
-    _need(dim == cache.head_dim and heads % cache.heads == 0,
-          lambda: f"q: {heads} heads of {dim} for a cache of {cache.heads} heads of {cache.head_dim}")
-    _need(kv_len is not None, "kv_len: lengths are wanted")
+    qs, shape = _need_tokens(q, "q"), q.shape
+    tokens, heads, dim = shape
+    if dim != cache.head_dim or heads % cache.heads or kv_len is None:
+        raise ValueError(f"q: {heads} heads of {dim} for a cache of {cache.heads} heads of {cache.head_dim}"
+                         if kv_len is not None else "kv_len: lengths are wanted")
     if out is None:
-        out = torch.empty(tokens, heads, dim, dtype=q.dtype, device=q.device)
-    _need_tokens(out, "out", q.shape)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
         lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device)
+    lse_at = None
     if lse is not None:
-        _need_array(lse, "lse", "float32", 2)
-        _need(lse.is_contiguous() and tuple(lse.shape) == (tokens, heads), "lse: contiguous [tokens, heads]")
+        lse_at = _need_array(lse, "lse", "f32", 2)
+        if lse.shape != (tokens, heads):
+            _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor")
     batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens)
-    need = h3fp4_kv_attention_workspace(tokens, heads, cache.heads, dim, batch.batch, max_tokens, max_kv)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    h3fp4_kv_attention(q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
-                       lse.data_ptr() if lse is not None else None, tokens, heads, cache.struct(), batch, max_kv,
-                       dim ** -0.5 if scale is None else scale, int(causal), window,
-                       workspace.data_ptr() if workspace is not None else None,
-                       workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream))
+    need = h3fp4_kv_attention_workspace(tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
+    at = have = 0
+    if workspace is not None:
+        at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _need_cuda(workspace)
+    elif need:
+        workspace, have = torch.empty(need, dtype=torch.uint8, device=q.device), need
+        at = workspace.data_ptr()
+    h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape), lse_at, tokens, heads, cache._struct, batch, max_kv,
+                       dim ** -0.5 if scale is None else scale, causal, window, at, have, _raw_stream(stream, q))
     return out, lse

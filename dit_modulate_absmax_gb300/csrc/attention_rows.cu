@@ -485,7 +485,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
 {
     constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = kWarps * kRows * kDim * 4;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<kDim, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = allow_shared<rows_kernel<kDim, kRows>>(kSmem);
     if (e != cudaSuccess)
         return e;
     const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);

@@ -523,7 +523,7 @@ cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     // More than half of an SM's shared memory even at dim 64: a second CTA on the SM would wait for the first one's TMEM.
     constexpr int kNeed = sizeof(Smem<kDim>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024, "fits an SM");
-    const cudaError_t e = cudaFuncSetAttribute(tile_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = allow_shared<tile_kernel<kDim>>(kSmem);
     if (e != cudaSuccess)
         return e;
     const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);

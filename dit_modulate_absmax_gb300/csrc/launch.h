@@ -1,6 +1,7 @@
 // launch.h -- internal launchers behind the C ABI (not exported).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -71,6 +72,22 @@ cudaError_t launch_quantize_pack_barrier_timeout(const uint16_t *x, int64_t ldx,
                                                 uint64_t wait_ns, cudaStream_t st);
 
 h3fp4_status read_device_error(uint32_t *code);
+
+// Lets a kernel use this much dynamic shared memory: set on its first call on
+// a device (threads that race on that set the same value).
+template <auto kKernel>
+cudaError_t allow_shared(int bytes)
+{
+    static std::atomic<uint64_t> done{0};   // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1) != 0))
+        return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64)
+        done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
 
 // ---------------------------------------------------------------------------
 // Rotary positions, the 8-bit cache and its attention: arguments by value.

@@ -1,7 +1,5 @@
 """Argument checks of the rotary, cache and attention entry points (CPU: every
 call here is refused before anything is enqueued, or has nothing to do)."""
-import ctypes
-
 import numpy as np
 import pytest
 
@@ -21,24 +19,25 @@ def L():
 
 def _rope(**kw):
     a = {**dict(positions=F, ld_positions=3, freqs=F, axes=3, dims=(44, 42, 42), layout=0, inverse=0), **kw}
-    return pkg.RopeStruct(a["positions"], a["ld_positions"], a["freqs"], a["axes"],
-                          (ctypes.c_int32 * 4)(*a["dims"]), a["layout"], a["inverse"])
+    return pkg._ROPE.pack(a["positions"] or 0, a["ld_positions"], a["freqs"] or 0, a["axes"],
+                          *(tuple(a["dims"]) + (0,) * 4)[:4], a["layout"], a["inverse"])
 
 
 def _cache(**kw):
     a = {**dict(kc=F, vc=F, ks=F, vs=F, pages=4, page=64, heads=4, dim=128), **kw}
-    return pkg.KVCacheStruct(a["kc"], a["vc"], a["ks"], a["vs"], a["pages"], a["page"], a["heads"], a["dim"])
+    return pkg._KV_CACHE.pack(a["kc"] or 0, a["vc"] or 0, a["ks"] or 0, a["vs"] or 0, a["pages"], a["page"], a["heads"],
+                              a["dim"])
 
 
 def _batch(**kw):
     a = {**dict(table=F, ld=4, len=F, cu=F, batch=2, most=5), **kw}
-    return pkg.KVBatchStruct(a["table"], a["ld"], a["len"], a["cu"], a["batch"], a["most"])
+    return pkg._KV_BATCH.pack(a["table"] or 0, a["ld"], a["len"] or 0, a["cu"] or 0, a["batch"], a["most"])
 
 
 def test_rope_refusals(L):
     def call(x=F, xt=512, xh=128, out=G, ot=512, oh=128, tokens=10, heads=4, dim=128, rope=None, **kw):
         r = _rope(**kw) if rope is None else rope
-        return L.h3fp4_rope_axes(x, xt, xh, out, ot, oh, tokens, heads, dim, ctypes.byref(r), None)
+        return L.h3fp4_rope_axes(x, xt, xh, out, ot, oh, tokens, heads, dim, r, None)
 
     assert L.h3fp4_rope_axes(F, 512, 128, G, 512, 128, 10, 4, 128, None, None) == NULL
     assert call(x=None) == NULL and call(out=None) == NULL
@@ -59,12 +58,12 @@ def test_rope_refusals(L):
 def test_cache_refusals(L):
     def write(c=None, b=None, k=F, kt=512, kh=128, v=F, vt=512, vh=128, tokens=10, rope=None):
         c, b = _cache() if c is None else c, _batch() if b is None else b
-        return L.h3fp4_kv_cache_write(ctypes.byref(c), ctypes.byref(b), k, kt, kh, v, vt, vh, tokens,
-                                      ctypes.byref(rope) if rope else None, None)
+        return L.h3fp4_kv_cache_write(c, b, k, kt, kh, v, vt, vh, tokens,
+                                      rope, None)
 
     def read(c=None, b=None, k=F, kt=512, kh=128, v=G, vt=512, vh=128, tokens=10):
         c, b = _cache() if c is None else c, _batch() if b is None else b
-        return L.h3fp4_kv_cache_read(ctypes.byref(c), ctypes.byref(b), k, kt, kh, v, vt, vh, tokens, None)
+        return L.h3fp4_kv_cache_read(c, b, k, kt, kh, v, vt, vh, tokens, None)
 
     for f in (write, read):
         assert f(c=_cache(kc=None)) == NULL and f(c=_cache(vs=None)) == NULL
@@ -85,7 +84,7 @@ def test_attention_refusals(L):
     def call(q=F, qt=1024, qh=128, out=G, ot=1024, oh=128, lse=None, tokens=10, heads=8, c=None, b=None, max_kv=256,
              scale=0.1, causal=1, window=0, ws=F, bytes=1 << 40):
         c, b = _cache() if c is None else c, _batch() if b is None else b
-        return L.h3fp4_kv_attention(q, qt, qh, out, ot, oh, lse, tokens, heads, ctypes.byref(c), ctypes.byref(b), max_kv,
+        return L.h3fp4_kv_attention(q, qt, qh, out, ot, oh, lse, tokens, heads, c, b, max_kv,
                                     scale, causal, window, ws, bytes, None)
 
     assert call(q=None) == NULL and call(out=None) == NULL and call(b=_batch(len=None)) == NULL
@@ -109,6 +108,32 @@ def test_workspace_grows_with_nothing_it_should_not(L):
     for args in ((2**31 - 1, 65535, 1, 128, 65535, 1_000_000, 1 << 30), (1, 65535, 65535, 128, 1, 1, 1 << 30),
                  (2**31 - 1, 8, 8, 64, 65535, 1, 1 << 30)):
         assert -1 <= L.h3fp4_kv_attention_workspace(*args) < 1 << 60
+
+
+def test_packed_structures_have_the_c_layout(tmp_path):
+    """Sizes and member offsets of the header's structures, printed by a C program, against the packers'."""
+    import os
+    import struct
+    import subprocess
+    src = tmp_path / "layout.c"
+    members = {"h3fp4_rope": ["positions", "ld_positions", "freqs", "axes", "dims", "layout", "inverse"],
+               "h3fp4_kv_cache": ["k_codes", "v_codes", "k_scale", "v_scale", "num_pages", "page_size", "heads", "head_dim"],
+               "h3fp4_kv_batch": ["page_table", "ld_table", "len", "cu_tokens", "batch", "max_tokens"]}
+    lines = [f'printf("%zu\\n", sizeof({s}));' + "".join(f'printf("%zu\\n", offsetof({s}, {m}));' for m in ms)
+             for s, ms in members.items()]
+    src.write_text('#include <stdio.h>\n#include "h3fp4.h"\nint main(void) {' + "".join(lines) + "return 0; }\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True).stdout.split()]
+    want = []
+    for packer, kinds in ((pkg._ROPE, ["P", "q", "P", "i", "4i", "i", "i"]), (pkg._KV_CACHE, list("PPPPiiii")),
+                          (pkg._KV_BATCH, list("PqPPii"))):
+        want.append(packer.size)
+        at = ""
+        for k in kinds:
+            want.append(struct.calcsize("@" + at + "0" + k[-1]))
+            at += k
+    assert got == want
 
 
 def test_python_checks_before_any_pointer_is_taken():
