@@ -36,7 +36,12 @@ constexpr int kTiles = 2;                      // row tiles of 128 per CTA
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups, for the register split; three warps idle
+// Registers per thread of the three kinds of warpgroup, out of the 128 that 512 threads launch with (run_tile checks):
+// a softmax thread holds its row's 128 scores.
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 104, kMmaRegs = 56;
+constexpr int kSplitRegs = 2 * kSoftmaxRegs + kConvertRegs + kMmaRegs;
+static_assert(kSplitRegs <= 4 * 128, "the launch's registers cover the split");
 constexpr int kStages = 2;
 constexpr int kEntrySlots = 4;
 constexpr float kLazy = 8.0f;                  // log2 of how far a maximum may pass its reference
@@ -50,7 +55,7 @@ struct __align__(1024) Smem {
     uint16_t nan_mask[kStages][kKeys][kDim / 16];   // edge steps: NaN codes of each value row
     uint16_t row_nan[kTiles * 128][kDim / 16];      // channels in which a row has met NaN in an edge step
     int32_t nan_step[kStages];                      // 1 + the last edge step in which a NaN was found
-    uint64_t q_full[kTiles], s_full[kTiles], p_full[kTiles], o_full[kTiles];
+    uint64_t q_full[kTiles], s_full[kTiles], p_half[kTiles], p_full[kTiles], o_full[kTiles];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], entry_full[kEntrySlots];
     uint64_t drained;
     uint32_t tmem;
@@ -74,6 +79,18 @@ __device__ __forceinline__ bool wait_for(const uint64_t &bar, uint32_t parity)
         return true;
     atomicOr(&g_error, ERR_ATTN_WAIT);
     return false;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void grow_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int kRegs>
+__device__ __forceinline__ void shrink_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 template <int kDim>
@@ -109,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kTiles; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 128);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_half[i]), 128);
             mbar_init(smem_u32(&sm.p_full[i]), 128);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
@@ -137,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto o_col = [&](int t) { return tmem + 256u + static_cast<uint32_t>(kDim) * t; };
 
     if (warp < kSoftmaxWarps) {
+        grow_registers<kSoftmaxRegs>();
         const int t = warp >> 2, in_tile = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int64_t r = row0 + 128 * t + in_tile;
@@ -182,29 +201,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
                 const int lo = see.lo - k0, hi = see.hi - k0;
+                float v[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_32x32b_x32(sc + 32 * c, reinterpret_cast<uint32_t (&)[32]>(v[c]));
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_wait_regs(reinterpret_cast<uint32_t (&)[32]>(v[c]));
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        v[i >> 5][i & 31] = i >= lo && i < hi ? v[i >> 5][i & 31] : -INFINITY;
+                }
                 float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(sc + 32 * c, v);
-                    tmem_ld_wait_regs(v);
+                for (int n = 0; n < 8; ++n) {
+                    const PageEntry e = pe[(16 * n) >> shift];
+                    const float *x = &v[n >> 1][16 * (n & 1)];
+                    float g = fmaxf(x[0], x[1]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const PageEntry e = pe[(32 * c + 16 * h) >> shift];
-                        float g = -INFINITY;
-                        if (edge) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int x = 32 * c + 16 * h + i;
-                                g = fmaxf(g, x >= lo && x < hi ? __uint_as_float(v[16 * h + i]) : -INFINITY);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                g = fmaxf(g, __uint_as_float(v[16 * h + i]));
-                        }
-                        top = fmaxf(top, g == -INFINITY ? g : fmaf(g, c_row * e.ks, e.lv));
-                    }
+                    for (int i = 2; i < 16; i += 2)
+                        g = fmaxf(g, fmaxf(x[i], x[i + 1]));
+                    top = fmaxf(top, g == -INFINITY ? g : fmaf(g, c_row * e.ks, e.lv));
                 }
                 const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -213,15 +231,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= f;
                     ref = next;
                     if (j > 0) {   // the accumulator's last product has completed: S of this step was issued after it
+#pragma unroll 1
+                        for (int c = 0; c < kDim / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16_wait(oc + 16 * c, o);
 #pragma unroll
-                        for (int c = 0; c < kDim / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_ld_32x32b_x32(oc + 32 * c, v);
-                            tmem_ld_wait_regs(v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                            tmem_st_32x32b_x32(oc + 32 * c, v);
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st_32x32b_x16(oc + 16 * c, o);
                         }
                     }
                 }
@@ -232,33 +249,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const auto weights = [&](auto careful) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32], p[16];
-                        tmem_ld_32x32b_x32(sc + 32 * c, v);
-                        tmem_ld_wait_regs(v);
+                        uint32_t p[16];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const PageEntry e = pe[(32 * c + 16 * h) >> shift];
-                            const float ck = c_row * e.ks, off = e.lv - at;
-                            float w[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float x = __uint_as_float(v[16 * h + i]);
-                                if constexpr (decltype(careful)::value) {
-                                    const int col = 32 * c + 16 * h + i;
-                                    w[i] = col >= lo && col < hi ? ex2(fmaf(x, ck, e.lv) - at) : 0.0f;
-                                } else {
-                                    w[i] = ex2(fmaf(x, ck, off));
-                                }
-                            }
-                            float sum = 0.0f;
+                            const float ck = c_row * e.ks;
+                            const float2 ck2 = make_float2(ck, ck), off2 = make_float2(e.lv - at, e.lv - at);
+                            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                sum += w[i] + w[i + 1];
-                                p[8 * h + i / 2] = pack_half2(w[i], w[i + 1]);
+                                const float2 x = make_float2(v[c][16 * h + i], v[c][16 * h + i + 1]);
+                                float2 w;
+                                if constexpr (decltype(careful)::value) {
+                                    w.x = x.x == -INFINITY ? 0.0f : ex2(fmaf(x.x, ck, e.lv) - at);
+                                    w.y = x.y == -INFINITY ? 0.0f : ex2(fmaf(x.y, ck, e.lv) - at);
+                                } else {
+                                    w = __ffma2_rn(x, ck2, off2);
+                                    w = make_float2(ex2(w.x), ex2(w.y));
+                                }
+                                sum = __fadd2_rn(sum, w);
+                                p[8 * h + i / 2] = pack_half2(w.x, w.y);
                             }
-                            l = fmaf(sum, e.inv_vs, l);
+                            l = fmaf(sum.x + sum.y, e.inv_vs, l);
                         }
-                        tmem_st_32x32b_x16(sc + 16 * c, p);   // columns of S that are read already
+                        tmem_st_32x32b_x16(sc + 16 * c, p);   // over columns of S that are in registers already
+                        if (c == 1) {   // the first half's product can start
+                            tmem_st_wait();
+                            tc_fence_before();
+                            mbar_arrive(smem_u32(&sm.p_half[t]));
+                        }
                     }
                 };
                 if (edge || __any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f))
@@ -341,27 +360,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------------ conversion
+        shrink_registers<kConvertRegs>();
         constexpr int kPieces = kDim / 16;                        // 16-byte pieces of codes per token
         constexpr int kRowStep = 32 * kConvertWarps / kPieces;    // tokens between a thread's pieces
         constexpr int kPer = kKeys / kRowStep;
         const int tid = threadIdx.x - 32 * kSoftmaxWarps, r0 = tid / kPieces, c = tid % kPieces;
         const int64_t head_off = static_cast<int64_t>(kh) * page;
-        const auto id_of = [&](int tok) -> int32_t {              // page of a token that any row sees, else -1
-            if (tok < out_lo || tok >= end)
-                return -1;
-            const int32_t id = a.batch.page_table[b * a.batch.ld_table + tok / page];
-            if (id < 0 || id >= a.cache.num_pages) {
+        // Lane p of each warp holds the number of page p of a step (8 at most), loaded two steps ahead and looked at
+        // only when its codes are loaded.
+        const int shift = 31 - __clz(page);
+        const auto page_ids = [&](int j) -> int32_t {
+            const int64_t tok = begin + static_cast<int64_t>(j) * kKeys + lane * page;
+            return lane < kKeys / page && tok < end && tok + page > out_lo ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift)] : -2;
+        };
+        const auto checked = [&](int32_t id) -> int32_t {        // -2: no page; out of range: -1, reported
+            if (id != -2 && (id < 0 || id >= a.cache.num_pages)) {
                 atomicOr(&g_error, ERR_KV_RANGE);
                 return -1;
             }
             return id;
         };
-        const auto load = [&](const uint8_t *codes, int k0, const int32_t (&id)[kPer], uint4 (&w)[kPer]) {
+        int32_t id[kPer];   // pages of the step whose codes are loaded next, by piece
+        const auto ids = [&](int32_t of_lane) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                id[i] = __shfl_sync(0xFFFFFFFFu, of_lane, (r0 + i * kRowStep) >> shift);
+        };
+        const auto load = [&](const uint8_t *codes, int k0, uint4 (&w)[kPer]) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int tok = k0 + r0 + i * kRowStep;
                 w[i] = make_uint4(0, 0, 0, 0);
-                if (id[i] >= 0)
+                if (id[i] >= 0 && tok >= out_lo && tok < end)   // positions that no row sees stay zero
                     w[i] = *reinterpret_cast<const uint4 *>(
                         codes + ((static_cast<int64_t>(id[i]) * a.cache.heads * page + head_off + (tok & (page - 1))) * kDim + 16 * c));
             }
@@ -384,19 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_shared_v4(dst + operand_at(r, 2 * c), h[0], h[1], h[2], h[3]);
             }
         };
-        int32_t id[kPer], id_next[kPer];
+        // A step's codes are loaded while the step before it is converted, its pages' numbers one step earlier still.
         uint4 kw[kPer], vw[kPer];
-        const auto ids = [&](int j, int32_t (&x)[kPer]) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                x[i] = id_of(begin + j * kKeys + r0 + i * kRowStep);
-        };
-        if (steps > 0) {
-            ids(0, id);
-            load(a.cache.k_codes, begin, id, kw);
-            load(a.cache.v_codes, begin, id, vw);
-            ids(1, id_next);
-        }
+        int32_t lane_id = checked(page_ids(0)), next_id = page_ids(1);
+        ids(lane_id);
+        load(a.cache.k_codes, begin, kw);
+        load(a.cache.v_codes, begin, vw);
         for (int j = 0; j < steps; ++j) {
             const int k0 = begin + j * kKeys, st = j % kStages;
             const bool edge = k0 < in_lo || k0 + kKeys > in_hi;
@@ -404,11 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
                 if (lane < kKeys / page) {
-                    const int32_t p = id_of(max(k0 + lane * page, out_lo));   // a page that a window cuts counts from there
-                    const bool any = k0 + lane * page < end && k0 + (lane + 1) * page > out_lo;
-                    const int64_t bh = static_cast<int64_t>(any && p >= 0 ? p : 0) * a.cache.heads + kh;
-                    PageEntry e{p, 1.0f, 0.0f, 1.0f};
-                    if (any && p >= 0) {
+                    PageEntry e{lane_id, 1.0f, 0.0f, 1.0f};
+                    if (lane_id >= 0) {
+                        const int64_t bh = static_cast<int64_t>(lane_id) * a.cache.heads + kh;
                         const float vs = a.cache.v_scale[bh];
                         e.ks = a.cache.k_scale[bh];
                         e.lv = lg2(vs);
@@ -425,8 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store(smem_u32(sm.k[st]), kw[i], r0 + i * kRowStep);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.k_full[st]));
-            if (j + 1 < steps)
-                load(a.cache.k_codes, k0 + kKeys, id_next, kw);
+            lane_id = checked(next_id);
+            next_id = page_ids(j + 2);
+            ids(lane_id);
+            load(a.cache.k_codes, k0 + kKeys, kw);   // zeros past the end
 
             if (!wait_for(sm.v_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
@@ -450,13 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.v_full[st]));
-            if (j + 1 < steps) {
-                load(a.cache.v_codes, k0 + kKeys, id_next, vw);
-                ids(j + 2, id_next);
-            }
+            load(a.cache.v_codes, k0 + kKeys, vw);
         }
     } else {
         // ------------------------------------------------------------------ MMA issue
+        shrink_registers<kMmaRegs>();
+    }
+    if (warp == kMmaWarp) {
         constexpr uint32_t kQk = idesc_f16(kKeys, false), kPv = idesc_f16(kDim, true);
         const auto qk = [&](int t, int st) {
             const uint32_t q = smem_u32(sm.q[t]), k = smem_u32(sm.k[st]);
@@ -466,43 +489,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_mma_f16_elect(s_col(t), smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), kQk, x > 0);
             }
         };
-        const auto pv = [&](int t, int st, bool accumulate) {
+        const auto pv = [&](int t, int st, int half, bool accumulate) {
             const uint32_t v = smem_u32(sm.v[st]);
 #pragma unroll
-            for (int x = 0; x < kKeys / 16; ++x)   // values: 8-token groups 1024 bytes apart, 64-channel blocks 16 KB
+            for (int y = 0; y < kKeys / 32; ++y) {   // values: 8-token groups 1024 bytes apart, 64-channel blocks 16 KB
+                const int x = half * (kKeys / 32) + y;
                 tc_mma_f16_ts_elect(o_col(t), s_col(t) + 8 * x, smem_desc(v + x * 2048, 128 * 128, 1024, 2), kPv,
                                     accumulate || x > 0);
+            }
         };
-        bool ok = true;
-        for (int t = 0; ok && steps > 0 && t < tiles; ++t) {
+        // Each tile goes round: first half of the weights ready -> half a product; second half -> the rest; that
+        // product done (the next S goes over the weights it reads) and the next keys there -> S.  Whichever tile is
+        // ready goes next, so that one's product runs while the other's completion is on its way.
+        int step[kTiles] = {0, 0}, phase[kTiles] = {2, 2};
+        uint32_t keys_used = 0, values_used = 0;   // bit st: one of two tiles is done with the stage (a tile may be a step ahead)
+        bool ok = steps > 0;
+        for (int t = 0; ok && t < tiles; ++t) {
             ok = wait_for(sm.q_full[t], 0) && wait_for(sm.k_full[0], 0);
-            if (!ok)
-                break;
-            tc_fence_after();
-            qk(t, 0);
-            tc_commit_elect(smem_u32(&sm.s_full[t]));
-        }
-        if (ok && steps > 0)
-            tc_commit_elect(smem_u32(&sm.k_empty[0]));
-        for (int j = 0; ok && j < steps; ++j) {
-            const int st = j % kStages, nx = (j + 1) % kStages;
-            for (int t = 0; t < tiles; ++t) {
-                if (!(ok = wait_for(sm.v_full[st], (j / kStages) & 1) && wait_for(sm.p_full[t], j & 1)))
-                    break;
+            if (ok) {
                 tc_fence_after();
-                pv(t, st, j > 0);
-                tc_commit_elect(smem_u32(&sm.o_full[t]));
-                if (t == tiles - 1)
-                    tc_commit_elect(smem_u32(&sm.v_empty[st]));
-                if (j + 1 < steps) {
-                    // the next S goes over the weights that this product reads: wait for it
-                    if (!(ok = wait_for(sm.k_full[nx], ((j + 1) / kStages) & 1) && wait_for(sm.o_full[t], j & 1)))
-                        break;
-                    tc_fence_after();
-                    qk(t, nx);
-                    tc_commit_elect(smem_u32(&sm.s_full[t]));
-                    if (t == tiles - 1)
-                        tc_commit_elect(smem_u32(&sm.k_empty[nx]));
+                qk(t, 0);
+                tc_commit_elect(smem_u32(&sm.s_full[t]));
+                phase[t] = 0;
+            }
+        }
+        if (ok)
+            tc_commit_elect(smem_u32(&sm.k_empty[0]));
+        int left = ok ? tiles * steps : 0;
+        uint64_t since = 0;
+        uint32_t idle = 0;   // rounds without progress; the timer is slow to read (about 1,000 cycles), so only now and then
+        while (left > 0) {
+            bool went = false;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const int j = step[t], st = j % kStages;
+                if (t >= tiles || j >= steps)
+                    continue;
+                if (phase[t] == 0) {
+                    if (mbar_test_wait(smem_u32(&sm.p_half[t]), j & 1) &&
+                        mbar_test_wait(smem_u32(&sm.v_full[st]), (j / kStages) & 1)) {
+                        tc_fence_after();
+                        pv(t, st, 0, j > 0);
+                        phase[t] = 1;
+                        went = true;
+                    }
+                } else if (phase[t] == 1) {
+                    if (mbar_test_wait(smem_u32(&sm.p_full[t]), j & 1)) {
+                        tc_fence_after();
+                        pv(t, st, 1, true);
+                        tc_commit_elect(smem_u32(&sm.o_full[t]));
+                        values_used ^= 1u << st;
+                        if (tiles == 1 || (values_used >> st & 1u) == 0)
+                            tc_commit_elect(smem_u32(&sm.v_empty[st]));
+                        phase[t] = 2;
+                        --left;
+                        went = true;
+                        if (j + 1 == steps)
+                            step[t] = steps;
+                    }
+                } else {
+                    const int nx = (j + 1) % kStages;
+                    if (mbar_test_wait(smem_u32(&sm.o_full[t]), j & 1) &&
+                        mbar_test_wait(smem_u32(&sm.k_full[nx]), ((j + 1) / kStages) & 1)) {
+                        tc_fence_after();
+                        qk(t, nx);
+                        tc_commit_elect(smem_u32(&sm.s_full[t]));
+                        keys_used ^= 1u << nx;
+                        if (tiles == 1 || (keys_used >> nx & 1u) == 0)
+                            tc_commit_elect(smem_u32(&sm.k_empty[nx]));
+                        step[t] = j + 1;
+                        phase[t] = 0;
+                        went = true;
+                    }
+                }
+            }
+            idle = went ? 0 : idle + 1;
+            if ((idle & 1023u) == 1023u) {
+                const uint64_t now = globaltimer_ns();
+                if (idle == 1023u) {
+                    since = now;
+                } else if (now - since > kWaitNs) {
+                    atomicOr(&g_error, ERR_ATTN_WAIT);
+                    break;
                 }
             }
         }
@@ -523,9 +591,15 @@ cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     // More than half of an SM's shared memory even at dim 64: a second CTA on the SM would wait for the first one's TMEM.
     constexpr int kNeed = sizeof(Smem<kDim>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024, "fits an SM");
-    const cudaError_t e = allow_shared<tile_kernel<kDim>>(kSmem);
+    cudaError_t e = allow_shared<tile_kernel<kDim>>(kSmem);
     if (e != cudaSuccess)
         return e;
+    static const bool registers_fit = [] {   // a property of the build
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, tile_kernel<kDim>) == cudaSuccess && 4 * f.numRegs >= kSplitRegs;
+    }();
+    if (!registers_fit)
+        return cudaErrorLaunchOutOfResources;
     const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
     const int64_t tiles = (rows + kTiles * 128 - 1) / (kTiles * 128), x = tiles * a.cache.heads * plan.splits;
     if (x > INT32_MAX)
