@@ -16,11 +16,9 @@
 //    exact, and into shared memory in the 128-byte-swizzled operand layout.
 //    Keys are the first product's K-major B operand; values have the same
 //    layout, read as the second product's MN-major B operand.
-//  - 1 warp issues the MMAs.
+//  - 2 warps issue the MMAs, one for each row tile.
 // Shared memory at dim 128: queries 64 KB, two stages of keys and of values 32
 // KB each.
-#include <type_traits>
-
 #include "attention.cuh"
 #include "ptx.cuh"
 
@@ -36,10 +34,10 @@ constexpr int kTiles = 2;                      // row tiles of 128 per CTA
 constexpr int kSoftmaxWarps = 4 * kTiles;
 constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups, for the register split; three warps idle
+constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups, for the register split; two warps idle
 // Registers per thread of the three kinds of warpgroup, out of the 128 that 512 threads launch with (run_tile checks):
 // a softmax thread holds its row's 128 scores.
-constexpr int kSoftmaxRegs = 176, kConvertRegs = 104, kMmaRegs = 56;
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 120, kMmaRegs = 40;
 constexpr int kSplitRegs = 2 * kSoftmaxRegs + kConvertRegs + kMmaRegs;
 static_assert(kSplitRegs <= 4 * 128, "the launch's registers cover the split");
 constexpr int kStages = 2;
@@ -52,9 +50,9 @@ struct __align__(1024) Smem {
     uint8_t k[kStages][kKeys * kDim * 2];
     uint8_t v[kStages][kKeys * kDim * 2];
     PageEntry entry[kEntrySlots][kKeys / 16];
-    uint16_t nan_mask[kStages][kKeys][kDim / 16];   // edge steps: NaN codes of each value row
+    uint16_t nan_mask[kStages][kKeys][kDim / 16];   // NaN codes of the value rows of a conversion warp that found any
     uint16_t row_nan[kTiles * 128][kDim / 16];      // channels in which a row has met NaN in an edge step
-    int32_t nan_step[kStages];                      // 1 + the last edge step in which a NaN was found
+    int32_t nan_step[kStages][kConvertWarps];       // 1 + the last edge step in which that warp found a NaN
     uint64_t q_full[kTiles], s_full[kTiles], p_half[kTiles], p_full[kTiles], o_full[kTiles];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], entry_full[kEntrySlots];
     uint64_t drained;
@@ -73,9 +71,11 @@ constexpr uint32_t idesc_f16(int n, bool b_mn_major)   // M = 128, FP32 accumula
     return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
 }
 
+// The outcome is a vote, so that control flow that hangs on it is warp-uniform (and operands computed there can live in
+// uniform registers).
 __device__ __forceinline__ bool wait_for(const uint64_t &bar, uint32_t parity)
 {
-    if (mbar_wait_bounded(smem_u32(&bar), parity, kWaitNs))
+    if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bar), parity, kWaitNs)))
         return true;
     atomicOr(&g_error, ERR_ATTN_WAIT);
     return false;
@@ -109,12 +109,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(&g_error, ERR_KV_RANGE);
         return;
     }
-    const int64_t rows = static_cast<int64_t>(s.n) * group;
-    const int64_t row0 = static_cast<int64_t>(a.causal ? row_tiles - 1 - tile : tile) * (kTiles * 128);   // causal: longest first
+    const int rows = s.n * group;   // below 2^31 (run_tile checks max_tokens)
+    const int row0 = (a.causal ? row_tiles - 1 - tile : tile) * (kTiles * 128);   // causal: longest first
     if (row0 >= rows || (split > 0 && split * plan.chunk >= s.len))
         return;
-    const int64_t row_end = row0 + kTiles * 128 < rows ? row0 + kTiles * 128 : rows;
-    const Span first = seen_by(a, s, static_cast<int>(row0 / group)), last = seen_by(a, s, static_cast<int>((row_end - 1) / group));
+    const int row_end = min(rows, row0 + kTiles * 128);
+    const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, (row_end - 1) / group);
     const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);     // seen by every row
     const int out_lo = min(first.lo, last.lo);                                    // seen by any
     const int begin = max(split * plan.chunk, out_lo & ~(kKeys - 1));
@@ -133,13 +133,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 32 * kConvertWarps);
             mbar_init(smem_u32(&sm.v_full[i]), 32 * kConvertWarps);
-            mbar_init(smem_u32(&sm.k_empty[i]), 1);
-            mbar_init(smem_u32(&sm.v_empty[i]), 1);
-            sm.nan_step[i] = 0;
+            mbar_init(smem_u32(&sm.k_empty[i]), tiles);
+            mbar_init(smem_u32(&sm.v_empty[i]), tiles);
+            for (int w = 0; w < kConvertWarps; ++w)
+                sm.nan_step[i][w] = 0;
         }
         for (int i = 0; i < kEntrySlots; ++i)
             mbar_init(smem_u32(&sm.entry_full[i]), 1);
-        mbar_init(smem_u32(&sm.drained), 1);
+        mbar_init(smem_u32(&sm.drained), tiles);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -150,22 +151,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    const auto s_col = [&](int t) { return tmem + 128u * t; };
-    const auto o_col = [&](int t) { return tmem + 256u + static_cast<uint32_t>(kDim) * t; };
+    // All 512 columns are this CTA's, so they start at 0: S of tile t at column 128 t, its output at 256 + kDim t.
+    if (sm.tmem != 0) {
+        if (threadIdx.x == 0)
+            atomicOr(&g_error, ERR_ATTN_WAIT);
+        __syncthreads();
+        if (warp == kMmaWarp)
+            tmem_dealloc(sm.tmem, 512);
+        return;
+    }
 
     if (warp < kSoftmaxWarps) {
         grow_registers<kSoftmaxRegs>();
         const int t = warp >> 2, in_tile = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int64_t r = row0 + 128 * t + in_tile;
+        const int r = row0 + 128 * t + in_tile;
         const bool live = r < rows;
         if (t < tiles) {
-            const int tok = live ? static_cast<int>(r / group) : 0, head = kh * group + (live ? static_cast<int>(r % group) : 0);
+            const int tok = live ? r / group : 0, head = kh * group + (live ? r % group : 0);
             const Span see = live ? seen_by(a, s, tok) : Span{0, 0};
             // what the tile's rows all see
-            const int64_t tr0 = row0 + 128 * t, tr1 = (tr0 + 128 < rows ? tr0 + 128 : rows) - 1;
-            const Span tf = seen_by(a, s, static_cast<int>(tr0 / group)), tl = seen_by(a, s, static_cast<int>(tr1 / group));
+            const Span tf = seen_by(a, s, (row0 + 128 * t) / group), tl = seen_by(a, s, (min(rows, row0 + 128 * t + 128) - 1) / group);
             const int t_lo = max(tf.lo, tl.lo), t_hi = min(tf.hi, tl.hi);
             float c_row;
             {
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float ref = -INFINITY, l = 0.0f;
             bool met_nan = false, ok = true;
             const int shift = 31 - __clz(page);
-            const uint32_t sc = s_col(t) + lanes, oc = o_col(t) + lanes;
+            const uint32_t sc = 128u * t + lanes, oc = 256u + static_cast<uint32_t>(kDim) * t + lanes;
             for (int j = 0; j < steps; ++j) {
                 const int k0 = begin + j * kKeys;
                 const bool edge = k0 < t_lo || k0 + kKeys > t_hi;
@@ -201,28 +207,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
                 const int lo = see.lo - k0, hi = see.hi - k0;
-                float v[4][32];
+                float v[4][32], top = -INFINITY;
+                if (!edge) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld_32x32b_x32(sc + 32 * c, reinterpret_cast<uint32_t (&)[32]>(v[c]));
+                    for (int c = 0; c < 4; ++c)
+                        tmem_ld_32x32b_x32(sc + 32 * c, reinterpret_cast<uint32_t (&)[32]>(v[c]));
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld_wait_regs(reinterpret_cast<uint32_t (&)[32]>(v[c]));
-                if (edge) {
+                    for (int c = 0; c < 4; ++c)
+                        tmem_ld_wait_regs(reinterpret_cast<uint32_t (&)[32]>(v[c]));
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        v[i >> 5][i & 31] = i >= lo && i < hi ? v[i >> 5][i & 31] : -INFINITY;
-                }
-                float top = -INFINITY;
+                    for (int n = 0; n < 8; ++n) {
+                        const PageEntry e = pe[(16 * n) >> shift];
+                        const float *x = &v[n >> 1][16 * (n & 1)];
+                        float g = fmaxf(x[0], x[1]);
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const PageEntry e = pe[(16 * n) >> shift];
-                    const float *x = &v[n >> 1][16 * (n & 1)];
-                    float g = fmaxf(x[0], x[1]);
+                        for (int i = 2; i < 16; i += 2)
+                            g = fmaxf(g, fmaxf(x[i], x[i + 1]));
+                        top = fmaxf(top, fmaf(g, c_row * e.ks, e.lv));
+                    }
+                } else {   // some rows do not see some keys; short code, scores read from TMEM again below
+#pragma unroll 1
+                    for (int n = 0; n < 8; ++n) {
+                        const PageEntry e = pe[(16 * n) >> shift];
+                        uint32_t x[16];
+                        tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
 #pragma unroll
-                    for (int i = 2; i < 16; i += 2)
-                        g = fmaxf(g, fmaxf(x[i], x[i + 1]));
-                    top = fmaxf(top, g == -INFINITY ? g : fmaf(g, c_row * e.ks, e.lv));
+                        for (int i = 0; i < 16; ++i)
+                            if (16 * n + i >= lo && 16 * n + i < hi)
+                                top = fmaxf(top, fmaf(__uint_as_float(x[i]), c_row * e.ks, e.lv));
+                    }
                 }
                 const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -246,7 +259,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Ordinary steps take the exponent in one fused multiply-add.  Past 2^20 the reference's own rounding
                 // would show in it (and could reach FP16's limit): there, as in edge steps, the score is rounded first,
                 // so that the largest one meets its own copy in the reference.
-                const auto weights = [&](auto careful) {
+                if (edge || __any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f)) {
+#pragma unroll 1
+                    for (int n = 0; n < 8; ++n) {
+                        const PageEntry e = pe[(16 * n) >> shift];
+                        uint32_t x[16], p[8];
+                        tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            float w[2];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int col = 16 * n + i + y;
+                                w[y] = col >= lo && col < hi ? ex2(fmaf(__uint_as_float(x[i + y]), c_row * e.ks, e.lv) - at) : 0.0f;
+                                sum += w[y];
+                            }
+                            p[i / 2] = pack_half2(w[0], w[1]);
+                        }
+                        l = fmaf(sum, e.inv_vs, l);
+                        tmem_st_32x32b_x8(sc + 8 * n, p);   // over columns of S that are read already
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sm.p_half[t]));
+                } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t p[16];
@@ -258,32 +295,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float2 x = make_float2(v[c][16 * h + i], v[c][16 * h + i + 1]);
-                                float2 w;
-                                if constexpr (decltype(careful)::value) {
-                                    w.x = x.x == -INFINITY ? 0.0f : ex2(fmaf(x.x, ck, e.lv) - at);
-                                    w.y = x.y == -INFINITY ? 0.0f : ex2(fmaf(x.y, ck, e.lv) - at);
-                                } else {
-                                    w = __ffma2_rn(x, ck2, off2);
-                                    w = make_float2(ex2(w.x), ex2(w.y));
-                                }
+                                float2 w = __ffma2_rn(make_float2(v[c][16 * h + i], v[c][16 * h + i + 1]), ck2, off2);
+                                w = make_float2(ex2(w.x), ex2(w.y));
                                 sum = __fadd2_rn(sum, w);
                                 p[8 * h + i / 2] = pack_half2(w.x, w.y);
                             }
                             l = fmaf(sum.x + sum.y, e.inv_vs, l);
                         }
-                        tmem_st_32x32b_x16(sc + 16 * c, p);   // over columns of S that are in registers already
+                        tmem_st_32x32b_x16(sc + 16 * c, p);
                         if (c == 1) {   // the first half's product can start
                             tmem_st_wait();
                             tc_fence_before();
                             mbar_arrive(smem_u32(&sm.p_half[t]));
                         }
                     }
-                };
-                if (edge || __any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f))
-                    weights(std::true_type{});
-                else
-                    weights(std::false_type{});
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 if (k0 < in_lo || k0 + kKeys > in_hi) {   // the conversion warps keep NaN out of such a step's values
@@ -291,12 +317,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (sm.nan_step[j % kStages] == j + 1) {
+                    constexpr int kRowsPerWarp = 32 / (kDim / 16);   // of a conversion warp, among kConvertWarps * that
+                    for (int w = 0; w < kConvertWarps; ++w) {
+                        if (sm.nan_step[j % kStages][w] != j + 1)
+                            continue;
                         uint16_t *mine = sm.row_nan[128 * t + in_tile];
                         for (int c = 0; c < kDim / 16; ++c) {
                             uint32_t m = met_nan ? mine[c] : 0u;
                             for (int x = max(lo, 0); x < min(hi, kKeys); ++x)
-                                m |= sm.nan_mask[j % kStages][x][c];
+                                if (x / kRowsPerWarp % kConvertWarps == w)
+                                    m |= sm.nan_mask[j % kStages][x][c];
                             mine[c] = static_cast<uint16_t>(m);
                         }
                         met_nan = true;
@@ -313,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = !final ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
                 uint16_t *out = a.out + row * a.ot + head * a.oh;
                 float *part = ws_out + (at * plan.splits + split) * kDim;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kDim / 32; ++c) {
                     uint32_t v[32];
                     if (steps > 0) {
@@ -329,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i)
                         o[i] = __uint_as_float(v[i]) * inv;
                     if (met_nan) {
+                        const uint32_t m = sm.row_nan[128 * t + in_tile][2 * c] | sm.row_nan[128 * t + in_tile][2 * c + 1] << 16;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (sm.row_nan[128 * t + in_tile][2 * c + (i >> 4)] >> (i & 15) & 1)
-                                o[i] = __uint_as_float(0x7FC00000u);
+                            o[i] = m >> i & 1 ? __uint_as_float(0x7FC00000u) : o[i];
                     }
                     if (live && final) {
 #pragma unroll
@@ -453,24 +483,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             if (!wait_for(sm.v_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
+            if (edge) {   // NaN that only some rows see stays out of the product (a weight of zero would not stop it)
+                uint32_t odd = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int r = r0 + i * kRowStep;
-                if (edge) {   // NaN that only some rows see stays out of the product (a weight of zero would not stop it)
-                    uint32_t x[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w}, m = 0;
+                for (int i = 0; i < kPer; ++i)
+                    odd |= nan_bytes(vw[i].x) | nan_bytes(vw[i].y) | nan_bytes(vw[i].z) | nan_bytes(vw[i].w);
+                if (__any_sync(0xFFFFFFFFu, odd != 0)) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const uint32_t n = nan_bytes(x[y]) >> 7;   // 1 in each NaN byte
-                        x[y] &= ~(n * 0xFFu);
-                        m |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * y);
+                    for (int i = 0; i < kPer; ++i) {
+                        uint32_t x[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w}, m = 0;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t n = nan_bytes(x[y]) >> 7;   // 1 in each NaN byte
+                            x[y] &= ~(n * 0xFFu);
+                            m |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * y);
+                        }
+                        vw[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        sm.nan_mask[st][r0 + i * kRowStep][c] = static_cast<uint16_t>(m);
                     }
-                    vw[i] = make_uint4(x[0], x[1], x[2], x[3]);
-                    sm.nan_mask[st][r][c] = static_cast<uint16_t>(m);
-                    if (m != 0)
-                        sm.nan_step[st] = j + 1;
+                    if (lane == 0)
+                        sm.nan_step[st][warp - kSoftmaxWarps] = j + 1;
                 }
-                store(smem_u32(sm.v[st]), vw[i], r);
             }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                store(smem_u32(sm.v[st]), vw[i], r0 + i * kRowStep);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.v_full[st]));
             load(a.cache.v_codes, k0 + kKeys, vw);
@@ -479,99 +516,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------------ MMA issue
         shrink_registers<kMmaRegs>();
     }
-    if (warp == kMmaWarp) {
+    if (warp >= kMmaWarp && warp - kMmaWarp < tiles) {
         constexpr uint32_t kQk = idesc_f16(kKeys, false), kPv = idesc_f16(kDim, true);
-        const auto qk = [&](int t, int st) {
-            const uint32_t q = smem_u32(sm.q[t]), k = smem_u32(sm.k[st]);
+        const uint32_t q_lo = (smem_u32(sm.q) & 0x3FFFFu) >> 4 | 1u << 16, k_lo = (smem_u32(sm.k) & 0x3FFFFu) >> 4 | 1u << 16;
+        const uint32_t v_lo = (smem_u32(sm.v) & 0x3FFFFu) >> 4 | (128u * 128u >> 4) << 16;   // 64-channel blocks 16 KB apart
+        constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;   // 8 rows 1 KB apart, version 1, 128-byte swizzle
+        constexpr uint32_t kTileUnits = 128 * kDim * 2 / 16;           // an operand tile in 16-byte units
+        const auto qk = [&](uint32_t t, uint32_t st) {
 #pragma unroll
             for (int x = 0; x < kDim / 16; ++x) {
-                const uint32_t off = (x >> 2) * (128 * 128) + (x & 3) * 32;
-                tc_mma_f16_elect(s_col(t), smem_desc(q + off, 16, 1024, 2), smem_desc(k + off, 16, 1024, 2), kQk, x > 0);
+                const uint32_t off = (x >> 2) * (128 * 128 / 16) + (x & 3) * 2;
+                tc_mma_f16_elect(128 * t, q_lo + t * kTileUnits + off, kHi, k_lo + st * kTileUnits + off, kHi, kQk, x > 0);
             }
+            tc_commit_elect(smem_u32(&sm.s_full[t]));
         };
-        const auto pv = [&](int t, int st, int half, bool accumulate) {
-            const uint32_t v = smem_u32(sm.v[st]);
+        const auto pv = [&](uint32_t t, uint32_t st, int half, bool accumulate) {
 #pragma unroll
-            for (int y = 0; y < kKeys / 32; ++y) {   // values: 8-token groups 1024 bytes apart, 64-channel blocks 16 KB
+            for (int y = 0; y < kKeys / 32; ++y) {   // 8-token groups 1 KB apart
                 const int x = half * (kKeys / 32) + y;
-                tc_mma_f16_ts_elect(o_col(t), s_col(t) + 8 * x, smem_desc(v + x * 2048, 128 * 128, 1024, 2), kPv,
+                tc_mma_f16_ts_elect(256 + kDim * t, 128 * t + 8 * x, v_lo + st * kTileUnits + x * (2048 / 16), kHi, kPv,
                                     accumulate || x > 0);
             }
         };
-        // Each tile goes round: first half of the weights ready -> half a product; second half -> the rest; that
-        // product done (the next S goes over the weights it reads) and the next keys there -> S.  Whichever tile is
-        // ready goes next, so that one's product runs while the other's completion is on its way.
-        int step[kTiles] = {0, 0}, phase[kTiles] = {2, 2};
-        uint32_t keys_used = 0, values_used = 0;   // bit st: one of two tiles is done with the stage (a tile may be a step ahead)
-        bool ok = steps > 0;
-        for (int t = 0; ok && t < tiles; ++t) {
-            ok = wait_for(sm.q_full[t], 0) && wait_for(sm.k_full[0], 0);
-            if (ok) {
-                tc_fence_after();
-                qk(t, 0);
-                tc_commit_elect(smem_u32(&sm.s_full[t]));
-                phase[t] = 0;
-            }
-        }
-        if (ok)
+        // A warp for each tile, with no more between a wait and an issue than the issue needs: scores, then for each
+        // step the first half's product, the second half's, and -- that done, for the next scores go over the weights
+        // it reads -- the next scores.
+        const uint32_t t = warp - kMmaWarp;
+        bool ok = steps > 0 && wait_for(sm.q_full[t], 0) && wait_for(sm.k_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            qk(t, 0);
             tc_commit_elect(smem_u32(&sm.k_empty[0]));
-        int left = ok ? tiles * steps : 0;
-        uint64_t since = 0;
-        uint32_t idle = 0;   // rounds without progress; the timer is slow to read (about 1,000 cycles), so only now and then
-        while (left > 0) {
-            bool went = false;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const int j = step[t], st = j % kStages;
-                if (t >= tiles || j >= steps)
-                    continue;
-                if (phase[t] == 0) {
-                    if (mbar_test_wait(smem_u32(&sm.p_half[t]), j & 1) &&
-                        mbar_test_wait(smem_u32(&sm.v_full[st]), (j / kStages) & 1)) {
-                        tc_fence_after();
-                        pv(t, st, 0, j > 0);
-                        phase[t] = 1;
-                        went = true;
-                    }
-                } else if (phase[t] == 1) {
-                    if (mbar_test_wait(smem_u32(&sm.p_full[t]), j & 1)) {
-                        tc_fence_after();
-                        pv(t, st, 1, true);
-                        tc_commit_elect(smem_u32(&sm.o_full[t]));
-                        values_used ^= 1u << st;
-                        if (tiles == 1 || (values_used >> st & 1u) == 0)
-                            tc_commit_elect(smem_u32(&sm.v_empty[st]));
-                        phase[t] = 2;
-                        --left;
-                        went = true;
-                        if (j + 1 == steps)
-                            step[t] = steps;
-                    }
-                } else {
-                    const int nx = (j + 1) % kStages;
-                    if (mbar_test_wait(smem_u32(&sm.o_full[t]), j & 1) &&
-                        mbar_test_wait(smem_u32(&sm.k_full[nx]), ((j + 1) / kStages) & 1)) {
-                        tc_fence_after();
-                        qk(t, nx);
-                        tc_commit_elect(smem_u32(&sm.s_full[t]));
-                        keys_used ^= 1u << nx;
-                        if (tiles == 1 || (keys_used >> nx & 1u) == 0)
-                            tc_commit_elect(smem_u32(&sm.k_empty[nx]));
-                        step[t] = j + 1;
-                        phase[t] = 0;
-                        went = true;
-                    }
-                }
-            }
-            idle = went ? 0 : idle + 1;
-            if ((idle & 1023u) == 1023u) {
-                const uint64_t now = globaltimer_ns();
-                if (idle == 1023u) {
-                    since = now;
-                } else if (now - since > kWaitNs) {
-                    atomicOr(&g_error, ERR_ATTN_WAIT);
+        }
+        for (int j = 0; ok && j < steps; ++j) {
+            const uint32_t st = j & (kStages - 1), nx = st ^ 1u;
+            if (!(ok = wait_for(sm.v_full[st], (j / kStages) & 1) && wait_for(sm.p_half[t], j & 1)))
+                break;
+            tc_fence_after();
+            pv(t, st, 0, j > 0);
+            if (!(ok = wait_for(sm.p_full[t], j & 1)))
+                break;
+            tc_fence_after();
+            pv(t, st, 1, true);
+            tc_commit_elect(smem_u32(&sm.o_full[t]));
+            tc_commit_elect(smem_u32(&sm.v_empty[st]));
+            if (j + 1 < steps) {
+                if (!(ok = wait_for(sm.k_full[nx], ((j + 1) / kStages) & 1) && wait_for(sm.o_full[t], j & 1)))
                     break;
-                }
+                tc_fence_after();
+                qk(t, nx);
+                tc_commit_elect(smem_u32(&sm.k_empty[nx]));
             }
         }
         tc_commit_elect(smem_u32(&sm.drained));   // nothing of this CTA is in the tensor cores when TMEM is freed
@@ -581,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(0, 512);
     }
 }
 
@@ -602,7 +596,7 @@ cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
         return cudaErrorLaunchOutOfResources;
     const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
     const int64_t tiles = (rows + kTiles * 128 - 1) / (kTiles * 128), x = tiles * a.cache.heads * plan.splits;
-    if (x > INT32_MAX)
+    if (x > INT32_MAX || tiles * (kTiles * 128) > INT32_MAX)
         return cudaErrorInvalidValue;
     tile_kernel<kDim><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(a, plan, static_cast<int>(tiles),
                                                                                            stat, part);
