@@ -37,6 +37,13 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
 {
     uint32_t r;

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = blockIdx.x % row_tiles, kh = blockIdx.x / row_tiles % a.cache.heads;
     const int split = blockIdx.x / row_tiles / a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-    if (!s.ok || s.len > a.max_kv || (s.len > 0 && (s.len - 1) / page >= a.batch.ld_table)) {
+    if (!s.ok || s.len > a.max_kv || (s.len > 0 && ((s.len - 1) / page >= a.batch.ld_table || a.cache.num_pages == 0))) {
         if (threadIdx.x == 0)
             atomicOr(&g_error, ERR_KV_RANGE);
         return;
@@ -207,23 +207,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
                 const int lo = see.lo - k0, hi = see.hi - k0;
-                float v[4][32], top = -INFINITY;
+                float v[128], top = -INFINITY;
                 if (!edge) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld_32x32b_x32(sc + 32 * c, reinterpret_cast<uint32_t (&)[32]>(v[c]));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld_wait_regs(reinterpret_cast<uint32_t (&)[32]>(v[c]));
+                    tmem_ld_32x32b_x64(sc, v);
+                    tmem_ld_32x32b_x64(sc + 64, v + 64);
+                    tmem_ld_wait_x64(v);
+                    tmem_ld_wait_x64(v + 64);
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
                         const PageEntry e = pe[(16 * n) >> shift];
-                        const float *x = &v[n >> 1][16 * (n & 1)];
-                        float g = fmaxf(x[0], x[1]);
+                        const float *x = v + 16 * n;
+                        float g = max3(x[0], x[1], x[2]);
 #pragma unroll
-                        for (int i = 2; i < 16; i += 2)
-                            g = fmaxf(g, fmaxf(x[i], x[i + 1]));
-                        top = fmaxf(top, fmaf(g, c_row * e.ks, e.lv));
+                        for (int i = 3; i < 15; i += 2)
+                            g = max3(g, x[i], x[i + 1]);
+                        top = fmaxf(top, fmaf(fmaxf(g, x[15]), c_row * e.ks, e.lv));
                     }
                 } else {   // some rows do not see some keys; short code, scores read from TMEM again below
 #pragma unroll 1
@@ -295,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                float2 w = __ffma2_rn(make_float2(v[c][16 * h + i], v[c][16 * h + i + 1]), ck2, off2);
+                                float2 w = __ffma2_rn(make_float2(v[32 * c + 16 * h + i], v[32 * c + 16 * h + i + 1]), ck2, off2);
                                 w = make_float2(ex2(w.x), ex2(w.y));
                                 sum = __fadd2_rn(sum, w);
                                 p[8 * h + i / 2] = pack_half2(w.x, w.y);
@@ -394,8 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kPieces = kDim / 16;                        // 16-byte pieces of codes per token
         constexpr int kRowStep = 32 * kConvertWarps / kPieces;    // tokens between a thread's pieces
         constexpr int kPer = kKeys / kRowStep;
-        const int tid = threadIdx.x - 32 * kSoftmaxWarps, r0 = tid / kPieces, c = tid % kPieces;
-        const int64_t head_off = static_cast<int64_t>(kh) * page;
+        // Each group of 8 lanes (a store's phase) takes 4 pieces of two adjacent rows: their swizzles differ in the lowest
+        // bit, so that the first halves of the pieces, at even places, and then the second fill all banks.
+        const int w0 = warp - kSoftmaxWarps;
+        const int r0 = kDim == 128 ? 4 * w0 + ((lane >> 2) & 1) + ((lane >> 4) << 1) : 8 * w0 + (lane >> 2);
+        const int c = kDim == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
         // Lane p of each warp holds the number of page p of a step (8 at most), loaded two steps ahead and looked at
         // only when its codes are loaded.
         const int shift = 31 - __clz(page);
@@ -403,12 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t tok = begin + static_cast<int64_t>(j) * kKeys + lane * page;
             return lane < kKeys / page && tok < end && tok + page > out_lo ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift)] : -2;
         };
-        const auto checked = [&](int32_t id) -> int32_t {        // -2: no page; out of range: -1, reported
-            if (id != -2 && (id < 0 || id >= a.cache.num_pages)) {
-                atomicOr(&g_error, ERR_KV_RANGE);
-                return -1;
-            }
-            return id;
+        const auto checked = [&](int32_t id) -> int32_t {        // -2: no page; out of range: reported, page 0 instead
+            if (id == -2 || (id >= 0 && id < a.cache.num_pages))
+                return id;
+            atomicOr(&g_error, ERR_KV_RANGE);
+            return 0;
         };
         int32_t id[kPer];   // pages of the step whose codes are loaded next, by piece
         const auto ids = [&](int32_t of_lane) {
@@ -416,33 +416,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kPer; ++i)
                 id[i] = __shfl_sync(0xFFFFFFFFu, of_lane, (r0 + i * kRowStep) >> shift);
         };
+        // A piece's group of kRowStep tokens lies in one page (dim 128: 16 tokens) or in two (dim 64: 32).
+        const int64_t page_bytes = static_cast<int64_t>(a.cache.heads) * page * kDim;
+        const int64_t mine = static_cast<int64_t>(kh) * page * kDim + 16 * c;
         const auto load = [&](const uint8_t *codes, int k0, uint4 (&w)[kPer]) {
+            const uint8_t *base = codes + mine;
+            if (k0 >= out_lo && k0 + kKeys <= end) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int tok = k0 + r0 + i * kRowStep;
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (id[i] >= 0 && tok >= out_lo && tok < end)   // positions that no row sees stay zero
-                    w[i] = *reinterpret_cast<const uint4 *>(
-                        codes + ((static_cast<int64_t>(id[i]) * a.cache.heads * page + head_off + (tok & (page - 1))) * kDim + 16 * c));
+                for (int i = 0; i < kPer; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + ((r0 + i * kRowStep) & (page - 1)) * kDim);
+            } else {   // positions that no row sees stay zero
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int tok = k0 + r0 + i * kRowStep;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (tok >= out_lo && tok < end)
+                        w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + (tok & (page - 1)) * kDim);
+                }
             }
         };
-        const auto store = [&](uint32_t dst, const uint4 &w, int r) {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-            uint32_t h[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[2 * i] = e4m3x2_to_f16x2(x[i] & 0xFFFFu);
-                h[2 * i + 1] = e4m3x2_to_f16x2(x[i] >> 16);
-            }
-            // the upper half of the pieces stores its second half first: the other banks
-            const int odd = (c >> 2) & 1;
-            if (odd == 0) {
-                st_shared_v4(dst + operand_at(r, 2 * c), h[0], h[1], h[2], h[3]);
-                st_shared_v4(dst + operand_at(r, 2 * c + 1), h[4], h[5], h[6], h[7]);
-            } else {
-                st_shared_v4(dst + operand_at(r, 2 * c + 1), h[4], h[5], h[6], h[7]);
-                st_shared_v4(dst + operand_at(r, 2 * c), h[0], h[1], h[2], h[3]);
-            }
+        const uint32_t piece0 = operand_at(r0, 2 * c), piece1 = operand_at(r0, 2 * c + 1);
+        const auto store = [&](uint32_t dst, const uint4 &w, int i) {
+            const uint2 x = e4m3x4_to_f16x4(w.x), y = e4m3x4_to_f16x4(w.y), z = e4m3x4_to_f16x4(w.z), u = e4m3x4_to_f16x4(w.w);
+            // rows kRowStep apart have the same swizzle
+            st_shared_v4(dst + piece0 + i * (kRowStep * 128), x.x, x.y, y.x, y.y);
+            st_shared_v4(dst + piece1 + i * (kRowStep * 128), z.x, z.y, u.x, u.y);
         };
         // A step's codes are loaded while the step before it is converted, its pages' numbers one step earlier still.
         uint4 kw[kPer], vw[kPer];
@@ -461,9 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane_id >= 0) {
                         const int64_t bh = static_cast<int64_t>(lane_id) * a.cache.heads + kh;
                         const float vs = a.cache.v_scale[bh];
-                        e.ks = a.cache.k_scale[bh];
-                        e.lv = lg2(vs);
-                        e.inv_vs = __frcp_rn(vs);
+                        e = PageEntry{lane_id, a.cache.k_scale[bh], lg2(vs), __frcp_rn(vs)};
                     }
                     sm.entry[j % kEntrySlots][lane] = e;
                 }
@@ -473,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                store(smem_u32(sm.k[st]), kw[i], r0 + i * kRowStep);
+                store(smem_u32(sm.k[st]), kw[i], i);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.k_full[st]));
             lane_id = checked(next_id);
@@ -502,12 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sm.nan_mask[st][r0 + i * kRowStep][c] = static_cast<uint16_t>(m);
                     }
                     if (lane == 0)
-                        sm.nan_step[st][warp - kSoftmaxWarps] = j + 1;
+                        sm.nan_step[st][w0] = j + 1;
                 }
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                store(smem_u32(sm.v[st]), vw[i], r0 + i * kRowStep);
+                store(smem_u32(sm.v[st]), vw[i], i);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.v_full[st]));
             load(a.cache.v_codes, k0 + kKeys, vw);

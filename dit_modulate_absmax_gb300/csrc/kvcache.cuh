@@ -40,6 +40,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c)
     return r;
 }
 
+// Four codes as two pairs of halves.
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t c)
+{
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(c));
+    return r;
+}
+
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t c)
 {
     const uint32_t h = e4m3x2_to_f16x2(c);
