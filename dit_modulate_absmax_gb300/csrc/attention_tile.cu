@@ -81,6 +81,14 @@ __device__ __forceinline__ bool wait_for(const uint64_t &bar, uint32_t parity)
     return false;
 }
 
+// One arrival for a warp whose lanes have each done (and fenced) their part.
+__device__ __forceinline__ void warp_arrive(const uint64_t &bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(smem_u32(&bar));
+}
+
 template <int kRegs>
 __device__ __forceinline__ void grow_registers()
 {
@@ -93,7 +101,7 @@ __device__ __forceinline__ void shrink_registers()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <int kDim>
+template <int kDim, int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(AttnArgs a, SplitPlan plan, int row_tiles, float2 *ws_stat, float *ws_out)
 {
@@ -124,15 +132,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTiles; ++i) {
-            mbar_init(smem_u32(&sm.q_full[i]), 128);
+            mbar_init(smem_u32(&sm.q_full[i]), 4);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.p_half[i]), 128);
-            mbar_init(smem_u32(&sm.p_full[i]), 128);
+            mbar_init(smem_u32(&sm.p_half[i]), 4);
+            mbar_init(smem_u32(&sm.p_full[i]), 4);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.k_full[i]), 32 * kConvertWarps);
-            mbar_init(smem_u32(&sm.v_full[i]), 32 * kConvertWarps);
+            mbar_init(smem_u32(&sm.k_full[i]), kConvertWarps);
+            mbar_init(smem_u32(&sm.v_full[i]), kConvertWarps);
             mbar_init(smem_u32(&sm.k_empty[i]), tiles);
             mbar_init(smem_u32(&sm.v_empty[i]), tiles);
             for (int w = 0; w < kConvertWarps; ++w)
@@ -191,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     st_shared_v4(smem_u32(sm.q[t]) + operand_at(in_tile, i), bf16x2_to_half2(w[i].x, f), bf16x2_to_half2(w[i].y, f),
                                  bf16x2_to_half2(w[i].z, f), bf16x2_to_half2(w[i].w, f));
                 fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&sm.q_full[t]));
+                warp_arrive(sm.q_full[t]);
             }
             float ref = -INFINITY, l = 0.0f;
             bool met_nan = false, ok = true;
@@ -214,14 +222,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_wait_x64(v);
                     tmem_ld_wait_x64(v + 64);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        const PageEntry e = pe[(16 * n) >> shift];
-                        const float *x = v + 16 * n;
-                        float g = max3(x[0], x[1], x[2]);
+                    for (int n = 0; n < kKeys / kGroup; ++n) {
+                        const PageEntry e = pe[(kGroup * n) >> shift];
+                        const float *x = v + kGroup * n;
+                        float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
 #pragma unroll
-                        for (int i = 3; i < 15; i += 2)
-                            g = max3(g, x[i], x[i + 1]);
-                        top = fmaxf(top, fmaf(fmaxf(g, x[15]), c_row * e.ks, e.lv));
+                        for (int i = 6; i + 3 < kGroup; i += 4) {
+                            g0 = max3(g0, x[i], x[i + 1]);
+                            g1 = max3(g1, x[i + 2], x[i + 3]);
+                        }
+                        top = fmaxf(top, fmaf(max3(g0, g1, fmaxf(x[kGroup - 2], x[kGroup - 1])), c_row * e.ks, e.lv));
                     }
                 } else {   // some rows do not see some keys; short code, scores read from TMEM again below
 #pragma unroll 1
@@ -257,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Ordinary steps take the exponent in one fused multiply-add.  Past 2^20 the reference's own rounding
                 // would show in it (and could reach FP16's limit): there, as in edge steps, the score is rounded first,
                 // so that the largest one meets its own copy in the reference.
-                if (edge || __any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f)) {
+                const bool plain = !edge && !__any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f);
+                if (!plain) {
 #pragma unroll 1
                     for (int n = 0; n < 8; ++n) {
                         const PageEntry e = pe[(16 * n) >> shift];
@@ -280,31 +291,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                    mbar_arrive(smem_u32(&sm.p_half[t]));
+                    warp_arrive(sm.p_half[t]);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t p[16];
+                        float *x = v + 32 * c;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const PageEntry e = pe[(32 * c + 16 * h) >> shift];
+                        for (int n = 0; n < 32; n += kGroup) {
+                            const PageEntry e = pe[(32 * c + n) >> shift];
                             const float ck = c_row * e.ks;
                             const float2 ck2 = make_float2(ck, ck), off2 = make_float2(e.lv - at, e.lv - at);
-                            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float2 w = __ffma2_rn(make_float2(v[32 * c + 16 * h + i], v[32 * c + 16 * h + i + 1]), ck2, off2);
-                                w = make_float2(ex2(w.x), ex2(w.y));
-                                sum = __fadd2_rn(sum, w);
-                                p[8 * h + i / 2] = pack_half2(w.x, w.y);
+                            for (int i = n; i < n + kGroup; i += 2) {
+                                const float2 w = __ffma2_rn(make_float2(x[i], x[i + 1]), ck2, off2);
+                                x[i] = ex2(w.x);
+                                x[i + 1] = ex2(w.y);
                             }
-                            l = fmaf(sum.x + sum.y, e.inv_vs, l);
                         }
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            p[i / 2] = pack_half2(x[i], x[i + 1]);
                         tmem_st_32x32b_x16(sc + 16 * c, p);
                         if (c == 1) {   // the first half's product can start
                             tmem_st_wait();
                             tc_fence_before();
-                            mbar_arrive(smem_u32(&sm.p_half[t]));
+                            warp_arrive(sm.p_half[t]);
                         }
                     }
                 }
@@ -330,7 +342,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         met_nan = true;
                     }
                 }
-                mbar_arrive(smem_u32(&sm.p_full[t]));
+                warp_arrive(sm.p_full[t]);
+                if (plain) {   // the sum, off the way to the product
+#pragma unroll
+                    for (int n = 0; n < kKeys / kGroup; ++n) {
+                        const float *x = v + kGroup * n;
+                        float2 s0 = make_float2(x[0], x[1]), s1 = make_float2(x[2], x[3]);
+#pragma unroll
+                        for (int i = 4; i < kGroup; i += 4) {
+                            s0 = __fadd2_rn(s0, make_float2(x[i], x[i + 1]));
+                            s1 = __fadd2_rn(s1, make_float2(x[i + 2], x[i + 3]));
+                        }
+                        s0 = __fadd2_rn(s0, s1);
+                        l = fmaf(s0.x + s0.y, pe[(kGroup * n) >> shift].inv_vs, l);
+                    }
+                }
             }
             if (ok && steps > 0)
                 ok = wait_for(sm.o_full[t], (steps - 1) & 1);
@@ -463,15 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     sm.entry[j % kEntrySlots][lane] = e;
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sm.entry_full[j % kEntrySlots]));
+                warp_arrive(sm.entry_full[j % kEntrySlots]);
             }
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
                 store(smem_u32(sm.k[st]), kw[i], i);
             fence_proxy_async_smem();
-            mbar_arrive(smem_u32(&sm.k_full[st]));
+            warp_arrive(sm.k_full[st]);
             lane_id = checked(next_id);
             next_id = page_ids(j + 2);
             ids(lane_id);
@@ -505,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kPer; ++i)
                 store(smem_u32(sm.v[st]), vw[i], i);
             fence_proxy_async_smem();
-            mbar_arrive(smem_u32(&sm.v_full[st]));
+            warp_arrive(sm.v_full[st]);
             load(a.cache.v_codes, k0 + kKeys, vw);
         }
     } else {
@@ -575,18 +599,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int kDim>
+// kGroup: scores in a row that are sure to lie in one page.
+template <int kDim, int kGroup>
 cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
 {
     // More than half of an SM's shared memory even at dim 64: a second CTA on the SM would wait for the first one's TMEM.
     constexpr int kNeed = sizeof(Smem<kDim>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024, "fits an SM");
-    cudaError_t e = allow_shared<tile_kernel<kDim>>(kSmem);
+    cudaError_t e = allow_shared<tile_kernel<kDim, kGroup>>(kSmem);
     if (e != cudaSuccess)
         return e;
     static const bool registers_fit = [] {   // a property of the build
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, tile_kernel<kDim>) == cudaSuccess && 4 * f.numRegs >= kSplitRegs;
+        return cudaFuncGetAttributes(&f, tile_kernel<kDim, kGroup>) == cudaSuccess && 4 * f.numRegs >= kSplitRegs;
     }();
     if (!registers_fit)
         return cudaErrorLaunchOutOfResources;
@@ -594,7 +619,7 @@ cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     const int64_t tiles = (rows + kTiles * 128 - 1) / (kTiles * 128), x = tiles * a.cache.heads * plan.splits;
     if (x > INT32_MAX || tiles * (kTiles * 128) > INT32_MAX)
         return cudaErrorInvalidValue;
-    tile_kernel<kDim><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(a, plan, static_cast<int>(tiles),
+    tile_kernel<kDim, kGroup><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(a, plan, static_cast<int>(tiles),
                                                                                            stat, part);
     return cudaGetLastError();
 }
@@ -616,7 +641,9 @@ SplitPlan plan_tile(const AttnShape &s)
 
 cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
 {
-    return a.cache.head_dim == 64 ? run_tile<64>(a, plan, stat, part, st) : run_tile<128>(a, plan, stat, part, st);
+    if (a.cache.page_size == 16)
+        return a.cache.head_dim == 64 ? run_tile<64, 16>(a, plan, stat, part, st) : run_tile<128, 16>(a, plan, stat, part, st);
+    return a.cache.head_dim == 64 ? run_tile<64, 32>(a, plan, stat, part, st) : run_tile<128, 32>(a, plan, stat, part, st);
 }
 
 cudaError_t read_attention_tile_error(uint32_t *code)
