@@ -71,14 +71,26 @@ constexpr uint32_t idesc_f16(int n, bool b_mn_major)   // M = 128, FP32 accumula
     return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
 }
 
-// The outcome is a vote, so that control flow that hangs on it is warp-uniform (and operands computed there can live in
-// uniform registers).
+// Waits for the phase with this parity, two seconds at most.  The timer is read once in 64 tries only: a read takes about
+// 1,000 cycles, and a try may come back empty-handed long before the phase completes.  The outcome is a vote, so that
+// control flow that hangs on it is warp-uniform (and operands computed there can live in uniform registers).
 __device__ __forceinline__ bool wait_for(const uint64_t &bar, uint32_t parity)
 {
-    if (__all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bar), parity, kWaitNs)))
-        return true;
-    atomicOr(&g_error, ERR_ATTN_WAIT);
-    return false;
+    const uint32_t at = smem_u32(&bar);
+    uint64_t since = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(0xFFFFFFFFu, mbar_try_wait(at, parity)))
+                return true;
+        const uint64_t now = globaltimer_ns();
+        if (since == 0)
+            since = now;
+        if (__any_sync(0xFFFFFFFFu, now - since > kWaitNs)) {
+            atomicOr(&g_error, ERR_ATTN_WAIT);
+            return false;
+        }
+    }
 }
 
 // One arrival for a warp whose lanes have each done (and fenced) their part.
@@ -264,29 +276,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float at = ref == -INFINITY ? 0.0f : ref;
-                // Ordinary steps take the exponent in one fused multiply-add.  Past 2^20 the reference's own rounding
-                // would show in it (and could reach FP16's limit): there, as in edge steps, the score is rounded first,
-                // so that the largest one meets its own copy in the reference.
-                const bool plain = !edge && !__any_sync(0xFFFFFFFFu, fabsf(at) > 0x1p20f);
+                // The exponent is one fused multiply-add.  For a row past 2^20 the reference's own rounding would show in
+                // it (and could reach FP16's limit): there the score is rounded first, so that the largest one meets its
+                // own copy in the reference.  Steps at an edge or with such a row take a short loop instead of the long
+                // straight code, with the same operations in the same order for every other row, so that a row's bits
+                // do not depend on its neighbours.
+                const bool far = fabsf(at) > 0x1p20f, plain = !edge && !__any_sync(0xFFFFFFFFu, far);
                 if (!plain) {
+                    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
 #pragma unroll 1
-                    for (int n = 0; n < 8; ++n) {
+                    for (int n = 0; n < kKeys / 16; ++n) {
                         const PageEntry e = pe[(16 * n) >> shift];
+                        const float ck = c_row * e.ks, off = e.lv - at;
                         uint32_t x[16], p[8];
                         tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
-                        float sum = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             float w[2];
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const int col = 16 * n + i + y;
-                                w[y] = col >= lo && col < hi ? ex2(fmaf(__uint_as_float(x[i + y]), c_row * e.ks, e.lv) - at) : 0.0f;
-                                sum += w[y];
+                                const float z = __uint_as_float(x[i + y]);
+                                w[y] = col >= lo && col < hi ? ex2(far ? fmaf(z, ck, e.lv) - at : fmaf(z, ck, off)) : 0.0f;
                             }
                             p[i / 2] = pack_half2(w[0], w[1]);
+                            float2 &sum = (i & 2) == 0 ? s0 : s1;
+                            sum = __fadd2_rn(sum, make_float2(w[0], w[1]));
                         }
-                        l = fmaf(sum, e.inv_vs, l);
+                        if ((16 * n + 16) % kGroup == 0) {
+                            s0 = __fadd2_rn(s0, s1);
+                            l = fmaf(s0.x + s0.y, e.inv_vs, l);
+                            s0 = s1 = make_float2(0.0f, 0.0f);
+                        }
                         tmem_st_32x32b_x8(sc + 8 * n, p);   // over columns of S that are read already
                     }
                     tmem_st_wait();
@@ -471,6 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A step's codes are loaded while the step before it is converted, its pages' numbers one step earlier still.
         uint4 kw[kPer], vw[kPer];
         int32_t lane_id = checked(page_ids(0)), next_id = page_ids(1);
+        float ks = 1.0f, vs = 1.0f;   // the scales of lane_id's page, loaded as early as its codes
+        const auto scales = [&] {
+            ks = vs = 1.0f;
+            if (warp == kSoftmaxWarps && lane_id >= 0) {
+                const int64_t bh = static_cast<int64_t>(lane_id) * a.cache.heads + kh;
+                ks = a.cache.k_scale[bh];
+                vs = a.cache.v_scale[bh];
+            }
+        };
+        scales();
         ids(lane_id);
         load(a.cache.k_codes, begin, kw);
         load(a.cache.v_codes, begin, vw);
@@ -480,15 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_for(sm.k_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
-                if (lane < kKeys / page) {
-                    PageEntry e{lane_id, 1.0f, 0.0f, 1.0f};
-                    if (lane_id >= 0) {
-                        const int64_t bh = static_cast<int64_t>(lane_id) * a.cache.heads + kh;
-                        const float vs = a.cache.v_scale[bh];
-                        e = PageEntry{lane_id, a.cache.k_scale[bh], lg2(vs), __frcp_rn(vs)};
-                    }
-                    sm.entry[j % kEntrySlots][lane] = e;
-                }
+                if (lane < kKeys / page)
+                    sm.entry[j % kEntrySlots][lane] = PageEntry{lane_id, ks, lg2(vs), __frcp_rn(vs)};
                 warp_arrive(sm.entry_full[j % kEntrySlots]);
             }
 #pragma unroll
@@ -498,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_arrive(sm.k_full[st]);
             lane_id = checked(next_id);
             next_id = page_ids(j + 2);
+            scales();
             ids(lane_id);
             load(a.cache.k_codes, k0 + kKeys, kw);   // zeros past the end
 
