@@ -319,7 +319,7 @@ h3fp4_status check_cache(const h3fp4_kv_cache *c)
 {
     if (c == nullptr)
         return H3FP4_ERR_NULL;
-    if (c->num_pages < 0 || c->heads < 1 || c->heads > 65535)
+    if (c->num_pages < 0 || c->heads < 1 || c->heads > 65535 || int64_t(c->num_pages) * c->heads > INT32_MAX)
         return H3FP4_ERR_SHAPE;
     if ((c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) ||
         (c->head_dim != 64 && c->head_dim != 128))

@@ -20,6 +20,8 @@
 
 namespace h3fp4 {
 
+constexpr uint32_t ERR_ATTN_WAIT = 1u << 10;   // a pipeline wait gave up
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

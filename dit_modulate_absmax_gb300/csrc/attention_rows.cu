@@ -6,7 +6,8 @@
 // most 16 rows, so it is bound by HBM.  What it takes to stay there:
 //  - The keys are split over CTAs until the SMs are covered; each of a CTA's 4
 //    warps runs its own online softmax over units of 32 tokens, fed by its own
-//    ring of asynchronous 16-byte copies, with no barrier in the loop.
+//    ring of TMA copies (one lane issues two a unit), with no barrier between
+//    warps in the loop.
 //  - Codes go from shared memory to registers as they lie and are converted to
 //    FP16 there (exact) for mma.sync m16n8k16 with FP32 accumulation.  The
 //    order of the contraction index is free, so a lane takes 4 adjacent
@@ -14,12 +15,15 @@
 //    reads each token's row in 16-byte pieces, and in O^T = V^T P^T a lane
 //    reads 16 channels of its 4 tokens and pairs up tokens with byte
 //    permutes.  S's accumulator layout is that product's B operand.
-//  - Shared-memory rows are XOR-swizzled in 16-byte pieces (dim 128: no bank
-//    conflicts; dim 64: two-way for the values).
+//  - The copies XOR-swizzle rows in 16-byte pieces (dim 128: no bank conflicts;
+//    dim 64: two-way for the values).
 // The tensor work is small next to the memory's (24 instructions per 4 KB of
 // codes at dim 128 and 8 rows), so the older warp-level instruction serves; a
 // 128-row tcgen05 tile would be 8-16 times padding.
+#include <cstring>
+
 #include "attention.cuh"
+#include "ptx.cuh"
 
 namespace h3fp4 {
 namespace {
@@ -29,7 +33,7 @@ __device__ uint32_t g_error;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;                 // tokens a warp takes at a time
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kMaxEntries = 512;          // pages of one part
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -40,36 +44,28 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int kLeft>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
-}
-
-// Byte offset of 16-byte piece c of row r of a [32][kDim] tile.
+// Byte offset of 16-byte piece c of row r of a [32][kDim] tile as the tensor map's swizzle lays it.
 template <int kDim>
 __device__ __forceinline__ uint32_t piece(int r, int c)
 {
-    const int l = r * (kDim / 16) + c, line = l >> 3;
-    return static_cast<uint32_t>((line << 7) | (((l & 7) ^ (line & 7)) << 4));
+    if (kDim == 128)
+        return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+    return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+constexpr uint64_t kWaitNs = 2000000000ull;
+
 template <int kDim, int kRows>
-__global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan plan, int row_tiles, float2 *ws_stat,
-                                                        float *ws_out)
+__global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan plan, int row_tiles, float2 *ws_stat, float *ws_out,
+                                                        const __grid_constant__ CUtensorMap k_map,
+                                                        const __grid_constant__ CUtensorMap v_map)
 {
     constexpr int kSteps = kDim / 16;            // k16 steps of Q K^T = 16-channel tiles of O^T
     constexpr int kHalf = kRows / 8;             // groups of 8 rows
     constexpr int kTile = kUnit * kDim;          // bytes of a unit's keys
-    extern __shared__ __align__(128) uint8_t dyn[];
+    extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ PageEntry entry[kMaxEntries];
+    __shared__ uint64_t full[kWarps][kStages];
     __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -100,30 +96,32 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
         }
         entry[i].id = id;
     }
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i)
+            mbar_init(smem_u32(&full[warp][i]), 1);
+    fence_mbar_init();
     __syncthreads();
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * (kStages * 2 * kTile);
-    const auto fetch = [&](int unit, int stage) {   // unit: first token
-        if (unit < end) {
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int c = lane + 32 * i, r = c / kSteps, tok = unit + r;
-                const int32_t id = tok < end ? entry[tok / page - page0].id : -1;
-                if (id >= 0) {
-                    const int64_t at =
-                        ((static_cast<int64_t>(id) * a.cache.heads + kh) * page + (tok & (page - 1))) * kDim + (c % kSteps) * 16;
-                    const uint32_t dst = ring + stage * (2 * kTile) + piece<kDim>(r, c % kSteps);
-                    copy16(dst, a.cache.k_codes + at);
-                    copy16(dst + kTile, a.cache.v_codes + at);
-                }
-            }
+    const int box = min(page, kUnit);
+    const auto fetch = [&](int unit, int stage) {   // one lane; unit: first token, below end
+        const uint32_t bar = smem_u32(&full[warp][stage]), dst = ring + stage * (2 * kTile);
+        const int32_t id0 = entry[unit / page - page0].id, id1 = page < kUnit && unit + page < end ? entry[unit / page + 1 - page0].id : -1;
+        mbar_arrive_expect_tx(bar, ((id0 >= 0) + (id1 >= 0)) * 2 * box * kDim);
+        if (id0 >= 0) {
+            tma_load_3d(dst, &k_map, 0, unit & (page - 1), id0 * a.cache.heads + kh, bar);
+            tma_load_3d(dst + kTile, &v_map, 0, unit & (page - 1), id0 * a.cache.heads + kh, bar);
         }
-        copy_commit();
+        if (id1 >= 0) {
+            tma_load_3d(dst + kTile / 2, &k_map, 0, 0, id1 * a.cache.heads + kh, bar);
+            tma_load_3d(dst + kTile + kTile / 2, &v_map, 0, 0, id1 * a.cache.heads + kh, bar);
+        }
     };
     const int unit0 = begin + warp * kUnit;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
-        fetch(unit0 + i * kWarps * kUnit, i);
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i)
+            if (unit0 + i * kWarps * kUnit < end)
+                fetch(unit0 + i * kWarps * kUnit, i);
     for (int i = threadIdx.x; i < pages; i += kThreads) {
         const int64_t bh = static_cast<int64_t>(max(entry[i].id, 0)) * a.cache.heads + kh;
         const float vs = a.cache.v_scale[bh];
@@ -184,9 +182,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
     }
 
     int stage = 0;
+    uint32_t parity = 0;
     for (int unit = unit0; unit < end; unit += kWarps * kUnit) {
-        copy_wait<kStages - 2>();
-        __syncwarp();
+        if (!mbar_wait_bounded(smem_u32(&full[warp][stage]), parity, kWaitNs))
+            atomicOr(&g_error, ERR_ATTN_WAIT);   // the copies have not come: go on, the outputs mean nothing
         const uint8_t *kt = dyn + warp * (kStages * 2 * kTile) + stage * (2 * kTile), *vt = kt + kTile;
 
         float sc[4][4];   // S of the unit's four groups of 8 tokens
@@ -201,7 +200,10 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
             sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
 #pragma unroll
             for (int st = 0; st < kSteps; ++st)
-                mma_f16(sc[n], q[st], e4m3x2_to_f16x2(w[st] & 0xFFFFu), e4m3x2_to_f16x2(w[st] >> 16));
+            {
+                const uint2 kb = e4m3x4_to_f16x4(w[st]);
+                mma_f16(sc[n], q[st], kb.x, kb.y);
+            }
         }
 
         const bool edge = unit < in_lo || unit + kUnit > in_hi;
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
                                     o[hf][j][e] = __uint_as_float(0x7FC00000u);
                         }
                     }
-                    const uint32_t av[4] = {e4m3x2_to_f16x2(c0 & 0xFFFFu), e4m3x2_to_f16x2(c1 & 0xFFFFu),
-                                            e4m3x2_to_f16x2(c0 >> 16), e4m3x2_to_f16x2(c1 >> 16)};
+                    const uint2 v0 = e4m3x4_to_f16x4(c0), v1 = e4m3x4_to_f16x4(c1);
+                    const uint32_t av[4] = {v0.x, v1.x, v0.y, v1.y};
 #pragma unroll
                     for (int hf = 0; hf < kHalf; ++hf)
                         mma_f16(o[hf][j], av, pb[hf][2 * hh], pb[hf][2 * hh + 1]);
@@ -340,10 +342,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
             }
         }
         __syncwarp();   // every lane has read the stage that the next copies overwrite
-        fetch(unit + (kStages - 1) * kWarps * kUnit, stage == 0 ? kStages - 1 : stage - 1);
+        if (lane == 0 && unit + kStages * kWarps * kUnit < end)
+            fetch(unit + kStages * kWarps * kUnit, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
+        parity ^= stage == 0;
     }
-    copy_wait<0>();
 
     // Join the warps: maxima and sums, then the outputs through shared memory (the rings are drained).
 #pragma unroll
@@ -493,8 +496,18 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     const int64_t x = tiles * a.cache.heads * plan.splits;
     if (x > INT32_MAX)
         return cudaErrorInvalidValue;
+    CUtensorMap k_map, v_map;
+    const int64_t blocks = static_cast<int64_t>(a.cache.num_pages) * a.cache.heads;
+    const int box = a.cache.page_size < kUnit ? a.cache.page_size : kUnit;
+    if (blocks == 0) {   // no pages: nothing is copied through the maps
+        memset(&k_map, 0, sizeof(k_map));
+        v_map = k_map;
+    } else if (!encode_cache_map(&k_map, a.cache.k_codes, kDim, a.cache.page_size, blocks, box) ||
+               !encode_cache_map(&v_map, a.cache.v_codes, kDim, a.cache.page_size, blocks, box)) {
+        return cudaErrorInvalidValue;
+    }
     rows_kernel<kDim, kRows><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(
-        a, plan, static_cast<int>(tiles), stat, part);
+        a, plan, static_cast<int>(tiles), stat, part, k_map, v_map);
     return cudaGetLastError();
 }
 

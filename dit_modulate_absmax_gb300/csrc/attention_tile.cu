@@ -26,7 +26,6 @@ namespace h3fp4 {
 namespace {
 
 __device__ uint32_t g_error;
-constexpr uint32_t ERR_ATTN_WAIT = 1u << 10;   // a pipeline wait gave up
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 constexpr int kKeys = 128;                     // keys per step

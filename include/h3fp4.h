@@ -315,7 +315,7 @@ H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_strid
  *
  *   codes   [num_pages, heads, page_size, head_dim] bytes, contiguous, 16-byte aligned
  *   scales  [num_pages, heads] float, contiguous
- *   page_size 16, 32, 64 or 128;  head_dim 64 or 128
+ *   page_size 16, 32, 64 or 128;  head_dim 64 or 128;  num_pages * heads below 2^31
  *
  * A page table names each sequence's pages: position p of sequence b is token
  * p % page_size of page page_table[b * ld_table + p / page_size].  A page may
@@ -476,7 +476,7 @@ H3FP4_API h3fp4_status h3fp4_swiglu_pack_noalloc(const void *gate_bf16, int64_t 
  * return.  Bits: GEMM waits 1 (a free stage), 2 (operands landed), 4 (a
  * finished accumulator), 8 (a drained accumulator), 16 (scale atoms landed);
  * 256 the cooperative producer's grid barrier; 512 an entry of a page table
- * or length array out of range (attention calls).
+ * or length array out of range, 1,024 a pipeline wait (attention calls).
  * Returns H3FP4_OK and stores the word in *code (0 = no error).
  */
 H3FP4_API h3fp4_status h3fp4_device_error(uint32_t *code);
