@@ -105,15 +105,18 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
     return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// A launch's split over the keys: `splits` parts of `chunk` tokens each.
+// How a launch spreads the keys.  Tiles: `splits` parts of `chunk` keys each.
+// Rows: clusters of `splits` CTAs, or `splits` CTAs with equal shares.
+// part_rows: rows of partial results (an output, a maximum and a sum) that the
+// workspace has room for.
 struct SplitPlan {
     int32_t splits, chunk;
+    int64_t part_rows;
+    bool cluster;
 };
 
 SplitPlan plan_rows(const AttnShape &s);
 cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
-cudaError_t launch_attention_join(const AttnArgs &a, const SplitPlan &plan, const float2 *stat, const float *part,
-                                  cudaStream_t st);
 SplitPlan plan_tile(const AttnShape &s);
 cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
 cudaError_t read_attention_tile_error(uint32_t *code);

@@ -4,7 +4,7 @@
 //
 // Reads every visible code once (2 * dim bytes a token and cache head) for at
 // most 16 rows, so it is bound by HBM.  What it takes to stay there:
-//  - The keys are split over CTAs until the SMs are covered; each of a CTA's 4
+//  - The keys are spread evenly over as many CTAs as fit; each of a CTA's 4
 //    warps runs its own online softmax over units of 32 tokens, fed by its own
 //    ring of TMA copies (one lane issues two a unit), with no barrier between
 //    warps in the loop.
@@ -55,80 +55,172 @@ __device__ __forceinline__ uint32_t piece(int r, int c)
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+// Adds a part with maximum m and sum l to the sums kept against mm >= m.
+__device__ __forceinline__ void join(float4 &sum, float &ll, const float4 &v, float l, float m, float mm)
+{
+    const float f = ex2(m - (mm == -INFINITY ? 0.0f : mm));
+    sum.x = fmaf(v.x, f, sum.x);
+    sum.y = fmaf(v.y, f, sum.y);
+    sum.z = fmaf(v.z, f, sum.z);
+    sum.w = fmaf(v.w, f, sum.w);
+    ll = fmaf(l, f, ll);
+}
+
+// CTAs that fit an SM: shared memory at 128 channels, registers at 64.
 template <int kDim, int kRows>
-__global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan plan, int row_tiles, float2 *ws_stat, float *ws_out,
-                                                        const __grid_constant__ CUtensorMap k_map,
-                                                        const __grid_constant__ CUtensorMap v_map)
+constexpr int resident()
+{
+    return kDim == 128 ? (kRows == 8 ? 3 : 2) : (kRows == 8 ? 4 : 3);
+}
+
+// Units of 128 tokens, one for each warp's 32, that a sequence's rows take: its
+// share of the work for each cache head and row tile.  0: nothing to do.
+struct Units {
+    int begin, count, tiles;   // first token (a multiple of 32), units, row tiles
+};
+
+template <int kRows>
+__device__ __forceinline__ Units units_of(const AttnArgs &a, const KvSequence &s)
+{
+    if (!s.ok || s.n == 0 || s.len > a.max_kv || (s.len > 0 && (s.len - 1) / a.cache.page_size >= a.batch.ld_table))
+        return Units{0, 0, 0};
+    const Span first = seen_by(a, s, 0), last = seen_by(a, s, s.n - 1);
+    const int begin = min(first.lo, last.lo) & ~(kUnit - 1), end = max(first.hi, last.hi);
+    constexpr int kTokens = kWarps * kUnit;
+    return Units{begin, max(1, (end - begin + kTokens - 1) / kTokens),   // rows that see nothing are written all the same
+                 (s.n * (a.heads / a.cache.heads) + kRows - 1) / kRows};
+}
+
+// CTA i of g (g <= T) takes the units [i T / g, (i + 1) T / g) of T, the
+// sequences one after another, within each its row tiles and cache heads.  The
+// CTA of unit x:
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) { return ((x + 1) * g - 1) / total; }
+
+template <int kDim, int kRows>
+__global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
+    rows_kernel(AttnArgs a, SplitPlan plan, float2 *ws_stat, float *ws_out, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap v_map)
 {
     constexpr int kSteps = kDim / 16;            // k16 steps of Q K^T = 16-channel tiles of O^T
     constexpr int kHalf = kRows / 8;             // groups of 8 rows
     constexpr int kTile = kUnit * kDim;          // bytes of a unit's keys
+    constexpr int kTokens = kWarps * kUnit;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ PageEntry entry[kMaxEntries];
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
+    __shared__ int64_t before[kThreads + 1];     // units before each thread's share of the sequences
+    __shared__ int64_t found_rest;
+    __shared__ int found_b;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int b = blockIdx.y, page = a.cache.page_size, group = a.heads / a.cache.heads;
-    const int tile = blockIdx.x % row_tiles, kh = blockIdx.x / row_tiles % a.cache.heads;
-    const int split = blockIdx.x / row_tiles / a.cache.heads;
-    const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-    if (!s.ok || s.len > a.max_kv || (s.len > 0 && (s.len - 1) / page >= a.batch.ld_table)) {
-        if (threadIdx.x == 0)
-            atomicOr(&g_error, ERR_KV_RANGE);
-        return;
-    }
-    const int rows = s.n * group, row0 = tile * kRows;   // n <= 2^20 and rows of this kernel are few: no overflow
-    if (row0 >= rows || (split > 0 && split * plan.chunk >= s.len))
-        return;
-    // what the tile's first and last rows see bounds what all of them see
-    const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, min(rows - 1, row0 + kRows - 1) / group);
-    const int begin = max(split * plan.chunk, min(first.lo, last.lo) & ~(kUnit - 1));
-    const int end = min(min((split + 1) * plan.chunk, s.len), max(first.hi, last.hi));
-
-    // Page entries of [begin, end), then the first copies, then the scales.
-    const int page0 = begin / page, pages = end > begin ? (end - 1) / page - page0 + 1 : 0;
-    for (int i = threadIdx.x; i < pages; i += kThreads) {
-        int32_t id = a.batch.page_table[b * a.batch.ld_table + page0 + i];
-        if (id < 0 || id >= a.cache.num_pages) {
-            atomicOr(&g_error, ERR_KV_RANGE);
-            id = -1;
-        }
-        entry[i].id = id;
-    }
+    const int page = a.cache.page_size, group = a.heads / a.cache.heads, heads = a.cache.heads;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * (kStages * 2 * kTile);
+    const int box = min(page, kUnit);
     if (lane == 0)
         for (int i = 0; i < kStages; ++i)
             mbar_init(smem_u32(&full[warp][i]), 1);
     fence_mbar_init();
-    __syncthreads();
 
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * (kStages * 2 * kTile);
-    const int box = min(page, kUnit);
-    const auto fetch = [&](int unit, int stage) {   // one lane; unit: first token, below end
-        const uint32_t bar = smem_u32(&full[warp][stage]), dst = ring + stage * (2 * kTile);
-        const int32_t id0 = entry[unit / page - page0].id, id1 = page < kUnit && unit + page < end ? entry[unit / page + 1 - page0].id : -1;
-        mbar_arrive_expect_tx(bar, ((id0 >= 0) + (id1 >= 0)) * 2 * box * kDim);
-        if (id0 >= 0) {
-            tma_load_3d(dst, &k_map, 0, unit & (page - 1), id0 * a.cache.heads + kh, bar);
-            tma_load_3d(dst + kTile, &v_map, 0, unit & (page - 1), id0 * a.cache.heads + kh, bar);
+    int64_t x = 0, x_end = 1;                    // units to do
+    const int share = (a.batch.batch + kThreads - 1) / kThreads;
+    if (!plan.cluster) {
+        int64_t mine = 0;
+        for (int b = threadIdx.x * share; b < min(a.batch.batch, (static_cast<int>(threadIdx.x) + 1) * share); ++b) {
+            const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+            const Units u = units_of<kRows>(a, s);
+            mine += static_cast<int64_t>(u.count) * u.tiles * heads;
+            if (u.count == 0 && s.n != 0 && blockIdx.x == 0)
+                atomicOr(&g_error, ERR_KV_RANGE);
         }
-        if (id1 >= 0) {
-            tma_load_3d(dst + kTile / 2, &k_map, 0, 0, id1 * a.cache.heads + kh, bar);
-            tma_load_3d(dst + kTile + kTile / 2, &v_map, 0, 0, id1 * a.cache.heads + kh, bar);
+        int64_t sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            sum += lane >= o ? y : 0;
         }
-    };
-    const int unit0 = begin + warp * kUnit;
-    if (lane == 0)
-        for (int i = 0; i < kStages; ++i)
-            if (unit0 + i * kWarps * kUnit < end)
-                fetch(unit0 + i * kWarps * kUnit, i);
-    for (int i = threadIdx.x; i < pages; i += kThreads) {
-        const int64_t bh = static_cast<int64_t>(max(entry[i].id, 0)) * a.cache.heads + kh;
-        const float vs = a.cache.v_scale[bh];
-        entry[i].ks = a.cache.k_scale[bh];
-        entry[i].lv = lg2(vs);
-        entry[i].inv_vs = __frcp_rn(vs);
+        before[threadIdx.x + 1] = sum;
+        __syncthreads();
+        int64_t off = 0;
+        for (int w = 0; w < warp; ++w)
+            off += before[32 * w + 32];
+        __syncthreads();
+        before[threadIdx.x + 1] = sum + off;
+        if (threadIdx.x == 0)
+            before[0] = 0;
+        __syncthreads();
+        const int64_t total = before[kThreads];
+        const int64_t takers = min(static_cast<int64_t>(gridDim.x), total);   // every one of them has a unit
+        x_end = 0;
+        if (blockIdx.x < takers) {
+            x = blockIdx.x * total / takers;
+            x_end = (blockIdx.x + 1) * total / takers;
+        }
     }
+    int stage = 0;
+    uint32_t parity = 0;
+    const int64_t x_first = x;
+    while (x < x_end) {   // the same in every thread
+    // The segment that unit x begins: a sequence, a row tile, a cache head and tokens [seg_begin, seg_end).
+    int b, tile, kh, seg_begin, seg_end;
+    bool whole = true;
+    int64_t next = x_end;
+    KvSequence s;
+    if (plan.cluster) {   // one unit a CTA, a cluster for the rows of a sequence and cache head
+        b = blockIdx.y;
+        tile = 0;
+        kh = blockIdx.x / plan.splits;
+        s = kv_sequence(a.batch, b, a.tokens);
+        const Units u = units_of<kRows>(a, s);
+        if (u.count == 0) {   // the same in the whole cluster
+            if (s.n != 0 && threadIdx.x == 0)
+                atomicOr(&g_error, ERR_KV_RANGE);
+            return;
+        }
+        __syncthreads();      // barriers initialised
+        seg_begin = u.begin + blockIdx.x % plan.splits * kTokens;
+        seg_end = seg_begin + kTokens;
+    } else {
+        if (threadIdx.x < 32) {   // whose share holds x, then which sequence of the share
+            int lo = 0;
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; ++i)
+                lo += __popc(__ballot_sync(0xFFFFFFFFu, before[32 * i + lane + 1] <= x));
+            if (lane == 0) {
+                int64_t rest = x - before[lo];
+                int at = lo * share;
+                for (;; ++at) {
+                    const Units u = units_of<kRows>(a, kv_sequence(a.batch, at, a.tokens));
+                    const int64_t n = static_cast<int64_t>(u.count) * u.tiles * heads;
+                    if (rest < n)
+                        break;
+                    rest -= n;
+                }
+                found_b = at;
+                found_rest = rest;
+            }
+        }
+        __syncthreads();
+        b = found_b;
+        const int64_t rest = found_rest;
+        s = kv_sequence(a.batch, b, a.tokens);
+        const Units u = units_of<kRows>(a, s);
+        const int item = static_cast<int>(rest / u.count), u0 = static_cast<int>(rest - static_cast<int64_t>(item) * u.count);
+        const int u1 = static_cast<int>(min(static_cast<int64_t>(u.count), u0 + (x_end - x)));
+        kh = item % heads;
+        tile = item / heads;
+        seg_begin = u.begin + u0 * kTokens;
+        seg_end = u.begin + u1 * kTokens;
+        whole = u0 == 0 && u1 == u.count;
+        next = x + (u1 - u0);
+    }
+    const int rows = s.n * group, row0 = tile * kRows;   // rows of this kernel are few: no overflow
+    // what the tile's first and last rows see bounds what all of them see
+    const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, min(rows - 1, row0 + kRows - 1) / group);
+    const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);   // seen by every row
+    const int out_lo = min(first.lo, last.lo), out_hi = max(first.hi, last.hi); // seen by any
+    seg_begin = max(seg_begin, out_lo & ~(kUnit - 1));
+    seg_end = min(seg_end, out_hi);
 
     // Q: rows g and g + 8; this lane's channels kDim/4 * t ...
     uint32_t q[kSteps][4];
@@ -164,10 +256,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
         c_row[hf] = fabsf(a.scale) * kLog2e * p.y;
         see[hf] = live ? seen_by(a, s, r / group) : Span{0, 0};
     }
-    const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);   // seen by every row
-    const int out_lo = min(first.lo, last.lo), out_hi = max(first.hi, last.hi); // seen by any
-    __syncthreads();   // scales
-
     float o[kHalf][kSteps][4];
     float m[kHalf], l[kHalf];
 #pragma unroll
@@ -181,9 +269,49 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
                 o[hf][j][e] = 0.0f;
     }
 
-    int stage = 0;
-    uint32_t parity = 0;
-    for (int unit = unit0; unit < end; unit += kWarps * kUnit) {
+
+    // In parts whose pages fit the table: their entries, the first copies, then the scales.
+    constexpr int kCap = (kMaxEntries - 2) * 16 / kTokens * kTokens;
+    for (int begin = seg_begin; begin < seg_end; begin += kCap) {
+    const int end = min(seg_end, begin + kCap);
+    const int page0 = begin / page, pages = (end - 1) / page - page0 + 1;
+    __syncthreads();   // the last part's readers are done
+    for (int i = threadIdx.x; i < pages; i += kThreads) {
+        int32_t id = a.batch.page_table[b * a.batch.ld_table + page0 + i];
+        if (id < 0 || id >= a.cache.num_pages) {
+            atomicOr(&g_error, ERR_KV_RANGE);
+            id = -1;
+        }
+        entry[i].id = id;
+    }
+    __syncthreads();
+    const auto fetch = [&](int unit, int stage) {   // one lane; unit: first token, below end
+        const uint32_t bar = smem_u32(&full[warp][stage]), dst = ring + stage * (2 * kTile);
+        const int32_t id0 = entry[unit / page - page0].id, id1 = page < kUnit && unit + page < end ? entry[unit / page + 1 - page0].id : -1;
+        mbar_arrive_expect_tx(bar, ((id0 >= 0) + (id1 >= 0)) * 2 * box * kDim);
+        if (id0 >= 0) {
+            tma_load_3d(dst, &k_map, 0, unit & (page - 1), id0 * heads + kh, bar);
+            tma_load_3d(dst + kTile, &v_map, 0, unit & (page - 1), id0 * heads + kh, bar);
+        }
+        if (id1 >= 0) {
+            tma_load_3d(dst + kTile / 2, &k_map, 0, 0, id1 * heads + kh, bar);
+            tma_load_3d(dst + kTile + kTile / 2, &v_map, 0, 0, id1 * heads + kh, bar);
+        }
+    };
+    const int unit0 = begin + warp * kUnit;
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i)
+            if (unit0 + i * kTokens < end)
+                fetch(unit0 + i * kTokens, (stage + i) % kStages);
+    for (int i = threadIdx.x; i < pages; i += kThreads) {
+        const int64_t bh = static_cast<int64_t>(max(entry[i].id, 0)) * heads + kh;
+        const float vs = a.cache.v_scale[bh];
+        entry[i].ks = a.cache.k_scale[bh];
+        entry[i].lv = lg2(vs);
+        entry[i].inv_vs = __frcp_rn(vs);
+    }
+    __syncthreads();   // scales
+    for (int unit = unit0; unit < end; unit += kTokens) {
         if (!mbar_wait_bounded(smem_u32(&full[warp][stage]), parity, kWaitNs))
             atomicOr(&g_error, ERR_ATTN_WAIT);   // the copies have not come: go on, the outputs mean nothing
         const uint8_t *kt = dyn + warp * (kStages * 2 * kTile) + stage * (2 * kTile), *vt = kt + kTile;
@@ -342,11 +470,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
             }
         }
         __syncwarp();   // every lane has read the stage that the next copies overwrite
-        if (lane == 0 && unit + kStages * kWarps * kUnit < end)
-            fetch(unit + kStages * kWarps * kUnit, stage);
+        if (lane == 0 && unit + kStages * kTokens < end)
+            fetch(unit + kStages * kTokens, stage);
         stage = stage + 1 == kStages ? 0 : stage + 1;
         parity ^= stage == 0;
     }
+    }   // of the segment
 
     // Join the warps: maxima and sums, then the outputs through shared memory (the rings are drained).
 #pragma unroll
@@ -369,6 +498,18 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
                 *reinterpret_cast<float2 *>(part + (warp * kRows + 8 * hf + 2 * t + e) * kDim + (kDim / 8) * g + 2 * j) =
                     make_float2(o[hf][j][e], o[hf][j][e + 2]);
     __syncthreads();
+    float *joined = part + kWarps * kRows * kDim;                                 // [row][kDim], with a cluster
+    float2 *joined_stat = reinterpret_cast<float2 *>(joined + kRows * kDim);      // [row]
+    const auto finish = [&](int r, int c, float mm, float ll, float4 sum) {
+        const int64_t row = s.row + (row0 + r) / group;
+        const int head = kh * group + (row0 + r) % group;
+        const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+        const __nv_bfloat162 x = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), y = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+        if (a.lse != nullptr && c == 0)
+            a.lse[row * a.heads + head] = (mm + lg2(ll)) * kLn2;
+    };
     for (int i = threadIdx.x; i < kRows * (kDim / 4); i += kThreads) {
         const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
         if (row0 + r >= rows)
@@ -380,53 +521,86 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(AttnArgs a, SplitPlan pl
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float ll = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(stat_m[w][r] - (mm == -INFINITY ? 0.0f : mm));
-            const float4 v = *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c);
-            sum.x = fmaf(v.x, f, sum.x);
-            sum.y = fmaf(v.y, f, sum.y);
-            sum.z = fmaf(v.z, f, sum.z);
-            sum.w = fmaf(v.w, f, sum.w);
-            ll = fmaf(stat_l[w][r], f, ll);
-        }
-        const int64_t row = s.row + (row0 + r) / group;
-        const int head = kh * group + (row0 + r) % group;
-        const int64_t at = row * a.heads + head;
-        if (plan.splits == 1) {
-            const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
-            const __nv_bfloat162 x = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), y = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
-            *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-            if (a.lse != nullptr && c == 0)
-                a.lse[at] = (mm + lg2(ll)) * kLn2;
-        } else {
-            *reinterpret_cast<float4 *>(ws_out + (at * plan.splits + split) * kDim + c) = sum;
+        for (int w = 0; w < kWarps; ++w)
+            join(sum, ll, *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c), stat_l[w][r], stat_m[w][r], mm);
+        if (plan.cluster) {
+            *reinterpret_cast<float4 *>(joined + r * kDim + c) = sum;
             if (c == 0)
-                ws_stat[at * plan.splits + split] = make_float2(mm, ll);
+                joined_stat[r] = make_float2(mm, ll);
+        } else if (whole) {
+            finish(r, c, mm, ll, sum);
+        } else {   // a CTA's first segment goes to its first place, another (its last) to the second
+            const int64_t at = (blockIdx.x * 2 + (x != x_first)) * kRows + r;
+            *reinterpret_cast<float4 *>(ws_out + at * kDim + c) = sum;
+            if (c == 0)
+                ws_stat[at] = make_float2(mm, ll);
         }
     }
+    if (plan.cluster) {   // each CTA joins a share of the rows' pieces over all parts
+        cluster_sync();
+        const uint32_t j0 = smem_u32(joined), s0 = smem_u32(joined_stat);
+        for (int i = (blockIdx.x % plan.splits) * kThreads + threadIdx.x; i < kRows * (kDim / 4); i += kThreads * plan.splits) {
+            const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
+            if (row0 + r >= rows)
+                continue;
+            float mm = -INFINITY, ll = 0.0f;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int p = 0; p < plan.splits; ++p)
+                mm = fmaxf(mm, ld_cluster_v2(mapa_shared(s0 + 8 * r, p)).x);
+            for (int p = 0; p < plan.splits; ++p) {
+                const float2 st = ld_cluster_v2(mapa_shared(s0 + 8 * r, p));
+                join(sum, ll, ld_cluster_v4(mapa_shared(j0 + (r * kDim + c) * 4, p)), st.y, st.x, mm);
+            }
+            finish(r, c, mm, ll, sum);
+        }
+        cluster_sync();   // nobody leaves while its part may be read
+    }
+    x = next;
+    fence_proxy_async_smem();   // the join's plain accesses come before the next segment's copies to the same place
+    __syncthreads();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the parts of each row: one warp per query token and head.
-template <int kDim>
-__global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, SplitPlan plan, const float2 *ws_stat, const float *ws_out)
+// Joins the parts of the rows whose units lie with several CTAs: one warp per
+// query token and head.
+template <int kDim, int kRows>
+__global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, const float2 *ws_stat, const float *ws_out)
 {
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-    if (!s.ok || s.len > a.max_kv || w >= static_cast<int64_t>(s.n) * a.heads)
-        return;
-    const int64_t row = s.row + w / a.heads;
-    const int head = static_cast<int>(w % a.heads);
-    const int64_t at = row * a.heads + head;
-    const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
-    const float2 *stat = ws_stat + at * plan.splits;
-    float mm = -INFINITY;
-    for (int i = lane; i < parts; i += 32)
-        mm = fmaxf(mm, stat[i].x);
+    const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
+    const Units u = units_of<kRows>(a, s);
+    int64_t ahead = 0, total = 0;   // units of the sequences before this one, and of all
+    for (int i = lane; i < a.batch.batch; i += 32) {
+        const Units v = units_of<kRows>(a, kv_sequence(a.batch, i, a.tokens));
+        const int64_t n = static_cast<int64_t>(v.count) * v.tiles * a.cache.heads;
+        total += n;
+        ahead += i < b ? n : 0;
+    }
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, o);
+    }
+    // Every warp waits here until the parts are written: this grid must not end before the one that it followed.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (u.count == 0 || w >= static_cast<int64_t>(s.n) * a.heads)
+        return;
+    const int head = static_cast<int>(w % a.heads), r = static_cast<int>(w / a.heads) * group + head % group;
+    const int64_t x0 = ahead + (static_cast<int64_t>(r / kRows) * a.cache.heads + head / group) * u.count;
+    const int64_t takers = min(static_cast<int64_t>(ctas), total);
+    const int64_t c0 = cta_of(x0, takers, total), c1 = cta_of(x0 + u.count - 1, takers, total);
+    if (c0 == c1)
+        return;   // one CTA had them all and has written the output
+    const int64_t slot0 = c0 * 2 + (c0 * total / takers != x0);   // the first part may be its CTA's second segment
+    const auto place = [&](int64_t c) { return (c == c0 ? slot0 : c * 2) * kRows + r % kRows; };
+    float mm = -INFINITY;
+    for (int64_t c = c0 + lane; c <= c1; c += 32)
+        mm = fmaxf(mm, ws_stat[place(c)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
     const float ref = mm == -INFINITY ? 0.0f : mm;
     constexpr int kPer = kDim / 32;
     float sum[kPer], ll = 0.0f;
@@ -434,11 +608,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, SplitPlan pl
     for (int c = 0; c < kPer; ++c)
         sum[c] = 0.0f;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const float2 st = stat[i];
+    for (int64_t i = c0; i <= c1; ++i) {
+        const float2 st = ws_stat[place(i)];
         const float f = ex2(st.x - ref);
         ll = fmaf(st.y, f, ll);
-        const float *src = ws_out + (at * plan.splits + i) * kDim + lane * kPer;
+        const float *src = ws_out + place(i) * kDim + lane * kPer;
 #pragma unroll
         for (int c = 0; c < kPer; c += 2) {
             const float2 v = *reinterpret_cast<const float2 *>(src + c);
@@ -446,6 +620,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, SplitPlan pl
             sum[c + 1] = fmaf(v.y, f, sum[c + 1]);
         }
     }
+    const int64_t row = s.row + w / a.heads;
     const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
     uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;
 #pragma unroll
@@ -454,31 +629,30 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, SplitPlan pl
         *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
     }
     if (a.lse != nullptr && lane == 0)
-        a.lse[at] = (mm + lg2(ll)) * kLn2;
+        a.lse[row * a.heads + head] = (mm + lg2(ll)) * kLn2;
 }
 
 }  // namespace
 
-// Parts of the keys: enough CTAs for kCtasPerSm on every SM, parts of 256
-// tokens at least (less leaves a warp fewer than two units) and at most what
-// kMaxEntries of the smallest pages hold.  Ragged batches launch as for their longest
-// sequence; the parts past a shorter one's end return at once.
+// Two ways to spread the keys.
+// Small calls, where each unit of 128 tokens can have a CTA of its own and a
+// row has 8 units at most: a cluster a row, joined over its shared memory.  No
+// workspace and no second launch (one request of 777 keys, 56 heads: 12.4 us
+// against 14.5).
+// Others: as many CTAs as the SMs hold, each with an equal share of all units,
+// whatever the lengths of the batch (equal parts per sequence, sized for the
+// longest, left SMs idle: 32 ragged requests 75 us); rows that lie with
+// several CTAs are joined by a second kernel.
 SplitPlan plan_rows(const AttnShape &s)
 {
-    constexpr int64_t kCtasPerSm = 4;
     const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);
     const int64_t tile = rows <= 8 ? 8 : 16;
-    const int64_t ctas = static_cast<int64_t>(s.batch) * s.kv_heads * ((rows + tile - 1) / tile);
-    const int64_t kv = s.max_kv < 1 ? 1 : s.max_kv;
-    int64_t splits = ctas > 0 ? (kCtasPerSm * sm_count() + ctas - 1) / ctas : 1;
-    const int64_t most = (kv + 255) / 256;
-    splits = splits > most ? most : splits;
-    int64_t chunk = (kv + splits - 1) / splits;
-    const int64_t round = kWarps * kUnit;
-    chunk = (chunk + round - 1) / round * round;
-    const int64_t cap = static_cast<int64_t>(kMaxEntries - 2) * 16 / round * round;
-    chunk = chunk > cap ? cap : chunk;
-    return SplitPlan{static_cast<int32_t>((kv + chunk - 1) / chunk), static_cast<int32_t>(chunk)};
+    const int64_t fit = sm_count() * (s.head_dim == 128 ? (tile == 8 ? resident<128, 8>() : resident<128, 16>())
+                                                        : (tile == 8 ? resident<64, 8>() : resident<64, 16>()));
+    const int64_t per_row = s.max_kv < 1 ? 1 : (s.max_kv + kWarps * kUnit - 1) / (kWarps * kUnit);
+    if (per_row <= 8 && rows <= 16 && per_row * s.batch * s.kv_heads <= fit)
+        return SplitPlan{static_cast<int32_t>(per_row), 0, 0, true};
+    return SplitPlan{static_cast<int32_t>(fit), 0, fit * 2 * tile, false};
 }
 
 namespace {
@@ -486,16 +660,11 @@ namespace {
 template <int kDim, int kRows>
 cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
 {
-    constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = kWarps * kRows * kDim * 4;
+    constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = (kWarps + 1) * kRows * kDim * 4 + kRows * 8;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-    const cudaError_t e = allow_shared<rows_kernel<kDim, kRows>>(kSmem);
+    cudaError_t e = allow_shared<rows_kernel<kDim, kRows>>(kSmem);
     if (e != cudaSuccess)
         return e;
-    const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
-    const int64_t tiles = (rows + kRows - 1) / kRows;
-    const int64_t x = tiles * a.cache.heads * plan.splits;
-    if (x > INT32_MAX)
-        return cudaErrorInvalidValue;
     CUtensorMap k_map, v_map;
     const int64_t blocks = static_cast<int64_t>(a.cache.num_pages) * a.cache.heads;
     const int box = a.cache.page_size < kUnit ? a.cache.page_size : kUnit;
@@ -506,9 +675,32 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
                !encode_cache_map(&v_map, a.cache.v_codes, kDim, a.cache.page_size, blocks, box)) {
         return cudaErrorInvalidValue;
     }
-    rows_kernel<kDim, kRows><<<dim3(static_cast<unsigned>(x), a.batch.batch), kThreads, kSmem, st>>>(
-        a, plan, static_cast<int>(tiles), stat, part, k_map, v_map);
-    return cudaGetLastError();
+    const int64_t warps = static_cast<int64_t>(a.batch.max_tokens) * a.heads, x = static_cast<int64_t>(plan.splits) * a.cache.heads;
+    if (x > INT32_MAX || (warps + kWarps - 1) / kWarps > INT32_MAX)
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr;
+    cfg.gridDim = plan.cluster ? dim3(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch))
+                               : dim3(static_cast<unsigned>(plan.splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(plan.splits);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.numAttrs = plan.cluster ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows>, a, plan, stat, part, k_map, v_map);
+    if (e != cudaSuccess || plan.cluster)
+        return e;
+    // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps), static_cast<unsigned>(a.batch.batch));
+    cfg.dynamicSmemBytes = 0;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows>, a, static_cast<int>(plan.splits), static_cast<const float2 *>(stat),
+                              static_cast<const float *>(part));
 }
 
 }  // namespace
@@ -519,20 +711,6 @@ cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, floa
     if (a.cache.head_dim == 64)
         return small ? run_rows<64, 8>(a, plan, stat, part, st) : run_rows<64, 16>(a, plan, stat, part, st);
     return small ? run_rows<128, 8>(a, plan, stat, part, st) : run_rows<128, 16>(a, plan, stat, part, st);
-}
-
-cudaError_t launch_attention_join(const AttnArgs &a, const SplitPlan &plan, const float2 *stat, const float *part,
-                                  cudaStream_t st)
-{
-    const int64_t x = (static_cast<int64_t>(a.batch.max_tokens) * a.heads + kWarps - 1) / kWarps;
-    if (x > INT32_MAX)
-        return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(x), a.batch.batch);
-    if (a.cache.head_dim == 64)
-        join_kernel<64><<<grid, kThreads, 0, st>>>(a, plan, stat, part);
-    else
-        join_kernel<128><<<grid, kThreads, 0, st>>>(a, plan, stat, part);
-    return cudaGetLastError();
 }
 
 cudaError_t read_attention_rows_error(uint32_t *code)

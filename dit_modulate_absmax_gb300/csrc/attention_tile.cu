@@ -623,6 +623,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+constexpr int kJoinThreads = 128;
+
+// Joins the parts of each row: one warp per query token and head.
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPlan plan, const float2 *ws_stat, const float *ws_out)
+{
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+    if (!s.ok || s.len > a.max_kv || w >= static_cast<int64_t>(s.n) * a.heads)
+        return;
+    const int64_t row = s.row + w / a.heads;
+    const int head = static_cast<int>(w % a.heads);
+    const int64_t at = row * a.heads + head;
+    const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
+    const float2 *stat = ws_stat + at * plan.splits;
+    float mm = -INFINITY;
+    for (int i = lane; i < parts; i += 32)
+        mm = fmaxf(mm, stat[i].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    constexpr int kPer = kDim / 32;
+    float sum[kPer], ll = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+        sum[c] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float2 st = stat[i];
+        const float f = ex2(st.x - ref);
+        ll = fmaf(st.y, f, ll);
+        const float *src = ws_out + (at * plan.splits + i) * kDim + lane * kPer;
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2) {
+            const float2 v = *reinterpret_cast<const float2 *>(src + c);
+            sum[c] = fmaf(v.x, f, sum[c]);
+            sum[c + 1] = fmaf(v.y, f, sum[c + 1]);
+        }
+    }
+    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+    uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(sum[c] * inv, sum[c + 1] * inv);
+        *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    if (a.lse != nullptr && lane == 0)
+        a.lse[at] = (mm + lg2(ll)) * kLn2;
+}
+
 // kGroup: scores in a row that are sure to lie in one page.
 template <int kDim, int kGroup>
 cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
@@ -660,14 +712,29 @@ SplitPlan plan_tile(const AttnShape &s)
     const int64_t most = (kv + 511) / 512;
     splits = splits > most ? most : splits < 1 ? 1 : splits;
     const int64_t chunk = ((kv + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
-    return SplitPlan{static_cast<int32_t>((kv + chunk - 1) / chunk), static_cast<int32_t>(chunk)};
+    splits = (kv + chunk - 1) / chunk;
+    return SplitPlan{static_cast<int32_t>(splits), static_cast<int32_t>(chunk), splits > 1 ? s.tokens * s.heads * splits : 0, false};
 }
 
 cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
 {
+    cudaError_t e;
     if (a.cache.page_size == 16)
-        return a.cache.head_dim == 64 ? run_tile<64, 16>(a, plan, stat, part, st) : run_tile<128, 16>(a, plan, stat, part, st);
-    return a.cache.head_dim == 64 ? run_tile<64, 32>(a, plan, stat, part, st) : run_tile<128, 32>(a, plan, stat, part, st);
+        e = a.cache.head_dim == 64 ? run_tile<64, 16>(a, plan, stat, part, st) : run_tile<128, 16>(a, plan, stat, part, st);
+    else
+        e = a.cache.head_dim == 64 ? run_tile<64, 32>(a, plan, stat, part, st) : run_tile<128, 32>(a, plan, stat, part, st);
+    if (e != cudaSuccess || plan.splits == 1)
+        return e;
+    constexpr int kJoinWarps = kJoinThreads / 32;
+    const int64_t x = (static_cast<int64_t>(a.batch.max_tokens) * a.heads + kJoinWarps - 1) / kJoinWarps;
+    if (x > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch));
+    if (a.cache.head_dim == 64)
+        join_kernel<64><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
+    else
+        join_kernel<128><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
+    return cudaGetLastError();
 }
 
 cudaError_t read_attention_tile_error(uint32_t *code)
