@@ -91,10 +91,18 @@ __device__ __forceinline__ Units units_of(const AttnArgs &a, const KvSequence &s
                  (s.n * (a.heads / a.cache.heads) + kRows - 1) / kRows};
 }
 
+// a / b of numbers that mostly fit 32 bits, where a division is several times shorter.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // CTA i of g (g <= T) takes the units [i T / g, (i + 1) T / g) of T, the
 // sequences one after another, within each its row tiles and cache heads.  The
 // CTA of unit x:
-__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) { return ((x + 1) * g - 1) / total; }
+__device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) { return divide((x + 1) * g - 1, total); }
 
 template <int kDim, int kRows>
 __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
@@ -109,21 +117,26 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     __shared__ PageEntry entry[kMaxEntries];
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
-    __shared__ int64_t before[kThreads + 1];     // units before each thread's share of the sequences
-    __shared__ int64_t found_rest;
+    __shared__ int64_t warp_units[kWarps], found_rest;
     __shared__ int found_b;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int page = a.cache.page_size, group = a.heads / a.cache.heads, heads = a.cache.heads;
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * (kStages * 2 * kTile);
-    const int box = min(page, kUnit);
+    const int box = min(page, kUnit), shift = 31 - __clz(page);
     if (lane == 0)
         for (int i = 0; i < kStages; ++i)
             mbar_init(smem_u32(&full[warp][i]), 1);
     fence_mbar_init();
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&k_map);
+        prefetch_tmap(&v_map);
+    }
 
     int64_t x = 0, x_end = 1;                    // units to do
+    // Each thread counts the units of a share of the sequences (one, mostly), [mine_lo, mine_hi) of all.
     const int share = (a.batch.batch + kThreads - 1) / kThreads;
+    int64_t mine_lo = 0, mine_hi = 0;
     if (!plan.cluster) {
         int64_t mine = 0;
         for (int b = threadIdx.x * share; b < min(a.batch.batch, (static_cast<int>(threadIdx.x) + 1) * share); ++b) {
@@ -133,28 +146,27 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             if (u.count == 0 && s.n != 0 && blockIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
         }
-        int64_t sum = mine;
+        mine_hi = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            sum += lane >= o ? y : 0;
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, mine_hi, o);
+            mine_hi += lane >= o ? y : 0;
         }
-        before[threadIdx.x + 1] = sum;
+        if (lane == 31)
+            warp_units[warp] = mine_hi;
         __syncthreads();
-        int64_t off = 0;
-        for (int w = 0; w < warp; ++w)
-            off += before[32 * w + 32];
-        __syncthreads();
-        before[threadIdx.x + 1] = sum + off;
-        if (threadIdx.x == 0)
-            before[0] = 0;
-        __syncthreads();
-        const int64_t total = before[kThreads];
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            mine_hi += w < warp ? warp_units[w] : 0;
+            total += warp_units[w];
+        }
+        mine_lo = mine_hi - mine;
         const int64_t takers = min(static_cast<int64_t>(gridDim.x), total);   // every one of them has a unit
         x_end = 0;
         if (blockIdx.x < takers) {
-            x = blockIdx.x * total / takers;
-            x_end = (blockIdx.x + 1) * total / takers;
+            x = divide(blockIdx.x * total, takers);
+            x_end = divide((blockIdx.x + 1) * total, takers);
         }
     }
     int stage = 0;
@@ -181,31 +193,26 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         seg_begin = u.begin + blockIdx.x % plan.splits * kTokens;
         seg_end = seg_begin + kTokens;
     } else {
-        if (threadIdx.x < 32) {   // whose share holds x, then which sequence of the share
-            int lo = 0;
-#pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i)
-                lo += __popc(__ballot_sync(0xFFFFFFFFu, before[32 * i + lane + 1] <= x));
-            if (lane == 0) {
-                int64_t rest = x - before[lo];
-                int at = lo * share;
+        if (mine_lo <= x && x < mine_hi) {   // one thread: in its share, which sequence
+            int64_t rest = x - mine_lo;
+            int at = threadIdx.x * share;
+            if (share > 1)
                 for (;; ++at) {
-                    const Units u = units_of<kRows>(a, kv_sequence(a.batch, at, a.tokens));
-                    const int64_t n = static_cast<int64_t>(u.count) * u.tiles * heads;
+                    const Units v = units_of<kRows>(a, kv_sequence(a.batch, at, a.tokens));
+                    const int64_t n = static_cast<int64_t>(v.count) * v.tiles * heads;
                     if (rest < n)
                         break;
                     rest -= n;
                 }
-                found_b = at;
-                found_rest = rest;
-            }
+            found_b = at;
+            found_rest = rest;
         }
         __syncthreads();
         b = found_b;
         const int64_t rest = found_rest;
         s = kv_sequence(a.batch, b, a.tokens);
         const Units u = units_of<kRows>(a, s);
-        const int item = static_cast<int>(rest / u.count), u0 = static_cast<int>(rest - static_cast<int64_t>(item) * u.count);
+        const int item = static_cast<int>(divide(rest, u.count)), u0 = static_cast<int>(rest - static_cast<int64_t>(item) * u.count);
         const int u1 = static_cast<int>(min(static_cast<int64_t>(u.count), u0 + (x_end - x)));
         kh = item % heads;
         tile = item / heads;
@@ -221,6 +228,10 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     const int out_lo = min(first.lo, last.lo), out_hi = max(first.hi, last.hi); // seen by any
     seg_begin = max(seg_begin, out_lo & ~(kUnit - 1));
     seg_end = min(seg_end, out_hi);
+    // The first pages' numbers are on their way while the queries are read.
+    const int first_page = (seg_begin >> shift) + threadIdx.x;
+    const int32_t first_id = seg_begin < seg_end && first_page <= (seg_end - 1) >> shift
+                                 ? a.batch.page_table[b * a.batch.ld_table + first_page] : 0;
 
     // Q: rows g and g + 8; this lane's channels kDim/4 * t ...
     uint32_t q[kSteps][4];
@@ -274,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     constexpr int kCap = (kMaxEntries - 2) * 16 / kTokens * kTokens;
     for (int begin = seg_begin; begin < seg_end; begin += kCap) {
     const int end = min(seg_end, begin + kCap);
-    const int page0 = begin / page, pages = (end - 1) / page - page0 + 1;
+    const int page0 = begin >> shift, pages = ((end - 1) >> shift) - page0 + 1;
     __syncthreads();   // the last part's readers are done
     for (int i = threadIdx.x; i < pages; i += kThreads) {
-        int32_t id = a.batch.page_table[b * a.batch.ld_table + page0 + i];
+        int32_t id = begin == seg_begin && i < kThreads ? first_id : a.batch.page_table[b * a.batch.ld_table + page0 + i];
         if (id < 0 || id >= a.cache.num_pages) {
             atomicOr(&g_error, ERR_KV_RANGE);
             id = -1;
@@ -287,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     __syncthreads();
     const auto fetch = [&](int unit, int stage) {   // one lane; unit: first token, below end
         const uint32_t bar = smem_u32(&full[warp][stage]), dst = ring + stage * (2 * kTile);
-        const int32_t id0 = entry[unit / page - page0].id, id1 = page < kUnit && unit + page < end ? entry[unit / page + 1 - page0].id : -1;
+        const int at = (unit >> shift) - page0;
+        const int32_t id0 = entry[at].id, id1 = page < kUnit && unit + page < end ? entry[at + 1].id : -1;
         mbar_arrive_expect_tx(bar, ((id0 >= 0) + (id1 >= 0)) * 2 * box * kDim);
         if (id0 >= 0) {
             tma_load_3d(dst, &k_map, 0, unit & (page - 1), id0 * heads + kh, bar);
@@ -339,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
 #pragma unroll
         for (int hf = 0; hf < kHalf; ++hf)
             top[hf] = -INFINITY;
-        const int e0 = unit / page - page0, e1 = min(pages - 1, (unit + 16) / page - page0);
+        const int e0 = (unit >> shift) - page0, e1 = min(pages - 1, ((unit + 16) >> shift) - page0);
         const PageEntry pe[2] = {entry[e0], entry[e1]};
 #pragma unroll
         for (int n = 0; n < 4; ++n)
@@ -562,13 +574,17 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the parts of the rows whose units lie with several CTAs: one warp per
-// query token and head.
+// Joins the parts of the rows whose units lie with several CTAs: a CTA for each
+// query token and head, its warps taking turns at the parts (one long row has
+// as many parts as there are CTAs for its cache head: 57 at 8 cache heads, and
+// one warp alone took 15 us over them).
 template <int kDim, int kRows>
 __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, const float2 *ws_stat, const float *ws_out)
 {
-    const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    constexpr int kPer = kDim / 32;
+    __shared__ float sums[kWarps][kDim], stats[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, group = a.heads / a.cache.heads;
+    const int i_row = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
     const Units u = units_of<kRows>(a, s);
     int64_t ahead = 0, total = 0;   // units of the sequences before this one, and of all
@@ -583,17 +599,17 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, co
         total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
         ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, o);
     }
-    // Every warp waits here until the parts are written: this grid must not end before the one that it followed.
+    // Every thread waits here until the parts are written: this grid must not end before the one that it followed.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (u.count == 0 || w >= static_cast<int64_t>(s.n) * a.heads)
+    if (u.count == 0 || i_row >= s.n)
         return;
-    const int head = static_cast<int>(w % a.heads), r = static_cast<int>(w / a.heads) * group + head % group;
+    const int r = i_row * group + head % group;
     const int64_t x0 = ahead + (static_cast<int64_t>(r / kRows) * a.cache.heads + head / group) * u.count;
     const int64_t takers = min(static_cast<int64_t>(ctas), total);
     const int64_t c0 = cta_of(x0, takers, total), c1 = cta_of(x0 + u.count - 1, takers, total);
     if (c0 == c1)
         return;   // one CTA had them all and has written the output
-    const int64_t slot0 = c0 * 2 + (c0 * total / takers != x0);   // the first part may be its CTA's second segment
+    const int64_t slot0 = c0 * 2 + (divide(c0 * total, takers) != x0);   // the first part may be its CTA's second segment
     const auto place = [&](int64_t c) { return (c == c0 ? slot0 : c * 2) * kRows + r % kRows; };
     float mm = -INFINITY;
     for (int64_t c = c0 + lane; c <= c1; c += 32)
@@ -602,13 +618,12 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, co
     for (int o = 16; o > 0; o >>= 1)
         mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
     const float ref = mm == -INFINITY ? 0.0f : mm;
-    constexpr int kPer = kDim / 32;
     float sum[kPer], ll = 0.0f;
 #pragma unroll
     for (int c = 0; c < kPer; ++c)
         sum[c] = 0.0f;
 #pragma unroll 4
-    for (int64_t i = c0; i <= c1; ++i) {
+    for (int64_t i = c0 + warp; i <= c1; i += kWarps) {
         const float2 st = ws_stat[place(i)];
         const float f = ex2(st.x - ref);
         ll = fmaf(st.y, f, ll);
@@ -620,15 +635,29 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, co
             sum[c + 1] = fmaf(v.y, f, sum[c + 1]);
         }
     }
-    const int64_t row = s.row + w / a.heads;
-    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
-    uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;
 #pragma unroll
-    for (int c = 0; c < kPer; c += 2) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(sum[c] * inv, sum[c + 1] * inv);
-        *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
+    for (int c = 0; c < kPer; ++c)
+        sums[warp][lane * kPer + c] = sum[c];
+    if (lane == 0)
+        stats[warp] = ll;
+    __syncthreads();
+    ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        ll += stats[w];
+    const int64_t row = s.row + i_row;
+    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
+    for (int c = 2 * threadIdx.x; c < kDim; c += 2 * kThreads) {
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            x += sums[w][c];
+            y += sums[w][c + 1];
+        }
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x * inv, y * inv);
+        *reinterpret_cast<uint32_t *>(a.out + row * a.ot + head * a.oh + c) = *reinterpret_cast<const uint32_t *>(&v);
     }
-    if (a.lse != nullptr && lane == 0)
+    if (a.lse != nullptr && threadIdx.x == 0)
         a.lse[row * a.heads + head] = (mm + lg2(ll)) * kLn2;
 }
 
@@ -675,8 +704,8 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
                !encode_cache_map(&v_map, a.cache.v_codes, kDim, a.cache.page_size, blocks, box)) {
         return cudaErrorInvalidValue;
     }
-    const int64_t warps = static_cast<int64_t>(a.batch.max_tokens) * a.heads, x = static_cast<int64_t>(plan.splits) * a.cache.heads;
-    if (x > INT32_MAX || (warps + kWarps - 1) / kWarps > INT32_MAX)
+    const int64_t joins = static_cast<int64_t>(a.batch.max_tokens) * a.heads, x = static_cast<int64_t>(plan.splits) * a.cache.heads;
+    if (x > INT32_MAX || joins > INT32_MAX)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr;
@@ -694,7 +723,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     if (e != cudaSuccess || plan.cluster)
         return e;
     // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + kWarps - 1) / kWarps), static_cast<unsigned>(a.batch.batch));
+    cfg.gridDim = dim3(static_cast<unsigned>(joins), static_cast<unsigned>(a.batch.batch));
     cfg.dynamicSmemBytes = 0;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
