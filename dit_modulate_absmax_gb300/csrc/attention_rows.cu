@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         prefetch_tmap(&k_map);
         prefetch_tmap(&v_map);
     }
+    // The join's CTAs may come as places fall free; they wait for this grid's end before they read its parts.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     int64_t x = 0, x_end = 1;                    // units to do
     // Each thread counts the units of a share of the sequences (one, mostly), [mine_lo, mine_hi) of all.
@@ -571,20 +573,23 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     fence_proxy_async_smem();   // the join's plain accesses come before the next segment's copies to the same place
     __syncthreads();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+constexpr int kJoinThreads = 1024;
+
 // Joins the parts of the rows whose units lie with several CTAs: a CTA for each
-// query token and head, its warps taking turns at the parts (one long row has
-// as many parts as there are CTAs for its cache head: 57 at 8 cache heads, and
-// one warp alone took 15 us over them).
+// sequence, row tile and cache head, a thread for 4 channels of a row and every
+// kGroups-th part (one long request has as many parts as there are CTAs for a
+// cache head, 57 at 8 of them: one warp a row took 15 us over those).
 template <int kDim, int kRows>
-__global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, const float2 *ws_stat, const float *ws_out)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas, const float2 *ws_stat, const float *ws_out)
 {
-    constexpr int kPer = kDim / 32;
-    __shared__ float sums[kWarps][kDim], stats[kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, group = a.heads / a.cache.heads;
-    const int i_row = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    constexpr int kPieces = kRows * kDim / 4;
+    constexpr int kGroups = kJoinThreads / kPieces;
+    __shared__ float4 sums[kGroups][kPieces];
+    __shared__ float lls[kGroups][kRows];
+    const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
+    const int kh = blockIdx.x % a.cache.heads, tile = blockIdx.x / a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
     const Units u = units_of<kRows>(a, s);
     int64_t ahead = 0, total = 0;   // units of the sequences before this one, and of all
@@ -599,65 +604,63 @@ __global__ void __launch_bounds__(kThreads) join_kernel(AttnArgs a, int ctas, co
         total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
         ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, o);
     }
+    int64_t c0 = 0, c1 = 0, slot0 = 0;
+    const bool mine = u.count > 0 && tile < u.tiles;
+    if (mine) {
+        const int64_t x0 = ahead + (static_cast<int64_t>(tile) * a.cache.heads + kh) * u.count;
+        const int64_t takers = min(static_cast<int64_t>(ctas), total);
+        c0 = cta_of(x0, takers, total);
+        c1 = cta_of(x0 + u.count - 1, takers, total);
+        slot0 = c0 * 2 + (divide(c0 * total, takers) != x0);   // the first part may be its CTA's second segment
+    }
     // Every thread waits here until the parts are written: this grid must not end before the one that it followed.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (u.count == 0 || i_row >= s.n)
-        return;
-    const int r = i_row * group + head % group;
-    const int64_t x0 = ahead + (static_cast<int64_t>(r / kRows) * a.cache.heads + head / group) * u.count;
-    const int64_t takers = min(static_cast<int64_t>(ctas), total);
-    const int64_t c0 = cta_of(x0, takers, total), c1 = cta_of(x0 + u.count - 1, takers, total);
     if (c0 == c1)
-        return;   // one CTA had them all and has written the output
-    const int64_t slot0 = c0 * 2 + (divide(c0 * total, takers) != x0);   // the first part may be its CTA's second segment
-    const auto place = [&](int64_t c) { return (c == c0 ? slot0 : c * 2) * kRows + r % kRows; };
-    float mm = -INFINITY;
-    for (int64_t c = c0 + lane; c <= c1; c += 32)
-        mm = fmaxf(mm, ws_stat[place(c)].x);
+        return;   // nothing, or one CTA had them all and has written the output
+    const int part0 = threadIdx.x / kPieces, piece = threadIdx.x % kPieces, r = piece / (kDim / 4), c = piece % (kDim / 4) * 4;
+    const int row_in = tile * kRows + r;
+    const bool live = row_in < s.n * group;
+    const auto place = [&](int64_t p) { return (p == c0 ? slot0 : p * 2) * kRows + r; };
+    float mm = -INFINITY, ll = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (live) {
+        for (int64_t p = c0 + lane % (kDim / 4); p <= c1; p += kDim / 4)   // a row's lanes: kDim / 4 neighbours
+            mm = fmaxf(mm, ws_stat[place(p)].x);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = kDim / 8; o > 0; o >>= 1)
         mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-    const float ref = mm == -INFINITY ? 0.0f : mm;
-    float sum[kPer], ll = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c)
-        sum[c] = 0.0f;
-#pragma unroll 4
-    for (int64_t i = c0 + warp; i <= c1; i += kWarps) {
-        const float2 st = ws_stat[place(i)];
-        const float f = ex2(st.x - ref);
-        ll = fmaf(st.y, f, ll);
-        const float *src = ws_out + place(i) * kDim + lane * kPer;
-#pragma unroll
-        for (int c = 0; c < kPer; c += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(src + c);
-            sum[c] = fmaf(v.x, f, sum[c]);
-            sum[c + 1] = fmaf(v.y, f, sum[c + 1]);
+    if (live) {
+#pragma unroll 8
+        for (int64_t p = c0 + part0; p <= c1; p += kGroups) {
+            const float2 st = ws_stat[place(p)];
+            join(sum, ll, *reinterpret_cast<const float4 *>(ws_out + place(p) * kDim + c), st.y, st.x, mm);
         }
     }
+    if (kGroups > 1) {
+        sums[part0][piece] = sum;
+        if (c == 0)
+            lls[part0][r] = ll;
+        __syncthreads();
+        if (part0 > 0)
+            return;
+        ll = lls[0][r];
 #pragma unroll
-    for (int c = 0; c < kPer; ++c)
-        sums[warp][lane * kPer + c] = sum[c];
-    if (lane == 0)
-        stats[warp] = ll;
-    __syncthreads();
-    ll = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        ll += stats[w];
-    const int64_t row = s.row + i_row;
+        for (int i = 1; i < kGroups; ++i) {
+            const float4 v = sums[i][piece];
+            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+            ll += lls[i][r];
+        }
+    }
+    if (!live)
+        return;
+    const int64_t row = s.row + row_in / group;
+    const int head = kh * group + row_in % group;
     const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
-    for (int c = 2 * threadIdx.x; c < kDim; c += 2 * kThreads) {
-        float x = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            x += sums[w][c];
-            y += sums[w][c + 1];
-        }
-        const __nv_bfloat162 v = __floats2bfloat162_rn(x * inv, y * inv);
-        *reinterpret_cast<uint32_t *>(a.out + row * a.ot + head * a.oh + c) = *reinterpret_cast<const uint32_t *>(&v);
-    }
-    if (a.lse != nullptr && threadIdx.x == 0)
+    const __nv_bfloat162 x = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), y = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+    *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    if (a.lse != nullptr && c == 0)
         a.lse[row * a.heads + head] = (mm + lg2(ll)) * kLn2;
 }
 
@@ -704,7 +707,8 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
                !encode_cache_map(&v_map, a.cache.v_codes, kDim, a.cache.page_size, blocks, box)) {
         return cudaErrorInvalidValue;
     }
-    const int64_t joins = static_cast<int64_t>(a.batch.max_tokens) * a.heads, x = static_cast<int64_t>(plan.splits) * a.cache.heads;
+    const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
+    const int64_t joins = (rows + kRows - 1) / kRows * a.cache.heads, x = static_cast<int64_t>(plan.splits) * a.cache.heads;
     if (x > INT32_MAX || joins > INT32_MAX)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
@@ -724,6 +728,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
         return e;
     // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
     cfg.gridDim = dim3(static_cast<unsigned>(joins), static_cast<unsigned>(a.batch.batch));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
