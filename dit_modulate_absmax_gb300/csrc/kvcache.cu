@@ -9,8 +9,12 @@
 // round the same value again and again.
 //
 // Writing moves 3 bytes a value and reading 3, both bound by HBM.  A CTA of
-// the writer holds its block's new values in registers between the maximum
-// and the encoding, so that each is read once.
+// the writer holds a head's new keys and values of its page in registers
+// between the maximum and the encoding, so that each is read once, and goes on
+// to its next head with one barrier between; the cosines and sines of its
+// tokens serve all its heads.
+#include <type_traits>
+
 #include "kvcache.cuh"
 #include "rope.cuh"
 
@@ -19,8 +23,15 @@ namespace {
 
 __device__ uint32_t g_error;
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
+constexpr int kReadThreads = 256;
 constexpr int kScaleExpMin = -40, kScaleExpMax = 119;
+
+__device__ __forceinline__ uint32_t bf_pack(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -108,27 +119,15 @@ struct WriteArgs {
     RopeArgs rope;                   // pairs = 0: none
 };
 
-// Maximum over the CTA, in every thread.
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *warp_max)
+// One CTA: a page's blocks of every head in [blockIdx.x * heads_per_cta, ...).
+// kPer chunks of 8 values per thread cover the page (kPer * blockDim.x * 8 =
+// page * dim), all at the same channels.  kRope: 0 none, 1 interleaved, 2 halves.
+template <int kPer, int kRope>
+__global__ void __launch_bounds__(kMaxThreads) write_kernel(WriteArgs a, int heads_per_cta)
 {
-    v = __reduce_max_sync(0xFFFFFFFFu, v);
-    __syncthreads();   // the last call's readers are done
-    if ((threadIdx.x & 31) == 0)
-        warp_max[threadIdx.x >> 5] = v;
-    __syncthreads();
-    uint32_t m = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w)
-        m = max(m, warp_max[w]);
-    return m;
-}
-
-// One CTA: a page's block of every head in [blockIdx.x * heads_per_cta, ...).
-// kPer chunks of 8 values per thread cover the page (kPer * blockDim.x * 8 = page * dim).
-template <int kPer>
-__global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a, int heads_per_cta)
-{
-    extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ uint32_t warp_max[kThreads / 32];
+    extern __shared__ __align__(16) float2 cs[];                              // [page][dim / 2], with a rotation
+    __shared__ uint32_t warp_max[2][2][kMaxThreads / 32];
+    __shared__ uint16_t swap[kRope == 2 ? kMaxThreads / 32 : 1][kRope == 2 ? 256 : 1];
     const int b = blockIdx.z, page = a.cache.page_size, dim = a.cache.head_dim, heads = a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
     // positions in 64 bits: lengths near 2^31 must not wrap
@@ -151,88 +150,100 @@ __global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a, int heads_
     const int hi = static_cast<int>(last - p0 < page ? last - p0 : page);
     const int64_t row0 = s.row + p0 - s.len;                                  // row of the page's token 0
 
-    const bool turn = a.rope.pairs > 0;
-    float2 *cs = reinterpret_cast<float2 *>(dyn);                             // [page][pairs]
-    uint16_t *tile = reinterpret_cast<uint16_t *>(dyn + sizeof(float2) * page * a.rope.pairs);   // [page][dim]
-    if (turn)
-        for (int i = threadIdx.x; i < page * a.rope.pairs; i += blockDim.x) {
-            const int t = i / a.rope.pairs, p = i - t * a.rope.pairs;
-            if (t >= lo && t < hi) {
+    const int per_row = dim >> 3, t0 = threadIdx.x / per_row, c0 = (threadIdx.x - t0 * per_row) * 8;
+    const int t_step = blockDim.x / per_row;
+    const int h0 = blockIdx.x * heads_per_cta, h_end = min(heads, h0 + heads_per_cta);
+    const auto load = [&](int kv, int h, uint4 (&v)[kPer]) {
+        const uint16_t *x = a.x[kv] + (row0 + t0) * a.token_stride[kv] + h * a.head_stride[kv] + c0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int t = t0 + u * t_step;
+            v[u] = t >= lo && t < hi ? *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(u * t_step) * a.token_stride[kv])
+                                     : make_uint4(0, 0, 0, 0);
+        }
+    };
+    uint4 x[2][kPer];
+    load(0, h0, x[0]);
+    load(1, h0, x[1]);
+    if constexpr (kRope != 0) {
+        for (int i = threadIdx.x; i < page * (dim / 2); i += blockDim.x) {
+            const int t = i / (dim / 2), p = i - t * (dim / 2);
+            if (t >= lo && t < hi && p < a.rope.pairs) {
                 const float pos = a.rope.positions[(row0 + t) * a.rope.ld_positions + rope_axis(a.rope, p)];
                 cs[i] = rope_cos_sin(a.rope.inverse ? -pos : pos, rope_turns(a.rope, p));
             }
         }
+        __syncthreads();
+    }
+    const RopeLane<kRope == 2 ? 1 : 0> lane_of(a.rope, c0, (threadIdx.x & 31) / per_row * per_row);
 
-    const int per_row = dim >> 3;
-    for (int h = blockIdx.x * heads_per_cta; h < min(heads, (static_cast<int>(blockIdx.x) + 1) * heads_per_cta); ++h) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-            const int64_t bh = static_cast<int64_t>(id) * heads + h;
-            uint8_t *codes = (kv == 0 ? a.cache.k_codes : a.cache.v_codes) + bh * page * dim;
-            float *scale = (kv == 0 ? a.cache.k_scale : a.cache.v_scale) + bh;
-            const uint16_t *x = a.x[kv] + h * a.head_stride[kv];
-            const float was = lo > 0 ? *scale : 0.0f;
-            uint4 v[kPer];
+    for (int h = h0; h < h_end; ++h) {
+        if (h > h0) {
+            load(0, h, x[0]);
+            load(1, h, x[1]);
+        }
+        const int64_t bh = static_cast<int64_t>(id) * heads + h;
+        float was[2] = {0.0f, 0.0f};
+        if (lo > 0) {
+            was[0] = a.cache.k_scale[bh];
+            was[1] = a.cache.v_scale[bh];
+        }
+        if constexpr (kRope != 0) {
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const int i = threadIdx.x + u * blockDim.x, t = i / per_row, c = (i - t * per_row) * 8;
-                v[u] = t >= lo && t < hi ? *reinterpret_cast<const uint4 *>(x + (row0 + t) * a.token_stride[kv] + c)
-                                         : make_uint4(0, 0, 0, 0);
-            }
-            if (kv == 0 && turn) {
-                __syncthreads();   // the last head's readers are done; cs is written
-#pragma unroll
-                for (int u = 0; u < kPer; ++u)
-                    reinterpret_cast<uint4 *>(tile)[threadIdx.x + u * blockDim.x] = v[u];
-                __syncthreads();
-#pragma unroll
-                for (int u = 0; u < kPer; ++u) {
-                    const int i = threadIdx.x + u * blockDim.x, t = i / per_row, c = (i - t * per_row) * 8;
-                    if (t < lo || t >= hi)
-                        continue;
-                    uint32_t w[4];
+                const int t = t0 + u * t_step;
+                uint32_t w[4] = {x[0][u].x, x[0][u].y, x[0][u].z, x[0][u].w};
+                float partner[8];
+                rope_partners(lane_of, w, swap[kRope == 2 ? threadIdx.x >> 5 : 0], partner);
+                if (t >= lo && t < hi) {
+                    const float2 *f = cs + t * (dim / 2);
+                    float y[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const RopeChannel ch = rope_channel(a.rope, c + e);
-                        const uint16_t own = tile[t * dim + c + e];
-                        uint32_t y = own;
-                        if (ch.pair >= 0) {
-                            const float2 f = cs[t * a.rope.pairs + ch.pair];
-                            const float r = rope_mix(__uint_as_float(static_cast<uint32_t>(own) << 16),
-                                                     __uint_as_float(static_cast<uint32_t>(tile[t * dim + ch.partner]) << 16),
-                                                     f.x, ch.first ? -f.y : f.y);
-                            y = __bfloat16_as_ushort(__float2bfloat16_rn(r));
-                        }
-                        w[e >> 1] = (e & 1) ? w[e >> 1] | y << 16 : y;
+                        const float own = (e & 1) != 0 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+                        const float2 v = f[kRope == 1 ? (c0 + e) >> 1 : lane_of.pair[e]];
+                        y[e] = (lane_of.turned >> e) & 1u ? rope_mix(own, partner[e], v.x, (lane_of.first >> e) & 1u ? -v.y : v.y) : own;
                     }
-                    v[u] = make_uint4(w[0], w[1], w[2], w[3]);
+                    x[0][u] = make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
                 }
             }
-            uint32_t m = 0;
-            uint32_t odd = 0;   // chunks with a value that is not finite
+        }
+        uint32_t m[2] = {0, 0}, odd[2] = {0, 0};   // maxima; chunks with a value that is not finite
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const uint32_t f = finite_absmax8(v[u]);
-                odd |= (f >> 16) << u;
-                m = max(m, f & 0xFFFFu);
+                const uint32_t f = finite_absmax8(x[kv][u]);
+                odd[kv] |= (f >> 16) << u;
+                m[kv] = max(m[kv], f & 0xFFFFu);
             }
-            m = cta_max(m, warp_max);
-            float s2 = block_scale_of(m);
+            m[kv] = __reduce_max_sync(0xFFFFFFFFu, m[kv]);
+            if ((threadIdx.x & 31) == 0)
+                warp_max[h & 1][kv][threadIdx.x >> 5] = m[kv];
+        }
+        __syncthreads();   // and the old scales are read; the next head uses the other half of warp_max
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            m[kv] = 0;
+            for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w)
+                m[kv] = max(m[kv], warp_max[h & 1][kv][w]);
+            float scale = block_scale_of(m[kv]);
             if (lo > 0)
-                s2 = fmaxf(s2, was);
-            const Divisor d = divisor(s2);
+                scale = fmaxf(scale, was[kv]);
+            const Divisor d = divisor(scale);
             if (threadIdx.x == 0)
-                *scale = s2;   // every thread read the old one before cta_max's barriers
-            const bool grown = lo > 0 && s2 != was;
+                (kv == 0 ? a.cache.k_scale : a.cache.v_scale)[bh] = scale;
+            const bool grown = lo > 0 && scale != was[kv];
+            uint2 *codes = reinterpret_cast<uint2 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + bh * page * dim) + threadIdx.x;
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const int i = threadIdx.x + u * blockDim.x, t = i / per_row;
-                uint2 *dst = reinterpret_cast<uint2 *>(codes) + i;
+                const int t = t0 + u * t_step;
+                uint2 *dst = codes + u * blockDim.x;
                 if (t >= lo && t < hi) {
-                    *dst = encode8(v[u], d, ((odd >> u) & 1u) == 0);
+                    *dst = encode8(x[kv][u], d, ((odd[kv] >> u) & 1u) == 0);
                 } else if (t < lo && grown) {
                     const uint2 c = *dst;
-                    *dst = make_uint2(reencode4(c.x, was, d), reencode4(c.y, was, d));
+                    *dst = make_uint2(reencode4(c.x, was[kv], d), reencode4(c.y, was[kv], d));
                 }
             }
         }
@@ -254,10 +265,11 @@ __device__ __forceinline__ uint32_t decode2(uint32_t c, float scale)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// One CTA: one page and head, keys and values.
-__global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a)
+// One CTA: a page of every head in [blockIdx.x * heads_per_cta, ...), 16 codes a
+// thread and turn, keys and values in flight together.
+__global__ void __launch_bounds__(kReadThreads) read_kernel(ReadArgs a, int heads_per_cta)
 {
-    const int b = blockIdx.z, h = blockIdx.x, page = a.cache.page_size, dim = a.cache.head_dim;
+    const int b = blockIdx.z, page = a.cache.page_size, dim = a.cache.head_dim, heads = a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
     const int64_t last = static_cast<int64_t>(s.len) + s.n;
     if (!s.ok || (s.n > 0 && (last - 1) / page >= a.batch.ld_table)) {
@@ -276,22 +288,38 @@ __global__ void __launch_bounds__(kThreads) read_kernel(ReadArgs a)
     }
     const int lo = static_cast<int>(s.len > p0 ? s.len - p0 : 0);
     const int hi = static_cast<int>(last - p0 < page ? last - p0 : page);
-    const int64_t bh = static_cast<int64_t>(id) * a.cache.heads + h;
-    const int per_row = dim >> 3;
-    for (int kv = 0; kv < 2; ++kv) {
-        if (a.x[kv] == nullptr)
-            continue;
-        const uint2 *codes = reinterpret_cast<const uint2 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + bh * page * dim);
-        const float scale = (kv == 0 ? a.cache.k_scale : a.cache.v_scale)[bh];
-        uint16_t *x = a.x[kv] + h * a.head_stride[kv];
-        for (int i = lo * per_row + threadIdx.x; i < hi * per_row; i += blockDim.x) {
-            const int t = i / per_row, c = (i - t * per_row) * 8;
-            const uint2 q = codes[i];
-            *reinterpret_cast<uint4 *>(x + (s.row + p0 - s.len + t) * a.token_stride[kv] + c) =
-                make_uint4(decode2(q.x & 0xFFFFu, scale), decode2(q.x >> 16, scale), decode2(q.y & 0xFFFFu, scale),
-                           decode2(q.y >> 16, scale));
-        }
+    const int per_row = dim >> 4, h0 = blockIdx.x * heads_per_cta, h_end = min(heads, h0 + heads_per_cta);
+    const int64_t row0 = s.row + p0 - s.len;
+    const int per_head = (hi - lo) * per_row, n = (h_end - h0) * per_head;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int dh = i / per_head, j = i - dh * per_head, t = lo + j / per_row, c = j % per_row * 16;
+        const int64_t bh = static_cast<int64_t>(id) * heads + h0 + dh, at = (bh * page + t) * dim + c;
+        uint4 q[2];
+        float scale[2];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            if (a.x[kv] != nullptr) {
+                q[kv] = *reinterpret_cast<const uint4 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + at);
+                scale[kv] = (kv == 0 ? a.cache.k_scale : a.cache.v_scale)[bh];
+            }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            if (a.x[kv] != nullptr) {
+                uint4 *x = reinterpret_cast<uint4 *>(a.x[kv] + (row0 + t) * a.token_stride[kv] + (h0 + dh) * a.head_stride[kv] + c);
+                const uint4 v = q[kv];
+                const float f = scale[kv];
+                x[0] = make_uint4(decode2(v.x & 0xFFFFu, f), decode2(v.x >> 16, f), decode2(v.y & 0xFFFFu, f), decode2(v.y >> 16, f));
+                x[1] = make_uint4(decode2(v.z & 0xFFFFu, f), decode2(v.z >> 16, f), decode2(v.w & 0xFFFFu, f), decode2(v.w >> 16, f));
+            }
     }
+}
+
+// Heads that a CTA takes one after another: enough CTAs to give each SM
+// `per_sm`, at most `most` heads.
+int heads_each(const KvCache &cache, const KvBatch &batch, unsigned blocks, int per_sm, int most)
+{
+    const int64_t n = static_cast<int64_t>(blocks) * batch.batch * cache.heads / (static_cast<int64_t>(sm_count()) * per_sm);
+    return n < 1 ? 1 : n > most ? most : static_cast<int>(n);
 }
 
 }  // namespace
@@ -302,27 +330,29 @@ cudaError_t launch_kv_write(const KvCache &cache, const KvBatch &batch, const ui
 {
     WriteArgs a{cache, batch, {k, v}, {kt, vt}, {kh, vh}, tokens, rope};
     const int chunks = cache.page_size * cache.head_dim / 8;
-    const int threads = chunks < kThreads ? chunks : kThreads;
-    const int heads_per_cta = rope.pairs > 0 ? 8 : 1;
+    const int threads = chunks < 256 ? chunks : chunks == 2048 ? 512 : 256;
     const unsigned blocks = static_cast<unsigned>((batch.max_tokens + cache.page_size - 2) / cache.page_size + 1);
+    const int heads_per_cta = heads_each(cache, batch, blocks, 4, 8);
     const dim3 grid(static_cast<unsigned>((cache.heads + heads_per_cta - 1) / heads_per_cta), blocks,
                     static_cast<unsigned>(batch.batch));
-    const size_t smem = rope.pairs > 0 ? static_cast<size_t>(cache.page_size) * (8 * rope.pairs + 2 * cache.head_dim) : 0;
-    const auto run = [&](auto kernel) {
-        if (smem > 47 * 1024) {   // 48 KB, the static part included, need no leave
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(smem));
-            if (e != cudaSuccess)
-                return e;
+    const int smem = rope.pairs > 0 ? cache.page_size * cache.head_dim / 2 * static_cast<int>(sizeof(float2)) : 0;
+    const auto run = [&](auto per) {
+        constexpr int kPer = decltype(per)::value;
+        cudaError_t e = cudaSuccess;
+        if (rope.pairs == 0) {
+            write_kernel<kPer, 0><<<grid, threads, 0, st>>>(a, heads_per_cta);
+        } else if (rope.layout == 0) {
+            if ((e = allow_shared<write_kernel<kPer, 1>>(64 * 1024)) == cudaSuccess)
+                write_kernel<kPer, 1><<<grid, threads, smem, st>>>(a, heads_per_cta);
+        } else if ((e = allow_shared<write_kernel<kPer, 2>>(64 * 1024)) == cudaSuccess) {
+            write_kernel<kPer, 2><<<grid, threads, smem, st>>>(a, heads_per_cta);
         }
-        kernel<<<grid, threads, smem, st>>>(a, heads_per_cta);
-        return cudaGetLastError();
+        return e != cudaSuccess ? e : cudaGetLastError();
     };
     switch (chunks / threads) {
-    case 1: return run(write_kernel<1>);
-    case 2: return run(write_kernel<2>);
-    case 4: return run(write_kernel<4>);
-    default: return run(write_kernel<8>);
+    case 1: return run(std::integral_constant<int, 1>{});
+    case 2: return run(std::integral_constant<int, 2>{});
+    default: return run(std::integral_constant<int, 4>{});
     }
 }
 
@@ -331,8 +361,10 @@ cudaError_t launch_kv_read(const KvCache &cache, const KvBatch &batch, uint16_t 
 {
     ReadArgs a{cache, batch, {k, v}, {kt, vt}, {kh, vh}, tokens};
     const unsigned blocks = static_cast<unsigned>((batch.max_tokens + cache.page_size - 2) / cache.page_size + 1);
-    const dim3 grid(static_cast<unsigned>(cache.heads), blocks, static_cast<unsigned>(batch.batch));
-    read_kernel<<<grid, kThreads, 0, st>>>(a);
+    const int heads_per_cta = heads_each(cache, batch, blocks, 16, 4);
+    const dim3 grid(static_cast<unsigned>((cache.heads + heads_per_cta - 1) / heads_per_cta), blocks,
+                    static_cast<unsigned>(batch.batch));
+    read_kernel<<<grid, kReadThreads, 0, st>>>(a, heads_per_cta);
     return cudaGetLastError();
 }
 

@@ -31,9 +31,7 @@ __global__ void __launch_bounds__(kThreads)
                 int heads, int dim, int heads_per_cta, RopeArgs r)
 {
     __shared__ float2 cs[kTokens][kRopeMaxPairs];
-    // halves: a warp's channels, member e of each lane's eight side by side, so that partners are read
-    // without bank conflicts
-    __shared__ uint16_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 8][32];
+    __shared__ uint16_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 256];
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
     for (int i = threadIdx.x; i < kTokens * r.pairs; i += kThreads) {
         const int tt = i / r.pairs, p = i - tt * r.pairs;
@@ -52,17 +50,13 @@ __global__ void __launch_bounds__(kThreads)
     const int sub = lane / per_head, c0 = (lane - sub * per_head) * 8;
     const bool live = sub < per_warp;
 
+    const RopeLane<kLayout> of(r, c0, live ? sub * per_head : 0);   // (lanes without a head stay within the buffer)
     float cosv[8], ss[8];
-    uint32_t turned = 0;      // channels that turn
-    int from[8];              // halves: where the partner stands in the warp's buffer
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const RopeChannel ch = rope_channel(r, c0 + e);
-        const float2 v = ch.pair >= 0 && live ? cs[tt][ch.pair] : make_float2(1.0f, 0.0f);
+        const float2 v = live ? cs[tt][of.pair[e]] : make_float2(1.0f, 0.0f);
         cosv[e] = v.x;
-        ss[e] = ch.first ? -v.y : v.y;
-        turned |= ch.pair >= 0 ? 1u << e : 0u;
-        from[e] = (ch.partner & 7) * 32 + sub * per_head + (ch.partner >> 3);
+        ss[e] = (of.first >> e) & 1u ? -v.y : v.y;
     }
     const int begin = blockIdx.y * heads_per_cta, end = min(heads, begin + heads_per_cta);
     const int step = kWarpsPerToken * per_warp;
@@ -85,24 +79,10 @@ __global__ void __launch_bounds__(kThreads)
                 v[2 * i] = bf_lo(w[i]);
                 v[2 * i + 1] = bf_hi(w[i]);
             }
-            if constexpr (kLayout == 0) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    partner[e] = v[e ^ 1];
-            } else {
-                uint16_t *buf = &swap[warp][0][0];
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    buf[e * 32 + lane] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    partner[e] = __uint_as_float(static_cast<uint32_t>(live ? buf[from[e]] : 0) << 16);
-            }
+            rope_partners(of, w, swap[kLayout == 0 ? 0 : warp], partner);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                y[e] = (turned >> e) & 1u ? rope_mix(v[e], partner[e], cosv[e], ss[e]) : v[e];
+                y[e] = (of.turned >> e) & 1u ? rope_mix(v[e], partner[e], cosv[e], ss[e]) : v[e];
             if (live && h < end)
                 *reinterpret_cast<uint4 *>(op + h * oh) =
                     make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));

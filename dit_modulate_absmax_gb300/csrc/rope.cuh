@@ -78,4 +78,50 @@ __device__ __forceinline__ float rope_mix(float x, float partner, float cosv, fl
     return __fmaf_rn(x, cosv, __fmul_rn(partner, ss));
 }
 
+// A lane's eight channels c0 .. c0 + 7 of a head whose lanes are neighbours:
+// which of them turn, which are a pair's first member, the pair of each, and
+// (halves) where the partner stands in the warp's exchange buffer.
+template <int kLayout>
+struct RopeLane {
+    uint32_t turned, first;
+    int16_t pair[8], from[8];
+
+    __device__ __forceinline__ RopeLane(const RopeArgs &r, int c0, int first_lane)
+    {
+        turned = first = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const RopeChannel ch = rope_channel(r, c0 + e);
+            turned |= ch.pair >= 0 ? 1u << e : 0u;
+            first |= ch.first ? 1u << e : 0u;
+            pair[e] = static_cast<int16_t>(max(ch.pair, 0));
+            from[e] = static_cast<int16_t>((ch.partner & 7) * 32 + first_lane + (ch.partner >> 3));
+        }
+    }
+};
+
+// The partners of a lane's eight bf16 values (words w).  Interleaved pairs lie
+// within the lane; halves meet in `swap`, 256 words of 16 bits of the warp's
+// own: member e of each lane's eight side by side, so that partners are read
+// without bank conflicts.  Whole warp.
+template <int kLayout>
+__device__ __forceinline__ void rope_partners(const RopeLane<kLayout> &l, const uint32_t (&w)[4], uint16_t *swap, float (&partner)[8])
+{
+    if constexpr (kLayout == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            partner[e ^ 1] = __uint_as_float((e & 1) != 0 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    } else {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            swap[e * 32 + lane] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            partner[e] = __uint_as_float(static_cast<uint32_t>(swap[l.from[e]]) << 16);
+    }
+}
+
 }  // namespace h3fp4
