@@ -36,7 +36,7 @@ constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups, for the register split; two warps idle
 // Registers per thread of the three kinds of warpgroup, out of the 128 that 512 threads launch with (run_tile checks):
 // a softmax thread holds its row's 128 scores.
-constexpr int kSoftmaxRegs = 176, kConvertRegs = 120, kMmaRegs = 40;
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 112, kMmaRegs = 32;
 constexpr int kSplitRegs = 2 * kSoftmaxRegs + kConvertRegs + kMmaRegs;
 static_assert(kSplitRegs <= 4 * 128, "the launch's registers cover the split");
 constexpr int kStages = 2;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float2 p = row_power(max(m2 & 0xFFFFu, m2 >> 16));
                 const float f = a.scale < 0.0f ? -p.x : p.x;
-                c_row = fabsf(a.scale) * kLog2e * p.y;
+                c_row = fmaxf(fabsf(a.scale) * kLog2e * p.y, 1e-30f);   // never 0: a hidden key's -infinity stays one
 #pragma unroll
                 for (int i = 0; i < kDim / 8; ++i)
                     st_shared_v4(smem_u32(sm.q[t]) + operand_at(in_tile, i), bf16x2_to_half2(w[i].x, f), bf16x2_to_half2(w[i].y, f),
@@ -226,35 +226,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
                 const int lo = see.lo - k0, hi = see.hi - k0;
-                float v[128], top = -INFINITY;
-                if (!edge) {
-                    tmem_ld_32x32b_x64(sc, v);
-                    tmem_ld_32x32b_x64(sc + 64, v + 64);
-                    tmem_ld_wait_x64(v);
-                    tmem_ld_wait_x64(v + 64);
-#pragma unroll
-                    for (int n = 0; n < kKeys / kGroup; ++n) {
-                        const PageEntry e = pe[(kGroup * n) >> shift];
-                        const float *x = v + kGroup * n;
-                        float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
-#pragma unroll
-                        for (int i = 6; i + 3 < kGroup; i += 4) {
-                            g0 = max3(g0, x[i], x[i + 1]);
-                            g1 = max3(g1, x[i + 2], x[i + 3]);
-                        }
-                        top = fmaxf(top, fmaf(max3(g0, g1, fmaxf(x[kGroup - 2], x[kGroup - 1])), c_row * e.ks, e.lv));
-                    }
-                } else {   // some rows do not see some keys; short code, scores read from TMEM again below
+                // A step in which some rows do not see some keys: minus infinity goes over those scores in TMEM, so that
+                // the straight code below is the same for all steps (masking its registers there, under a branch, made
+                // every step 13 % slower).
+                if (edge) {
 #pragma unroll 1
-                    for (int n = 0; n < 8; ++n) {
-                        const PageEntry e = pe[(16 * n) >> shift];
+                    for (int n = 0; n < kKeys / 16; ++n) {
                         uint32_t x[16];
                         tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (16 * n + i >= lo && 16 * n + i < hi)
-                                top = fmaxf(top, fmaf(__uint_as_float(x[i]), c_row * e.ks, e.lv));
+                            x[i] = 16 * n + i >= lo && 16 * n + i < hi ? x[i] : 0xFF800000u;
+                        tmem_st_32x32b_x16(sc + 16 * n, x);
                     }
+                    tmem_st_wait();
+                }
+                float v[128], top = -INFINITY;
+                tmem_ld_32x32b_x64(sc, v);
+                tmem_ld_32x32b_x64(sc + 64, v + 64);
+                tmem_ld_wait_x64(v);
+                tmem_ld_wait_x64(v + 64);
+#pragma unroll
+                for (int n = 0; n < kKeys / kGroup; ++n) {
+                    const PageEntry e = pe[(kGroup * n) >> shift];
+                    const float *x = v + kGroup * n;
+                    float g0 = max3(x[0], x[1], x[2]), g1 = max3(x[3], x[4], x[5]);
+#pragma unroll
+                    for (int i = 6; i + 3 < kGroup; i += 4) {
+                        g0 = max3(g0, x[i], x[i + 1]);
+                        g1 = max3(g1, x[i + 2], x[i + 3]);
+                    }
+                    top = fmaxf(top, fmaf(max3(g0, g1, fmaxf(x[kGroup - 2], x[kGroup - 1])), c_row * e.ks, e.lv));
                 }
                 const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -277,10 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float at = ref == -INFINITY ? 0.0f : ref;
                 // The exponent is one fused multiply-add.  For a row past 2^20 the reference's own rounding would show in
                 // it (and could reach FP16's limit): there the score is rounded first, so that the largest one meets its
-                // own copy in the reference.  Steps at an edge or with such a row take a short loop instead of the long
-                // straight code, with the same operations in the same order for every other row, so that a row's bits
-                // do not depend on its neighbours.
-                const bool far = fabsf(at) > 0x1p20f, plain = !edge && !__any_sync(0xFFFFFFFFu, far);
+                // own copy in the reference.  A step with such a row takes a short loop instead of the long straight
+                // code, with the same operations in the same order for every other row, so that a row's bits do not
+                // depend on its neighbours.
+                const bool far = fabsf(at) > 0x1p20f, plain = !__any_sync(0xFFFFFFFFu, far);
                 if (!plain) {
                     float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
 #pragma unroll 1

@@ -11,7 +11,7 @@
 // Writing moves 3 bytes a value and reading 3, both bound by HBM.  A CTA of
 // the writer holds a head's new keys and values of its page in registers
 // between the maximum and the encoding, so that each is read once, and goes on
-// to its next head with one barrier between; the cosines and sines of its
+// to the next with one barrier between, its loads under way meanwhile; the cosines and sines of its
 // tokens serve all its heads.
 #include <type_traits>
 
@@ -23,8 +23,9 @@ namespace {
 
 __device__ uint32_t g_error;
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024;
 constexpr int kReadThreads = 256;
+constexpr int kReadTurns = 4;             // chunks of keys and of values in flight per thread
 constexpr int kScaleExpMin = -40, kScaleExpMax = 119;
 
 __device__ __forceinline__ uint32_t bf_pack(float lo, float hi)
@@ -82,25 +83,31 @@ __device__ __forceinline__ float over(float x, const Divisor &d)
     return d.pow2 ? __fmul_rn(x, d.inv) : __fdiv_rn(x, d.scale);
 }
 
-__device__ __forceinline__ uint32_t encode2(uint32_t w, const Divisor &d)
+// Codes of eight values under a power-of-two scale, its inverse given.
+__device__ __forceinline__ uint2 encode8_pow2(const uint4 &v, float inv)
 {
-    return floats_to_e4m3x2(over(bf_lo(w), d), over(bf_hi(w), d));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = __fmul2_rn(make_float2(bf_lo(w[i]), bf_hi(w[i])), make_float2(inv, inv));
+        c[i] = floats_to_e4m3x2(q.x, q.y);
+    }
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
-__device__ __forceinline__ uint2 encode8(const uint4 &v, const Divisor &d, bool all_finite)
+// ... under any scale, with values that may not be finite: infinities would
+// saturate, they become NaN like NaNs.
+__device__ __noinline__ uint2 encode8_any(uint4 v, Divisor d)
 {
-    uint32_t lo = encode2(v.x, d) | encode2(v.y, d) << 16, hi = encode2(v.z, d) | encode2(v.w, d) << 16;
-    if (!all_finite) {   // infinities would saturate: they become NaN like NaNs
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (((w[i >> 1] >> (16 * (i & 1))) & 0x7F80u) == 0x7F80u) {
-                uint32_t &o = i < 4 ? lo : hi;
-                o = (o & ~(0xFFu << (8 * (i & 3)))) | 0x7Fu << (8 * (i & 3));
-            }
-        }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[2] = {0, 0};
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t x = w[i >> 1] >> (16 * (i & 1)) & 0xFFFFu;
+        const uint32_t c = (x & 0x7F80u) == 0x7F80u ? 0x7Fu : floats_to_e4m3x2(over(__uint_as_float(x << 16), d), 0.0f) & 0xFFu;
+        o[i >> 2] |= c << (8 * (i & 3));
     }
-    return make_uint2(lo, hi);
+    return make_uint2(o[0], o[1]);
 }
 
 __device__ __forceinline__ uint32_t reencode4(uint32_t c, float was, const Divisor &d)
@@ -126,7 +133,7 @@ template <int kPer, int kRope>
 __global__ void __launch_bounds__(kMaxThreads) write_kernel(WriteArgs a, int heads_per_cta)
 {
     extern __shared__ __align__(16) float2 cs[];                              // [page][dim / 2], with a rotation
-    __shared__ uint32_t warp_max[2][2][kMaxThreads / 32];
+    __shared__ uint32_t warp_max[2][kMaxThreads / 32];
     __shared__ uint16_t swap[kRope == 2 ? kMaxThreads / 32 : 1][kRope == 2 ? 256 : 1];
     const int b = blockIdx.z, page = a.cache.page_size, dim = a.cache.head_dim, heads = a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
@@ -164,89 +171,93 @@ __global__ void __launch_bounds__(kMaxThreads) write_kernel(WriteArgs a, int hea
     };
     uint4 x[2][kPer];
     load(0, h0, x[0]);
-    load(1, h0, x[1]);
     if constexpr (kRope != 0) {
+        __shared__ float2 turns[64];   // FP64 is slow here: once a pair, not once a pair and token
+        for (int p = threadIdx.x; p < a.rope.pairs; p += blockDim.x)
+            turns[p] = rope_turns(a.rope, p);
+        __syncthreads();
         for (int i = threadIdx.x; i < page * (dim / 2); i += blockDim.x) {
             const int t = i / (dim / 2), p = i - t * (dim / 2);
             if (t >= lo && t < hi && p < a.rope.pairs) {
                 const float pos = a.rope.positions[(row0 + t) * a.rope.ld_positions + rope_axis(a.rope, p)];
-                cs[i] = rope_cos_sin(a.rope.inverse ? -pos : pos, rope_turns(a.rope, p));
+                cs[i] = rope_cos_sin(a.rope.inverse ? -pos : pos, turns[p]);
             }
         }
         __syncthreads();
     }
     const RopeLane<kRope == 2 ? 1 : 0> lane_of(a.rope, c0, (threadIdx.x & 31) / per_row * per_row);
 
-    for (int h = h0; h < h_end; ++h) {
-        if (h > h0) {
-            load(0, h, x[0]);
-            load(1, h, x[1]);
-        }
+    // One of a head's two blocks, whose values are in registers.
+    const auto block_of = [&](auto kv_constant, int h) {
+        constexpr int kKv = decltype(kv_constant)::value;
         const int64_t bh = static_cast<int64_t>(id) * heads + h;
-        float was[2] = {0.0f, 0.0f};
-        if (lo > 0) {
-            was[0] = a.cache.k_scale[bh];
-            was[1] = a.cache.v_scale[bh];
-        }
-        if constexpr (kRope != 0) {
+        float *const scale_at = (kKv == 0 ? a.cache.k_scale : a.cache.v_scale) + bh;
+        const float was = lo > 0 ? *scale_at : 0.0f;
+        if constexpr (kRope != 0 && kKv == 0) {
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
                 const int t = t0 + u * t_step;
                 uint32_t w[4] = {x[0][u].x, x[0][u].y, x[0][u].z, x[0][u].w};
                 float partner[8];
                 rope_partners(lane_of, w, swap[kRope == 2 ? threadIdx.x >> 5 : 0], partner);
-                if (t >= lo && t < hi) {
-                    const float2 *f = cs + t * (dim / 2);
-                    float y[8];
+                if (t < lo || t >= hi)
+                    continue;
+                const float2 *f = cs + t * (dim / 2);
+                float y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float own = (e & 1) != 0 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
-                        const float2 v = f[kRope == 1 ? (c0 + e) >> 1 : lane_of.pair[e]];
-                        y[e] = (lane_of.turned >> e) & 1u ? rope_mix(own, partner[e], v.x, (lane_of.first >> e) & 1u ? -v.y : v.y) : own;
-                    }
-                    x[0][u] = make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
+                for (int e = 0; e < 8; ++e) {
+                    const float2 v = f[kRope == 1 ? (c0 + e) >> 1 : lane_of.pair[e]];
+                    const bool first = kRope == 1 ? (e & 1) == 0 : (lane_of.first >> e & 1u) != 0;
+                    y[e] = rope_mix((e & 1) != 0 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]), partner[e], v.x, first ? -v.y : v.y);
                 }
+                if (lane_of.turned != 0xFFu)   // channels past the axes
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if ((lane_of.turned >> e & 1u) == 0)
+                            y[e] = (e & 1) != 0 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+                x[0][u] = make_uint4(bf_pack(y[0], y[1]), bf_pack(y[2], y[3]), bf_pack(y[4], y[5]), bf_pack(y[6], y[7]));
             }
         }
-        uint32_t m[2] = {0, 0}, odd[2] = {0, 0};   // maxima; chunks with a value that is not finite
+        uint32_t m = 0, odd = 0;   // maximum; chunks with a value that is not finite
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const uint32_t f = finite_absmax8(x[kv][u]);
-                odd[kv] |= (f >> 16) << u;
-                m[kv] = max(m[kv], f & 0xFFFFu);
-            }
-            m[kv] = __reduce_max_sync(0xFFFFFFFFu, m[kv]);
-            if ((threadIdx.x & 31) == 0)
-                warp_max[h & 1][kv][threadIdx.x >> 5] = m[kv];
+        for (int u = 0; u < kPer; ++u) {
+            const uint32_t f = finite_absmax8(x[kKv][u]);
+            odd |= (f >> 16) << u;
+            m = max(m, f & 0xFFFFu);
         }
-        __syncthreads();   // and the old scales are read; the next head uses the other half of warp_max
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if ((threadIdx.x & 31) == 0)
+            warp_max[kKv][threadIdx.x >> 5] = m;
+        __syncthreads();   // and the old scale is read; the next block uses the other half of warp_max
+        m = 0;
+        for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w)
+            m = max(m, warp_max[kKv][w]);
+        float scale = block_scale_of(m);
+        if (lo > 0)
+            scale = fmaxf(scale, was);
+        const Divisor d = divisor(scale);
+        if (threadIdx.x == 0)
+            *scale_at = scale;
+        const bool grown = lo > 0 && scale != was;
+        uint2 *codes = reinterpret_cast<uint2 *>((kKv == 0 ? a.cache.k_codes : a.cache.v_codes) + bh * page * dim) + threadIdx.x;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            m[kv] = 0;
-            for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w)
-                m[kv] = max(m[kv], warp_max[h & 1][kv][w]);
-            float scale = block_scale_of(m[kv]);
-            if (lo > 0)
-                scale = fmaxf(scale, was[kv]);
-            const Divisor d = divisor(scale);
-            if (threadIdx.x == 0)
-                (kv == 0 ? a.cache.k_scale : a.cache.v_scale)[bh] = scale;
-            const bool grown = lo > 0 && scale != was[kv];
-            uint2 *codes = reinterpret_cast<uint2 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + bh * page * dim) + threadIdx.x;
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const int t = t0 + u * t_step;
-                uint2 *dst = codes + u * blockDim.x;
-                if (t >= lo && t < hi) {
-                    *dst = encode8(x[kv][u], d, ((odd[kv] >> u) & 1u) == 0);
-                } else if (t < lo && grown) {
-                    const uint2 c = *dst;
-                    *dst = make_uint2(reencode4(c.x, was[kv], d), reencode4(c.y, was[kv], d));
-                }
+        for (int u = 0; u < kPer; ++u) {
+            const int t = t0 + u * t_step;
+            uint2 *dst = codes + u * blockDim.x;
+            if (t >= lo && t < hi) {
+                *dst = d.pow2 && ((odd >> u) & 1u) == 0 ? encode8_pow2(x[kKv][u], d.inv) : encode8_any(x[kKv][u], d);
+            } else if (t < lo && grown) {
+                const uint2 c = *dst;
+                *dst = make_uint2(reencode4(c.x, was, d), reencode4(c.y, was, d));
             }
         }
+    };
+    for (int h = h0; h < h_end; ++h) {   // one block's loads are on their way while the other is encoded
+        load(1, h, x[1]);
+        block_of(std::integral_constant<int, 0>{}, h);
+        if (h + 1 < h_end)
+            load(0, h + 1, x[0]);
+        block_of(std::integral_constant<int, 1>{}, h);
     }
 }
 
@@ -265,8 +276,9 @@ __device__ __forceinline__ uint32_t decode2(uint32_t c, float scale)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// One CTA: a page of every head in [blockIdx.x * heads_per_cta, ...), 16 codes a
-// thread and turn, keys and values in flight together.
+// One CTA: a page of every head in [blockIdx.x * heads_per_cta, ...), 8 codes a
+// thread and turn (16-byte stores side by side: 16 codes a thread, whose two
+// stores leave gaps for each other, took 10 % longer), several in flight.
 __global__ void __launch_bounds__(kReadThreads) read_kernel(ReadArgs a, int heads_per_cta)
 {
     const int b = blockIdx.z, page = a.cache.page_size, dim = a.cache.head_dim, heads = a.cache.heads;
@@ -288,31 +300,43 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(ReadArgs a, int head
     }
     const int lo = static_cast<int>(s.len > p0 ? s.len - p0 : 0);
     const int hi = static_cast<int>(last - p0 < page ? last - p0 : page);
-    const int per_row = dim >> 4, h0 = blockIdx.x * heads_per_cta, h_end = min(heads, h0 + heads_per_cta);
+    const int per_row = dim >> 3, h0 = blockIdx.x * heads_per_cta, h_end = min(heads, h0 + heads_per_cta);
     const int64_t row0 = s.row + p0 - s.len;
-    const int per_head = (hi - lo) * per_row, n = (h_end - h0) * per_head;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int dh = i / per_head, j = i - dh * per_head, t = lo + j / per_row, c = j % per_row * 16;
-        const int64_t bh = static_cast<int64_t>(id) * heads + h0 + dh, at = (bh * page + t) * dim + c;
-        uint4 q[2];
-        float scale[2];
+    const int n = (hi - lo) * per_row;
+    for (int h = h0; h < h_end; ++h) {
+        const int64_t bh = static_cast<int64_t>(id) * heads + h;
+        const float scale[2] = {a.x[0] != nullptr ? a.cache.k_scale[bh] : 0.0f, a.x[1] != nullptr ? a.cache.v_scale[bh] : 0.0f};
+        const int64_t at = (bh * page + lo) * dim;
+        for (int i0 = threadIdx.x; i0 < n; i0 += kReadTurns * blockDim.x) {
+            uint2 q[kReadTurns][2];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-            if (a.x[kv] != nullptr) {
-                q[kv] = *reinterpret_cast<const uint4 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + at);
-                scale[kv] = (kv == 0 ? a.cache.k_scale : a.cache.v_scale)[bh];
+            for (int u = 0; u < kReadTurns; ++u) {
+                const int i = i0 + u * blockDim.x;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv)
+                    if (i < n && a.x[kv] != nullptr)
+                        q[u][kv] = *reinterpret_cast<const uint2 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + at + 8 * i);
             }
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-            if (a.x[kv] != nullptr) {
-                uint4 *x = reinterpret_cast<uint4 *>(a.x[kv] + (row0 + t) * a.token_stride[kv] + (h0 + dh) * a.head_stride[kv] + c);
-                const uint4 v = q[kv];
-                const float f = scale[kv];
-                x[0] = make_uint4(decode2(v.x & 0xFFFFu, f), decode2(v.x >> 16, f), decode2(v.y & 0xFFFFu, f), decode2(v.y >> 16, f));
-                x[1] = make_uint4(decode2(v.z & 0xFFFFu, f), decode2(v.z >> 16, f), decode2(v.w & 0xFFFFu, f), decode2(v.w >> 16, f));
+            for (int u = 0; u < kReadTurns; ++u) {
+                const int i = i0 + u * blockDim.x, t = lo + i / per_row, c = i % per_row * 8;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv)
+                    if (i < n && a.x[kv] != nullptr) {
+                        const uint2 v = q[u][kv];
+                        const float f = scale[kv];
+                        *reinterpret_cast<uint4 *>(a.x[kv] + (row0 + t) * a.token_stride[kv] + h * a.head_stride[kv] + c) =
+                            make_uint4(decode2(v.x & 0xFFFFu, f), decode2(v.x >> 16, f), decode2(v.y & 0xFFFFu, f), decode2(v.y >> 16, f));
+                    }
             }
+        }
     }
 }
+
+template <auto kKernel>
+struct kernel_constant {
+    static constexpr auto value = kKernel;
+};
 
 // Heads that a CTA takes one after another: enough CTAs to give each SM
 // `per_sm`, at most `most` heads.
@@ -330,30 +354,35 @@ cudaError_t launch_kv_write(const KvCache &cache, const KvBatch &batch, const ui
 {
     WriteArgs a{cache, batch, {k, v}, {kt, vt}, {kh, vh}, tokens, rope};
     const int chunks = cache.page_size * cache.head_dim / 8;
-    const int threads = chunks < 256 ? chunks : chunks == 2048 ? 512 : 256;
+    // A rotation needs registers of its own: two chunks of keys and of values a thread at most, else four (5,042 tokens of
+    // 56 heads of 128, pages of 64: 78 us turned with two chunks, 84 with four; plain 54 and 46).
+    const int per = rope.pairs > 0 ? 2 : 4;
+    const int threads = chunks < 256 ? chunks : chunks / per < 256 ? 256 : chunks / per;
     const unsigned blocks = static_cast<unsigned>((batch.max_tokens + cache.page_size - 2) / cache.page_size + 1);
-    const int heads_per_cta = heads_each(cache, batch, blocks, 4, 8);
+    const int heads_per_cta = rope.pairs > 0 ? heads_each(cache, batch, blocks, 4, 6) : heads_each(cache, batch, blocks, 8, 4);
     const dim3 grid(static_cast<unsigned>((cache.heads + heads_per_cta - 1) / heads_per_cta), blocks,
                     static_cast<unsigned>(batch.batch));
     const int smem = rope.pairs > 0 ? cache.page_size * cache.head_dim / 2 * static_cast<int>(sizeof(float2)) : 0;
-    const auto run = [&](auto per) {
-        constexpr int kPer = decltype(per)::value;
-        cudaError_t e = cudaSuccess;
-        if (rope.pairs == 0) {
-            write_kernel<kPer, 0><<<grid, threads, 0, st>>>(a, heads_per_cta);
-        } else if (rope.layout == 0) {
-            if ((e = allow_shared<write_kernel<kPer, 1>>(64 * 1024)) == cudaSuccess)
-                write_kernel<kPer, 1><<<grid, threads, smem, st>>>(a, heads_per_cta);
-        } else if ((e = allow_shared<write_kernel<kPer, 2>>(64 * 1024)) == cudaSuccess) {
-            write_kernel<kPer, 2><<<grid, threads, smem, st>>>(a, heads_per_cta);
-        }
+    const auto turned = [&](auto kernel_of) {
+        constexpr auto kernel = decltype(kernel_of)::value;
+        const cudaError_t e = allow_shared<kernel>(64 * 1024);
+        if (e == cudaSuccess)
+            kernel<<<grid, threads, smem, st>>>(a, heads_per_cta);
         return e != cudaSuccess ? e : cudaGetLastError();
     };
-    switch (chunks / threads) {
-    case 1: return run(std::integral_constant<int, 1>{});
-    case 2: return run(std::integral_constant<int, 2>{});
-    default: return run(std::integral_constant<int, 4>{});
+    const int each = chunks / threads;
+    if (rope.pairs == 0) {
+        if (each == 1)
+            write_kernel<1, 0><<<grid, threads, 0, st>>>(a, heads_per_cta);
+        else if (each == 2)
+            write_kernel<2, 0><<<grid, threads, 0, st>>>(a, heads_per_cta);
+        else
+            write_kernel<4, 0><<<grid, threads, 0, st>>>(a, heads_per_cta);
+        return cudaGetLastError();
     }
+    if (rope.layout == 0)
+        return each == 1 ? turned(kernel_constant<write_kernel<1, 1>>{}) : turned(kernel_constant<write_kernel<2, 1>>{});
+    return each == 1 ? turned(kernel_constant<write_kernel<1, 2>>{}) : turned(kernel_constant<write_kernel<2, 2>>{});
 }
 
 cudaError_t launch_kv_read(const KvCache &cache, const KvBatch &batch, uint16_t *k, int64_t kt, int64_t kh,
@@ -361,7 +390,7 @@ cudaError_t launch_kv_read(const KvCache &cache, const KvBatch &batch, uint16_t 
 {
     ReadArgs a{cache, batch, {k, v}, {kt, vt}, {kh, vh}, tokens};
     const unsigned blocks = static_cast<unsigned>((batch.max_tokens + cache.page_size - 2) / cache.page_size + 1);
-    const int heads_per_cta = heads_each(cache, batch, blocks, 16, 4);
+    const int heads_per_cta = 1;
     const dim3 grid(static_cast<unsigned>((cache.heads + heads_per_cta - 1) / heads_per_cta), blocks,
                     static_cast<unsigned>(batch.batch));
     read_kernel<<<grid, kReadThreads, 0, st>>>(a, heads_per_cta);

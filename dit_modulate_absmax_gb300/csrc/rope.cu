@@ -32,12 +32,16 @@ __global__ void __launch_bounds__(kThreads)
 {
     __shared__ float2 cs[kTokens][kRopeMaxPairs];
     __shared__ uint16_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 256];
+    __shared__ float2 turns[kRopeMaxPairs];   // FP64 is slow here: once a pair, not once a pair and token
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+    for (int p = threadIdx.x; p < r.pairs; p += kThreads)
+        turns[p] = rope_turns(r, p);
+    __syncthreads();
     for (int i = threadIdx.x; i < kTokens * r.pairs; i += kThreads) {
         const int tt = i / r.pairs, p = i - tt * r.pairs;
         if (t0 + tt < tokens) {
             const float pos = r.positions[(t0 + tt) * r.ld_positions + rope_axis(r, p)];
-            cs[tt][p] = rope_cos_sin(r.inverse ? -pos : pos, rope_turns(r, p));
+            cs[tt][p] = rope_cos_sin(r.inverse ? -pos : pos, turns[p]);
         }
     }
     __syncthreads();
