@@ -2,8 +2,8 @@
 // rows against a part of the keys, joined afterwards where there are several
 // parts.
 //
-// Reads every visible code once (2 * dim bytes a token and cache head) for at
-// most 16 rows, so it is bound by HBM.  What it takes to stay there:
+// Reads every visible code once (2 * dim bytes a token and cache head) for each
+// 16 rows, of which there are 32 at most, so it is bound by HBM.  What it takes to stay there:
 //  - The keys are spread evenly over as many CTAs as fit; each of a CTA's 4
 //    warps runs its own online softmax over units of 32 tokens, fed by its own
 //    ring of TMA copies (one lane issues two a unit), with no barrier between
