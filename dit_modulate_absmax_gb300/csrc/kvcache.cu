@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kMaxThreads) write_kernel(WriteArgs a, int hea
 {
     extern __shared__ __align__(16) float2 cs[];                              // [page][dim / 2], with a rotation
     __shared__ uint32_t warp_max[2][kMaxThreads / 32];
-    __shared__ uint16_t swap[kRope == 2 ? kMaxThreads / 32 : 1][kRope == 2 ? 256 : 1];
+    __shared__ uint32_t swap[kRope == 2 ? kMaxThreads / 32 : 1][kRope == 2 ? 128 : 1];
     const int b = blockIdx.z, page = a.cache.page_size, dim = a.cache.head_dim, heads = a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
     // positions in 64 bits: lengths near 2^31 must not wrap

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kThreads)
                 int heads, int dim, int heads_per_cta, RopeArgs r)
 {
     __shared__ float2 cs[kTokens][kRopeMaxPairs];
-    __shared__ uint16_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 256];
+    __shared__ uint32_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 128];
     __shared__ float2 turns[kRopeMaxPairs];   // FP64 is slow here: once a pair, not once a pair and token
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
     for (int p = threadIdx.x; p < r.pairs; p += kThreads)
