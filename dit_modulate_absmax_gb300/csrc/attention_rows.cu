@@ -17,6 +17,9 @@
 //    permutes.  S's accumulator layout is that product's B operand.
 //  - The copies XOR-swizzle rows in 16-byte pieces (dim 128: no bank conflicts;
 //    dim 64: two-way for the values).
+// Measured: one sequence of 262,143 keys, 8 cache heads of 128 channels, 97 us
+// (5.6 TB/s; 1,048,576 keys 6.6 TB/s), 32 ragged ones of up to 8,190 keys 73 us
+// (4.7 TB/s): beyond the copying, a CTA's start and the join's launch.
 // The tensor work is small next to the memory's (24 instructions per 4 KB of
 // codes at dim 128 and 8 rows), so the older warp-level instruction serves; a
 // 128-row tcgen05 tile would be 8-16 times padding.

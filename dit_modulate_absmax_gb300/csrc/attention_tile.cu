@@ -1,9 +1,9 @@
 // attention_tile.cu -- attention of many queries: two tiles of 128 rows per
 // CTA against tiles of 128 keys, both products on the tcgen05 tensor cores.
 //
-// The work is 4 * dim FLOP a visible pair and row; the bound is the FP16
-// tensor rate (bf16's: 2.1 MFLOP-pairs, 512 SM cycles, a 128 x 128 x 128
-// product) next to the exponentials and shared memory.  The parts:
+// The work is 4 * dim FLOP a visible pair and row; the floor is the FP16 tensor
+// rate (4 x 512 SM cycles a step of 256 rows and 128 keys at dim 128).  The
+// parts:
 //  - 8 softmax warps, a thread a row: S from TMEM (tcgen05.ld), one pass for
 //    the maximum and one for the weights, which go back to TMEM as FP16 over
 //    S's own columns, the A operand of the second product.  The two row tiles
@@ -19,6 +19,16 @@
 //  - 2 warps issue the MMAs, one for each row tile.
 // Shared memory at dim 128: queries 64 KB, two stages of keys and of values 32
 // KB each.
+//
+// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.04
+// to 5.09 ms, 1.07 to 1.08 PFLOP/s, about 4,100 cycles a step.  No pipe is full
+// (tensor 50 %, exponentials 20 %, issue 46 %, shared memory 30 %), and leaving
+// out any one part of the arithmetic but the exponentials changes nothing: what
+// is left is the length of a tile's chain -- scores, softmax, weights, product,
+// the next scores -- with two tiles, all that TMEM has room for, in turn.
+// Tried and slower: half steps of 64 keys with two score buffers (5.65 ms), the
+// next scores' first half issued while the softmax works (4 %), two threads a
+// row (8.2 ms), a quarter of the exponentials as polynomials (16 %).
 #include "attention.cuh"
 #include "ptx.cuh"
 

@@ -409,7 +409,7 @@ H3FP4_API h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3
  *   heads             a multiple of the cache's heads, at most 65535
  *   max_kv            the most keys that any sequence has (sizes the launch; longer ones are
  *                     reported as out of range); at most 2^30
- *   softmax_scale     finite; scales of the cache's pages must be positive and finite
+ *   softmax_scale     finite; scales of the cache's pages lie in [2^-60, 2^120] (those that a write sets do)
  *   workspace         h3fp4_kv_attention_workspace bytes of device scratch, 16-byte aligned (contents on
  *                     entry are ignored; two calls that overlap on the GPU must not share it); may be NULL
  *                     where that is 0
