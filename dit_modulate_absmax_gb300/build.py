@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libh3fp4.so")
 SOURCES = ["api.cu", "producer.cu", "gemm.cu", "noalloc.cu", "rope.cu", "kvcache.cu", "attention.cu",
            "attention_rows.cu", "attention_tile.cu"]
-HEADERS = ["ptx.cuh", "launch.h", "rope.cuh", "kvcache.cuh", "attention.cuh"]
+HEADERS = ["ptx.cuh", "launch.h", "rope.cuh", "kvcache.cuh", "attention.cuh", "ptx_attention.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -23,10 +23,14 @@
 // The tensor work is small next to the memory's (24 instructions per 4 KB of
 // codes at dim 128 and 8 rows), so the older warp-level instruction serves; a
 // 128-row tcgen05 tile would be 8-16 times padding.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cstring>
+#include <mutex>
 
 #include "attention.cuh"
-#include "ptx.cuh"
+#include "ptx_attention.cuh"
 
 namespace h3fp4 {
 namespace {
@@ -691,6 +695,30 @@ SplitPlan plan_rows(const AttnShape &s)
 }
 
 namespace {
+
+// Tensor map over a cache's codes [blocks, page_size, head_dim] (a block: a page
+// of one head), boxes of box_tokens tokens, 16-byte pieces swizzled by the
+// 128-byte line (all eight of a line at 128 channels, four of a row at 64).
+bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page_size, int64_t blocks, int box_tokens)
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(head_dim), page = static_cast<cuuint64_t>(page_size);
+    const cuuint64_t dims[3] = {row, page, static_cast<cuuint64_t>(blocks)}, strides[2] = {row, row * page};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(head_dim), static_cast<cuuint32_t>(box_tokens), 1}, step[3] = {1, 1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int kDim, int kRows>
 cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)

@@ -30,7 +30,7 @@
 // next scores' first half issued while the softmax works (4 %), two threads a
 // row (8.2 ms), a quarter of the exponentials as polynomials (16 %).
 #include "attention.cuh"
-#include "ptx.cuh"
+#include "ptx_attention.cuh"
 
 namespace h3fp4 {
 namespace {

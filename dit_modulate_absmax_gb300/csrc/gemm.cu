@@ -1149,19 +1149,6 @@ h3fp4_status launch_gemm_wait_timeout(const uint8_t *a_q, const uint8_t *a_sf, c
     return launch_pair_cp(a_q, a_sf, a_ts, b_q, b_sf, b_ts, c, ldc, m, m_pad, n, k, 0, nullptr, st, wait_ns, 1);
 }
 
-bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page_size, int64_t blocks, int box_tokens)
-{
-    auto fn = encode_fn();
-    if (!fn)
-        return false;
-    const cuuint64_t row = static_cast<cuuint64_t>(head_dim), page = static_cast<cuuint64_t>(page_size);
-    const cuuint64_t dims[3] = {row, page, static_cast<cuuint64_t>(blocks)}, strides[2] = {row, row * page};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(head_dim), static_cast<cuuint32_t>(box_tokens), 1}, step[3] = {1, 1, 1};
-    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(codes), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 h3fp4_status read_device_error(uint32_t *code)
 {
     uint32_t v = 0;

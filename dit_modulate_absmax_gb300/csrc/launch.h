@@ -1,8 +1,6 @@
 // launch.h -- internal launchers behind the C ABI (not exported).
 #pragma once
 
-#include <cuda.h>
-
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -135,11 +133,6 @@ struct AttnShape {
     int64_t tokens;
     int32_t heads, kv_heads, head_dim, batch, max_tokens, max_kv;
 };
-
-// Tensor map over a cache's codes [blocks, page_size, head_dim] (a block: a page
-// of one head), boxes of box_tokens tokens, 16-byte pieces swizzled by the
-// 128-byte line (all eight of a line at 128 channels, four of a row at 64).
-bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page_size, int64_t blocks, int box_tokens);
 
 int64_t attention_workspace(const AttnShape &s);
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st);
