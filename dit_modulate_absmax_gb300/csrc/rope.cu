@@ -101,7 +101,8 @@ cudaError_t launch_rope(const uint16_t *x, int64_t xt, int64_t xh, uint16_t *out
                         int64_t tokens, int heads, int dim, const RopeArgs &r, cudaStream_t st)
 {
     const int64_t groups = (tokens + kTokens - 1) / kTokens;
-    // Few tokens: their heads are spread over several CTAs until every SM has one.
+    // Few tokens: their heads are spread over several CTAs until every SM has one (a token of 112 heads: 3.1 us, 6.2 in one
+    // CTA; 100 tokens 4.1, 6.5).
     const int per_pass = kWarpsPerToken * (32 / (dim / 8));
     int64_t split = (sm_count() + groups - 1) / groups;
     const int64_t most = (heads + per_pass - 1) / per_pass;
