@@ -8,9 +8,9 @@ namespace {
 // Most rows (query tokens times query heads of a cache head) of a sequence
 // that the row kernel takes.  It reads the codes once for 16 rows, the tile
 // kernel once for 256 but with all of a tile's work for one row.  32 rows: 32
-// sequences of up to 8,192 keys, 8 heads, 144 us (tile kernel 254), 131,072
-// keys 116 us (138), 8 of 1,000 keys 12.4 us (15.5), one of 8,192 keys 21.5 us
-// (20.3).  48 rows: 207 us (253), 167 (139), 14.9 (15.7), 27.0 (21.0).
+// sequences of up to 8,192 keys, 8 heads, 144 us (tile kernel 252), 131,072
+// keys 116 us (137), 8 of 1,000 keys 12.3 us (13.1), one of 8,192 keys 21.5 us
+// (20.4).  48 rows: 207 us (253), 167 (138), 14.8 (13.4), 27.0 (21.1).
 constexpr int64_t kMostRows = 32;
 
 bool few_rows(const AttnShape &s) { return static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads) <= kMostRows; }
