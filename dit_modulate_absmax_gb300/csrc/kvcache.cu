@@ -294,11 +294,13 @@ __device__ __forceinline__ uint32_t decode2(uint32_t c, float scale)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// One CTA: a page and a head, 8 codes a thread and turn (16-byte stores side by
-// side: 16 codes a thread, whose two stores leave gaps for each other, took
-// 10 % longer), several in flight.  Registers for 6 CTAs an SM: 37,810 tokens
-// of 56 heads 240 us (for 5: 243, for 8: 270).
-__global__ void __launch_bounds__(kReadThreads, 6) read_kernel(ReadArgs a)
+// One CTA: a page of a head, or of several where that has fewer codes than a turn
+// of all threads (pages of 16, 64 channels, 51 heads of 31 ragged sequences: 33
+// us, 92 a head each); 8 codes a thread and turn (16-byte stores side by side:
+// 16 codes a thread, whose two stores leave gaps for each other, took 10 %
+// longer), several in flight.  Registers for 5 CTAs an SM: 37,810 tokens of 56
+// heads 240 us (for 4: 249, for 6: 283).
+__global__ void __launch_bounds__(kReadThreads, 5) read_kernel(ReadArgs a, int heads_per_cta)
 {
     const int b = blockIdx.z, page = a.cache.page_size, dim = a.cache.head_dim, heads = a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
@@ -319,30 +321,31 @@ __global__ void __launch_bounds__(kReadThreads, 6) read_kernel(ReadArgs a)
     }
     const int lo = static_cast<int>(s.len > p0 ? s.len - p0 : 0);
     const int hi = static_cast<int>(last - p0 < page ? last - p0 : page);
-    const int per_row = dim >> 3, h = blockIdx.x;
-    const int64_t row0 = s.row + p0 - s.len;
-    const int n = (hi - lo) * per_row;
-    const int64_t bh = static_cast<int64_t>(id) * heads + h;
-    const float scale[2] = {a.x[0] != nullptr ? a.cache.k_scale[bh] : 0.0f, a.x[1] != nullptr ? a.cache.v_scale[bh] : 0.0f};
-    const int64_t at = (bh * page + lo) * dim;
+    const int row_log = dim == 128 ? 4 : 3, head_log = row_log + 31 - __clz(page);   // chunks of a row, of a page and head
+    const int h0 = blockIdx.x * heads_per_cta, n = min(heads_per_cta, heads - h0) << head_log;
+    const int64_t row0 = s.row + p0 - s.len, bh = static_cast<int64_t>(id) * heads + h0, at = bh * page * dim;
     for (int i0 = threadIdx.x; i0 < n; i0 += kReadTurns * blockDim.x) {
         uint2 q[kReadTurns][2];
+        float scale[kReadTurns][2];
 #pragma unroll
         for (int u = 0; u < kReadTurns; ++u) {
-            const int i = i0 + u * blockDim.x;
+            const int i = i0 + u * blockDim.x, t = (i >> row_log) & (page - 1);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv)
-                if (i < n && a.x[kv] != nullptr)
+                if (i < n && t >= lo && t < hi && a.x[kv] != nullptr) {
                     q[u][kv] = *reinterpret_cast<const uint2 *>((kv == 0 ? a.cache.k_codes : a.cache.v_codes) + at + 8 * i);
+                    scale[u][kv] = (kv == 0 ? a.cache.k_scale : a.cache.v_scale)[bh + (i >> head_log)];
+                }
         }
 #pragma unroll
         for (int u = 0; u < kReadTurns; ++u) {
-            const int i = i0 + u * blockDim.x, t = lo + i / per_row, c = i % per_row * 8;
+            const int i = i0 + u * blockDim.x, t = (i >> row_log) & (page - 1), c = (i & ((1 << row_log) - 1)) * 8;
+            const int h = h0 + (i >> head_log);
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv)
-                if (i < n && a.x[kv] != nullptr) {
+                if (i < n && t >= lo && t < hi && a.x[kv] != nullptr) {
                     const uint2 v = q[u][kv];
-                    const float f = scale[kv];
+                    const float f = scale[u][kv];
                     *reinterpret_cast<uint4 *>(a.x[kv] + (row0 + t) * a.token_stride[kv] + h * a.head_stride[kv] + c) =
                         make_uint4(decode2(v.x & 0xFFFFu, f), decode2(v.x >> 16, f), decode2(v.y & 0xFFFFu, f), decode2(v.y >> 16, f));
                 }
@@ -410,8 +413,11 @@ cudaError_t launch_kv_read(const KvCache &cache, const KvBatch &batch, uint16_t 
 {
     ReadArgs a{cache, batch, {k, v}, {kt, vt}, {kh, vh}, tokens};
     const unsigned blocks = static_cast<unsigned>((batch.max_tokens + cache.page_size - 2) / cache.page_size + 1);
-    const dim3 grid(static_cast<unsigned>(cache.heads), blocks, static_cast<unsigned>(batch.batch));
-    read_kernel<<<grid, kReadThreads, 0, st>>>(a);
+    const int block = cache.page_size * cache.head_dim, turn = 8 * kReadThreads * kReadTurns;
+    const int heads_per_cta = block >= turn ? 1 : turn / block < cache.heads ? turn / block : cache.heads;
+    const dim3 grid(static_cast<unsigned>((cache.heads + heads_per_cta - 1) / heads_per_cta), blocks,
+                    static_cast<unsigned>(batch.batch));
+    read_kernel<<<grid, kReadThreads, 0, st>>>(a, heads_per_cta);
     return cudaGetLastError();
 }
 
