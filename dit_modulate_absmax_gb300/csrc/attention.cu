@@ -27,7 +27,8 @@ int64_t attention_workspace(const AttnShape &s)
 
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st)
 {
-    const AttnShape s{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv};
+    const AttnShape s{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv,
+                      a.causal ? a.window : 0};   // (the parts are no more than without: the workspace does for both)
     const SplitPlan plan = plan_of(s);
     float *part = static_cast<float *>(workspace);
     float2 *stat = reinterpret_cast<float2 *>(part + plan.part_rows * s.head_dim);

@@ -748,8 +748,15 @@ SplitPlan plan_tile(const AttnShape &s)
     int64_t splits = ctas > 0 ? sm_count() / ctas : 1;
     const int64_t most = (kv + 255) / 256;
     splits = splits > most ? most : splits < 1 ? 1 : splits;
-    const int64_t chunk = ((kv + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
+    int64_t chunk = ((kv + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
     splits = (kv + chunk - 1) / chunk;
+    // Under a window that lies within a part most parts have nothing to do but to write that down (4,674 tokens of 2 heads,
+    // window 5: 24.2 us in one part, 32.4 in four).
+    const int64_t tokens = kTiles * 128 / (s.heads / s.kv_heads) + 1;   // of a CTA's rows
+    if (s.reach > 0 && s.reach + tokens <= chunk) {
+        splits = 1;
+        chunk = (kv + kKeys - 1) / kKeys * kKeys;
+    }
     return SplitPlan{static_cast<int32_t>(splits), static_cast<int32_t>(chunk), splits > 1 ? s.tokens * s.heads * splits : 0, false};
 }
 

@@ -132,6 +132,7 @@ struct AttnArgs {
 struct AttnShape {
     int64_t tokens;
     int32_t heads, kv_heads, head_dim, batch, max_tokens, max_kv;
+    int32_t reach = 0;   // most keys that a query sees under a causal window; 0: all
 };
 
 int64_t attention_workspace(const AttnShape &s);
