@@ -380,7 +380,11 @@ cudaError_t launch_kv_write(const KvCache &cache, const KvBatch &batch, const ui
     // A rotation needs registers of its own: two chunks of keys and of values a thread at most, else four (5,042 tokens of
     // 56 heads of 128, pages of 64: 72 us turned with two chunks, 71 with four, in halves 98 and 123; plain 54 and 46).
     const int per = rope.pairs > 0 ? 2 : 4;
-    const int threads = chunks < 256 ? chunks : chunks / per < 256 ? 256 : chunks / per;
+    // Fewer threads with more loads each, down to 64, are faster where pages are full of new tokens (5 prompts of 3,001
+    // tokens, 16 heads of 64, from cold caches: 22.5 us, 29.7 with 256 at least), but not where few are (64 single tokens:
+    // 10.2, 8.2).
+    const int least = batch.max_tokens < cache.page_size ? 256 : 64;
+    const int threads = chunks < least ? chunks : chunks / per < least ? least : chunks / per;
     const unsigned blocks = static_cast<unsigned>((batch.max_tokens + cache.page_size - 2) / cache.page_size + 1);
     const int heads_per_cta = heads_each(cache, batch, blocks, rope.pairs > 0 ? 4 : 8, rope.pairs > 0 ? 8 : 4);
     const dim3 grid(static_cast<unsigned>((cache.heads + heads_per_cta - 1) / heads_per_cta), blocks,
