@@ -2,10 +2,10 @@
 //
 // Reads and writes each value once: 4 bytes a channel, bound by HBM (37,810
 // tokens of 112 heads of 128 channels: 328 us, 6.6 TB/s).  A CTA takes 4 tokens
-// and a range of heads.  It first computes the cosines and sines of its tokens'
-// pairs into shared memory (they serve every head), then two warps walk each
-// token's heads, a lane holding 8 channels (16 bytes) and their coefficients in
-// registers.
+// (or 8) and a range of heads.  It first computes the cosines and sines of its
+// tokens' pairs into shared memory (they serve every head), then two warps (or
+// one) walk each token's heads, a lane holding 8 channels (16 bytes) and their
+// coefficients in registers.
 #include <cuda_bf16.h>
 
 #include "rope.cuh"
@@ -14,8 +14,6 @@ namespace h3fp4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;                       // tokens per CTA
-constexpr int kWarpsPerToken = kThreads / 32 / kTokens;
 constexpr int kInFlight = 4;                     // head groups in flight per warp
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -26,11 +24,12 @@ __device__ __forceinline__ uint32_t bf_pack(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <int kLayout>
+template <int kLayout, int kTokens>   // kTokens per CTA
 __global__ void __launch_bounds__(kThreads)
     rope_kernel(const uint16_t *x, int64_t xt, int64_t xh, uint16_t *out, int64_t ot, int64_t oh, int64_t tokens,
                 int heads, int dim, int heads_per_cta, RopeArgs r)
 {
+    constexpr int kWarpsPerToken = kThreads / 32 / kTokens;
     __shared__ float2 cs[kTokens][kRopeMaxPairs];
     __shared__ uint32_t swap[kLayout == 0 ? 1 : kThreads / 32][kLayout == 0 ? 1 : 128];
     __shared__ float2 turns[kRopeMaxPairs];   // FP64 is slow here: once a pair, not once a pair and token
@@ -100,19 +99,21 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_rope(const uint16_t *x, int64_t xt, int64_t xh, uint16_t *out, int64_t ot, int64_t oh,
                         int64_t tokens, int heads, int dim, const RopeArgs &r, cudaStream_t st)
 {
-    const int64_t groups = (tokens + kTokens - 1) / kTokens;
+    // Halves take a warp some time to find its partners, which more tokens' worth of heads pay for: 8 tokens a CTA, a warp
+    // each, once that gives every SM two CTAs (5,042 tokens of 56 heads 31.6 us, 33.4 with 4; 20,000: 100, 115; 500: 7.1,
+    // 6.2; interleaved 29.0, 28.4).
+    const int each = r.layout == 1 && tokens >= 16 * sm_count() ? 8 : 4;
+    const int64_t groups = (tokens + each - 1) / each;
     // Few tokens: their heads are spread over several CTAs until every SM has one (a token of 112 heads: 3.1 us, 6.2 in one
     // CTA; 100 tokens 4.1, 6.5).
-    const int per_pass = kWarpsPerToken * (32 / (dim / 8));
+    const int per_pass = kThreads / 32 / each * (32 / (dim / 8));
     int64_t split = (sm_count() + groups - 1) / groups;
     const int64_t most = (heads + per_pass - 1) / per_pass;
     split = split < 1 ? 1 : split > most ? most : split;
     const int heads_per_cta = static_cast<int>(((heads + split - 1) / split + per_pass - 1) / per_pass) * per_pass;
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>((heads + heads_per_cta - 1) / heads_per_cta));
-    if (r.layout == 0)
-        rope_kernel<0><<<grid, kThreads, 0, st>>>(x, xt, xh, out, ot, oh, tokens, heads, dim, heads_per_cta, r);
-    else
-        rope_kernel<1><<<grid, kThreads, 0, st>>>(x, xt, xh, out, ot, oh, tokens, heads, dim, heads_per_cta, r);
+    const auto kernel = r.layout == 0 ? rope_kernel<0, 4> : each == 4 ? rope_kernel<1, 4> : rope_kernel<1, 8>;
+    kernel<<<grid, kThreads, 0, st>>>(x, xt, xh, out, ot, oh, tokens, heads, dim, heads_per_cta, r);
     return cudaGetLastError();
 }
 

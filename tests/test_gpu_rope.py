@@ -143,3 +143,18 @@ def test_offsets_past_32_bits(h3):
     h3.rope_axes(wide[:, :1], r, out=wide[:, :1])
     want = h3.rope_axes(tail[:, :1], h3.Rope(pos[-5:], r.freqs, dims))
     assert torch.equal(wide[-5:, :1], want) and torch.equal(wide[-5:, 1:], tail[:, 1:])
+
+
+@pytest.mark.parametrize("heads,dim,dims,layout", [(3, 128, (44, 42, 42), "halves"), (1, 80, (20, 30, 30), "halves"), (5, 64, (16, 24, 24), "halves"),
+                                                   (2, 256, (64, 64, 64, 64), "halves"), (3, 128, (32, 48, 48), "interleaved")])
+def test_many_tokens_give_the_bits_of_few(h3, heads, dim, dims, layout):
+    """A long call (5,003 tokens) against the definition, and against its own tokens in calls of a few."""
+    wide, pos = _inputs(5_003, heads, dim, dims, 9, 1)
+    x, freqs = wide[:, 1:], h3.rope_frequencies(dims)
+    y = h3.rope_axes(x, h3.Rope(pos, freqs, dims, layout=layout))
+    xv = O.bf16_values(x.cpu().contiguous().view(torch.int16).numpy().view(np.uint16))
+    ref, mag = O.rope(xv, pos.cpu().numpy(), freqs.cpu().numpy(), dims, layout, False)
+    _check(y, ref, mag)
+    for at, n in ((0, 13), (2_431, 20), (4_996, 7)):
+        part = h3.rope_axes(x[at:at + n], h3.Rope(pos[at:at + n].contiguous(), freqs, dims, layout=layout))
+        assert torch.equal(part.view(torch.int16), y[at:at + n].view(torch.int16))
