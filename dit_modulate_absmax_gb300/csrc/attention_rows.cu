@@ -89,8 +89,9 @@ struct Units {
 template <int kRows>
 __device__ __forceinline__ Units units_of(const AttnArgs &a, const KvSequence &s)
 {
-    if (!s.ok || s.n == 0 || s.len > a.max_kv || (s.len > 0 && (s.len - 1) / a.cache.page_size >= a.batch.ld_table))
-        return Units{0, 0, 0};
+    if (!s.ok || s.n == 0 || s.len > a.max_kv ||
+        (s.len > 0 && ((s.len - 1) / a.cache.page_size >= a.batch.ld_table || a.cache.num_pages == 0)))
+        return Units{0, 0, 0};   // (a cache without pages has no arrays either: nothing of it may be read)
     const Span first = seen_by(a, s, 0), last = seen_by(a, s, s.n - 1);
     const int begin = min(first.lo, last.lo) & ~(kUnit - 1), end = max(first.hi, last.hi);
     constexpr int kTokens = kWarps * kUnit;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         for (int i = 0; i < kStages; ++i)
             mbar_init(smem_u32(&full[warp][i]), 1);
     fence_mbar_init();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && a.cache.num_pages > 0) {   // (without pages there are no maps)
         prefetch_tmap(&k_map);
         prefetch_tmap(&v_map);
     }
@@ -325,9 +326,10 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             if (unit0 + i * kTokens < end)
                 fetch(unit0 + i * kTokens, (stage + i) % kStages);
     for (int i = threadIdx.x; i < pages; i += kThreads) {
-        const int64_t bh = static_cast<int64_t>(max(entry[i].id, 0)) * heads + kh;
-        const float vs = a.cache.v_scale[bh];
-        entry[i].ks = a.cache.k_scale[bh];
+        const int32_t id = entry[i].id;
+        const int64_t bh = static_cast<int64_t>(id) * heads + kh;
+        const float vs = id >= 0 ? a.cache.v_scale[bh] : 1.0f;
+        entry[i].ks = id >= 0 ? a.cache.k_scale[bh] : 1.0f;
         entry[i].lv = lg2(vs);
         entry[i].inv_vs = __frcp_rn(vs);
     }
