@@ -3,7 +3,9 @@
 Python binding of the C-ABI library ``libh3fp4.so`` (see ``include/h3fp4.h``).
 The ``h3fp4_*`` functions mirror the C entry points one to one and take raw
 device pointers (ints); the short-named helpers below them take torch tensors,
-allocate outputs with torch and pass pointers plus torch's current stream.
+allocate outputs with torch and pass pointers plus torch's current stream, or
+the one given as ``stream``; what they allocate belongs to that stream, as if
+made under ``torch.cuda.stream(stream)``.
 Every arithmetic step runs in the library's CUDA kernels: there is no CPU or
 PyTorch fallback, and every call raises if the library is missing or returns
 an error status.
@@ -238,6 +240,17 @@ def _stream(stream):
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
+def _empty(stream, *shape, **kw):
+    """Uninitialised memory that belongs to the stream the call's kernels run on (None: torch's current one).  torch's
+    allocator hands a block out again in the order of its own stream: a block of another stream may still be in use
+    there, or come into use again before these kernels have finished with it."""
+    import torch
+    if stream is None:
+        return torch.empty(*shape, **kw)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, **kw)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -250,9 +263,9 @@ def modulate_absmax(x, shift, scale, seg_row_offsets, *, tensor_scale=None, scra
     _need_cuda(x, shift, scale)
     m, d = x.shape
     if tensor_scale is None:
-        tensor_scale = torch.empty(1, dtype=torch.float32, device=x.device)
+        tensor_scale = _empty(stream, 1, dtype=torch.float32, device=x.device)
     if scratch is None:
-        scratch = torch.empty(2, dtype=torch.int32, device=x.device)
+        scratch = _empty(stream, 2, dtype=torch.int32, device=x.device)
     h3fp4_modulate_absmax(x.data_ptr(), x.stride(0), m, d, shift.data_ptr(), scale.data_ptr(), shift.stride(0),
                           seg_row_offsets, tensor_scale.data_ptr(), scratch.data_ptr(), _stream(stream))
     return tensor_scale
@@ -264,9 +277,9 @@ def modulate_pack(x, shift, scale, seg_row_offsets, tensor_scale, m_pad, *, qdat
     _need_cuda(x, shift, scale, tensor_scale)
     m, d = x.shape
     if qdata is None:
-        qdata = torch.empty(m_pad, d // 2, dtype=torch.uint8, device=x.device)
+        qdata = _empty(stream, m_pad, d // 2, dtype=torch.uint8, device=x.device)
     if sfa is None:
-        sfa = torch.empty(sf_bytes(m_pad, d), dtype=torch.uint8, device=x.device)
+        sfa = _empty(stream, sf_bytes(m_pad, d), dtype=torch.uint8, device=x.device)
     h3fp4_modulate_pack(x.data_ptr(), x.stride(0), m, m_pad, d, shift.data_ptr(), scale.data_ptr(), shift.stride(0),
                         seg_row_offsets, tensor_scale.data_ptr(), qdata.data_ptr(), sfa.data_ptr(), _stream(stream))
     return qdata, sfa
@@ -280,13 +293,13 @@ def modulate_produce(x, shift, scale, seg_row_offsets, m_pad, *, tensor_scale=No
     m, d = x.shape
     dev = x.device
     if tensor_scale is None:
-        tensor_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        tensor_scale = _empty(stream, 1, dtype=torch.float32, device=dev)
     if scratch is None:
-        scratch = torch.empty(2, dtype=torch.int32, device=dev)
+        scratch = _empty(stream, 2, dtype=torch.int32, device=dev)
     if qdata is None:
-        qdata = torch.empty(m_pad, d // 2, dtype=torch.uint8, device=dev)
+        qdata = _empty(stream, m_pad, d // 2, dtype=torch.uint8, device=dev)
     if sfa is None:
-        sfa = torch.empty(sf_bytes(m_pad, d), dtype=torch.uint8, device=dev)
+        sfa = _empty(stream, sf_bytes(m_pad, d), dtype=torch.uint8, device=dev)
     h3fp4_modulate_produce(x.data_ptr(), x.stride(0), m, m_pad, d, shift.data_ptr(), scale.data_ptr(),
                            shift.stride(0), seg_row_offsets, tensor_scale.data_ptr(), scratch.data_ptr(),
                            qdata.data_ptr(), sfa.data_ptr(), _stream(stream))
@@ -301,13 +314,13 @@ def swiglu_pack(gate, up, m_pad, *, h_workspace=None, tensor_scale=None, scratch
     m, f = gate.shape
     dev = gate.device
     if tensor_scale is None:
-        tensor_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        tensor_scale = _empty(stream, 1, dtype=torch.float32, device=dev)
     if scratch is None:
-        scratch = torch.empty(2, dtype=torch.int32, device=dev)
+        scratch = _empty(stream, 2, dtype=torch.int32, device=dev)
     if qdata is None:
-        qdata = torch.empty(m_pad, f // 2, dtype=torch.uint8, device=dev)
+        qdata = _empty(stream, m_pad, f // 2, dtype=torch.uint8, device=dev)
     if sfa is None:
-        sfa = torch.empty(sf_bytes(m_pad, f), dtype=torch.uint8, device=dev)
+        sfa = _empty(stream, sf_bytes(m_pad, f), dtype=torch.uint8, device=dev)
     h3fp4_swiglu_pack(gate.data_ptr(), gate.stride(0), up.data_ptr(), up.stride(0), m, m_pad, f,
                       tensor_scale.data_ptr(), scratch.data_ptr(), qdata.data_ptr(), sfa.data_ptr(),
                       h_workspace.data_ptr() if h_workspace is not None else None, _stream(stream))
@@ -321,13 +334,13 @@ def quantize_pack(x, m_pad, *, tensor_scale=None, scratch=None, qdata=None, sfa=
     m, d = x.shape
     dev = x.device
     if tensor_scale is None:
-        tensor_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        tensor_scale = _empty(stream, 1, dtype=torch.float32, device=dev)
     if scratch is None:
-        scratch = torch.empty(2, dtype=torch.int32, device=dev)
+        scratch = _empty(stream, 2, dtype=torch.int32, device=dev)
     if qdata is None:
-        qdata = torch.empty(m_pad, d // 2, dtype=torch.uint8, device=dev)
+        qdata = _empty(stream, m_pad, d // 2, dtype=torch.uint8, device=dev)
     if sfa is None:
-        sfa = torch.empty(sf_bytes(m_pad, d), dtype=torch.uint8, device=dev)
+        sfa = _empty(stream, sf_bytes(m_pad, d), dtype=torch.uint8, device=dev)
     h3fp4_quantize_pack(x.data_ptr(), x.stride(0), m, m_pad, d, tensor_scale.data_ptr(), scratch.data_ptr(),
                         qdata.data_ptr(), sfa.data_ptr(), _stream(stream))
     return tensor_scale, qdata, sfa
@@ -340,7 +353,7 @@ def gemm(a_q, a_sf, a_ts, b_q, b_sf, b_ts, m, *, out=None, cfg: GemmConfig | Non
     m_pad, kh = a_q.shape
     n = b_q.shape[0]
     if out is None:
-        out = torch.empty(m, n, dtype=torch.int16, device=a_q.device)
+        out = _empty(stream, m, n, dtype=torch.int16, device=a_q.device)
     h3fp4_gemm(a_q.data_ptr(), a_sf.data_ptr(), a_ts.data_ptr(), b_q.data_ptr(), b_sf.data_ptr(), b_ts.data_ptr(),
                out.data_ptr(), out.stride(0), m, m_pad, n, 2 * kh, cfg, _stream(stream))
     return out
@@ -355,7 +368,7 @@ def gemm_gated_residual(a_q, a_sf, a_ts, b_q, b_sf, b_ts, m, gate, seg_row_offse
     m_pad, kh = a_q.shape
     n = b_q.shape[0]
     if out is None:
-        out = torch.empty(m, n, dtype=torch.int16, device=a_q.device)
+        out = _empty(stream, m, n, dtype=torch.int16, device=a_q.device)
     h3fp4_gemm_gated_residual(a_q.data_ptr(), a_sf.data_ptr(), a_ts.data_ptr(), b_q.data_ptr(), b_sf.data_ptr(),
                               b_ts.data_ptr(), gate.data_ptr(), gate.stride(0), seg_row_offsets,
                               residual.data_ptr(), residual.stride(0), out.data_ptr(), out.stride(0), m, m_pad, n,
@@ -369,7 +382,7 @@ def swizzle_scales(sf_logical, *, out=None, stream=None):
     _need_cuda(sf_logical, out)
     rows, cols = sf_logical.shape
     if out is None:
-        out = torch.empty(sf_rows(rows) * cols, dtype=torch.uint8, device=sf_logical.device)
+        out = _empty(stream, sf_rows(rows) * cols, dtype=torch.uint8, device=sf_logical.device)
     h3fp4_swizzle_scales(sf_logical.data_ptr(), rows, cols, sf_logical.stride(0), out.data_ptr(), _stream(stream))
     return out
 
@@ -461,7 +474,7 @@ def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
     xs, shape = _need_tokens(x, "x"), x.shape
     _positions_for(rope, shape[0])
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(stream, shape, dtype=x.dtype, device=x.device)
     h3fp4_rope_axes(*xs, *_need_tokens(out, "out", shape), *shape, rope.struct(inverse), _raw_stream(stream, x))
     return out
 
@@ -531,9 +544,9 @@ def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_toke
     import torch
     shape = (tokens, cache.heads, cache.head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+        k = _empty(stream, shape, dtype=torch.bfloat16, device=cache.k_codes.device)
     if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+        v = _empty(stream, shape, dtype=torch.bfloat16, device=cache.k_codes.device)
     h3fp4_kv_cache_read(cache._struct, _kv_batch(page_table, start, cu_tokens, max_tokens), *_need_tokens(k, "k", shape),
                         *_need_tokens(v, "v", shape), tokens, _raw_stream(stream, k))
     return k, v
@@ -553,9 +566,9 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
         raise ValueError(f"q: {heads} heads of {dim} for a cache of {cache.heads} heads of {cache.head_dim}"
                          if kv_len is not None else "kv_len: lengths are wanted")
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = _empty(stream, shape, dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty(tokens, heads, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, tokens, heads, dtype=torch.float32, device=q.device)
     lse_at = None
     if lse is not None:
         lse_at = _need_array(lse, "lse", "f32", 2)
@@ -568,7 +581,7 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
         at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         _need_cuda(workspace)
     elif need:
-        workspace, have = torch.empty(need, dtype=torch.uint8, device=q.device), need
+        workspace, have = _empty(stream, need, dtype=torch.uint8, device=q.device), need
         at = workspace.data_ptr()
     h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape), lse_at, tokens, heads, cache._struct, batch, max_kv,
                        dim ** -0.5 if scale is None else scale, causal, window, at, have, _raw_stream(stream, q))
