@@ -104,6 +104,10 @@ __device__ __forceinline__ bool wait_for(const uint64_t &bar, uint32_t parity)
     }
 }
 
+// What turns a score's product into the exponent: the row's factor times the keys' scale.  Never 0, so that a hidden
+// key's -infinity stays one; at the least normal number all of a step's products (below 2^32) still come to nothing.
+__device__ __forceinline__ float step_factor(float c_row, float ks) { return fmaxf(c_row * ks, 0x1p-126f); }
+
 // One arrival for a warp whose lanes have each done (and fenced) their part.
 __device__ __forceinline__ void warp_arrive(const uint64_t &bar)
 {
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float2 p = row_power(max(m2 & 0xFFFFu, m2 >> 16));
                 const float f = a.scale < 0.0f ? -p.x : p.x;
-                c_row = fmaxf(fabsf(a.scale) * kLog2e * p.y, 1e-30f);   // never 0: a hidden key's -infinity stays one
+                c_row = fabsf(a.scale) * kLog2e * p.y;
 #pragma unroll
                 for (int i = 0; i < kDim / 8; ++i)
                     st_shared_v4(smem_u32(sm.q[t]) + operand_at(in_tile, i), bf16x2_to_half2(w[i].x, f), bf16x2_to_half2(w[i].y, f),
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         g0 = max3(g0, x[i], x[i + 1]);
                         g1 = max3(g1, x[i + 2], x[i + 3]);
                     }
-                    top = fmaxf(top, fmaf(max3(g0, g1, fmaxf(x[kGroup - 2], x[kGroup - 1])), c_row * e.ks, e.lv));
+                    top = fmaxf(top, fmaf(max3(g0, g1, fmaxf(x[kGroup - 2], x[kGroup - 1])), step_factor(c_row, e.ks), e.lv));
                 }
                 const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int n = 0; n < kKeys / 16; ++n) {
                         const PageEntry e = pe[(16 * n) >> shift];
-                        const float ck = c_row * e.ks, off = e.lv - at;
+                        const float ck = step_factor(c_row, e.ks), off = e.lv - at;
                         uint32_t x[16], p[8];
                         tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
 #pragma unroll
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int n = 0; n < 32; n += kGroup) {
                             const PageEntry e = pe[(32 * c + n) >> shift];
-                            const float ck = c_row * e.ks;
+                            const float ck = step_factor(c_row, e.ks);
                             const float2 ck2 = make_float2(ck, ck), off2 = make_float2(e.lv - at, e.lv - at);
 #pragma unroll
                             for (int i = n; i < n + kGroup; i += 2) {
