@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int kh = rest % a.cache.heads, split = rest / a.cache.heads % plan.splits, b = rest / a.cache.heads / plan.splits;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+    if (s.n == 0)
+        return;   // without queries its length and pages are not looked at
     if (!s.ok || s.len > a.max_kv || (s.len > 0 && ((s.len - 1) / page >= a.batch.ld_table || a.cache.num_pages == 0))) {
         if (threadIdx.x == 0)
             atomicOr(&g_error, ERR_KV_RANGE);

@@ -19,7 +19,7 @@ struct KvSequence {
     int64_t row;    // first row in the packed token arrays
     int n;          // its tokens in this call
     int len;        // len[b] (0 without a length array)
-    bool ok;        // rows and counts in range
+    bool ok;        // rows and counts in range (without tokens in this call nothing of it is looked at)
 };
 
 __device__ __forceinline__ KvSequence kv_sequence(const KvBatch &bt, int b, int64_t tokens)
@@ -28,7 +28,7 @@ __device__ __forceinline__ KvSequence kv_sequence(const KvBatch &bt, int b, int6
     s.row = bt.cu_tokens[b];
     s.n = bt.cu_tokens[b + 1] - bt.cu_tokens[b];
     s.len = bt.len != nullptr ? bt.len[b] : 0;
-    s.ok = s.row >= 0 && s.n >= 0 && s.n <= bt.max_tokens && s.row + s.n <= tokens && s.len >= 0;
+    s.ok = s.n == 0 || (s.row >= 0 && s.n > 0 && s.n <= bt.max_tokens && s.row + s.n <= tokens && s.len >= 0);
     return s;
 }
 

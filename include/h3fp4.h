@@ -336,7 +336,8 @@ typedef struct h3fp4_kv_cache {
  * range (a page outside the cache or past the table, rows outside the token
  * arrays, more tokens than max_tokens) is not followed, and bit 512 is
  * reported through h3fp4_device_error.  What such a sequence's outputs hold is
- * then unspecified.
+ * then unspecified.  Of a sequence without tokens in the call neither the
+ * length nor the pages are looked at.
  */
 typedef struct h3fp4_kv_batch {
     const int32_t *page_table;  /* device [batch, ld_table] */

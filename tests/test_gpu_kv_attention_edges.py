@@ -1,5 +1,5 @@
-"""Attention over the 8-bit paged cache at the edges of what its arguments may
-hold.  Bounds as in test_gpu_kv_attention where a test gives none of its own."""
+"""The 8-bit paged cache and its attention at the edges of what their arguments
+may hold.  Bounds as in test_gpu_kv_attention where a test gives none of its own."""
 import numpy as np
 import pytest
 import torch
@@ -45,3 +45,36 @@ def test_factors_far_from_one(h3, new, size, scale, log_k_scale):
     out, lse = _run(h3, q, c, table, lengths, cu, new, causal=True, **kw)
     _check(h3, q, c, table, lengths, cu, out, lse, causal=True, **kw)
     assert h3.h3fp4_device_error() == 0
+
+
+@pytest.mark.parametrize("most", [1, 16, 140])
+def test_a_sequence_without_queries_is_not_looked_at(h3, most):
+    """An idle slot of a batch, whatever its length and its row of the table hold, is no error in either kernel."""
+    rng = np.random.default_rng(22)
+    lengths, page = [64, 64, 50], 16
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, 2, page, 64)
+    cu = [0, most, most, most + 1]
+    q = torch.randn(most + 1, 4, 64, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    want = h3.kv_attention(q, c, _dev(table), _dev(lengths), _dev(cu), most, 64, causal=True)[0]
+    for idle in (0, 65, 10_000, 2**31 - 1, -3):
+        table[1] = -1
+        got = h3.kv_attention(q, c, _dev(table), _dev(np.array([64, idle, 50])), _dev(cu), most, 64, causal=True)[0]
+        assert torch.equal(got, want)
+        assert h3.h3fp4_device_error() == 0, idle
+
+
+def test_a_sequence_without_tokens_is_not_looked_at_by_the_cache(h3):
+    rng = np.random.default_rng(23)
+    table, pages = _tables(rng, [20, 20, 20], 16)
+    x = torch.randn(9, 2, 64, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    cu = _dev([0, 5, 5, 9])
+    caches = [h3.KVCache.empty(pages, 16, 2, 64) for _ in range(2)]
+    table[1] = -1
+    for idle, c in ((0, caches[0]), (10_000, caches[1]), (2**31 - 1, caches[1]), (-3, caches[1])):
+        held = _dev(np.array([0, idle, 0]))
+        h3.kv_cache_write(c, x, x, _dev(table), held, cu, 5)
+        got = h3.kv_cache_read(c, _dev(table), held, cu, 9, 5)
+        want = h3.kv_cache_read(caches[0], _dev(table), _dev([0, 0, 0]), cu, 9, 5)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert h3.h3fp4_device_error() == 0, idle
