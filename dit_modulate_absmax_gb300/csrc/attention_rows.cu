@@ -299,7 +299,11 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     __syncthreads();   // the last part's readers are done
     for (int i = threadIdx.x; i < pages; i += kThreads) {
         int32_t id = begin == seg_begin && i < kThreads ? first_id : a.batch.page_table[b * a.batch.ld_table + page0 + i];
-        if (id < 0 || id >= a.cache.num_pages) {
+        // Units begin at multiples of 32 tokens, so that a page of 16 may lie before all that the rows see: whatever the
+        // table holds for it (it may be given up under a window), it is not copied.
+        if ((page0 + i + 1) << shift <= out_lo) {
+            id = -1;
+        } else if (id < 0 || id >= a.cache.num_pages) {
             atomicOr(&g_error, ERR_KV_RANGE);
             id = -1;
         }

@@ -403,7 +403,8 @@ H3FP4_API h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3
  * FP16 but for channels below 2^-28 of the row's largest, and the weights
  * exp(s_j - max) enter the second product rounded to FP16.  A query that sees
  * nothing gets out = 0 and lse = -infinity.  Positions that a query does not
- * see have no effect on it, whatever their codes hold.
+ * see have no effect on it, whatever their codes hold, and pages of which no
+ * query sees anything are not looked at, whatever the table holds for them.
  *
  *   q_bf16, out_bf16  [tokens, heads, head_dim] bf16, strides as for h3fp4_rope_axes, no overlap
  *   lse               NULL, or [tokens, heads] float, contiguous

@@ -78,3 +78,26 @@ def test_a_sequence_without_tokens_is_not_looked_at_by_the_cache(h3):
         want = h3.kv_cache_read(caches[0], _dev(table), _dev([0, 0, 0]), cu, 9, 5)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert h3.h3fp4_device_error() == 0, idle
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("new,heads", [(1, 2), (3, 8), (9, 4), (140, 2)])
+def test_pages_before_a_window_may_be_given_up(h3, new, heads, page):
+    """Table entries before all that the queries see hold anything: the same bits and no report."""
+    rng = np.random.default_rng(24)
+    lengths = [1_200, 777]
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, 2, page, 64)
+    cu = [0, new, 2 * new]
+    q = torch.randn(2 * new, heads, 64, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    for window in (1, 5, 17, 33, 40, 100, 129, 500):
+        for causal in (True, False):
+            want, lse = _run(h3, q, c, table, lengths, cu, new, causal=causal, window=window)
+            _check(h3, q, c, table, lengths, cu, want, lse, causal=causal, window=window)
+            freed = table.copy()
+            for b, n in enumerate(lengths):
+                gone = max(0, n - new - window + 1) // page      # whole pages before the first query's window
+                freed[b, :gone] = rng.choice([-1, pages, 2**31 - 1], gone)
+            got = h3.kv_attention(q, c, _dev(freed), _dev(lengths), _dev(cu), new, max(lengths), causal=causal, window=window)[0]
+            assert torch.equal(got, want)
+            assert h3.h3fp4_device_error() == 0, (window, causal)
