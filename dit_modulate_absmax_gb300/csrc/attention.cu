@@ -22,7 +22,7 @@ SplitPlan plan_of(const AttnShape &s) { return few_rows(s) ? plan_rows(s) : plan
 int64_t attention_workspace(const AttnShape &s)
 {
     const int64_t rows = s.tokens == 0 || s.batch == 0 || s.max_tokens == 0 ? 0 : plan_of(s).part_rows;
-    return rows > (int64_t(1) << 50) ? -1 : rows * (4 * s.head_dim + 8);   // an output and a (maximum, sum)
+    return rows > (int64_t(1) << 50) ? -1 : rows * (4 * s.head_dim + 8);   // a mean, and its sum's logarithm (or the sum and what it is kept against)
 }
 
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st)
@@ -31,8 +31,9 @@ cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st
                       a.causal ? a.window : 0};   // (the parts are no more than without: the workspace does for both)
     const SplitPlan plan = plan_of(s);
     float *part = static_cast<float *>(workspace);
-    float2 *stat = reinterpret_cast<float2 *>(part + plan.part_rows * s.head_dim);
-    return few_rows(s) ? launch_attention_rows(a, plan, stat, part, st) : launch_attention_tile(a, plan, stat, part, st);
+    float *stat = part + plan.part_rows * s.head_dim;
+    return few_rows(s) ? launch_attention_rows(a, plan, stat, part, st)
+                       : launch_attention_tile(a, plan, reinterpret_cast<float2 *>(stat), part, st);
 }
 
 cudaError_t read_attention_error(uint32_t *code)

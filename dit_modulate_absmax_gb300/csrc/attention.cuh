@@ -13,7 +13,16 @@
 // The weight that meets the value codes is 2^(s'_j - m'), with m' the running
 // maximum of s': the largest CONTRIBUTION to the output, not the largest
 // probability, is 1, so FP16's range serves it whatever the pages' scales.
-// Dividing a page's weights by its scale gives the softmax's own sum.
+// Dividing a page's weights by its scale gives the softmax's own sum -- as long
+// as the values' scales of a part's pages lie within 2^80 of each other.  Where
+// they may not, a key that counts in the sum may have a weight below FP32's
+// smallest; from the first step with such pages on the sum has a reference of
+// its own, the running maximum of S_j * (c * k_scale_P), and exponentials of
+// its own.
+//
+// A part of the keys leaves its mean (output over sum) and log2 of its sum, or
+// the sum and its reference; parts are joined as the means weighted by their
+// sums, whatever those were kept against.
 #pragma once
 
 #include "kvcache.cuh"
@@ -92,8 +101,24 @@ __device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w, float f)
     return pack_half2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
 }
 
-// A page's table entry as the kernels keep it: id (< 0: out of range), the
-// keys' scale, log2 of the values' scale and its inverse.
+// A page's values' scale further than this (log2) from the part's first one: the sum gets a reference of its own.  Up to
+// twice that apart, 2^-126 as the least weight leaves out keys below 2^-46 of the largest probability.
+constexpr int kFarScales = 40;
+
+__device__ __forceinline__ int exponent(float scale) { return static_cast<int>(__float_as_uint(scale) >> 23 & 0xFFu); }
+
+// 1 / sum; a row that has seen nothing stays zero, NaN stays NaN.
+__device__ __forceinline__ float reciprocal_sum(float sum) { return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f; }
+
+// A sum against its own logarithm: 1, or still nothing, or NaN.
+__device__ __forceinline__ float own_sum(float sum) { return sum > 0.0f ? 1.0f : sum; }
+
+// 2^(log - top), nothing for two that have seen nothing.
+__device__ __forceinline__ float of_top(float log, float top) { return ex2(log - (top == -INFINITY ? 0.0f : top)); }
+
+// A page's table entry as the kernels keep it: id (few rows: < 0 for none;
+// many: 1 if the values' scales so far lie far apart), the keys' scale, log2
+// of the values' scale and its inverse.
 struct PageEntry {
     int32_t id;
     float ks, lv, inv_vs;
@@ -107,8 +132,8 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
 
 // How a launch spreads the keys.  Tiles: `splits` parts of `chunk` keys each.
 // Rows: clusters of `splits` CTAs, or `splits` CTAs with equal shares.
-// part_rows: rows of partial results (an output, a maximum and a sum) that the
-// workspace has room for.
+// part_rows: rows of partial results (a mean and its sum) that the workspace
+// has room for.
 struct SplitPlan {
     int32_t splits, chunk;
     int64_t part_rows;
@@ -116,7 +141,7 @@ struct SplitPlan {
 };
 
 SplitPlan plan_rows(const AttnShape &s);
-cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
+cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st);
 SplitPlan plan_tile(const AttnShape &s);
 cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
 cudaError_t read_attention_tile_error(uint32_t *code);

@@ -62,15 +62,13 @@ __device__ __forceinline__ uint32_t piece(int r, int c)
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Adds a part with maximum m and sum l to the sums kept against mm >= m.
-__device__ __forceinline__ void join(float4 &sum, float &ll, const float4 &v, float l, float m, float mm)
+// Adds a part's mean v with its share of the row's sum.
+__device__ __forceinline__ void join(float4 &mean, const float4 &v, float share)
 {
-    const float f = ex2(m - (mm == -INFINITY ? 0.0f : mm));
-    sum.x = fmaf(v.x, f, sum.x);
-    sum.y = fmaf(v.y, f, sum.y);
-    sum.z = fmaf(v.z, f, sum.z);
-    sum.w = fmaf(v.w, f, sum.w);
-    ll = fmaf(l, f, ll);
+    mean.x = fmaf(v.x, share, mean.x);
+    mean.y = fmaf(v.y, share, mean.y);
+    mean.z = fmaf(v.z, share, mean.z);
+    mean.w = fmaf(v.w, share, mean.w);
 }
 
 // CTAs that fit an SM: shared memory at 128 channels, registers at 64.
@@ -114,7 +112,7 @@ __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) {
 
 template <int kDim, int kRows>
 __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
-    rows_kernel(AttnArgs a, SplitPlan plan, float2 *ws_stat, float *ws_out, const __grid_constant__ CUtensorMap k_map,
+    rows_kernel(AttnArgs a, SplitPlan plan, float *ws_log, float *ws_out, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map)
 {
     constexpr int kSteps = kDim / 16;            // k16 steps of Q K^T = 16-channel tiles of O^T
@@ -124,7 +122,9 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ PageEntry entry[kMaxEntries];
     __shared__ uint64_t full[kWarps][kStages];
-    __shared__ float stat_m[kWarps][16], stat_l[kWarps][16];
+    __shared__ float part_log[kWarps][16];       // a warp's log2 of the sum of each row
+    __shared__ float sum_ref[kWarps][16];        // with far scales: what a warp's sum of a row is kept against
+    __shared__ int scale_lo, scale_hi;           // exponents of the segment's value scales so far
     __shared__ int64_t warp_units[kWarps], found_rest;
     __shared__ int found_b;
 
@@ -292,6 +292,11 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
 
 
     // In parts whose pages fit the table: their entries, the first copies, then the scales.
+    bool far_scales = false;
+    if (threadIdx.x == 0) {
+        scale_lo = 255;
+        scale_hi = 0;
+    }
     constexpr int kCap = (kMaxEntries - 2) * 16 / kTokens * kTokens;
     for (int begin = seg_begin; begin < seg_end; begin += kCap) {
     const int end = min(seg_end, begin + kCap);
@@ -329,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         for (int i = 0; i < kStages; ++i)
             if (unit0 + i * kTokens < end)
                 fetch(unit0 + i * kTokens, (stage + i) % kStages);
+    int lo_exp = 255, hi_exp = 0;
     for (int i = threadIdx.x; i < pages; i += kThreads) {
         const int32_t id = entry[i].id;
         const int64_t bh = static_cast<int64_t>(id) * heads + kh;
@@ -336,8 +342,30 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         entry[i].ks = id >= 0 ? a.cache.k_scale[bh] : 1.0f;
         entry[i].lv = lg2(vs);
         entry[i].inv_vs = __frcp_rn(vs);
+        if (id >= 0) {
+            lo_exp = min(lo_exp, exponent(vs));
+            hi_exp = max(hi_exp, exponent(vs));
+        }
+    }
+    lo_exp = __reduce_min_sync(0xFFFFFFFFu, lo_exp);
+    hi_exp = __reduce_max_sync(0xFFFFFFFFu, hi_exp);
+    if (lane == 0 && lo_exp <= hi_exp) {
+        atomicMin(&scale_lo, lo_exp);
+        atomicMax(&scale_hi, hi_exp);
     }
     __syncthreads();   // scales
+    if (!far_scales && scale_hi - scale_lo > 2 * kFarScales) {
+        far_scales = true;
+#pragma unroll
+        for (int hf = 0; hf < kHalf; ++hf) {   // the sum so far, kept against m, becomes 1 against its logarithm
+            l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 1);
+            l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 2);
+            if (t == 0)
+                sum_ref[warp][g + 8 * hf] = m[hf] + lg2(l[hf]);
+            l[hf] = t == 0 ? own_sum(l[hf]) : 0.0f;
+        }
+        __syncwarp();
+    }
     for (int unit = unit0; unit < end; unit += kTokens) {
         if (!mbar_wait_bounded(smem_u32(&full[warp][stage]), parity, kWaitNs))
             atomicOr(&g_error, ERR_ATTN_WAIT);   // the copies have not come: go on, the outputs mean nothing
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
             for (int hf = 0; hf < kHalf; ++hf) {
-                l[hf] *= keep[hf];
+                l[hf] *= far_scales ? 1.0f : keep[hf];
                 // the accumulator holds rows 2t and 2t + 1, whose factors are in lanes 8t and 8t + 4
                 const float f0 = __shfl_sync(0xFFFFFFFFu, keep[hf], 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, keep[hf], 8 * t + 4);
 #pragma unroll
@@ -408,6 +436,27 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                     o[hf][j][2] *= f0;
                     o[hf][j][3] *= f1;
                 }
+            }
+        }
+        if (far_scales) {   // the same in the whole CTA
+#pragma unroll
+            for (int hf = 0; hf < kHalf; ++hf) {
+                float u = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    u = fmaxf(u, fmaxf(sc[n][2 * hf], sc[n][2 * hf + 1]) - pe[n >> 1].lv);
+                u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, 1));
+                u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, 2));
+                float &kept = sum_ref[warp][g + 8 * hf];
+                const float was = kept, next = fmaxf(was, u), base = next == -INFINITY ? 0.0f : next;
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    sum += ex2(sc[n][2 * hf] - pe[n >> 1].lv - base) + ex2(sc[n][2 * hf + 1] - pe[n >> 1].lv - base);
+                l[hf] = fmaf(l[hf], ex2(was - base), sum);
+                __syncwarp();
+                if (t == 0)
+                    kept = next;
+                __syncwarp();
             }
         }
         uint32_t pb[kHalf][4];   // weights of the four token groups, FP16 pairs
@@ -422,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                     sum += p0 + p1;
                     pb[hf][n] = pack_half2(p0, p1);
                 }
-                l[hf] = fmaf(sum, pe[n2].inv_vs, l[hf]);
+                if (!far_scales)
+                    l[hf] = fmaf(sum, pe[n2].inv_vs, l[hf]);
             }
         }
 
@@ -504,14 +554,22 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     }
     }   // of the segment
 
-    // Join the warps: maxima and sums, then the outputs through shared memory (the rings are drained).
+    // Join the warps: each one's mean and the logarithm of its sum, the means through shared memory (the rings are drained).
 #pragma unroll
     for (int hf = 0; hf < kHalf; ++hf) {
         l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 1);
         l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 2);
-        if (t == 0) {
-            stat_m[warp][g + 8 * hf] = m[hf];
-            stat_l[warp][g + 8 * hf] = l[hf];
+        const float ref = far_scales ? sum_ref[warp][g + 8 * hf] : m[hf];
+        const float inv = reciprocal_sum(l[hf]) * (far_scales && l[hf] > 0.0f ? ex2(m[hf] - ref) : 1.0f);
+        if (t == 0)
+            part_log[warp][g + 8 * hf] = ref + lg2(l[hf]);
+        const float f0 = __shfl_sync(0xFFFFFFFFu, inv, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, inv, 8 * t + 4);   // as above
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+            o[hf][j][0] *= f0;
+            o[hf][j][1] *= f1;
+            o[hf][j][2] *= f0;
+            o[hf][j][3] *= f1;
         }
     }
     __syncthreads();
@@ -526,59 +584,63 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                     make_float2(o[hf][j][e], o[hf][j][e + 2]);
     __syncthreads();
     float *joined = part + kWarps * kRows * kDim;                                 // [row][kDim], with a cluster
-    float2 *joined_stat = reinterpret_cast<float2 *>(joined + kRows * kDim);      // [row]
-    const auto finish = [&](int r, int c, float mm, float ll, float4 sum) {
+    float *joined_log = joined + kRows * kDim;                                    // [row]
+    const auto finish = [&](int r, int c, float log, float4 mean) {
         const int64_t row = s.row + (row0 + r) / group;
         const int head = kh * group + (row0 + r) % group;
-        const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
-        const __nv_bfloat162 x = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), y = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+        const __nv_bfloat162 x = __floats2bfloat162_rn(mean.x, mean.y), y = __floats2bfloat162_rn(mean.z, mean.w);
         *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
         if (a.lse != nullptr && c == 0)
-            a.lse[row * a.heads + head] = (mm + lg2(ll)) * kLn2;
+            a.lse[row * a.heads + head] = log * kLn2;
     };
     for (int i = threadIdx.x; i < kRows * (kDim / 4); i += kThreads) {
         const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
         if (row0 + r >= rows)
             continue;
-        float mm = stat_m[0][r];
+        float top = part_log[0][r], total = 0.0f;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w)
-            mm = fmaxf(mm, stat_m[w][r]);
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float ll = 0.0f;
+            top = fmaxf(top, part_log[w][r]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-            join(sum, ll, *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c), stat_l[w][r], stat_m[w][r], mm);
+            total += of_top(part_log[w][r], top);
+        const float inv = reciprocal_sum(total), log = top + lg2(total);
+        float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            join(mean, *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c), of_top(part_log[w][r], top) * inv);
         if (plan.cluster) {
-            *reinterpret_cast<float4 *>(joined + r * kDim + c) = sum;
+            *reinterpret_cast<float4 *>(joined + r * kDim + c) = mean;
             if (c == 0)
-                joined_stat[r] = make_float2(mm, ll);
+                joined_log[r] = log;
         } else if (whole) {
-            finish(r, c, mm, ll, sum);
+            finish(r, c, log, mean);
         } else {   // a CTA's first segment goes to its first place, another (its last) to the second
             const int64_t at = (blockIdx.x * 2 + (x != x_first)) * kRows + r;
-            *reinterpret_cast<float4 *>(ws_out + at * kDim + c) = sum;
+            *reinterpret_cast<float4 *>(ws_out + at * kDim + c) = mean;
             if (c == 0)
-                ws_stat[at] = make_float2(mm, ll);
+                ws_log[at] = log;
         }
     }
     if (plan.cluster) {   // each CTA joins a share of the rows' pieces over all parts
         cluster_sync();
-        const uint32_t j0 = smem_u32(joined), s0 = smem_u32(joined_stat);
+        const uint32_t j0 = smem_u32(joined), s0 = smem_u32(joined_log);
         for (int i = (blockIdx.x % plan.splits) * kThreads + threadIdx.x; i < kRows * (kDim / 4); i += kThreads * plan.splits) {
             const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
             if (row0 + r >= rows)
                 continue;
-            float mm = -INFINITY, ll = 0.0f;
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float top = -INFINITY, total = 0.0f;
             for (int p = 0; p < plan.splits; ++p)
-                mm = fmaxf(mm, ld_cluster_v2(mapa_shared(s0 + 8 * r, p)).x);
-            for (int p = 0; p < plan.splits; ++p) {
-                const float2 st = ld_cluster_v2(mapa_shared(s0 + 8 * r, p));
-                join(sum, ll, ld_cluster_v4(mapa_shared(j0 + (r * kDim + c) * 4, p)), st.y, st.x, mm);
-            }
-            finish(r, c, mm, ll, sum);
+                top = fmaxf(top, ld_cluster_f32(mapa_shared(s0 + 4 * r, p)));
+            for (int p = 0; p < plan.splits; ++p)
+                total += of_top(ld_cluster_f32(mapa_shared(s0 + 4 * r, p)), top);
+            const float inv = reciprocal_sum(total);
+            float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int p = 0; p < plan.splits; ++p)
+                join(mean, ld_cluster_v4(mapa_shared(j0 + (r * kDim + c) * 4, p)),
+                     of_top(ld_cluster_f32(mapa_shared(s0 + 4 * r, p)), top) * inv);
+            finish(r, c, top + lg2(total), mean);
         }
         cluster_sync();   // nobody leaves while its part may be read
     }
@@ -595,12 +657,11 @@ constexpr int kJoinThreads = 1024;
 // kGroups-th part (one long request has as many parts as there are CTAs for a
 // cache head, 57 at 8 of them: one warp a row took 15 us over those).
 template <int kDim, int kRows>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas, const float2 *ws_stat, const float *ws_out)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas, const float *ws_log, const float *ws_out)
 {
     constexpr int kPieces = kRows * kDim / 4;
     constexpr int kGroups = kJoinThreads / kPieces;
-    __shared__ float4 sums[kGroups][kPieces];
-    __shared__ float lls[kGroups][kRows];
+    __shared__ float4 means[kGroups][kPieces];
     const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
     const int kh = blockIdx.x % a.cache.heads, tile = blockIdx.x / a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
@@ -634,47 +695,48 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     const int row_in = tile * kRows + r;
     const bool live = row_in < s.n * group;
     const auto place = [&](int64_t p) { return (p == c0 ? slot0 : p * 2) * kRows + r; };
-    float mm = -INFINITY, ll = 0.0f;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = -INFINITY, sum = 0.0f;   // of the row's logarithms: their maximum, and the sum against it
     if (live) {
         for (int64_t p = c0 + lane % (kDim / 4); p <= c1; p += kDim / 4)   // a row's lanes: kDim / 4 neighbours
-            mm = fmaxf(mm, ws_stat[place(p)].x);
+            top = fmaxf(top, ws_log[place(p)]);
     }
 #pragma unroll
     for (int o = kDim / 8; o > 0; o >>= 1)
-        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (live) {
+        for (int64_t p = c0 + lane % (kDim / 4); p <= c1; p += kDim / 4)
+            sum += of_top(ws_log[place(p)], top);
+    }
+#pragma unroll
+    for (int o = kDim / 8; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const float inv = reciprocal_sum(sum);
+    float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (live) {
 #pragma unroll 8
-        for (int64_t p = c0 + part0; p <= c1; p += kGroups) {
-            const float2 st = ws_stat[place(p)];
-            join(sum, ll, *reinterpret_cast<const float4 *>(ws_out + place(p) * kDim + c), st.y, st.x, mm);
-        }
+        for (int64_t p = c0 + part0; p <= c1; p += kGroups)
+            join(mean, *reinterpret_cast<const float4 *>(ws_out + place(p) * kDim + c), of_top(ws_log[place(p)], top) * inv);
     }
     if (kGroups > 1) {
-        sums[part0][piece] = sum;
-        if (c == 0)
-            lls[part0][r] = ll;
+        means[part0][piece] = mean;
         __syncthreads();
         if (part0 > 0)
             return;
-        ll = lls[0][r];
 #pragma unroll
         for (int i = 1; i < kGroups; ++i) {
-            const float4 v = sums[i][piece];
-            sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
-            ll += lls[i][r];
+            const float4 v = means[i][piece];
+            mean = make_float4(mean.x + v.x, mean.y + v.y, mean.z + v.z, mean.w + v.w);
         }
     }
     if (!live)
         return;
     const int64_t row = s.row + row_in / group;
     const int head = kh * group + row_in % group;
-    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(sum.x * inv, sum.y * inv), y = __floats2bfloat162_rn(sum.z * inv, sum.w * inv);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(mean.x, mean.y), y = __floats2bfloat162_rn(mean.z, mean.w);
     *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     if (a.lse != nullptr && c == 0)
-        a.lse[row * a.heads + head] = (mm + lg2(ll)) * kLn2;
+        a.lse[row * a.heads + head] = (top + lg2(sum)) * kLn2;
 }
 
 }  // namespace
@@ -727,9 +789,9 @@ bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page
 }
 
 template <int kDim, int kRows>
-cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
 {
-    constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = (kWarps + 1) * kRows * kDim * 4 + kRows * 8;
+    constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = (kWarps + 1) * kRows * kDim * 4 + kRows * 4;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
     cudaError_t e = allow_shared<rows_kernel<kDim, kRows>>(kSmem);
     if (e != cudaSuccess)
@@ -760,7 +822,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     attr.val.clusterDim.x = static_cast<unsigned>(plan.splits);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.numAttrs = plan.cluster ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows>, a, plan, stat, part, k_map, v_map);
+    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows>, a, plan, logs, part, k_map, v_map);
     if (e != cudaSuccess || plan.cluster)
         return e;
     // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
@@ -770,18 +832,18 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows>, a, static_cast<int>(plan.splits), static_cast<const float2 *>(stat),
+    return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows>, a, static_cast<int>(plan.splits), static_cast<const float *>(logs),
                               static_cast<const float *>(part));
 }
 
 }  // namespace
 
-cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
 {
     const bool small = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads) <= 8;
     if (a.cache.head_dim == 64)
-        return small ? run_rows<64, 8>(a, plan, stat, part, st) : run_rows<64, 16>(a, plan, stat, part, st);
-    return small ? run_rows<128, 8>(a, plan, stat, part, st) : run_rows<128, 16>(a, plan, stat, part, st);
+        return small ? run_rows<64, 8>(a, plan, logs, part, st) : run_rows<64, 16>(a, plan, logs, part, st);
+    return small ? run_rows<128, 8>(a, plan, logs, part, st) : run_rows<128, 16>(a, plan, logs, part, st);
 }
 
 cudaError_t read_attention_rows_error(uint32_t *code)

@@ -30,6 +30,7 @@
 // next scores' first half issued while the softmax works (4 %), two threads a
 // row (8.2 ms), a quarter of the exponentials as polynomials (16 %).
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "ptx_attention.cuh"
@@ -68,6 +69,7 @@ struct __align__(1024) Smem {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], entry_full[kEntrySlots];
     uint64_t drained;
     uint32_t tmem;
+    int32_t first_exp;   // exponent of the values' scales in the first step (the largest)
 };
 
 // Byte offset of 16-byte piece c (8 halves) of row r in the operand layout: blocks of 64 channels, rows of 128 bytes
@@ -239,16 +241,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_arrive(sm.q_full[t]);
             }
             float ref = -INFINITY, l = 0.0f;
-            bool met_nan = false, ok = true;
+            bool met_nan = false;
             const int shift = 31 - __clz(page);
             const uint32_t sc = 128u * t + lanes, oc = 256u + static_cast<uint32_t>(kDim) * t + lanes;
-            for (int j = 0; j < steps; ++j) {
+            float apart_ref = -INFINITY, apart_l = 0.0f;   // with far scales: a sum against a reference of its own
+            // One step; false: a wait gave up.  kFar: a page of this step or an earlier one has a scale far from the first
+            // ones.  That is a loop of its own, so that it costs the other steps one look at the entry (a chunk's step takes
+            // 2.5 % longer with the second loop behind it; with the choice inside of one loop it took 6 %).
+            const auto step = [&](auto far_scales, int j) -> bool {
+                constexpr bool kFar = decltype(far_scales)::value;
                 const int k0 = begin + j * kKeys;
                 const bool edge = k0 < t_lo || k0 + kKeys > t_hi;
-                if (!wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) || !wait_for(sm.s_full[t], j & 1)) {
-                    ok = false;
-                    break;
-                }
+                if (!wait_for(sm.s_full[t], j & 1))
+                    return false;
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
                 const int lo = see.lo - k0, hi = see.hi - k0;
@@ -310,8 +315,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // own copy in the reference.  A step with such a row takes a short loop instead of the long straight
                 // code, with the same operations in the same order for every other row, so that a row's bits do not
                 // depend on its neighbours.
-                const bool far = fabsf(at) > 0x1p20f, plain = !__any_sync(0xFFFFFFFFu, far);
+                const bool far = fabsf(at) > 0x1p20f, plain = !kFar && !__any_sync(0xFFFFFFFFu, far);
                 if (!plain) {
+                    if constexpr (kFar) {
+                        float u = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+                        for (int n = 0; n < kKeys / 16; ++n) {
+                            const float ck = step_factor(c_row, pe[(16 * n) >> shift].ks);
+                            uint32_t x[16];
+                            tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                u = fmaxf(u, __fmul_rn(__uint_as_float(x[i]), ck));
+                        }
+                        const float was = apart_ref, next = fmaxf(was, u), base = next == -INFINITY ? 0.0f : next;
+#pragma unroll 1
+                        for (int n = 0; n < kKeys / 16; ++n) {
+                            const float ck = step_factor(c_row, pe[(16 * n) >> shift].ks);
+                            uint32_t x[16];
+                            tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                sum += ex2(__fmul_rn(__uint_as_float(x[i]), ck) - base);
+                        }
+                        apart_l = fmaf(apart_l, ex2(was - base), sum);
+                        apart_ref = next;
+                    }
                     float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
 #pragma unroll 1
                     for (int n = 0; n < kKeys / 16; ++n) {
@@ -373,10 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 if (k0 < in_lo || k0 + kKeys > in_hi) {   // the conversion warps keep NaN out of such a step's values
-                    if (!wait_for(sm.v_full[j % kStages], (j / kStages) & 1)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!wait_for(sm.v_full[j % kStages], (j / kStages) & 1))
+                        return false;
                     constexpr int kRowsPerWarp = 32 / (kDim / 16);   // of a conversion warp, among kConvertWarps * that
                     for (int w = 0; w < kConvertWarps; ++w) {
                         if (sm.nan_step[j % kStages][w] != j + 1)
@@ -407,6 +434,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l = fmaf(s0.x + s0.y, pe[(kGroup * n) >> shift].inv_vs, l);
                     }
                 }
+                return true;
+            };
+            int j = 0;
+            bool ok = true;
+            for (; ok && j < steps; ++j) {
+                ok = wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1);
+                if (!ok || sm.entry[j % kEntrySlots][0].id != 0)
+                    break;
+                ok = step(std::false_type{}, j);
+            }
+            float o_factor = 1.0f;
+            if (ok && j < steps) {
+                apart_ref = ref + lg2(l);
+                apart_l = own_sum(l);
+                for (; ok && j < steps; ++j)
+                    ok = wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) && step(std::true_type{}, j);
+                o_factor = apart_l > 0.0f ? ex2(ref - apart_ref) : 1.0f;
+                ref = apart_ref;
+                l = apart_l;
             }
             if (ok && steps > 0)
                 ok = wait_for(sm.o_full[t], (steps - 1) & 1);
@@ -414,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const int64_t row = s.row + tok, at = row * a.heads + head;
                 const bool final = plan.splits == 1;
-                const float inv = !final ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                const float inv = reciprocal_sum(l) * o_factor;
                 uint16_t *out = a.out + row * a.ot + head * a.oh;
                 float *part = ws_out + (at * plan.splits + split) * kDim;
 #pragma unroll 1
@@ -540,8 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_for(sm.k_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
+                const int of_vs = exponent(vs);
+                if (j == 0) {
+                    sm.first_exp = __reduce_max_sync(0xFFFFFFFFu, lane_id >= 0 ? of_vs : 0);
+                    __syncwarp();
+                }
+                const int far = __any_sync(0xFFFFFFFFu, lane_id >= 0 && abs(of_vs - sm.first_exp) > kFarScales);
                 if (lane < kKeys / page)
-                    sm.entry[j % kEntrySlots][lane] = PageEntry{lane_id, ks, lg2(vs), __frcp_rn(vs)};
+                    sm.entry[j % kEntrySlots][lane] = PageEntry{far, ks, lg2(vs), __frcp_rn(vs)};
                 warp_arrive(sm.entry_full[j % kEntrySlots]);
             }
 #pragma unroll
@@ -669,40 +721,44 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
     const int64_t at = row * a.heads + head;
     const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
     const float2 *stat = ws_stat + at * plan.splits;
-    float mm = -INFINITY;
+    const auto log_of = [&](int i) { return stat[i].x + lg2(stat[i].y); };
+    float top = -INFINITY;
     for (int i = lane; i < parts; i += 32)
-        mm = fmaxf(mm, stat[i].x);
+        top = fmaxf(top, log_of(i));
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1)
-        mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
-    const float ref = mm == -INFINITY ? 0.0f : mm;
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    float sum = 0.0f;
+    for (int i = lane; i < parts; i += 32)
+        sum += of_top(log_of(i), top);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    const float inv = reciprocal_sum(sum);
     constexpr int kPer = kDim / 32;
-    float sum[kPer], ll = 0.0f;
+    float mean[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; ++c)
-        sum[c] = 0.0f;
+        mean[c] = 0.0f;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
-        const float2 st = stat[i];
-        const float f = ex2(st.x - ref);
-        ll = fmaf(st.y, f, ll);
+        const float share = of_top(log_of(i), top) * inv;
         const float *src = ws_out + (at * plan.splits + i) * kDim + lane * kPer;
 #pragma unroll
         for (int c = 0; c < kPer; c += 2) {
             const float2 v = *reinterpret_cast<const float2 *>(src + c);
-            sum[c] = fmaf(v.x, f, sum[c]);
-            sum[c + 1] = fmaf(v.y, f, sum[c + 1]);
+            mean[c] = fmaf(v.x, share, mean[c]);
+            mean[c + 1] = fmaf(v.y, share, mean[c + 1]);
         }
     }
-    const float inv = ll > 0.0f || ll != ll ? 1.0f / ll : 0.0f;
     uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;
 #pragma unroll
     for (int c = 0; c < kPer; c += 2) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(sum[c] * inv, sum[c + 1] * inv);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(mean[c], mean[c + 1]);
         *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
     }
     if (a.lse != nullptr && lane == 0)
-        a.lse[at] = (mm + lg2(ll)) * kLn2;
+        a.lse[at] = (top + lg2(sum)) * kLn2;
 }
 
 // kGroup: scores in a row that are sure to lie in one page.

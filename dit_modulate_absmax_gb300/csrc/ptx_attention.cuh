@@ -28,10 +28,10 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr)
     return v;
 }
 
-__device__ __forceinline__ float2 ld_cluster_v2(uint32_t cluster_addr)
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
 {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
     return v;
 }
 

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import attention as O
 from test_gpu_kv_attention import _check, _filled, _run
 from test_gpu_kv_cache import _dev, _tables
 
@@ -101,3 +102,33 @@ def test_pages_before_a_window_may_be_given_up(h3, new, heads, page):
             got = h3.kv_attention(q, c, _dev(freed), _dev(lengths), _dev(cu), new, max(lengths), causal=causal, window=window)[0]
             assert torch.equal(got, want)
             assert h3.h3fp4_device_error() == 0, (window, causal)
+
+
+@pytest.mark.parametrize("gap", [0, 40])
+@pytest.mark.parametrize("order", ["turn by turn", "small ones first", "large ones first"])
+@pytest.mark.parametrize("new,length", [(1, 90), (1, 300), (9, 300), (140, 300), (1, 9_000), (20, 4_000), (140, 2_500)])
+def test_value_scales_far_apart(h3, new, length, order, gap):
+    """Pages whose values' scales are those of an all-zero page (2^-40) and the largest a write can set (2^119): every
+    page counts in the softmax's sum, with scores alike or those of the large pages lower by 40."""
+    rng = np.random.default_rng(25)
+    page, dim = 32, 128
+    lengths = [length, 70]
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, 2, page, dim)
+    c.k_scale.fill_(0.25)
+    n = table.shape[1]
+    large = {"turn by turn": np.arange(n) % 2 == 1, "small ones first": np.arange(n) >= n // 2,
+             "large ones first": np.arange(n) < n // 2}[order]
+    q = torch.randn(2 * new, 4, dim, generator=torch.Generator().manual_seed(9)).abs().mul(0.5).bfloat16().cuda()
+    q[:, :, 0] = 4.0
+    lower = -gap / (4.0 * dim ** -0.5)                       # channel 0 carries the gap
+    for b, most in enumerate(lengths):
+        for i in range(-(-most // page)):
+            p = int(table[b, i])
+            c.v_scale[p] = 2.0 ** (119 if large[i] else -40)
+            used = c.k_codes[p, :, :min(page, most - i * page), 0]
+            used.fill_(int(O.e4m3_encode(lower * 4)) if large[i] else 0)
+    cu = [0, new, 2 * new]
+    out, lse = _run(h3, q, c, table, lengths, cu, new, causal=True)
+    _check(h3, q, c, table, lengths, cu, out, lse, causal=True)
+    assert h3.h3fp4_device_error() == 0
