@@ -11,8 +11,9 @@
 // channel to [2^14, 2^15) (exact in FP16 but for channels below 2^-28 of it)
 // and c = |softmax_scale| * log2(e) / that power (the sign goes into q~).
 // The weight that meets the value codes is 2^(s'_j - m'), with m' the running
-// maximum of s': the largest CONTRIBUTION to the output, not the largest
-// probability, is 1, so FP16's range serves it whatever the pages' scales.
+// maximum of s' less a constant: the largest CONTRIBUTION to the output, not
+// the largest probability, stands near the top of FP16's range, and that range
+// serves it whatever the pages' scales.
 // Dividing a page's weights by its scale gives the softmax's own sum -- as long
 // as the values' scales of a part's pages lie within 2^80 of each other.  Where
 // they may not, a key that counts in the sum may have a weight below FP32's

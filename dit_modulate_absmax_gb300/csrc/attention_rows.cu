@@ -42,6 +42,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;                 // tokens a warp takes at a time
 constexpr int kStages = 2;
 constexpr int kMaxEntries = 512;          // pages of one part
+// Weights are FP16 and stand against the row's maximum less this (log2): the largest is 2^15, below FP16's limit of nearly
+// 2^16, one 2^-29 as large is still a normal number, one 2^-40 as large not yet nothing.
+constexpr float kLift = 15.0f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         for (int hf = 0; hf < kHalf; ++hf) {
             top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 1));
             top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 2));
-            const float mm = fmaxf(m[hf], top[hf]);
+            const float mm = fmaxf(m[hf], fabsf(top[hf]) < 0x1p22f ? top[hf] - kLift : top[hf]);   // (exact, or not at all)
             ref[hf] = mm == -INFINITY ? 0.0f : mm;
             keep[hf] = ex2(m[hf] - ref[hf]);
             grew |= mm > m[hf];

@@ -9,8 +9,8 @@
 //    S's own columns, the A operand of the second product.  The two row tiles
 //    alternate, one in the tensor cores while the other is in the softmax.
 //    The output accumulator in TMEM is rescaled only when a row's maximum has
-//    grown by more than 2^8 since the reference it is kept against; FP16 and
-//    FP32 hold weights up to 2^8 as well as up to 1.
+//    grown by more than 2^8 since it was last; FP16 and FP32 hold weights of up
+//    to 2^15 as well as up to 1.
 //  - 4 conversion warps: codes straight from global memory to registers (they
 //    are in L2: every row tile of a head reads them), E4M3 -> FP16, which is
 //    exact, and into shared memory in the 128-byte-swizzled operand layout.
@@ -54,7 +54,10 @@ constexpr int kSplitRegs = 2 * kSoftmaxRegs + kConvertRegs + kMmaRegs;
 static_assert(kSplitRegs <= 4 * 128 && kConvertRegs <= 128 && kMmaRegs <= 128, "the launch's registers cover the split");
 constexpr int kStages = 2;
 constexpr int kEntrySlots = 4;
-constexpr float kLazy = 8.0f;                  // log2 of how far a maximum may pass its reference
+// Weights are FP16 and stand against a reference: the row's maximum less kLift when it was set, held until a maximum passes
+// it by kPast (log2).  So the largest weight lies between 2^kLift and 2^kPast, below FP16's limit of nearly 2^16, and one
+// 2^-21 as large is still a normal number, one 2^-32 as large not yet nothing.
+constexpr float kLift = 7.0f, kPast = 15.0f;
 
 template <int kDim>
 struct __align__(1024) Smem {
@@ -291,9 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     top = fmaxf(top, fmaf(max3(g0, g1, fmaxf(x[kGroup - 2], x[kGroup - 1])), step_factor(c_row, e.ks), e.lv));
                 }
-                const bool move = top > ref + kLazy || (ref == -INFINITY && top > -INFINITY);
+                const bool move = top - ref > kPast;   // (a difference, which is exact on any grid; two infinities: no)
                 if (__any_sync(0xFFFFFFFFu, move)) {
-                    const float next = move ? top : ref;
+                    const float next = move ? top - kLift : ref;
                     const float f = ref == -INFINITY ? 0.0f : ex2(ref - next);
                     l *= f;
                     ref = next;

@@ -401,7 +401,9 @@ H3FP4_API h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3
  * with sums, the softmax and its statistics in FP32.  The products take the
  * stored codes exactly; q is scaled by a power of two per row and exact in
  * FP16 but for channels below 2^-28 of the row's largest, and the weights
- * exp(s_j - max) enter the second product rounded to FP16.  A query that sees
+ * exp(s_j - max) enter the second product rounded to FP16: by 2^-11 down to
+ * 2^-21 of the largest (a weight counts here times its page's value scale),
+ * to a multiple of 2^-31 of it below that.  A query that sees
  * nothing gets out = 0 and lse = -infinity.  Positions that a query does not
  * see have no effect on it, whatever their codes hold, and pages of which no
  * query sees anything are not looked at, whatever the table holds for them.

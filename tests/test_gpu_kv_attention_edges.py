@@ -132,3 +132,79 @@ def test_value_scales_far_apart(h3, new, length, order, gap):
     out, lse = _run(h3, q, c, table, lengths, cu, new, causal=True)
     _check(h3, q, c, table, lengths, cu, out, lse, causal=True)
     assert h3.h3fp4_device_error() == 0
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("value", [0, 0x7E])
+@pytest.mark.parametrize("drop", [25.1, 28.0, 31.0])
+@pytest.mark.parametrize("new,heads,length", [(1, 2, 262_143), (1, 2, 700), (16, 2, 37_810), (140, 2, 37_810), (140, 80, 3_000)])
+def test_many_keys_far_below_one(h3, new, heads, length, drop, value, first):
+    """One key stands 2^drop above all others, which together still count (alone, where its own value is 0).
+
+    Bound: 2^-8 of the result for its rounding, 2^-10 + 4 e of the mean of |v| as elsewhere, and for weights below FP16's
+    normal numbers half a step each: 2^-25 in units in which the largest weight is 2^15 (few rows) or 2^7 at least (many),
+    times the largest code, 448, of its page.  All other values are positive, so that what is lost shows."""
+    rng = np.random.default_rng(26)
+    page, dim = 128, 128
+    n = -(-length // page)
+    c = h3.KVCache.empty(n, page, heads, dim)
+    k, v = np.zeros((n, heads, page, dim), dtype=np.uint8), rng.integers(0x68, 0x7F, (n, heads, page, dim)).astype(np.uint8)
+    at = 0 if first else length - 1
+    k[at // page, :, at % page, 0] = O.e4m3_encode(8.0)
+    v[at // page, :, at % page] = value
+    scale = np.float32(drop * np.log(2) / 32)                   # q . k = 32 scale: 2^drop
+    c.k_codes.copy_(_dev(k, torch.uint8))
+    c.v_codes.copy_(_dev(v, torch.uint8))
+    c.k_scale.fill_(float(scale))
+    c.v_scale.fill_(0.125)
+    q = torch.zeros(new, heads, dim, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 4.0
+    table = np.arange(n, dtype=np.int32)[None]
+    out, lse = _run(h3, q, c, table, [length], [0, new], new, scale=1.0)
+    w = np.full(length, np.exp(-32.0 * float(scale)))
+    w[at] = 1.0
+    e = 2.0 ** -17 * 32.0 * float(scale)
+    lift = 15 if new <= 32 else 7
+    for h in (0, heads - 1):
+        vv = O.TABLE[v[:, h].reshape(-1, dim)[:length]] * 0.125
+        ref = w @ vv / w.sum()
+        tol = 2.0 ** -8 * ref + (2.0 ** -10 + 4 * e) * ref + length * 2.0 ** (-25 - lift) * 56 / w.sum()
+        got = out[:, h].double().cpu().numpy()
+        assert (np.abs(got - ref) <= tol).all(), (h, float((np.abs(got - ref) / tol).max()))
+        want = 32.0 * float(scale) + np.log(w.sum())
+        assert (np.abs(lse[:, h].double().cpu().numpy() - want) <= e + 2.0 ** -20 * (1 + abs(want))).all()
+
+
+@pytest.mark.parametrize("new", [1, 140])
+@pytest.mark.parametrize("size", [1.0, 1e4, 1e6, 3e7, 1e8, 3e9, 1e12, 1e20])
+def test_scores_of_every_size_stay_in_range(h3, new, size):
+    """Scores up to 1e21, growing along the keys and falling: no weight leaves FP16's range, the largest one wins."""
+    rng = np.random.default_rng(27)
+    lengths, page = [700, 333], 32
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, 2, page, 64)
+    cu = [0, new, 2 * new]
+    q = torch.randn(2 * new, 4, 64, generator=torch.Generator().manual_seed(9)).mul(size).bfloat16().cuda()
+    out, lse = _run(h3, q, c, table, lengths, cu, new, causal=True)
+    _check(h3, q, c, table, lengths, cu, out, lse, causal=True)
+
+
+@pytest.mark.parametrize("new", [1, 16, 140])
+@pytest.mark.parametrize("rise", [1.0, 4.9, 7.9, 8.1, 14.9, 15.1, 40.0])
+def test_scores_rising_along_the_keys(h3, new, rise):
+    """Each 128 keys stand 2^rise / 8 above those before, and the last ones 2^rise above the first: references that are
+    held and ones that move."""
+    rng = np.random.default_rng(28)
+    length, page, dim = 1_100, 16, 64
+    n = -(-length // page)
+    table = np.arange(n, dtype=np.int32)[None]
+    c = _filled(h3, rng, table, [length], n, 2, page, dim, spread=1)
+    steps = np.minimum(np.arange(n) * page // 128, 8)
+    k = np.zeros((n, 2, page, dim), dtype=np.uint8)
+    k[..., 0] = O.e4m3_encode(steps.astype(float))[:, None, None]
+    c.k_codes.copy_(_dev(k, torch.uint8))
+    c.k_scale.fill_(float(np.float32(rise * np.log(2) / 8)))
+    q = torch.zeros(new, 4, dim, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    out, lse = _run(h3, q, c, table, [length], [0, new], new, scale=1.0)
+    _check(h3, q, c, table, [length], [0, new], out, lse, scale=1.0)
