@@ -211,7 +211,6 @@ def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, 
           heads, cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream)
 
 
-@functools.lru_cache(maxsize=256)          # a function of the sizes alone
 def h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv) -> int:
     n = lib().h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv)
     if n < 0:
@@ -552,6 +551,11 @@ def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_toke
     return k, v
 
 
+@functools.lru_cache(maxsize=256)          # a function of the sizes and the device's SMs
+def _attention_workspace(device, *sizes):
+    return h3fp4_kv_attention_workspace(*sizes)
+
+
 def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, max_kv, *, scale=None, causal=False,
                  window=0, out=None, lse=None, return_lse=False, workspace=None, stream=None):
     """Attention of q [tokens, heads, head_dim] over the cache.  kv_len[b] counts all keys
@@ -575,7 +579,7 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
         if lse.shape != (tokens, heads):
             _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor")
     batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens)
-    need = h3fp4_kv_attention_workspace(tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
+    need = _attention_workspace(q.get_device(), tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
     at = have = 0
     if workspace is not None:
         at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()

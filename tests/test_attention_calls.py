@@ -1,0 +1,74 @@
+"""The Python calls of the cache and its attention (CPU): what they check and
+pass on, with tensors that are stand-ins and entry points that only record."""
+import pytest
+import torch
+
+import dit_modulate_absmax_gb300 as pkg
+
+
+class Fake:
+    """A contiguous device tensor as far as the calls look at one."""
+
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.int32, device=0, at=0x10000, stride=None):
+        self.shape, self.dtype, self._device, self._at = torch.Size(shape), dtype, device, at
+        self.device = torch.device("cuda", device)
+        self._stride = stride or torch.empty(shape, device="meta").stride()
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+    def is_contiguous(self):
+        return self._stride == torch.empty(self.shape, device="meta").stride()
+
+    def data_ptr(self):
+        return self._at
+
+    def get_device(self):
+        return self._device
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+
+def _cache(device=0, **other):
+    d = {n: device for n in ("kc", "ks", "vc", "vs")} | other
+    return pkg.KVCache(Fake(4, 2, 16, 64, dtype=torch.uint8, device=d["kc"]), Fake(4, 2, dtype=torch.float32, device=d["ks"]),
+                       Fake(4, 2, 16, 64, dtype=torch.uint8, device=d["vc"]), Fake(4, 2, dtype=torch.float32, device=d["vs"]))
+
+
+def _x(tokens=3, heads=2, device=0, at=0x10000):
+    return Fake(tokens, heads, 64, dtype=torch.bfloat16, device=device, at=at)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Arguments of the C entry points that were reached; the current stream of a device is its number."""
+    got = []
+    for name in ("h3fp4_rope_axes", "h3fp4_kv_cache_write", "h3fp4_kv_cache_read", "h3fp4_kv_attention"):
+        monkeypatch.setattr(pkg, name, lambda *a, name=name: got.append((name, a)))
+    monkeypatch.setattr(pkg, "_raw_stream", lambda stream, t: t.get_device())
+    return got
+
+
+def test_workspace_of_one_device_is_not_anothers(calls, monkeypatch):
+    """Devices may differ in their SMs, and with them the parts of the keys."""
+    sizes = {0: 1_000, 1: 5_000}
+    device = [0]
+    monkeypatch.setattr(pkg, "h3fp4_kv_attention_workspace", lambda *a: sizes[device[0]])
+    made = []
+    monkeypatch.setattr(pkg, "_empty", lambda stream, n, dtype, device: (made.append(n), Fake(n, dtype=dtype))[1])
+    pkg._attention_workspace.cache_clear()
+    for device[0] in (0, 1, 0, 1):
+        d = device[0]
+        pkg.kv_attention(_x(device=d), _cache(d), Fake(1, 4, device=d), Fake(1, device=d), Fake(2, device=d), 3, 64,
+                         out=_x(device=d, at=0x90000))
+    pkg._attention_workspace.cache_clear()
+    assert made == [1_000, 5_000, 1_000, 5_000]
