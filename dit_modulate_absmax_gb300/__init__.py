@@ -108,6 +108,13 @@ def _call(name: str, *args) -> None:
         raise H3FP4Error(name, st)
 
 
+def _need_int32(func: str, *values) -> None:
+    """ctypes drops the high bits of an integer that does not fit, without a word."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7FFFFFFF:
+            raise H3FP4Error(func, 3)
+
+
 def _offsets(seg_row_offsets):
     arr = (ctypes.c_int32 * len(seg_row_offsets))(*[int(v) for v in seg_row_offsets])
     return arr, len(seg_row_offsets) - 1
@@ -189,6 +196,7 @@ def h3fp4_diag_gemm_wait_timeout(a_q, a_sf, a_ts, b_q, b_sf, b_ts, c, ldc, m, m_
 def h3fp4_rope_axes(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads, head_dim,
                     rope, stream=0):
     """`rope` (and `cache`, `batch` below): the structure's bytes, or None where the C entry takes NULL."""
+    _need_int32("h3fp4_rope_axes", heads, head_dim)
     _call("h3fp4_rope_axes", x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads,
           head_dim, rope, stream)
 
@@ -207,11 +215,13 @@ def h3fp4_kv_cache_read(cache, batch, k, k_token_stride, k_head_stride, v, v_tok
 
 def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens, heads,
                        cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream=0):
+    _need_int32("h3fp4_kv_attention", heads, max_kv, causal, window)
     _call("h3fp4_kv_attention", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
           heads, cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream)
 
 
 def h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv) -> int:
+    _need_int32("h3fp4_kv_attention_workspace", heads, kv_heads, head_dim, batch, max_tokens, max_kv)
     n = lib().h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv)
     if n < 0:
         raise H3FP4Error("h3fp4_kv_attention_workspace", 3)

@@ -1,9 +1,12 @@
 """The Python calls of the cache and its attention (CPU): what they check and
 pass on, with tensors that are stand-ins and entry points that only record."""
+import struct
+
 import pytest
 import torch
 
 import dit_modulate_absmax_gb300 as pkg
+from dit_modulate_absmax_gb300 import build as B
 
 
 class Fake:
@@ -38,6 +41,10 @@ class Fake:
         return self.dtype.itemsize
 
 
+class FakeStream:
+    cuda_stream = 0
+
+
 def _cache(device=0, **other):
     d = {n: device for n in ("kc", "ks", "vc", "vs")} | other
     return pkg.KVCache(Fake(4, 2, 16, 64, dtype=torch.uint8, device=d["kc"]), Fake(4, 2, dtype=torch.float32, device=d["ks"]),
@@ -46,6 +53,11 @@ def _cache(device=0, **other):
 
 def _x(tokens=3, heads=2, device=0, at=0x10000):
     return Fake(tokens, heads, 64, dtype=torch.bfloat16, device=device, at=at)
+
+
+@pytest.fixture(autouse=True)
+def built():
+    B.build()
 
 
 @pytest.fixture
@@ -72,3 +84,24 @@ def test_workspace_of_one_device_is_not_anothers(calls, monkeypatch):
                          out=_x(device=d, at=0x90000))
     pkg._attention_workspace.cache_clear()
     assert made == [1_000, 5_000, 1_000, 5_000]
+
+
+@pytest.mark.parametrize("name,value", [("window", 2**32 + 5), ("window", -2**32), ("max_kv", 2**32 + 64), ("max_kv", 2**31),
+                                        ("max_tokens", 2**32 + 3), ("causal", 2**32)])
+def test_integers_that_do_not_fit_are_refused(name, value):
+    """... and not cut to 32 bits (the call has no tokens, so that it would do nothing if it were let through)."""
+    kw = {"max_tokens": 3, "max_kv": 64, "causal": 0, "window": 0} | {name: value}
+    most, kv = kw.pop("max_tokens"), kw.pop("max_kv")
+    with pytest.raises((pkg.H3FP4Error, ValueError, struct.error)):
+        pkg.kv_attention(_x(0), _cache(), Fake(1, 4), Fake(1), Fake(2), most, kv, out=_x(0, at=0x90000), stream=FakeStream(), **kw)
+
+
+@pytest.mark.parametrize("call", ["h3fp4_kv_attention_workspace", "h3fp4_rope_axes"])
+def test_integers_of_the_mirrors_that_do_not_fit_are_refused(call):
+    sizes = [1, 8, 8, 64, 1, 1, 100]
+    with pytest.raises(pkg.H3FP4Error):
+        if call == "h3fp4_rope_axes":
+            rope = pkg._ROPE.pack(0x10000, 1, 0x10000, 1, 0, 0, 0, 0, 0, 0)
+            pkg.h3fp4_rope_axes(0x10000, 128, 64, 0x90000, 128, 64, 0, 2**32 + 2, 64, rope)
+        else:
+            pkg.h3fp4_kv_attention_workspace(*sizes[:6], 2**32 + 100)
