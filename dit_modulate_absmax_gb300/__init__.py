@@ -437,6 +437,14 @@ def _refuse(t, name, what):
                      f"{t.device}")
 
 
+def _one_device(*ts):
+    device = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"the call's tensors lie on devices {device} and {t.get_device()}")
+    return device
+
+
 def _raw_stream(stream, t):
     if stream is not None:
         return stream.cuda_stream
@@ -457,6 +465,7 @@ class Rope:
         if not 1 <= n <= ROPE_MAX_AXES or positions.shape[1] < n or 2 * freqs.shape[0] < sum(dims) or layout not in ROPE_LAYOUTS:
             raise ValueError(f"rope: dims {tuple(dims)}, layout {layout!r} (one of {sorted(ROPE_LAYOUTS)}) with positions "
                              f"{tuple(positions.shape)} and {freqs.shape[0]} frequencies")
+        _one_device(positions, freqs)
         self.positions, self.freqs, self.dims, self.layout = positions, freqs, tuple(dims), layout
         self._struct = _ROPE.pack(p, positions.shape[1], f, n, *self.dims, *(0,) * (ROPE_MAX_AXES - n),
                                   ROPE_LAYOUTS[layout], 0)
@@ -484,7 +493,9 @@ def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
     _positions_for(rope, shape[0])
     if out is None:
         out = _empty(stream, shape, dtype=x.dtype, device=x.device)
-    h3fp4_rope_axes(*xs, *_need_tokens(out, "out", shape), *shape, rope.struct(inverse), _raw_stream(stream, x))
+    outs = _need_tokens(out, "out", shape)
+    _one_device(x, out, rope.positions)
+    h3fp4_rope_axes(*xs, *outs, *shape, rope.struct(inverse), _raw_stream(stream, x))
     return out
 
 
@@ -501,6 +512,7 @@ class KVCache:
         if v_codes.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
             raise ValueError(f"cache: codes {tuple(shape)} and {tuple(v_codes.shape)} with scales {tuple(k_scale.shape)} and "
                              f"{tuple(v_scale.shape)}")
+        _one_device(k_codes, k_scale, v_codes, v_scale)
         self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
         self.num_pages, self.heads, self.page_size, self.head_dim = shape
         self._struct = _KV_CACHE.pack(kc, vc, ks, vs, shape[0], shape[2], shape[1], shape[3])
@@ -542,7 +554,9 @@ def kv_cache_write(cache: KVCache, k, v, page_table, held, cu_tokens, max_tokens
         raise ValueError("held: lengths before the call are wanted")
     if rope is not None:
         _positions_for(rope, shape[0])
-    h3fp4_kv_cache_write(cache._struct, _kv_batch(page_table, held, cu_tokens, max_tokens), *ks, *vs, shape[0],
+    batch = _kv_batch(page_table, held, cu_tokens, max_tokens)
+    _one_device(k, v, cache.k_codes, page_table, held, cu_tokens, rope and rope.positions)
+    h3fp4_kv_cache_write(cache._struct, batch, *ks, *vs, shape[0],
                          rope._struct if rope is not None else None, _raw_stream(stream, k))
 
 
@@ -556,8 +570,9 @@ def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_toke
         k = _empty(stream, shape, dtype=torch.bfloat16, device=cache.k_codes.device)
     if v is None:
         v = _empty(stream, shape, dtype=torch.bfloat16, device=cache.k_codes.device)
-    h3fp4_kv_cache_read(cache._struct, _kv_batch(page_table, start, cu_tokens, max_tokens), *_need_tokens(k, "k", shape),
-                        *_need_tokens(v, "v", shape), tokens, _raw_stream(stream, k))
+    batch, ks, vs = _kv_batch(page_table, start, cu_tokens, max_tokens), _need_tokens(k, "k", shape), _need_tokens(v, "v", shape)
+    _one_device(k, v, cache.k_codes, page_table, start, cu_tokens)
+    h3fp4_kv_cache_read(cache._struct, batch, *ks, *vs, tokens, _raw_stream(stream, k))
     return k, v
 
 
@@ -589,11 +604,11 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
         if lse.shape != (tokens, heads):
             _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor")
     batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens)
-    need = _attention_workspace(q.get_device(), tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
+    device = _one_device(q, out, lse, cache.k_codes, page_table, kv_len, cu_tokens, workspace)
+    need = _attention_workspace(device, tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
     at = have = 0
     if workspace is not None:
         at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _need_cuda(workspace)
     elif need:
         workspace, have = _empty(stream, need, dtype=torch.uint8, device=q.device), need
         at = workspace.data_ptr()

@@ -105,3 +105,41 @@ def test_integers_of_the_mirrors_that_do_not_fit_are_refused(call):
             pkg.h3fp4_rope_axes(0x10000, 128, 64, 0x90000, 128, 64, 0, 2**32 + 2, 64, rope)
         else:
             pkg.h3fp4_kv_attention_workspace(*sizes[:6], 2**32 + 100)
+
+
+def test_tensors_of_one_call_lie_on_one_device(calls):
+    ok = [Fake(1, 4), Fake(1), Fake(2)]
+    pos, freqs = dict(dtype=torch.float32), dict(dtype=torch.float64)
+    rope = lambda d=0: pkg.Rope(Fake(3, 1, device=d, **pos), Fake(32, device=d, **freqs), (64,))
+    pkg.kv_attention(_x(), _cache(), *ok, 3, 64, out=_x(at=0x90000), workspace=Fake(1 << 20, dtype=torch.uint8))
+    pkg.kv_cache_write(_cache(), _x(), _x(), *ok, 3, rope=rope())
+    pkg.kv_cache_write(_cache(), _x(), _x(), *ok, 3)
+    pkg.kv_cache_read(_cache(), *ok, 3, 3, k=_x(), v=_x(at=0x90000))
+    pkg.kv_cache_read(_cache(), ok[0], None, ok[2], 3, 3, k=_x(), v=_x(at=0x90000))
+    pkg.rope_axes(_x(), rope(), out=_x(at=0x90000))
+    assert len(calls) == 6
+    for name in ("kc", "ks", "vc", "vs"):
+        with pytest.raises(ValueError):
+            _cache(**{name: 1})
+    with pytest.raises(ValueError):
+        pkg.Rope(Fake(3, 1, device=1, **pos), Fake(32, **freqs), (64,))
+    for i in range(3):
+        arrays = list(ok)
+        arrays[i] = Fake(*ok[i].shape, device=1)
+        for call in (lambda: pkg.kv_attention(_x(), _cache(), *arrays, 3, 64, out=_x(at=0x90000)),
+                     lambda: pkg.kv_cache_write(_cache(), _x(), _x(), *arrays, 3),
+                     lambda: pkg.kv_cache_read(_cache(), *arrays, 3, 3, k=_x(), v=_x(at=0x90000))):
+            with pytest.raises(ValueError):
+                call()
+    far, out = _x(device=1), _x(at=0x90000)
+    lse = Fake(3, 2, dtype=torch.float32, device=1)
+    for call in (lambda: pkg.kv_attention(_x(), _cache(1), *ok, 3, 64, out=out), lambda: pkg.kv_attention(_x(), _cache(), *ok, 3, 64, out=far),
+                 lambda: pkg.kv_attention(_x(), _cache(), *ok, 3, 64, out=out, lse=lse),
+                 lambda: pkg.kv_attention(_x(), _cache(), *ok, 3, 64, out=out, workspace=Fake(1 << 20, dtype=torch.uint8, device=1)),
+                 lambda: pkg.kv_cache_write(_cache(1), _x(), _x(), *ok, 3), lambda: pkg.kv_cache_write(_cache(), _x(), far, *ok, 3),
+                 lambda: pkg.kv_cache_write(_cache(), _x(), _x(), *ok, 3, rope=rope(1)),
+                 lambda: pkg.kv_cache_read(_cache(1), *ok, 3, 3, k=_x(), v=out), lambda: pkg.kv_cache_read(_cache(), *ok, 3, 3, k=_x(), v=far),
+                 lambda: pkg.rope_axes(_x(), rope(), out=far), lambda: pkg.rope_axes(_x(), rope(1), out=out)):
+        with pytest.raises(ValueError):
+            call()
+    assert len(calls) == 6
