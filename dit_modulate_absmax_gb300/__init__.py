@@ -608,6 +608,8 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
     need = _attention_workspace(device, tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
     at = have = 0
     if workspace is not None:
+        if not workspace.is_contiguous():        # its bytes are written as they lie
+            _refuse(workspace, "workspace", "a contiguous tensor")
         at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
         workspace, have = _empty(stream, need, dtype=torch.uint8, device=q.device), need

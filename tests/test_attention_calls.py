@@ -143,3 +143,13 @@ def test_tensors_of_one_call_lie_on_one_device(calls):
         with pytest.raises(ValueError):
             call()
     assert len(calls) == 6
+
+
+@pytest.mark.parametrize("shape,stride", [((1 << 20,), (0,)), ((1 << 10, 1 << 10), (1 << 11, 1)), ((1 << 20,), (2,))])
+def test_a_workspace_with_gaps_is_refused(calls, shape, stride):
+    """Its bytes are counted by its elements and written one after another: an expanded one has fewer, one with gaps has
+    someone else's between."""
+    with pytest.raises(ValueError, match="workspace"):
+        pkg.kv_attention(_x(), _cache(), Fake(1, 4), Fake(1), Fake(2), 3, 64, out=_x(at=0x90000),
+                         workspace=Fake(*shape, dtype=torch.uint8, stride=stride))
+    assert not calls
