@@ -284,6 +284,31 @@ bool ranges_overlap(const Strided &a, const Strided &b, int64_t tokens, int64_t 
     return pa < pb + bytes(b) && pb < pa + bytes(a);
 }
 
+// Whether two outputs (check_strided_out) of the same strides have an element in common, as interleaved ones do not though
+// their ranges overlap; of other strides, whether their ranges do.
+bool rows_overlap(const Strided &a, const Strided &b, int64_t tokens, int64_t heads, int64_t dim)
+{
+    if (!ranges_overlap(a, b, tokens, heads, dim))
+        return false;
+    if ((tokens > 1 && a.token != b.token) || (heads > 1 && a.head != b.head))
+        return true;
+    const int64_t d = (static_cast<const char *>(b.p) - static_cast<const char *>(a.p)) / 2;   // 16-byte aligned, both
+    const bool token_outer = heads == 1 || (tokens > 1 && a.token >= a.head);
+    const int64_t inner = token_outer ? a.head : a.token, outer = token_outer ? a.token : a.head;
+    const int64_t n_inner = token_outer ? heads : tokens, n_outer = token_outer ? tokens : heads;
+    // Rows i outer + j inner apart, for i and j between the two: those nearest to -d.
+    const int64_t i0 = n_outer > 1 ? -d / outer : 0;
+    for (int64_t i = i0 - 2; i <= i0 + 2; ++i) {
+        if (i <= -n_outer || i >= n_outer)
+            continue;
+        const int64_t rest = d + i * outer, j0 = n_inner > 1 ? -rest / inner : 0;
+        for (int64_t j = j0 - 1; j <= j0 + 1; ++j)
+            if (j > -n_inner && j < n_inner && rest + j * inner < dim && rest + j * inner > -dim)
+                return true;
+    }
+    return false;
+}
+
 h3fp4_status make_rope(const h3fp4_rope *r, int64_t dim, int64_t tokens, h3fp4::RopeArgs *out)
 {
     if (r == nullptr)
@@ -417,6 +442,8 @@ h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3fp4_kv_bat
     if ((k.p != nullptr && (s = check_strided_out(k, tokens, cache->heads, cache->head_dim)) != H3FP4_OK) ||
         (v.p != nullptr && (s = check_strided_out(v, tokens, cache->heads, cache->head_dim)) != H3FP4_OK))
         return s;
+    if (k.p != nullptr && v.p != nullptr && rows_overlap(k, v, tokens, cache->heads, cache->head_dim))
+        return H3FP4_ERR_UNSUPPORTED;
     return from_cuda(h3fp4::launch_kv_read(*cache, *batch, static_cast<uint16_t *>(k_bf16), k.token, k.head,
                                            static_cast<uint16_t *>(v_bf16), v.token, v.head, tokens,
                                            as_stream(stream)));

@@ -380,7 +380,8 @@ H3FP4_API h3fp4_status h3fp4_kv_cache_write(const h3fp4_kv_cache *cache, const h
  * sequence), its number of tokens cu_tokens[b+1] - cu_tokens[b].
  *
  *   k_bf16, v_bf16  [tokens, heads, head_dim] bf16 outputs, strides as for h3fp4_rope_axes; one of the
- *                   two may be NULL
+ *                   two may be NULL.  They have no element in common (else H3FP4_ERR_UNSUPPORTED): of
+ *                   the same strides they may be interleaved, of others their ranges are apart
  */
 H3FP4_API h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch, void *k_bf16,
                                            int64_t k_token_stride, int64_t k_head_stride, void *v_bf16,
