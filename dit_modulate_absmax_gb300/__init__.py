@@ -452,13 +452,25 @@ def _raw_stream(stream, t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-class Rope:
+_put = object.__setattr__
+
+
+class _Fixed:
+    """Something whose C structure is packed when it is made: other tensors need another one."""
+
+    __slots__ = ("_struct",)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new {type(self).__name__}")
+
+
+class Rope(_Fixed):
     """Rotary positions of a call's tokens: ``positions`` [tokens, axes] float32,
     ``freqs`` [sum(dims)/2] float64 in radians per unit of position (the pairs of
     axis 0 first), ``dims`` the channels each axis turns, ``layout`` how a pair lies
     in its axis' channels: "interleaved" (2j, 2j+1) or "halves" (j, j + dims/2)."""
 
-    __slots__ = ("positions", "freqs", "dims", "layout", "_struct")
+    __slots__ = ("positions", "freqs", "dims", "layout")
 
     def __init__(self, positions, freqs, dims, layout="interleaved"):
         p, f, n = _need_array(positions, "positions", "f32", 2), _need_array(freqs, "freqs", "f64", 1), len(dims)
@@ -466,9 +478,11 @@ class Rope:
             raise ValueError(f"rope: dims {tuple(dims)}, layout {layout!r} (one of {sorted(ROPE_LAYOUTS)}) with positions "
                              f"{tuple(positions.shape)} and {freqs.shape[0]} frequencies")
         _one_device(positions, freqs)
-        self.positions, self.freqs, self.dims, self.layout = positions, freqs, tuple(dims), layout
-        self._struct = _ROPE.pack(p, positions.shape[1], f, n, *self.dims, *(0,) * (ROPE_MAX_AXES - n),
-                                  ROPE_LAYOUTS[layout], 0)
+        _put(self, "positions", positions)
+        _put(self, "freqs", freqs)
+        _put(self, "dims", tuple(dims))
+        _put(self, "layout", layout)
+        _put(self, "_struct", _ROPE.pack(p, positions.shape[1], f, n, *dims, *(0,) * (ROPE_MAX_AXES - n), ROPE_LAYOUTS[layout], 0))
 
     def struct(self, inverse=False) -> bytes:
         return self._struct[:-8] + struct.pack("@i4x", 1) if inverse else self._struct
@@ -499,11 +513,11 @@ def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
     return out
 
 
-class KVCache:
+class KVCache(_Fixed):
     """Keys and values in E4M3 pages: codes [num_pages, heads, page_size, head_dim]
     uint8 and scales [num_pages, heads] float32, for keys and values each."""
 
-    __slots__ = ("k_codes", "k_scale", "v_codes", "v_scale", "num_pages", "heads", "page_size", "head_dim", "_struct")
+    __slots__ = ("k_codes", "k_scale", "v_codes", "v_scale")
 
     def __init__(self, k_codes, k_scale, v_codes, v_scale):
         kc, vc = _need_array(k_codes, "k_codes", "u8", 4), _need_array(v_codes, "v_codes", "u8", 4)
@@ -513,9 +527,13 @@ class KVCache:
             raise ValueError(f"cache: codes {tuple(shape)} and {tuple(v_codes.shape)} with scales {tuple(k_scale.shape)} and "
                              f"{tuple(v_scale.shape)}")
         _one_device(k_codes, k_scale, v_codes, v_scale)
-        self.k_codes, self.k_scale, self.v_codes, self.v_scale = k_codes, k_scale, v_codes, v_scale
-        self.num_pages, self.heads, self.page_size, self.head_dim = shape
-        self._struct = _KV_CACHE.pack(kc, vc, ks, vs, shape[0], shape[2], shape[1], shape[3])
+        _put(self, "k_codes", k_codes)
+        _put(self, "k_scale", k_scale)
+        _put(self, "v_codes", v_codes)
+        _put(self, "v_scale", v_scale)
+        _put(self, "_struct", _KV_CACHE.pack(kc, vc, ks, vs, shape[0], shape[2], shape[1], shape[3]))
+
+    num_pages, heads, page_size, head_dim = (property(lambda self, i=i: self.k_codes.shape[i]) for i in range(4))
 
     @classmethod
     def empty(cls, num_pages, page_size, heads, head_dim, device="cuda"):

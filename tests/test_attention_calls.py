@@ -153,3 +153,18 @@ def test_a_workspace_with_gaps_is_refused(calls, shape, stride):
         pkg.kv_attention(_x(), _cache(), Fake(1, 4), Fake(1), Fake(2), 3, 64, out=_x(at=0x90000),
                          workspace=Fake(*shape, dtype=torch.uint8, stride=stride))
     assert not calls
+
+
+def test_a_cache_or_rotation_does_not_change_its_tensors():
+    """The addresses that the kernels get are those of the tensors it was made of: another tensor put in their place would
+    be ignored, and the old one's memory used after it is freed."""
+    rope = pkg.Rope(Fake(3, 1, dtype=torch.float32), Fake(32, dtype=torch.float64), (64,))
+    cache = _cache()
+    for of, names in ((rope, ("positions", "freqs", "dims", "layout")), (cache, ("k_codes", "k_scale", "v_codes", "v_scale", "heads"))):
+        for name in names:
+            before = getattr(of, name)
+            with pytest.raises(AttributeError):
+                setattr(of, name, before)
+            assert getattr(of, name) is before
+    assert (cache.num_pages, cache.heads, cache.page_size, cache.head_dim) == (4, 2, 16, 64)
+    assert (rope.dims, rope.layout) == ((64,), "interleaved")
