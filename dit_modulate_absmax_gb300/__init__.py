@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 
@@ -108,11 +109,10 @@ def _call(name: str, *args) -> None:
         raise H3FP4Error(name, st)
 
 
-def _need_int32(func: str, *values) -> None:
-    """ctypes drops the high bits of an integer that does not fit, without a word."""
-    for v in values:
-        if not -0x80000000 <= v <= 0x7FFFFFFF:
-            raise H3FP4Error(func, 3)
+def _too_large(func: str):
+    """For 32-bit arguments whose `or` does not fit: ctypes drops high bits without a word.  (A negative one could hide a
+    large one there, but negative ones are refused by the C entry in any case.)"""
+    return H3FP4Error(func, 3)
 
 
 def _offsets(seg_row_offsets):
@@ -196,7 +196,8 @@ def h3fp4_diag_gemm_wait_timeout(a_q, a_sf, a_ts, b_q, b_sf, b_ts, c, ldc, m, m_
 def h3fp4_rope_axes(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads, head_dim,
                     rope, stream=0):
     """`rope` (and `cache`, `batch` below): the structure's bytes, or None where the C entry takes NULL."""
-    _need_int32("h3fp4_rope_axes", heads, head_dim)
+    if not -1 <= (heads | head_dim) >> 31 <= 0:
+        raise _too_large("h3fp4_rope_axes")
     _call("h3fp4_rope_axes", x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads,
           head_dim, rope, stream)
 
@@ -215,13 +216,15 @@ def h3fp4_kv_cache_read(cache, batch, k, k_token_stride, k_head_stride, v, v_tok
 
 def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens, heads,
                        cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream=0):
-    _need_int32("h3fp4_kv_attention", heads, max_kv, causal, window)
+    if not -1 <= (heads | max_kv | causal | window) >> 31 <= 0:
+        raise _too_large("h3fp4_kv_attention")
     _call("h3fp4_kv_attention", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
           heads, cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream)
 
 
 def h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv) -> int:
-    _need_int32("h3fp4_kv_attention_workspace", heads, kv_heads, head_dim, batch, max_tokens, max_kv)
+    if not -1 <= (heads | kv_heads | head_dim | batch | max_tokens | max_kv) >> 31 <= 0:
+        raise _too_large("h3fp4_kv_attention_workspace")
     n = lib().h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv)
     if n < 0:
         raise H3FP4Error("h3fp4_kv_attention_workspace", 3)
@@ -249,15 +252,15 @@ def _stream(stream):
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
-def _empty(stream, *shape, **kw):
+def _empty(stream, *shape, dtype, device):
     """Uninitialised memory that belongs to the stream the call's kernels run on (None: torch's current one).  torch's
     allocator hands a block out again in the order of its own stream: a block of another stream may still be in use
     there, or come into use again before these kernels have finished with it."""
     import torch
     if stream is None:
-        return torch.empty(*shape, **kw)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(*shape, **kw)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def _need_cuda(*ts):
@@ -415,34 +418,32 @@ def _dtypes():
     return _types
 
 
-def _need_array(t, name, dtype, ndim):
-    """A contiguous device array of this element type; returns its address."""
-    if not (t.is_cuda and t.dtype is _dtypes()[dtype] and t.dim() == ndim and t.is_contiguous()):
-        _refuse(t, name, f"a contiguous {ndim}-D {_dtypes()[dtype]} tensor")
+def _need_array(t, name, dtype, ndim, device):
+    """A contiguous array of this element type on the device; returns its address."""
+    if not (t.get_device() == device >= 0 and t.dtype is _dtypes()[dtype] and t.dim() == ndim and t.is_contiguous()):
+        _refuse(t, name, f"a contiguous {ndim}-D {_dtypes()[dtype]} tensor", device)
     return t.data_ptr()
 
 
-def _need_tokens(t, name, shape=None):
-    """A [tokens, heads, head_dim] array of bf16 values or patterns; returns its address and strides."""
-    s = t.stride()
-    if not (t.is_cuda and t.dtype in _dtypes()["bf16"] and len(s) == 3 and (s[2] == 1 or t.shape[2] == 1)
+def _need_tokens(t, name, shape=None, device=None):
+    """A [tokens, heads, head_dim] array of bf16 values or patterns on the device (None: any); returns its address and
+    strides."""
+    s, at = t.stride(), t.get_device()
+    if not (at >= 0 and (at == device or device is None) and t.dtype in _dtypes()["bf16"] and len(s) == 3 and (s[2] == 1 or t.shape[2] == 1)
             and (shape is None or t.shape == shape)):
         _refuse(t, name, f"a [tokens, heads, head_dim] tensor {'' if shape is None else tuple(shape)} of bf16 values "
-                         "(bfloat16 or int16) with contiguous channels")
+                         "(bfloat16 or int16) with contiguous channels", -1 if device is None else device)
     return t.data_ptr(), s[0], s[1]
 
 
-def _refuse(t, name, what):
-    raise ValueError(f"{name}: {what} on a CUDA device is wanted, got {tuple(t.shape)} {t.dtype} strides {t.stride()} on "
-                     f"{t.device}")
+def _need_device(of, name, device):
+    if of._device != device:
+        raise ValueError(f"{name}: its tensors lie on CUDA device {of._device}, the call's on {device}")
 
 
-def _one_device(*ts):
-    device = ts[0].get_device()
-    for t in ts:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"the call's tensors lie on devices {device} and {t.get_device()}")
-    return device
+def _refuse(t, name, what, device):
+    raise ValueError(f"{name}: {what} on {'a CUDA device' if device < 0 else f'CUDA device {device}'} is wanted, got "
+                     f"{tuple(t.shape)} {t.dtype} strides {t.stride()} on {t.device}")
 
 
 def _raw_stream(stream, t):
@@ -452,37 +453,29 @@ def _raw_stream(stream, t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-_put = object.__setattr__
+def _fixed(*names):
+    """Attributes that are set once, in __init__, under a leading underscore: the C structure is packed there too, and
+    another tensor in their place would need another one."""
+    return (property(operator.attrgetter("_" + n)) for n in names)
 
 
-class _Fixed:
-    """Something whose C structure is packed when it is made: other tensors need another one."""
-
-    __slots__ = ("_struct",)
-
-    def __setattr__(self, name, value):
-        raise AttributeError(f"{type(self).__name__}.{name} is fixed: make a new {type(self).__name__}")
-
-
-class Rope(_Fixed):
+class Rope:
     """Rotary positions of a call's tokens: ``positions`` [tokens, axes] float32,
     ``freqs`` [sum(dims)/2] float64 in radians per unit of position (the pairs of
     axis 0 first), ``dims`` the channels each axis turns, ``layout`` how a pair lies
     in its axis' channels: "interleaved" (2j, 2j+1) or "halves" (j, j + dims/2)."""
 
-    __slots__ = ("positions", "freqs", "dims", "layout")
+    __slots__ = ("_positions", "_freqs", "_dims", "_layout", "_device", "_struct")
+    positions, freqs, dims, layout, device = _fixed("positions", "freqs", "dims", "layout", "device")
 
     def __init__(self, positions, freqs, dims, layout="interleaved"):
-        p, f, n = _need_array(positions, "positions", "f32", 2), _need_array(freqs, "freqs", "f64", 1), len(dims)
+        device, n = positions.get_device(), len(dims)
+        p, f = _need_array(positions, "positions", "f32", 2, device), _need_array(freqs, "freqs", "f64", 1, device)
         if not 1 <= n <= ROPE_MAX_AXES or positions.shape[1] < n or 2 * freqs.shape[0] < sum(dims) or layout not in ROPE_LAYOUTS:
             raise ValueError(f"rope: dims {tuple(dims)}, layout {layout!r} (one of {sorted(ROPE_LAYOUTS)}) with positions "
                              f"{tuple(positions.shape)} and {freqs.shape[0]} frequencies")
-        _one_device(positions, freqs)
-        _put(self, "positions", positions)
-        _put(self, "freqs", freqs)
-        _put(self, "dims", tuple(dims))
-        _put(self, "layout", layout)
-        _put(self, "_struct", _ROPE.pack(p, positions.shape[1], f, n, *dims, *(0,) * (ROPE_MAX_AXES - n), ROPE_LAYOUTS[layout], 0))
+        self._positions, self._freqs, self._dims, self._layout, self._device = positions, freqs, tuple(dims), layout, device
+        self._struct = _ROPE.pack(p, positions.shape[1], f, n, *dims, *(0,) * (ROPE_MAX_AXES - n), ROPE_LAYOUTS[layout], 0)
 
     def struct(self, inverse=False) -> bytes:
         return self._struct[:-8] + struct.pack("@i4x", 1) if inverse else self._struct
@@ -494,46 +487,44 @@ def rope_frequencies(dims, theta=10000.0, device="cuda"):
     return torch.cat([theta ** (-torch.arange(0, d, 2, dtype=torch.float64) / max(d, 1)) for d in dims]).to(device)
 
 
-def _positions_for(rope, tokens):
-    if rope.positions.shape[0] < tokens:
-        raise ValueError(f"rope: {rope.positions.shape[0]} positions for {tokens} tokens")
+def _positions_for(rope, tokens, device):
+    _need_device(rope, "rope", device)
+    if rope._positions.shape[0] < tokens:
+        raise ValueError(f"rope: {rope._positions.shape[0]} positions for {tokens} tokens")
 
 
 def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
     """x [tokens, heads, head_dim] turned by its tokens' positions; inverse=True turns
     back (and is the gradient).  out=x works in place.  Returns out."""
-    import torch
-    xs, shape = _need_tokens(x, "x"), x.shape
-    _positions_for(rope, shape[0])
+    device, shape = x.get_device(), x.shape
+    xs = _need_tokens(x, "x")
+    _positions_for(rope, shape[0], device)
     if out is None:
-        out = _empty(stream, shape, dtype=x.dtype, device=x.device)
-    outs = _need_tokens(out, "out", shape)
-    _one_device(x, out, rope.positions)
-    h3fp4_rope_axes(*xs, *outs, *shape, rope.struct(inverse), _raw_stream(stream, x))
+        out = x.new_empty(shape) if stream is None else _empty(stream, shape, dtype=x.dtype, device=x.device)
+    h3fp4_rope_axes(*xs, *_need_tokens(out, "out", shape, device), *shape, rope.struct(inverse), _raw_stream(stream, x))
     return out
 
 
-class KVCache(_Fixed):
+class KVCache:
     """Keys and values in E4M3 pages: codes [num_pages, heads, page_size, head_dim]
     uint8 and scales [num_pages, heads] float32, for keys and values each."""
 
-    __slots__ = ("k_codes", "k_scale", "v_codes", "v_scale")
+    __slots__ = ("_k_codes", "_k_scale", "_v_codes", "_v_scale", "_num_pages", "_heads", "_page_size", "_head_dim", "_device",
+                 "_struct")
+    k_codes, k_scale, v_codes, v_scale = _fixed("k_codes", "k_scale", "v_codes", "v_scale")
+    num_pages, heads, page_size, head_dim, device = _fixed("num_pages", "heads", "page_size", "head_dim", "device")
 
     def __init__(self, k_codes, k_scale, v_codes, v_scale):
-        kc, vc = _need_array(k_codes, "k_codes", "u8", 4), _need_array(v_codes, "v_codes", "u8", 4)
-        ks, vs = _need_array(k_scale, "k_scale", "f32", 2), _need_array(v_scale, "v_scale", "f32", 2)
+        device = k_codes.get_device()
+        kc, vc = _need_array(k_codes, "k_codes", "u8", 4, device), _need_array(v_codes, "v_codes", "u8", 4, device)
+        ks, vs = _need_array(k_scale, "k_scale", "f32", 2, device), _need_array(v_scale, "v_scale", "f32", 2, device)
         shape = k_codes.shape
         if v_codes.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
             raise ValueError(f"cache: codes {tuple(shape)} and {tuple(v_codes.shape)} with scales {tuple(k_scale.shape)} and "
                              f"{tuple(v_scale.shape)}")
-        _one_device(k_codes, k_scale, v_codes, v_scale)
-        _put(self, "k_codes", k_codes)
-        _put(self, "k_scale", k_scale)
-        _put(self, "v_codes", v_codes)
-        _put(self, "v_scale", v_scale)
-        _put(self, "_struct", _KV_CACHE.pack(kc, vc, ks, vs, shape[0], shape[2], shape[1], shape[3]))
-
-    num_pages, heads, page_size, head_dim = (property(lambda self, i=i: self.k_codes.shape[i]) for i in range(4))
+        self._k_codes, self._k_scale, self._v_codes, self._v_scale, self._device = k_codes, k_scale, v_codes, v_scale, device
+        self._num_pages, self._heads, self._page_size, self._head_dim = shape
+        self._struct = _KV_CACHE.pack(kc, vc, ks, vs, shape[0], shape[2], shape[1], shape[3])
 
     @classmethod
     def empty(cls, num_pages, page_size, heads, head_dim, device="cuda"):
@@ -547,12 +538,12 @@ class KVCache(_Fixed):
         return self._struct
 
 
-def _kv_batch(page_table, length, cu_tokens, max_tokens) -> bytes:
-    table, cu = _need_array(page_table, "page_table", "i32", 2), _need_array(cu_tokens, "cu_tokens", "i32", 1)
+def _kv_batch(page_table, length, cu_tokens, max_tokens, device) -> bytes:
+    table, cu = _need_array(page_table, "page_table", "i32", 2, device), _need_array(cu_tokens, "cu_tokens", "i32", 1, device)
     batch, pages = page_table.shape
     n = 0
     if length is not None:
-        n = _need_array(length, "lengths", "i32", 1)
+        n = _need_array(length, "lengths", "i32", 1, device)
     if cu_tokens.shape[0] != batch + 1 or (length is not None and length.shape[0] != batch):
         raise ValueError(f"page_table has {batch} sequences: cu_tokens of {batch + 1} and lengths of {batch} are wanted, got "
                          f"{cu_tokens.shape[0]} and {None if length is None else length.shape[0]}")
@@ -566,15 +557,13 @@ def kv_cache_write(cache: KVCache, k, v, page_table, held, cu_tokens, max_tokens
     (page_table [batch, pages], held [batch], cu_tokens [batch+1]: device int32);
     max_tokens is the most new tokens of any sequence.  With ``rope`` the keys are
     turned first.  The caller advances its lengths."""
-    shape = (k.shape[0], cache.heads, cache.head_dim)
-    ks, vs = _need_tokens(k, "k", shape), _need_tokens(v, "v", shape)
+    device, shape = cache._device, (k.shape[0], cache._heads, cache._head_dim)
+    ks, vs = _need_tokens(k, "k", shape, device), _need_tokens(v, "v", shape, device)
     if held is None:
         raise ValueError("held: lengths before the call are wanted")
     if rope is not None:
-        _positions_for(rope, shape[0])
-    batch = _kv_batch(page_table, held, cu_tokens, max_tokens)
-    _one_device(k, v, cache.k_codes, page_table, held, cu_tokens, rope and rope.positions)
-    h3fp4_kv_cache_write(cache._struct, batch, *ks, *vs, shape[0],
+        _positions_for(rope, shape[0], device)
+    h3fp4_kv_cache_write(cache._struct, _kv_batch(page_table, held, cu_tokens, max_tokens, device), *ks, *vs, shape[0],
                          rope._struct if rope is not None else None, _raw_stream(stream, k))
 
 
@@ -583,14 +572,15 @@ def kv_cache_read(cache: KVCache, page_table, start, cu_tokens, tokens, max_toke
     None: from 0), into rows cu_tokens[b] .. cu_tokens[b+1]-1 of [tokens, heads,
     head_dim] outputs.  Returns (k, v)."""
     import torch
-    shape = (tokens, cache.heads, cache.head_dim)
+    shape = (tokens, cache._heads, cache._head_dim)
     if k is None:
-        k = _empty(stream, shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+        k = _empty(stream, shape, dtype=torch.bfloat16, device=cache._k_codes.device)
     if v is None:
-        v = _empty(stream, shape, dtype=torch.bfloat16, device=cache.k_codes.device)
-    batch, ks, vs = _kv_batch(page_table, start, cu_tokens, max_tokens), _need_tokens(k, "k", shape), _need_tokens(v, "v", shape)
-    _one_device(k, v, cache.k_codes, page_table, start, cu_tokens)
-    h3fp4_kv_cache_read(cache._struct, batch, *ks, *vs, tokens, _raw_stream(stream, k))
+        v = _empty(stream, shape, dtype=torch.bfloat16, device=cache._k_codes.device)
+    device = cache._device
+    h3fp4_kv_cache_read(cache._struct, _kv_batch(page_table, start, cu_tokens, max_tokens, device),
+                        *_need_tokens(k, "k", shape, device), *_need_tokens(v, "v", shape, device), tokens,
+                        _raw_stream(stream, k))
     return k, v
 
 
@@ -607,31 +597,32 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
     before it (window > 0).  scale defaults to head_dim ** -0.5.  Returns (out, lse); lse
     [tokens, heads] float32 is None unless asked for."""
     import torch
-    qs, shape = _need_tokens(q, "q"), q.shape
+    device, shape = q.get_device(), q.shape
+    qs = _need_tokens(q, "q")
+    _need_device(cache, "cache", device)
     tokens, heads, dim = shape
-    if dim != cache.head_dim or heads % cache.heads or kv_len is None:
+    if dim != cache._head_dim or heads % cache._heads or kv_len is None:
         raise ValueError(f"q: {heads} heads of {dim} for a cache of {cache.heads} heads of {cache.head_dim}"
                          if kv_len is not None else "kv_len: lengths are wanted")
     if out is None:
-        out = _empty(stream, shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(shape) if stream is None else _empty(stream, shape, dtype=q.dtype, device=q.device)
     if lse is None and return_lse:
         lse = _empty(stream, tokens, heads, dtype=torch.float32, device=q.device)
     lse_at = None
     if lse is not None:
-        lse_at = _need_array(lse, "lse", "f32", 2)
+        lse_at = _need_array(lse, "lse", "f32", 2, device)
         if lse.shape != (tokens, heads):
-            _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor")
-    batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens)
-    device = _one_device(q, out, lse, cache.k_codes, page_table, kv_len, cu_tokens, workspace)
-    need = _attention_workspace(device, tokens, heads, cache.heads, dim, page_table.shape[0], max_tokens, max_kv)
+            _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor", device)
+    batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
+    need = _attention_workspace(device, tokens, heads, cache._heads, dim, page_table.shape[0], max_tokens, max_kv)
     at = have = 0
     if workspace is not None:
-        if not workspace.is_contiguous():        # its bytes are written as they lie
-            _refuse(workspace, "workspace", "a contiguous tensor")
+        if workspace.get_device() != device or not workspace.is_contiguous():   # (its bytes are written as they lie)
+            _refuse(workspace, "workspace", "a contiguous tensor", device)
         at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
         workspace, have = _empty(stream, need, dtype=torch.uint8, device=q.device), need
         at = workspace.data_ptr()
-    h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape), lse_at, tokens, heads, cache._struct, batch, max_kv,
+    h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, batch, max_kv,
                        dim ** -0.5 if scale is None else scale, causal, window, at, have, _raw_stream(stream, q))
     return out, lse
