@@ -49,6 +49,8 @@ _SIGNATURES = {
     "h3fp4_kv_cache_read": ([_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _P], _STATUS),
     "h3fp4_kv_attention": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _I32, ctypes.c_float, _I32, _I32,
                             _P, _I64, _P], _STATUS),
+    "h3fp4_diag_attention_wait_timeout": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _I32, _P, _I64,
+                                           ctypes.c_uint32, _P], _STATUS),
     "h3fp4_kv_attention_workspace": ([_I64, _I32, _I32, _I32, _I32, _I32, _I32], _I64),
     "h3fp4_status_string": ([_STATUS], ctypes.c_char_p),
     "h3fp4_build_info": ([], ctypes.c_char_p),
@@ -220,6 +222,13 @@ def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, 
         raise _too_large("h3fp4_kv_attention")
     _call("h3fp4_kv_attention", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
           heads, cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream)
+
+
+def h3fp4_diag_attention_wait_timeout(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
+                                      heads, cache, batch, max_kv, workspace, workspace_bytes, limit_us, stream=0):
+    """Runs few-query attention with copies that never complete (failure detection, see h3fp4.h)."""
+    _call("h3fp4_diag_attention_wait_timeout", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse,
+          tokens, heads, cache, batch, max_kv, workspace, workspace_bytes, limit_us, stream)
 
 
 def h3fp4_kv_attention_workspace(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv) -> int:

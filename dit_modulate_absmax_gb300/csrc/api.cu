@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <optional>
 
 #include "h3fp4.h"
 #include "launch.h"
@@ -457,11 +458,13 @@ int64_t h3fp4_kv_attention_workspace(int64_t tokens, int32_t heads, int32_t kv_h
     return h3fp4::attention_workspace(h3fp4::AttnShape{tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv});
 }
 
-h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, void *out_bf16,
-                                int64_t out_token_stride, int64_t out_head_stride, float *lse, int64_t tokens,
-                                int32_t heads, const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch,
-                                int32_t max_kv, float softmax_scale, int32_t causal, int32_t window, void *workspace,
-                                int64_t workspace_bytes, void *stream)
+namespace {
+
+// Checks of an attention call; *out is set where there is something to do.
+h3fp4_status check_attention(const Strided &q, const Strided &out, float *lse, int64_t tokens, int32_t heads,
+                             const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch, int32_t max_kv,
+                             float softmax_scale, int32_t causal, int32_t window, const void *workspace,
+                             int64_t workspace_bytes, std::optional<h3fp4::AttnArgs> *args)
 {
     h3fp4_status s = check_cache(cache);
     if (s != H3FP4_OK || (s = check_batch(batch, true, tokens)) != H3FP4_OK)
@@ -471,7 +474,6 @@ h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int6
         return H3FP4_ERR_SHAPE;
     if (batch->batch == 0 || tokens == 0 || batch->max_tokens == 0)
         return H3FP4_OK;
-    const Strided q{q_bf16, q_token_stride, q_head_stride}, out{out_bf16, out_token_stride, out_head_stride};
     if ((s = check_strided(q)) != H3FP4_OK ||
         (s = check_strided_out(out, tokens, heads, cache->head_dim)) != H3FP4_OK)
         return s;
@@ -485,10 +487,26 @@ h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int6
         return H3FP4_ERR_SHAPE;
     if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
         return H3FP4_ERR_ALIGN;
-    const h3fp4::AttnArgs a{static_cast<const uint16_t *>(q_bf16), q.token, q.head, static_cast<uint16_t *>(out_bf16),
-                            out.token, out.head, lse, tokens, heads, *cache, *batch, max_kv, softmax_scale, causal,
+    *args = h3fp4::AttnArgs{static_cast<const uint16_t *>(q.p), q.token, q.head,
+                            static_cast<uint16_t *>(const_cast<void *>(out.p)), out.token, out.head, lse, tokens, heads,
+                            *cache, *batch, max_kv, softmax_scale, causal,
                             window > max_kv ? 0 : window};   // a window past every position hides nothing
-    return from_cuda(h3fp4::launch_attention(a, workspace, as_stream(stream)));
+    return H3FP4_OK;
+}
+
+}  // namespace
+
+h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, void *out_bf16,
+                                int64_t out_token_stride, int64_t out_head_stride, float *lse, int64_t tokens,
+                                int32_t heads, const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch,
+                                int32_t max_kv, float softmax_scale, int32_t causal, int32_t window, void *workspace,
+                                int64_t workspace_bytes, void *stream)
+{
+    std::optional<h3fp4::AttnArgs> a;
+    const h3fp4_status s = check_attention({q_bf16, q_token_stride, q_head_stride},
+                                           {out_bf16, out_token_stride, out_head_stride}, lse, tokens, heads, cache, batch,
+                                           max_kv, softmax_scale, causal, window, workspace, workspace_bytes, &a);
+    return a ? from_cuda(h3fp4::launch_attention(*a, workspace, as_stream(stream))) : s;
 }
 
 h3fp4_status h3fp4_swizzle_scales(const uint8_t *sf_logical, int64_t rows, int64_t cols, int64_t ld,
@@ -537,6 +555,26 @@ h3fp4_status h3fp4_diag_gemm_wait_timeout(const uint8_t *a_q, const uint8_t *a_s
     return h3fp4::launch_gemm_wait_timeout(a_q, a_sf, a_tensor_scale, b_q, b_sf, b_tensor_scale,
                                            static_cast<uint16_t *>(c_bf16), ldc, m, m_pad, n, k,
                                            static_cast<uint64_t>(limit_us) * 1000u, as_stream(stream));
+}
+
+h3fp4_status h3fp4_diag_attention_wait_timeout(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                                               void *out_bf16, int64_t out_token_stride, int64_t out_head_stride,
+                                               float *lse, int64_t tokens, int32_t heads, const h3fp4_kv_cache *cache,
+                                               const h3fp4_kv_batch *batch, int32_t max_kv, void *workspace,
+                                               int64_t workspace_bytes, uint32_t limit_us, void *stream)
+{
+    std::optional<h3fp4::AttnArgs> a;
+    const h3fp4_status s = check_attention({q_bf16, q_token_stride, q_head_stride},
+                                           {out_bf16, out_token_stride, out_head_stride}, lse, tokens, heads, cache, batch,
+                                           max_kv, 1.0f, 0, 0, workspace, workspace_bytes, &a);
+    if (s != H3FP4_OK || !a)
+        return s;
+    if (limit_us == 0 || limit_us > 2000000u)
+        return H3FP4_ERR_SHAPE;
+    if (!h3fp4::attention_timeout_ok(*a))
+        return H3FP4_ERR_UNSUPPORTED;
+    return from_cuda(h3fp4::launch_attention_wait_timeout(*a, workspace, static_cast<uint64_t>(limit_us) * 1000u,
+                                                          as_stream(stream)));
 }
 
 h3fp4_status h3fp4_device_error(uint32_t *code)

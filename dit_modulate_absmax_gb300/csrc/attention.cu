@@ -15,6 +15,12 @@ constexpr int64_t kMostRows = 32;
 
 bool few_rows(const AttnShape &s) { return static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads) <= kMostRows; }
 
+AttnShape shape_of(const AttnArgs &a)
+{
+    return AttnShape{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv,
+                     a.causal ? a.window : 0};
+}
+
 SplitPlan plan_of(const AttnShape &s) { return few_rows(s) ? plan_rows(s) : plan_tile(s); }
 
 }  // namespace
@@ -27,13 +33,24 @@ int64_t attention_workspace(const AttnShape &s)
 
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st)
 {
-    const AttnShape s{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv,
-                      a.causal ? a.window : 0};   // (the parts are no more than without: the workspace does for both)
+    const AttnShape s = shape_of(a);   // (the parts are no more than without the reach: the workspace does for both)
     const SplitPlan plan = plan_of(s);
     float *part = static_cast<float *>(workspace);
     float *stat = part + plan.part_rows * s.head_dim;
     return few_rows(s) ? launch_attention_rows(a, plan, stat, part, st)
                        : launch_attention_tile(a, plan, reinterpret_cast<float2 *>(stat), part, st);
+}
+
+bool attention_timeout_ok(const AttnArgs &a)
+{
+    return a.cache.head_dim == 128 && int64_t(a.batch.max_tokens) * (a.heads / a.cache.heads) <= 8;
+}
+
+cudaError_t launch_attention_wait_timeout(const AttnArgs &a, void *workspace, uint64_t wait_ns, cudaStream_t st)
+{
+    const SplitPlan plan = plan_of(shape_of(a));
+    float *part = static_cast<float *>(workspace);
+    return launch_attention_rows_timeout(a, plan, part + plan.part_rows * a.cache.head_dim, part, wait_ns, st);
 }
 
 cudaError_t read_attention_error(uint32_t *code)

@@ -143,6 +143,8 @@ struct SplitPlan {
 
 SplitPlan plan_rows(const AttnShape &s);
 cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st);
+cudaError_t launch_attention_rows_timeout(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, uint64_t wait_ns,
+                                          cudaStream_t st);   // 128 channels, 8 rows at most
 SplitPlan plan_tile(const AttnShape &s);
 cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
 cudaError_t read_attention_tile_error(uint32_t *code);

@@ -113,10 +113,11 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
 // CTA of unit x:
 __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) { return divide((x + 1) * g - 1, total); }
 
-template <int kDim, int kRows>
+// kWithhold: for a check that waits end.  Each copy is announced larger than it is, so that none completes.
+template <int kDim, int kRows, bool kWithhold = false>
 __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     rows_kernel(AttnArgs a, SplitPlan plan, float *ws_log, float *ws_out, const __grid_constant__ CUtensorMap k_map,
-                const __grid_constant__ CUtensorMap v_map)
+                const __grid_constant__ CUtensorMap v_map, uint64_t wait_ns)
 {
     constexpr int kSteps = kDim / 16;            // k16 steps of Q K^T = 16-channel tiles of O^T
     constexpr int kHalf = kRows / 8;             // groups of 8 rows
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     }
     int stage = 0;
     uint32_t parity = 0;
+    bool ok = true;   // of a warp: no wait has given up
     const int64_t x_first = x;
     while (x < x_end) {   // the same in every thread
     // The segment that unit x begins: a sequence, a row tile, a cache head and tokens [seg_begin, seg_end).
@@ -304,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     for (int begin = seg_begin; begin < seg_end; begin += kCap) {
     const int end = min(seg_end, begin + kCap);
     const int page0 = begin >> shift, pages = ((end - 1) >> shift) - page0 + 1;
-    __syncthreads();   // the last part's readers are done
+    if (__syncthreads_or(!ok))   // the last part's readers are done
+        break;
     for (int i = threadIdx.x; i < pages; i += kThreads) {
         int32_t id = begin == seg_begin && i < kThreads ? first_id : a.batch.page_table[b * a.batch.ld_table + page0 + i];
         // Units begin at multiples of 32 tokens, so that a page of 16 may lie before all that the rows see: whatever the
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         const uint32_t bar = smem_u32(&full[warp][stage]), dst = ring + stage * (2 * kTile);
         const int at = (unit >> shift) - page0;
         const int32_t id0 = entry[at].id, id1 = page < kUnit && unit + page < end ? entry[at + 1].id : -1;
-        mbar_arrive_expect_tx(bar, ((id0 >= 0) + (id1 >= 0)) * 2 * box * kDim);
+        mbar_arrive_expect_tx(bar, ((id0 >= 0) + (id1 >= 0)) * 2 * box * kDim + (kWithhold ? 16 : 0));
         if (id0 >= 0) {
             tma_load_3d(dst, &k_map, 0, unit & (page - 1), id0 * heads + kh, bar);
             tma_load_3d(dst + kTile, &v_map, 0, unit & (page - 1), id0 * heads + kh, bar);
@@ -370,8 +373,15 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         __syncwarp();
     }
     for (int unit = unit0; unit < end; unit += kTokens) {
-        if (!mbar_wait_bounded(smem_u32(&full[warp][stage]), parity, kWaitNs))
-            atomicOr(&g_error, ERR_ATTN_WAIT);   // the copies have not come: go on, the outputs mean nothing
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&full[warp][stage]), parity, wait_ns))) {
+            // The copies have not come: the CTA ends, once those of this warp that are on their way had as long again.
+            ok = false;
+            const int other = (stage + 1) % kStages;
+            mbar_wait_bounded(smem_u32(&full[warp][stage]), parity, wait_ns);
+            if (unit + kTokens < end)
+                mbar_wait_bounded(smem_u32(&full[warp][other]), parity ^ (other == 0), wait_ns);
+            break;
+        }
         const uint8_t *kt = dyn + warp * (kStages * 2 * kTile) + stage * (2 * kTile), *vt = kt + kTile;
 
         float sc[4][4];   // S of the unit's four groups of 8 tokens
@@ -575,7 +585,15 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             o[hf][j][3] *= f1;
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(!ok)) {   // the same in the whole CTA; what it would have written stays as it was
+        if (threadIdx.x == 0)
+            atomicOr(&g_error, ERR_ATTN_WAIT);
+        if (plan.cluster) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
     float *part = reinterpret_cast<float *>(dyn);   // [warp][row][kDim]
 #pragma unroll
     for (int hf = 0; hf < kHalf; ++hf)
@@ -791,12 +809,12 @@ bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kDim, int kRows>
-cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
+template <int kDim, int kRows, bool kWithhold = false>
+cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st, uint64_t wait_ns = kWaitNs)
 {
     constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = (kWarps + 1) * kRows * kDim * 4 + kRows * 4;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-    cudaError_t e = allow_shared<rows_kernel<kDim, kRows>>(kSmem);
+    cudaError_t e = allow_shared<rows_kernel<kDim, kRows, kWithhold>>(kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap k_map, v_map;
@@ -825,8 +843,8 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
     attr.val.clusterDim.x = static_cast<unsigned>(plan.splits);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.numAttrs = plan.cluster ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows>, a, plan, logs, part, k_map, v_map);
-    if (e != cudaSuccess || plan.cluster)
+    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows, kWithhold>, a, plan, logs, part, k_map, v_map, wait_ns);
+    if (e != cudaSuccess || plan.cluster || kWithhold)
         return e;
     // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
     cfg.gridDim = dim3(static_cast<unsigned>(joins), static_cast<unsigned>(a.batch.batch));
@@ -847,6 +865,12 @@ cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, floa
     if (a.cache.head_dim == 64)
         return small ? run_rows<64, 8>(a, plan, logs, part, st) : run_rows<64, 16>(a, plan, logs, part, st);
     return small ? run_rows<128, 8>(a, plan, logs, part, st) : run_rows<128, 16>(a, plan, logs, part, st);
+}
+
+cudaError_t launch_attention_rows_timeout(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, uint64_t wait_ns,
+                                          cudaStream_t st)
+{
+    return run_rows<128, 8, true>(a, plan, logs, part, st, wait_ns);
 }
 
 cudaError_t read_attention_rows_error(uint32_t *code)

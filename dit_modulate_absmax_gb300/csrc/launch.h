@@ -138,6 +138,10 @@ struct AttnShape {
 int64_t attention_workspace(const AttnShape &s);
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st);
 
+// Failure detection: few queries with copies that never complete.
+bool attention_timeout_ok(const AttnArgs &a);
+cudaError_t launch_attention_wait_timeout(const AttnArgs &a, void *workspace, uint64_t wait_ns, cudaStream_t st);
+
 cudaError_t read_kvcache_error(uint32_t *code);
 cudaError_t read_attention_error(uint32_t *code);
 

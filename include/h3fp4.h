@@ -507,6 +507,14 @@ H3FP4_API h3fp4_status h3fp4_device_error(uint32_t *code);
  * withheld: the scale-copy, MMA and epilogue warps' waits run out after
  * limit_us and record bits 16, 2 and 4.  c_bf16 is not written and no
  * operand is read.
+ *
+ * h3fp4_diag_attention_wait_timeout -- the attention kernel of few queries
+ * (arguments and checks of h3fp4_kv_attention, every key seen, a scale of 1;
+ * 128 channels, at most 8 query rows a cache head, else H3FP4_ERR_UNSUPPORTED)
+ * with its copies of the codes announced larger than they are: the first wait
+ * of each warp runs out after limit_us, as do those for the copies still on
+ * their way, and the call ends after about three times limit_us with bit 1,024,
+ * however many keys there are.  out_bf16 and lse are not written.
  */
 H3FP4_API h3fp4_status h3fp4_diag_producer_barrier_timeout(const void *x_bf16, int64_t ldx, int64_t m,
                                                            int64_t m_pad, int64_t d, float *tensor_scale,
@@ -517,6 +525,12 @@ H3FP4_API h3fp4_status h3fp4_diag_gemm_wait_timeout(const uint8_t *a_q, const ui
                                                     const uint8_t *b_sf, const float *b_tensor_scale, void *c_bf16,
                                                     int64_t ldc, int64_t m, int64_t m_pad, int64_t n, int64_t k,
                                                     uint32_t limit_us, void *stream);
+H3FP4_API h3fp4_status h3fp4_diag_attention_wait_timeout(const void *q_bf16, int64_t q_token_stride,
+                                                         int64_t q_head_stride, void *out_bf16,
+                                                         int64_t out_token_stride, int64_t out_head_stride, float *lse,
+                                                         int64_t tokens, int32_t heads, const h3fp4_kv_cache *cache,
+                                                         const h3fp4_kv_batch *batch, int32_t max_kv, void *workspace,
+                                                         int64_t workspace_bytes, uint32_t limit_us, void *stream);
 
 /* Human-readable name of a status code (static string). */
 H3FP4_API const char *h3fp4_status_string(h3fp4_status status);

@@ -168,3 +168,18 @@ def test_a_cache_or_rotation_does_not_change_its_tensors():
             assert getattr(of, name) is before
     assert (cache.num_pages, cache.heads, cache.page_size, cache.head_dim) == (4, 2, 16, 64)
     assert (rope.dims, rope.layout) == ((64,), "interleaved")
+
+
+def test_wait_diagnostic_refusals():
+    """Arguments that are refused before anything is enqueued."""
+    F, G = 0x100000, 0x90000000
+    L = pkg.lib()
+
+    def call(q=F, heads=8, dim=128, most=1, limit=1000, ws=F, have=1 << 40, max_kv=256):
+        cache = pkg._KV_CACHE.pack(F, F, F, F, 4, 64, 8, dim)
+        return L.h3fp4_diag_attention_wait_timeout(q, heads * dim, dim, G, heads * dim, dim, None, 2, heads, cache,
+                                                   pkg._KV_BATCH.pack(F, 4, F, F, 2, most), max_kv, ws, have, limit, None)
+
+    assert call(q=None) == 1 and call(heads=12) == 3 and call(limit=0) == 3 and call(limit=2_000_001) == 3
+    assert call(heads=72) == 4 and call(most=9) == 4 and call(dim=64) == 4 and call(max_kv=-1) == 3
+    assert call(max_kv=1 << 20, ws=None) == 1 and call(max_kv=1 << 20, have=16) == 3
