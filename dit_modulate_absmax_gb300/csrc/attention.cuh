@@ -117,9 +117,8 @@ __device__ __forceinline__ float own_sum(float sum) { return sum > 0.0f ? 1.0f :
 // 2^(log - top), nothing for two that have seen nothing.
 __device__ __forceinline__ float of_top(float log, float top) { return ex2(log - (top == -INFINITY ? 0.0f : top)); }
 
-// A page's table entry as the kernels keep it: id (few rows: < 0 for none;
-// many: 1 if the values' scales so far lie far apart), the keys' scale, log2
-// of the values' scale and its inverse.
+// A page's table entry as the kernels keep it: id (< 0: none), the keys'
+// scale, log2 of the values' scale and its inverse.
 struct PageEntry {
     int32_t id;
     float ks, lv, inv_vs;

@@ -73,6 +73,7 @@ struct __align__(1024) Smem {
     uint64_t drained;
     uint32_t tmem;
     int32_t first_exp;   // exponent of the values' scales in the first step (the largest)
+    int32_t far_from;    // first step with far scales
 };
 
 // Byte offset of 16-byte piece c (8 halves) of row r in the operand layout: blocks of 64 channels, rows of 128 bytes
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < kConvertWarps; ++w)
                 sm.nan_step[i][w] = 0;
         }
+        sm.far_from = INT32_MAX;
         for (int i = 0; i < kEntrySlots; ++i)
             mbar_init(smem_u32(&sm.entry_full[i]), 1);
         mbar_init(smem_u32(&sm.drained), tiles);
@@ -248,14 +250,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int shift = 31 - __clz(page);
             const uint32_t sc = 128u * t + lanes, oc = 256u + static_cast<uint32_t>(kDim) * t + lanes;
             float apart_ref = -INFINITY, apart_l = 0.0f;   // with far scales: a sum against a reference of its own
-            // One step; false: a wait gave up.  kFar: a page of this step or an earlier one has a scale far from the first
-            // ones.  That is a loop of its own, so that it costs the other steps one look at the entry (a chunk's step takes
-            // 2.5 % longer with the second loop behind it; with the choice inside of one loop it took 6 %).
+            // One step; false: a wait gave up, or (kFar false) the first step with far scales has come.  Those that follow are a
+            // loop of their own, so that they cost the others a comparison (a chunk 5,118 us, prompts 99-100; with a choice
+            // inside of one loop 5,420 and 104).
             const auto step = [&](auto far_scales, int j) -> bool {
                 constexpr bool kFar = decltype(far_scales)::value;
                 const int k0 = begin + j * kKeys;
                 const bool edge = k0 < t_lo || k0 + kKeys > t_hi;
-                if (!wait_for(sm.s_full[t], j & 1))
+                if (!wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) || (!kFar && j >= sm.far_from) ||
+                    !wait_for(sm.s_full[t], j & 1))
                     return false;
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
@@ -440,19 +443,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             int j = 0;
-            bool ok = true;
-            for (; ok && j < steps; ++j) {
-                ok = wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1);
-                if (!ok || sm.entry[j % kEntrySlots][0].id != 0)
-                    break;
-                ok = step(std::false_type{}, j);
-            }
+            while (j < steps && step(std::false_type{}, j))
+                ++j;
+            bool ok = j == steps || j >= sm.far_from;
             float o_factor = 1.0f;
             if (ok && j < steps) {
                 apart_ref = ref + lg2(l);
                 apart_l = own_sum(l);
                 for (; ok && j < steps; ++j)
-                    ok = wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) && step(std::true_type{}, j);
+                    ok = step(std::true_type{}, j);
                 o_factor = apart_l > 0.0f ? ex2(ref - apart_ref) : 1.0f;
                 ref = apart_ref;
                 l = apart_l;
@@ -594,9 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sm.first_exp = __reduce_max_sync(0xFFFFFFFFu, lane_id >= 0 ? of_vs : 0);
                     __syncwarp();
                 }
-                const int far = __any_sync(0xFFFFFFFFu, lane_id >= 0 && abs(of_vs - sm.first_exp) > kFarScales);
+                if (__any_sync(0xFFFFFFFFu, lane_id >= 0 && abs(of_vs - sm.first_exp) > kFarScales) && lane == 0)
+                    sm.far_from = min(sm.far_from, j);
                 if (lane < kKeys / page)
-                    sm.entry[j % kEntrySlots][lane] = PageEntry{far, ks, lg2(vs), __frcp_rn(vs)};
+                    sm.entry[j % kEntrySlots][lane] = PageEntry{lane_id, ks, lg2(vs), __frcp_rn(vs)};
                 warp_arrive(sm.entry_full[j % kEntrySlots]);
             }
 #pragma unroll
