@@ -15,11 +15,10 @@
 // the largest probability, stands near the top of FP16's range, and that range
 // serves it whatever the pages' scales.
 // Dividing a page's weights by its scale gives the softmax's own sum -- as long
-// as the values' scales of a part's pages lie within 2^80 of each other.  Where
-// they may not, a key that counts in the sum may have a weight below FP32's
-// smallest; from the first step with such pages on the sum has a reference of
-// its own, the running maximum of S_j * (c * k_scale_P), and exponentials of
-// its own.
+// as the values' scales do not lie too far apart.  Where they may (far_scale),
+// a key that counts in the sum may have a weight below FP32's smallest; from
+// the first step with such a page on the sum has a reference of its own, the
+// running maximum of S_j * (c * k_scale_P), and exponentials of its own.
 //
 // A part of the keys leaves its mean (output over sum) and log2 of its sum, or
 // the sum and its reference; parts are joined as the means weighted by their
@@ -102,11 +101,10 @@ __device__ __forceinline__ uint32_t bf16x2_to_half2(uint32_t w, float f)
     return pack_half2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
 }
 
-// A page's values' scale further than this (log2) from the part's first one: the sum gets a reference of its own.  Up to
-// twice that apart, 2^-126 as the least weight leaves out keys below 2^-46 of the largest probability.
-constexpr int kFarScales = 40;
-
-__device__ __forceinline__ int exponent(float scale) { return static_cast<int>(__float_as_uint(scale) >> 23 & 0xFFu); }
+// Whether a values' scale lies outside [2^-40, 2^41): a part with such a page keeps its sum against a reference of its own.
+// All others lie within 2^81 of each other, where 2^-126 as the least weight leaves out keys below 2^-45 of the largest
+// probability.  (Of the scales that a write sets, those of values from 2^49 on are outside.)
+__device__ __forceinline__ bool far_scale(float scale) { return abs(static_cast<int>(__float_as_uint(scale) >> 23 & 0xFFu) - 127) > 40; }
 
 // 1 / sum; a row that has seen nothing stays zero, NaN stays NaN.
 __device__ __forceinline__ float reciprocal_sum(float sum) { return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f; }

@@ -128,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float part_log[kWarps][16];       // a warp's log2 of the sum of each row
     __shared__ float sum_ref[kWarps][16];        // with far scales: what a warp's sum of a row is kept against
-    __shared__ int scale_lo, scale_hi;           // exponents of the segment's value scales so far
     __shared__ int64_t warp_units[kWarps], found_rest;
     __shared__ int found_b;
 
@@ -297,11 +296,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
 
 
     // In parts whose pages fit the table: their entries, the first copies, then the scales.
-    bool far_scales = false;
-    if (threadIdx.x == 0) {
-        scale_lo = 255;
-        scale_hi = 0;
-    }
+    bool far_scales = false;   // the same in the whole CTA
     constexpr int kCap = (kMaxEntries - 2) * 16 / kTokens * kTokens;
     for (int begin = seg_begin; begin < seg_end; begin += kCap) {
     const int end = min(seg_end, begin + kCap);
@@ -340,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         for (int i = 0; i < kStages; ++i)
             if (unit0 + i * kTokens < end)
                 fetch(unit0 + i * kTokens, (stage + i) % kStages);
-    int lo_exp = 255, hi_exp = 0;
+    bool far = false;
     for (int i = threadIdx.x; i < pages; i += kThreads) {
         const int32_t id = entry[i].id;
         const int64_t bh = static_cast<int64_t>(id) * heads + kh;
@@ -348,19 +343,9 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         entry[i].ks = id >= 0 ? a.cache.k_scale[bh] : 1.0f;
         entry[i].lv = lg2(vs);
         entry[i].inv_vs = __frcp_rn(vs);
-        if (id >= 0) {
-            lo_exp = min(lo_exp, exponent(vs));
-            hi_exp = max(hi_exp, exponent(vs));
-        }
+        far = far || far_scale(vs);
     }
-    lo_exp = __reduce_min_sync(0xFFFFFFFFu, lo_exp);
-    hi_exp = __reduce_max_sync(0xFFFFFFFFu, hi_exp);
-    if (lane == 0 && lo_exp <= hi_exp) {
-        atomicMin(&scale_lo, lo_exp);
-        atomicMax(&scale_hi, hi_exp);
-    }
-    __syncthreads();   // scales
-    if (!far_scales && scale_hi - scale_lo > 2 * kFarScales) {
+    if (__syncthreads_or(far) && !far_scales) {   // scales are there
         far_scales = true;
 #pragma unroll
         for (int hf = 0; hf < kHalf; ++hf) {   // the sum so far, kept against m, becomes 1 against its logarithm
@@ -451,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                 }
             }
         }
-        if (far_scales) {   // the same in the whole CTA
+        if (far_scales) {
 #pragma unroll
             for (int hf = 0; hf < kHalf; ++hf) {
                 float u = -INFINITY, sum = 0.0f;

@@ -72,8 +72,7 @@ struct __align__(1024) Smem {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], entry_full[kEntrySlots];
     uint64_t drained;
     uint32_t tmem;
-    int32_t first_exp;   // exponent of the values' scales in the first step (the largest)
-    int32_t far_from;    // first step with far scales
+    int32_t far_from;   // first step with a far scale
 };
 
 // Byte offset of 16-byte piece c (8 halves) of row r in the operand layout: blocks of 64 channels, rows of 128 bytes
@@ -250,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int shift = 31 - __clz(page);
             const uint32_t sc = 128u * t + lanes, oc = 256u + static_cast<uint32_t>(kDim) * t + lanes;
             float apart_ref = -INFINITY, apart_l = 0.0f;   // with far scales: a sum against a reference of its own
-            // One step; false: a wait gave up, or (kFar false) the first step with far scales has come.  Those that follow are a
+            // One step; false: a wait gave up, or (kFar false) the first step with a far scale has come.  Those that follow are a
             // loop of their own, so that they cost the others a comparison (a chunk 5,118 us, prompts 99-100; with a choice
             // inside of one loop 5,420 and 104).
             const auto step = [&](auto far_scales, int j) -> bool {
@@ -588,12 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_for(sm.k_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
-                const int of_vs = exponent(vs);
-                if (j == 0) {
-                    sm.first_exp = __reduce_max_sync(0xFFFFFFFFu, lane_id >= 0 ? of_vs : 0);
-                    __syncwarp();
-                }
-                if (__any_sync(0xFFFFFFFFu, lane_id >= 0 && abs(of_vs - sm.first_exp) > kFarScales) && lane == 0)
+                if (__any_sync(0xFFFFFFFFu, lane_id >= 0 && far_scale(vs)) && lane == 0)
                     sm.far_from = min(sm.far_from, j);
                 if (lane < kKeys / page)
                     sm.entry[j % kEntrySlots][lane] = PageEntry{lane_id, ks, lg2(vs), __frcp_rn(vs)};
