@@ -115,6 +115,14 @@ __device__ __forceinline__ float own_sum(float sum) { return sum > 0.0f ? 1.0f :
 // 2^(log - top), nothing for two that have seen nothing.
 __device__ __forceinline__ float of_top(float log, float top) { return ex2(log - (top == -INFINITY ? 0.0f : top)); }
 
+// Adds its * 2^log to a sum kept against top.  (Added in either order the result is the same to the bit.)
+__device__ __forceinline__ void add_log(float &top, float &sum, float log, float its)
+{
+    const float next = fmaxf(top, log);
+    sum = sum * of_top(top, next) + its * of_top(log, next);
+    top = next;
+}
+
 // A page's table entry as the kernels keep it: id (< 0: none), the keys'
 // scale, log2 of the values' scale and its inverse.
 struct PageEntry {

@@ -704,18 +704,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     float top = -INFINITY, sum = 0.0f;   // of the row's logarithms: their maximum, and the sum against it
     if (live) {
         for (int64_t p = c0 + lane % (kDim / 4); p <= c1; p += kDim / 4)   // a row's lanes: kDim / 4 neighbours
-            top = fmaxf(top, ws_log[place(p)]);
+            add_log(top, sum, ws_log[place(p)], 1.0f);
     }
 #pragma unroll
-    for (int o = kDim / 8; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (live) {
-        for (int64_t p = c0 + lane % (kDim / 4); p <= c1; p += kDim / 4)
-            sum += of_top(ws_log[place(p)], top);
+    for (int o = kDim / 8; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, top, o), its = __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        add_log(top, sum, other, its);
     }
-#pragma unroll
-    for (int o = kDim / 8; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     const float inv = reciprocal_sum(sum);
     float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (live) {

@@ -719,18 +719,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
     const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
     const float2 *stat = ws_stat + at * plan.splits;
     const auto log_of = [&](int i) { return stat[i].x + lg2(stat[i].y); };
-    float top = -INFINITY;
+    float top = -INFINITY, sum = 0.0f;
     for (int i = lane; i < parts; i += 32)
-        top = fmaxf(top, log_of(i));
+        add_log(top, sum, log_of(i), 1.0f);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-    float sum = 0.0f;
-    for (int i = lane; i < parts; i += 32)
-        sum += of_top(log_of(i), top);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    for (int x = 16; x > 0; x >>= 1) {
+        const float other = __shfl_xor_sync(0xFFFFFFFFu, top, x), its = __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        add_log(top, sum, other, its);
+    }
     const float inv = reciprocal_sum(sum);
     constexpr int kPer = kDim / 32;
     float mean[kPer];
