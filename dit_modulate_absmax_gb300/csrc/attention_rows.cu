@@ -65,13 +65,15 @@ __device__ __forceinline__ uint32_t piece(int r, int c)
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Adds a part's mean v with its share of the row's sum.
-__device__ __forceinline__ void join(float4 &mean, const float4 &v, float share)
+// Adds a part's mean v times its share of the row's sum, half^2 inv: the square alone may be below the smallest number where
+// v is very large.
+__device__ __forceinline__ void join(float4 &mean, const float4 &v, float half, float inv)
 {
-    mean.x = fmaf(v.x, share, mean.x);
-    mean.y = fmaf(v.y, share, mean.y);
-    mean.z = fmaf(v.z, share, mean.z);
-    mean.w = fmaf(v.w, share, mean.w);
+    const float rest = half * inv;
+    mean.x = fmaf(v.x * half, rest, mean.x);
+    mean.y = fmaf(v.y * half, rest, mean.y);
+    mean.z = fmaf(v.z * half, rest, mean.z);
+    mean.w = fmaf(v.w * half, rest, mean.w);
 }
 
 // CTAs that fit an SM: shared memory at 128 channels, registers at 64.
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-            join(mean, *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c), of_top(part_log[w][r], top) * inv);
+            join(mean, *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kDim + c), half_of_top(part_log[w][r], top), inv);
         if (plan.cluster) {
             *reinterpret_cast<float4 *>(joined + r * kDim + c) = mean;
             if (c == 0)
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             for (int p = 0; p < plan.splits; ++p)
                 join(mean, ld_cluster_v4(mapa_shared(j0 + (r * kDim + c) * 4, p)),
-                     of_top(ld_cluster_f32(mapa_shared(s0 + 4 * r, p)), top) * inv);
+                     half_of_top(ld_cluster_f32(mapa_shared(s0 + 4 * r, p)), top), inv);
             finish(r, c, top + lg2(total), mean);
         }
         cluster_sync();   // nobody leaves while its part may be read
@@ -716,7 +718,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     if (live) {
 #pragma unroll 8
         for (int64_t p = c0 + part0; p <= c1; p += kGroups)
-            join(mean, *reinterpret_cast<const float4 *>(ws_out + place(p) * kDim + c), of_top(ws_log[place(p)], top) * inv);
+            join(mean, *reinterpret_cast<const float4 *>(ws_out + place(p) * kDim + c), half_of_top(ws_log[place(p)], top), inv);
     }
     if (kGroups > 1) {
         means[part0][piece] = mean;

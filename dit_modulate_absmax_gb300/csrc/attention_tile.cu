@@ -735,13 +735,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
         mean[c] = 0.0f;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
-        const float share = of_top(log_of(i), top) * inv;
+        const float half = half_of_top(log_of(i), top), rest = half * inv;   // of the part's share (see there)
         const float *src = ws_out + (at * plan.splits + i) * kDim + lane * kPer;
 #pragma unroll
         for (int c = 0; c < kPer; c += 2) {
             const float2 v = *reinterpret_cast<const float2 *>(src + c);
-            mean[c] = fmaf(v.x, share, mean[c]);
-            mean[c + 1] = fmaf(v.y, share, mean[c + 1]);
+            mean[c] = fmaf(v.x * half, rest, mean[c]);
+            mean[c + 1] = fmaf(v.y * half, rest, mean[c + 1]);
         }
     }
     uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;

@@ -110,6 +110,18 @@ def test_pages_before_a_window_may_be_given_up(h3, new, heads, page):
 def test_value_scales_far_apart(h3, new, length, order, gap):
     """Pages whose values' scales are those of an all-zero page (2^-40) and the largest a write can set (2^119): every
     page counts in the softmax's sum, with scores alike or those of the large pages lower by 40."""
+    _far_apart(h3, new, length, order, gap, 4.0)
+
+
+@pytest.mark.parametrize("order", ["turn by turn", "small ones first", "large ones first"])
+@pytest.mark.parametrize("new,length", [(1, 300), (9, 300), (140, 300), (1, 9_000), (20, 4_000), (140, 2_500)])
+def test_large_values_of_small_probability(h3, new, length, order):
+    """... or lower by 92: probabilities below FP32's smallest normal number whose values are large enough to be all of
+    the output, also where they lie in a part of the keys of their own."""
+    _far_apart(h3, new, length, order, 92, 12.0)
+
+
+def _far_apart(h3, new, length, order, gap, q0):
     rng = np.random.default_rng(25)
     page, dim = 32, 128
     lengths = [length, 70]
@@ -120,8 +132,8 @@ def test_value_scales_far_apart(h3, new, length, order, gap):
     large = {"turn by turn": np.arange(n) % 2 == 1, "small ones first": np.arange(n) >= n // 2,
              "large ones first": np.arange(n) < n // 2}[order]
     q = torch.randn(2 * new, 4, dim, generator=torch.Generator().manual_seed(9)).abs().mul(0.5).bfloat16().cuda()
-    q[:, :, 0] = 4.0
-    lower = -gap / (4.0 * dim ** -0.5)                       # channel 0 carries the gap
+    q[:, :, 0] = q0
+    lower = -gap / (q0 * dim ** -0.5)                       # channel 0 carries the gap
     for b, most in enumerate(lengths):
         for i in range(-(-most // page)):
             p = int(table[b, i])
