@@ -109,6 +109,16 @@ __device__ __forceinline__ bool far_scale(float scale) { return abs(static_cast<
 // 1 / sum; a row that has seen nothing stays zero, NaN stays NaN.
 __device__ __forceinline__ float reciprocal_sum(float sum) { return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f; }
 
+// ref + log2(sum), the sum's exponent taken apart: lg2's error is 2^-22 of its result, which near 0 is small and at a
+// lifted reference or a scale of 2^-40 is not.  (Exact at powers of two.)
+__device__ __forceinline__ float log_of_sum(float ref, float sum)
+{
+    if (!(sum >= 0x1p-126f && sum < INFINITY))
+        return ref + lg2(sum);   // nothing, or not a number
+    const uint32_t bits = __float_as_uint(sum);
+    return (ref + static_cast<float>(static_cast<int>(bits >> 23) - 127)) + lg2(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
+}
+
 // A sum against its own logarithm: 1, or still nothing, or NaN.
 __device__ __forceinline__ float own_sum(float sum) { return sum > 0.0f ? 1.0f : sum; }
 
@@ -127,7 +137,8 @@ __device__ __forceinline__ void add_log(float &top, float &sum, float log, float
 }
 
 // A page's table entry as the kernels keep it: id (< 0: none), the keys'
-// scale, log2 of the values' scale and its inverse.
+// scale, log2 of the values' scale and its inverse: that of the logarithm as
+// it was rounded, so that the two cancel in the sum.
 struct PageEntry {
     int32_t id;
     float ks, lv, inv_vs;

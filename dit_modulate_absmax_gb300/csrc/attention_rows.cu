@@ -343,8 +343,9 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         const int64_t bh = static_cast<int64_t>(id) * heads + kh;
         const float vs = id >= 0 ? a.cache.v_scale[bh] : 1.0f;
         entry[i].ks = id >= 0 ? a.cache.k_scale[bh] : 1.0f;
-        entry[i].lv = lg2(vs);
-        entry[i].inv_vs = __frcp_rn(vs);
+        const float lv = lg2(vs);
+        entry[i].lv = lv;
+        entry[i].inv_vs = ex2(-lv);
         far = far || far_scale(vs);
     }
     if (__syncthreads_or(far) && !far_scales) {   // scales are there
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 1);
             l[hf] += __shfl_xor_sync(0xFFFFFFFFu, l[hf], 2);
             if (t == 0)
-                sum_ref[warp][g + 8 * hf] = m[hf] + lg2(l[hf]);
+                sum_ref[warp][g + 8 * hf] = log_of_sum(m[hf], l[hf]);
             l[hf] = t == 0 ? own_sum(l[hf]) : 0.0f;
         }
         __syncwarp();
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         const float ref = far_scales ? sum_ref[warp][g + 8 * hf] : m[hf];
         const float inv = reciprocal_sum(l[hf]) * (far_scales && l[hf] > 0.0f ? ex2(m[hf] - ref) : 1.0f);
         if (t == 0)
-            part_log[warp][g + 8 * hf] = ref + lg2(l[hf]);
+            part_log[warp][g + 8 * hf] = log_of_sum(ref, l[hf]);
         const float f0 = __shfl_sync(0xFFFFFFFFu, inv, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, inv, 8 * t + 4);   // as above
 #pragma unroll
         for (int j = 0; j < kSteps; ++j) {
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             total += of_top(part_log[w][r], top);
-        const float inv = reciprocal_sum(total), log = top + lg2(total);
+        const float inv = reciprocal_sum(total), log = log_of_sum(top, total);
         float4 mean = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             for (int p = 0; p < plan.splits; ++p)
                 join(mean, ld_cluster_v4(mapa_shared(j0 + (r * kDim + c) * 4, p)),
                      half_of_top(ld_cluster_f32(mapa_shared(s0 + 4 * r, p)), top), inv);
-            finish(r, c, top + lg2(total), mean);
+            finish(r, c, log_of_sum(top, total), mean);
         }
         cluster_sync();   // nobody leaves while its part may be read
     }
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     if (a.lse != nullptr && c == 0)
-        a.lse[row * a.heads + head] = (top + lg2(sum)) * kLn2;
+        a.lse[row * a.heads + head] = log_of_sum(top, sum) * kLn2;
 }
 
 }  // namespace

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = j == steps || j >= sm.far_from;
             float o_factor = 1.0f;
             if (ok && j < steps) {
-                apart_ref = ref + lg2(l);
+                apart_ref = log_of_sum(ref, l);
                 apart_l = own_sum(l);
                 for (; ok && j < steps; ++j)
                     ok = step(std::true_type{}, j);
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (live && !final)
                     ws_stat[at * plan.splits + split] = make_float2(ref, l);
                 else if (live && a.lse != nullptr)
-                    a.lse[at] = (ref + lg2(l)) * kLn2;
+                    a.lse[at] = log_of_sum(ref, l) * kLn2;
                 tc_fence_before();
             }
         }
@@ -589,8 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
                 if (__any_sync(0xFFFFFFFFu, lane_id >= 0 && far_scale(vs)) && lane == 0)
                     sm.far_from = min(sm.far_from, j);
+                const float lv = lg2(vs);
                 if (lane < kKeys / page)
-                    sm.entry[j % kEntrySlots][lane] = PageEntry{lane_id, ks, lg2(vs), __frcp_rn(vs)};
+                    sm.entry[j % kEntrySlots][lane] = PageEntry{lane_id, ks, lv, ex2(-lv)};
                 warp_arrive(sm.entry_full[j % kEntrySlots]);
             }
 #pragma unroll
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
     const int64_t at = row * a.heads + head;
     const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
     const float2 *stat = ws_stat + at * plan.splits;
-    const auto log_of = [&](int i) { return stat[i].x + lg2(stat[i].y); };
+    const auto log_of = [&](int i) { return log_of_sum(stat[i].x, stat[i].y); };
     float top = -INFINITY, sum = 0.0f;
     for (int i = lane; i < parts; i += 32)
         add_log(top, sum, log_of(i), 1.0f);
@@ -751,7 +752,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
         *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
     }
     if (a.lse != nullptr && lane == 0)
-        a.lse[at] = (top + lg2(sum)) * kLn2;
+        a.lse[at] = log_of_sum(top, sum) * kLn2;
 }
 
 // kGroup: scores in a row that are sure to lie in one page.

@@ -220,3 +220,26 @@ def test_scores_rising_along_the_keys(h3, new, rise):
     q[:, :, 0] = 1.0
     out, lse = _run(h3, q, c, table, [length], [0, new], new, scale=1.0)
     _check(h3, q, c, table, [length], [0, new], out, lse, scale=1.0)
+
+
+@pytest.mark.parametrize("new", [1, 20, 140])
+@pytest.mark.parametrize("log_v_scale", [-40, -7, 0, 30, 100])
+@pytest.mark.parametrize("window", [1, 2, 64, 0])
+def test_logarithm_of_plain_counts(h3, new, log_v_scale, window):
+    """With a softmax scale of 0 the log-sum-exp is the logarithm of the number of keys seen, whatever the values' scales:
+    2^-21 for its rounding, and as much again for that of a base-2 logarithm below 12 (2^-22 of a part in [0, 1), the
+    sum's own roundings 2^-24 each along at most four joins)."""
+    rng = np.random.default_rng(29)
+    lengths, page = [1_500, 260], 64
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, 2, page, 64)
+    c.v_scale.fill_(2.0 ** log_v_scale)
+    cu = [0, new, 2 * new]
+    q = torch.randn(2 * new, 4, 64, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    out, lse = _run(h3, q, c, table, lengths, cu, new, scale=0.0, causal=True, window=window)
+    _check(h3, q, c, table, lengths, cu, out, lse, scale=0.0, causal=True, window=window)
+    for b, n in enumerate(lengths):
+        seen = np.minimum(np.arange(n - new, n) + 1, window if window else n)
+        want = np.log(seen)[:, None]
+        got = lse[cu[b]:cu[b + 1]].double().cpu().numpy()
+        assert (np.abs(got - want) <= 2.0 ** -21 * np.maximum(np.abs(want), 1) + 2.0 ** -21).all(), float(np.abs(got - want).max())
