@@ -125,7 +125,7 @@ __device__ __forceinline__ float own_sum(float sum) { return sum > 0.0f ? 1.0f :
 // 2^(log - top), nothing for two that have seen nothing.
 __device__ __forceinline__ float of_top(float log, float top) { return ex2(log - (top == -INFINITY ? 0.0f : top)); }
 
-// Its square root, so that 2^-252 is still a number.
+// Its square root: a part's mean times this twice keeps what is left of very large values down to shares of 2^-252.
 __device__ __forceinline__ float half_of_top(float log, float top) { return ex2(0.5f * (log - (top == -INFINITY ? 0.0f : top))); }
 
 // Adds its * 2^log to a sum kept against top.  (Added in either order the result is the same to the bit.)

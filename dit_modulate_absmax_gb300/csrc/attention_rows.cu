@@ -17,9 +17,10 @@
 //    permutes.  S's accumulator layout is that product's B operand.
 //  - The copies XOR-swizzle rows in 16-byte pieces (dim 128: no bank conflicts;
 //    dim 64: two-way for the values).
-// Measured: one sequence of 262,143 keys, 8 cache heads of 128 channels, 97 us
-// (5.6 TB/s; 1,048,576 keys 6.6 TB/s), 32 ragged ones of up to 8,190 keys 73 us
-// (4.7 TB/s): beyond the copying, a CTA's start and the join's launch.
+// Measured: one sequence of 262,143 keys, 8 cache heads of 128 channels, 96 us
+// (5.6 TB/s; 1,048,576 keys 6.6 TB/s), 32 ragged ones of up to 8,190 keys 75 us
+// (4.6 TB/s): beyond the copying, a CTA's start, the copies that run dry where
+// a CTA goes from one sequence to the next, and the join.
 // The tensor work is small next to the memory's (24 instructions per 4 KB of
 // codes at dim 128 and 8 rows), so the older warp-level instruction serves; a
 // 128-row tcgen05 tile would be 8-16 times padding.
@@ -752,8 +753,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
 // against 14.5).
 // Others: as many CTAs as the SMs hold, each with an equal share of all units,
 // whatever the lengths of the batch (equal parts per sequence, sized for the
-// longest, left SMs idle: 32 ragged requests 75 us); rows that lie with
-// several CTAs are joined by a second kernel.
+// longest, left SMs idle: 32 ragged requests took 87 us, then 73); rows that
+// lie with several CTAs are joined by a second kernel.
 SplitPlan plan_rows(const AttnShape &s)
 {
     const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);

@@ -20,12 +20,14 @@
 // Shared memory at dim 128: queries 64 KB, two stages of keys and of values 32
 // KB each.
 //
-// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.04
-// to 5.09 ms, 1.07 to 1.08 PFLOP/s, about 4,100 cycles a step.  No pipe is full
-// (tensor 50 %, exponentials 20 %, issue 46 %, shared memory 30 %), and leaving
-// out any one part of the arithmetic but the exponentials changes nothing: what
-// is left is the length of a tile's chain -- scores, softmax, weights, product,
-// the next scores -- with two tiles, all that TMEM has room for, in turn.
+// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.12
+// ms, 1.07 PFLOP/s, about 4,100 cycles a step.  No pipe is full (tensor 43 to
+// 50 %, exponentials 21 %, issue 45 %, shared memory 32 %), and leaving out any
+// one part of the arithmetic but the exponentials changes nothing.  What is
+// left is the length of a tile's chain -- scores, softmax, weights, product,
+// the next scores, of which some 500 cycles lie between a product's end and the
+// issue of the next scores -- with two tiles in turn, and the last wave: 1,120
+// CTAs of equal length on 152 SMs are 7.4 waves run as 8.
 // Tried and slower: half steps of 64 keys with two score buffers (5.65 ms), the
 // next scores' first half issued while the softmax works (4 %), two threads a
 // row (8.2 ms), a quarter of the exponentials as polynomials (16 %).
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
         mean[c] = 0.0f;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
-        const float half = half_of_top(log_of(i), top), rest = half * inv;   // of the part's share (see there)
+        const float half = half_of_top(log_of(i), top), rest = half * inv;   // the part's share in two halves: see half_of_top
         const float *src = ws_out + (at * plan.splits + i) * kDim + lane * kPer;
 #pragma unroll
         for (int c = 0; c < kPer; c += 2) {

@@ -14,7 +14,9 @@
 // to the next with one barrier between, its loads under way meanwhile; the
 // cosines and sines of its tokens serve all its heads.  37,810 tokens of 56
 // heads of 128 channels are read back in 240 us, at the rate of a plain copy;
-// 5,042 such tokens are written in 45 us (4.8 TB/s), with a rotation in 68.
+// 5,042 such tokens are written in 45 us (4.8 TB/s), with a rotation in 68 (in
+// halves 98): neither HBM (35 %) nor issue (62 %) is full there, so that form
+// has no bound yet.
 #include <type_traits>
 
 #include "kvcache.cuh"
@@ -131,6 +133,8 @@ struct WriteArgs {
 // One CTA: a page's blocks of every head in [blockIdx.x * heads_per_cta, ...).
 // kPer chunks of 8 values per thread cover the page (kPer * blockDim.x * 8 =
 // page * dim), all at the same channels.  kRope: 0 none, 1 interleaved, 2 halves.
+// Its largest launch, 1,024 threads (pages of 128 with 128 channels, rotated),
+// leaves every form 64 registers: <2, 2> spills 64 bytes, <4, 0> 20.
 template <int kPer, int kRope>
 __global__ void __launch_bounds__(kMaxThreads) write_kernel(WriteArgs a, int heads_per_cta)
 {
@@ -358,10 +362,13 @@ struct kernel_constant {
     static constexpr auto value = kKernel;
 };
 
-// Heads that a CTA takes one after another: so many that all CTAs run at once,
-// `per_sm` on an SM, but `most` at most (where the grid is many waves anyway).
+// Heads that a CTA takes one after another: so many that no more than `per_sm`
+// CTAs come to an SM, but `most` at most (where the grid is many waves anyway).
 // 5,042 tokens of 56 heads, with a rotation: 68 us with 8 heads, 72 with 6 (a
 // second wave), 76 with 12, 127 with one; plain 45 us with 4, 47 with one.
+// per_sm is what fits with the 256 threads and more of those sizes; of smaller
+// CTAs (64 threads, see launch_kv_write) more would fit, and the rule gives
+// each of them more heads than filling the SMs takes.
 int heads_each(const KvCache &cache, const KvBatch &batch, unsigned blocks, int per_sm, int most)
 {
     const int64_t slots = static_cast<int64_t>(sm_count()) * per_sm;

@@ -1,7 +1,10 @@
 // rope.cu -- rotary positions with several axes (h3fp4_rope_axes).
 //
 // Reads and writes each value once: 4 bytes a channel, bound by HBM (37,810
-// tokens of 112 heads of 128 channels: 328 us, 6.6 TB/s).  A CTA takes 4 tokens
+// tokens of 112 heads of 128 channels: 328 us, 6.6 TB/s).  Times here are those
+// of a launch among others in a graph; launched by itself each takes 2 to 3 us
+// longer (a token of 112 heads 6.2, and 14 called from Python; 5,042 tokens of
+// 56 heads in halves 34 to 35).  A CTA takes 4 tokens
 // (or 8) and a range of heads.  It first computes the cosines and sines of its
 // tokens' pairs into shared memory (they serve every head), then two warps (or
 // one) walk each token's heads, a lane holding 8 channels (16 bytes) and their

@@ -300,7 +300,7 @@ typedef struct h3fp4_rope {
  *                     heads in elements (multiples of 8, not negative), 16-byte aligned.  out either is x
  *                     (same pointer and strides: in place) or does not overlap it (the two address ranges
  *                     from first to last element; else H3FP4_ERR_UNSUPPORTED).  Queries and keys in the
- *                     rows of a QKV projection are one call with heads = 2 H.
+ *                     rows of a QKV projection are one call with heads = 2 H.  Strides: at most 2^30.
  *   head_dim          multiple of 8, 8 .. 256
  */
 H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_stride, int64_t x_head_stride,
@@ -319,7 +319,7 @@ H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_strid
  *
  * A page table names each sequence's pages: position p of sequence b is token
  * p % page_size of page page_table[b * ld_table + p / page_size].  A page may
- * appear in several tables as long as no call writes it for more than one.
+ * appear in several places as long as no call writes it for more than one.
  */
 typedef struct h3fp4_kv_cache {
     uint8_t *k_codes, *v_codes;
@@ -414,7 +414,9 @@ H3FP4_API h3fp4_status h3fp4_kv_cache_read(const h3fp4_kv_cache *cache, const h3
  *   heads             a multiple of the cache's heads, at most 65535
  *   max_kv            the most keys that any sequence has (sizes the launch; longer ones are
  *                     reported as out of range); at most 2^30
- *   softmax_scale     finite; scales of the cache's pages lie in [2^-60, 2^120] (those that a write sets do)
+ *   softmax_scale     finite; scales of the cache's pages lie in [2^-60, 2^120] (those that a write sets do).
+ *                     Scores have FP32's accuracy where softmax_scale times the row's largest channel is
+ *                     0 or 2^-100 at least; past FP32's range they are infinities
  *   workspace         h3fp4_kv_attention_workspace bytes of device scratch, 16-byte aligned (contents on
  *                     entry are ignored; two calls that overlap on the GPU must not share it); may be NULL
  *                     where that is 0
