@@ -5,7 +5,9 @@ The ``h3fp4_*`` functions mirror the C entry points one to one and take raw
 device pointers (ints); the short-named helpers below them take torch tensors,
 allocate outputs with torch and pass pointers plus torch's current stream, or
 the one given as ``stream``; what they allocate belongs to that stream, as if
-made under ``torch.cuda.stream(stream)``.
+made under ``torch.cuda.stream(stream)``.  As with torch's own operators, the
+order of the streams and the life of the tensors given are the caller's
+(``Tensor.record_stream`` where one is dropped while that stream may use it).
 Every arithmetic step runs in the library's CUDA kernels: there is no CPU or
 PyTorch fallback, and every call raises if the library is missing or returns
 an error status.

@@ -128,11 +128,12 @@ __device__ __forceinline__ float of_top(float log, float top) { return ex2(log -
 // Its square root: a part's mean times this twice keeps what is left of very large values down to shares of 2^-252.
 __device__ __forceinline__ float half_of_top(float log, float top) { return ex2(0.5f * (log - (top == -INFINITY ? 0.0f : top))); }
 
-// Adds its * 2^log to a sum kept against top.  (Added in either order the result is the same to the bit.)
+// Adds its * 2^log to a sum kept against top.  Products and sum are rounded apart, so that two lanes that exchange theirs
+// come to the same bits.
 __device__ __forceinline__ void add_log(float &top, float &sum, float log, float its)
 {
     const float next = fmaxf(top, log);
-    sum = sum * of_top(top, next) + its * of_top(log, next);
+    sum = __fadd_rn(__fmul_rn(sum, of_top(top, next)), __fmul_rn(its, of_top(log, next)));
     top = next;
 }
 
