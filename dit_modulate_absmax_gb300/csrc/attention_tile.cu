@@ -20,7 +20,7 @@
 // Shared memory at dim 128: queries 64 KB, two stages of keys and of values 32
 // KB each.
 //
-// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.12
+// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.13
 // ms, 1.07 PFLOP/s, about 4,100 cycles a step.  No pipe is full (tensor 43 to
 // 50 %, exponentials 21 %, issue 45 %, shared memory 32 %), and leaving out any
 // one part of the arithmetic but the exponentials changes nothing.  What is
