@@ -19,6 +19,7 @@ import functools
 import operator
 import os
 import struct
+import typing
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libh3fp4.so")
@@ -54,6 +55,15 @@ _SIGNATURES = {
     "h3fp4_diag_attention_wait_timeout": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _I32, _P, _I64,
                                            ctypes.c_uint32, _P], _STATUS),
     "h3fp4_kv_attention_workspace": ([_I64, _I32, _I32, _I32, _I32, _I32, _I32], _I64),
+    "h3fp4_norm_rope": ([_P, _P, _I64, _I32, ctypes.c_float, _P, _P], _STATUS),
+    "h3fp4_norm_rope_backward": ([_P, _P, _I64, _I32, ctypes.c_float, _P, _P, _I64, _P], _STATUS),
+    "h3fp4_norm_rope_backward_workspace": ([_I32], _I64),
+    "h3fp4_kv_attention_sinks": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _I32, ctypes.c_float, _I32, _I32,
+                                  _I32, _P, _I64, _P], _STATUS),
+    "h3fp4_kv_attention_shared": ([_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _I32, _P, _I32, ctypes.c_float,
+                                   _I32, _P, _I64, _P], _STATUS),
+    "h3fp4_kv_attention_shared_workspace": ([_I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], _I64),
+    "h3fp4_kv_tables": ([_P, _P], _STATUS),
     "h3fp4_status_string": ([_STATUS], ctypes.c_char_p),
     "h3fp4_build_info": ([], ctypes.c_char_p),
 }
@@ -76,10 +86,13 @@ ROPE_MAX_AXES = 4
 ROPE_LAYOUTS = {"interleaved": 0, "halves": 1}
 
 
-# h3fp4_rope, h3fp4_kv_cache and h3fp4_kv_batch in the platform's C layout.
+# The header's structures in the platform's C layout.
 _ROPE = struct.Struct("@PqPi4iii4x")
 _KV_CACHE = struct.Struct("@PPPPiiii")
 _KV_BATCH = struct.Struct("@PqPPii")
+_NORM_HEADS = struct.Struct("@PqqPqqPii")
+_NORM_GRADS = struct.Struct("@PqqPqqPqqPPii")
+_KV_REQUESTS = struct.Struct("@PPPqPPPPPPPqiiiii4x")
 
 
 _lib = None
@@ -206,6 +219,26 @@ def h3fp4_rope_axes(x, x_token_stride, x_head_stride, out, out_token_stride, out
           head_dim, rope, stream)
 
 
+def h3fp4_norm_rope(q, k, tokens, head_dim, eps, rope=None, stream=0):
+    """`q` and `k` (of the gradients too): the structure's bytes, or None."""
+    if not -1 <= head_dim >> 31 <= 0:
+        raise _too_large("h3fp4_norm_rope")
+    _call("h3fp4_norm_rope", q, k, tokens, head_dim, eps, rope, stream)
+
+
+def h3fp4_norm_rope_backward(q, k, tokens, head_dim, eps, rope, workspace, workspace_bytes, stream=0):
+    if not -1 <= head_dim >> 31 <= 0:
+        raise _too_large("h3fp4_norm_rope_backward")
+    _call("h3fp4_norm_rope_backward", q, k, tokens, head_dim, eps, rope, workspace, workspace_bytes, stream)
+
+
+def h3fp4_norm_rope_backward_workspace(head_dim) -> int:
+    n = lib().h3fp4_norm_rope_backward_workspace(head_dim) if -1 <= head_dim >> 31 <= 0 else -1
+    if n < 0:
+        raise H3FP4Error("h3fp4_norm_rope_backward_workspace", 3)
+    return n
+
+
 def h3fp4_kv_cache_write(cache, batch, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, tokens,
                          rope=None, stream=0):
     _call("h3fp4_kv_cache_write", cache, batch, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
@@ -224,6 +257,39 @@ def h3fp4_kv_attention(q, q_token_stride, q_head_stride, out, out_token_stride, 
         raise _too_large("h3fp4_kv_attention")
     _call("h3fp4_kv_attention", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
           heads, cache, batch, max_kv, softmax_scale, causal, window, workspace, workspace_bytes, stream)
+
+
+def h3fp4_kv_attention_sinks(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens, heads,
+                             cache, batch, max_kv, softmax_scale, causal, window, sinks, workspace, workspace_bytes, stream=0):
+    if not -1 <= (heads | max_kv | causal | window | sinks) >> 31 <= 0:
+        raise _too_large("h3fp4_kv_attention_sinks")
+    _call("h3fp4_kv_attention_sinks", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
+          heads, cache, batch, max_kv, softmax_scale, causal, window, sinks, workspace, workspace_bytes, stream)
+
+
+def h3fp4_kv_attention_shared(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens, heads,
+                              cache, prefix, max_prefix, batch, max_kv, softmax_scale, causal, workspace, workspace_bytes,
+                              stream=0):
+    if not -1 <= (heads | max_prefix | max_kv | causal) >> 31 <= 0:
+        raise _too_large("h3fp4_kv_attention_shared")
+    _call("h3fp4_kv_attention_shared", q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
+          heads, cache, prefix, max_prefix, batch, max_kv, softmax_scale, causal, workspace, workspace_bytes, stream)
+
+
+def h3fp4_kv_attention_shared_workspace(tokens, heads, kv_heads, head_dim, groups, max_group_tokens, max_prefix, batch,
+                                        max_tokens, max_kv) -> int:
+    sizes = (heads, kv_heads, head_dim, groups, max_group_tokens, max_prefix, batch, max_tokens, max_kv)
+    if not all(-1 <= x >> 31 <= 0 for x in sizes):
+        raise _too_large("h3fp4_kv_attention_shared_workspace")
+    n = lib().h3fp4_kv_attention_shared_workspace(tokens, *sizes)
+    if n < 0:
+        raise H3FP4Error("h3fp4_kv_attention_shared_workspace", 3)
+    return n
+
+
+def h3fp4_kv_tables(requests, stream=0):
+    """`requests`: the structure's bytes."""
+    _call("h3fp4_kv_tables", requests, stream)
 
 
 def h3fp4_diag_attention_wait_timeout(q, q_token_stride, q_head_stride, out, out_token_stride, out_head_stride, lse, tokens,
@@ -424,8 +490,8 @@ def _dtypes():
     global _types
     if _types is None:
         import torch
-        _types = {"bf16": (torch.bfloat16, torch.int16), "i32": torch.int32, "f32": torch.float32, "f64": torch.float64,
-                  "u8": torch.uint8}
+        _types = {"bf16": (torch.bfloat16, torch.int16), "i32": torch.int32, "i64": torch.int64, "f32": torch.float32,
+                  "f64": torch.float64, "u8": torch.uint8}
     return _types
 
 
@@ -516,6 +582,93 @@ def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
     return out
 
 
+def _norm_side(x, name, weight, shape, device):
+    """A side's array, weight and what the structures say of the weight."""
+    at = _need_tokens(x, name, (shape[0], x.shape[1] if x.dim() == 3 else -1, shape[2]), device)
+    if weight is None:
+        return at, 0, 0
+    wide = weight.dtype is _dtypes()["f32"]
+    if not (weight.get_device() == device and weight.shape == shape[2:] and weight.is_contiguous()
+            and (wide or weight.dtype in _dtypes()["bf16"])):
+        _refuse(weight, f"{name}_weight", f"a contiguous [{shape[2]}] tensor of bf16 values or float32", device)
+    return at, weight.data_ptr(), int(wide)
+
+
+def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope: Rope | None = None, eps=1e-6, q_out=None, k_out=None,
+              stream=None):
+    """RMS norm over the channels of every head of q (and k) [tokens, heads, head_dim], times the side's weight
+    [head_dim] (bf16 or float32; None: ones), then turned by ``rope`` (None: not), rounded once.  q and k may have
+    different numbers of heads; q_out=q works in place.  Returns (q_out, k_out); k_out is None without k."""
+    device, shape = q.get_device(), q.shape
+    _need_tokens(q, "q")
+    sides, outs = [], []
+    for x, name, weight, out in ((q, "q", q_weight, q_out), (k, "k", k_weight, k_out)):
+        if x is None:
+            if weight is not None or out is not None:
+                raise ValueError(f"{name}: a weight or an output without {name}")
+            sides.append(None)
+            outs.append(None)
+            continue
+        at, w, wide = _norm_side(x, name, weight, shape, device)
+        if out is None:
+            out = x.new_empty(x.shape) if stream is None else _empty(stream, x.shape, dtype=x.dtype, device=x.device)
+        sides.append(_NORM_HEADS.pack(*at, *_need_tokens(out, f"{name}_out", x.shape, device), w, x.shape[1], wide))
+        outs.append(out)
+    if rope is not None:
+        _positions_for(rope, shape[0], device)
+    h3fp4_norm_rope(*sides, shape[0], shape[2], eps, rope._struct if rope is not None else None, _raw_stream(stream, q))
+    return tuple(outs)
+
+
+def norm_rope_backward(q_grad, k_grad, q, k=None, *, q_weight=None, k_weight=None, rope: Rope | None = None, eps=1e-6,
+                       q_out=None, k_out=None, q_weight_grad=None, k_weight_grad=None, workspace=None, stream=None):
+    """Gradients of ``norm_rope`` from those of its outputs and its inputs (nothing else is kept of the forward pass).
+    Returns (dq, dk, dq_weight, dk_weight): dq and dk like q and k (q_out=q_grad works in place), the weights' float32
+    [head_dim], None where there is no weight."""
+    import torch
+    device, shape = q.get_device(), q.shape
+    _need_tokens(q, "q")
+    sides, outs, sums = [], [], []
+    for g, x, name, weight, out, dw in ((q_grad, q, "q", q_weight, q_out, q_weight_grad),
+                                        (k_grad, k, "k", k_weight, k_out, k_weight_grad)):
+        if x is None:
+            if g is not None or weight is not None or out is not None or dw is not None:
+                raise ValueError(f"{name}: gradients, a weight or an output without {name}")
+            sides.append(None)
+            outs.append(None)
+            sums.append(None)
+            continue
+        at, w, wide = _norm_side(x, name, weight, shape, device)
+        gt = _need_tokens(g, f"{name}_grad", x.shape, device)
+        if out is None:
+            out = x.new_empty(x.shape) if stream is None else _empty(stream, x.shape, dtype=x.dtype, device=x.device)
+        if weight is None:
+            if dw is not None:
+                raise ValueError(f"{name}_weight_grad: there is no {name}_weight")
+        elif dw is None:
+            dw = _empty(stream, shape[2], dtype=torch.float32, device=x.device)
+        dw_at = 0
+        if dw is not None:
+            dw_at = _need_array(dw, f"{name}_weight_grad", "f32", 1, device)
+            if dw.shape != shape[2:]:
+                _refuse(dw, f"{name}_weight_grad", f"a contiguous [{shape[2]}] tensor", device)
+        sides.append(_NORM_GRADS.pack(*gt, *at, *_need_tokens(out, f"{name}_out", x.shape, device), w, dw_at, x.shape[1], wide))
+        outs.append(out)
+        sums.append(dw)
+    if rope is not None:
+        _positions_for(rope, shape[0], device)
+    at, have, workspace = _workspace(workspace, _norm_workspace(device, shape[2]) if any(t is not None for t in sums) else 0,
+                                     device, stream, q)
+    h3fp4_norm_rope_backward(*sides, shape[0], shape[2], eps, rope._struct if rope is not None else None, at, have,
+                             _raw_stream(stream, q))
+    return (*outs, *sums)
+
+
+@functools.lru_cache(maxsize=64)           # a function of the head's channels and the device's SMs
+def _norm_workspace(device, head_dim):
+    return h3fp4_norm_rope_backward_workspace(head_dim)
+
+
 class KVCache:
     """Keys and values in E4M3 pages: codes [num_pages, heads, page_size, head_dim]
     uint8 and scales [num_pages, heads] float32, for keys and values each."""
@@ -601,12 +754,30 @@ def _attention_workspace(device, *sizes):
 
 
 def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, max_kv, *, scale=None, causal=False,
-                 window=0, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+                 window=0, sinks=0, out=None, lse=None, return_lse=False, workspace=None, stream=None):
     """Attention of q [tokens, heads, head_dim] over the cache.  kv_len[b] counts all keys
     of sequence b, its new tokens' among them; query i of n stands at kv_len[b] - n + i and
     sees the keys before kv_len[b] that are not after it (causal) and not window or more
-    before it (window > 0).  scale defaults to head_dim ** -0.5.  Returns (out, lse); lse
-    [tokens, heads] float32 is None unless asked for."""
+    before it (window > 0), unless they are among the first ``sinks``.  scale defaults to
+    head_dim ** -0.5.  Returns (out, lse); lse [tokens, heads] float32 is None unless asked
+    for."""
+    device, shape, qs, out, lse, lse_at = _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream)
+    tokens, heads, dim = shape
+    batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
+    need = _attention_workspace(device, tokens, heads, cache._heads, dim, page_table.shape[0], max_tokens, max_kv)
+    at, have, workspace = _workspace(workspace, need, device, stream, q)
+    if sinks:
+        h3fp4_kv_attention_sinks(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, batch,
+                                 max_kv, dim ** -0.5 if scale is None else scale, causal, window, sinks, at, have,
+                                 _raw_stream(stream, q))
+    else:
+        h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, batch, max_kv,
+                           dim ** -0.5 if scale is None else scale, causal, window, at, have, _raw_stream(stream, q))
+    return out, lse
+
+
+def _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream):
+    """Checks of what every attention call takes, and its outputs."""
     import torch
     device, shape = q.get_device(), q.shape
     qs = _need_tokens(q, "q")
@@ -624,16 +795,105 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
         lse_at = _need_array(lse, "lse", "f32", 2, device)
         if lse.shape != (tokens, heads):
             _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor", device)
-    batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
-    need = _attention_workspace(device, tokens, heads, cache._heads, dim, page_table.shape[0], max_tokens, max_kv)
-    at = have = 0
+    return device, shape, qs, out, lse, lse_at
+
+
+def _workspace(workspace, need, device, stream, like):
+    """Address and bytes of the caller's workspace, or of one made for the call (which the third result keeps)."""
+    import torch
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():   # (its bytes are written as they lie)
             _refuse(workspace, "workspace", "a contiguous tensor", device)
-        at, have = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif need:
-        workspace, have = _empty(stream, need, dtype=torch.uint8, device=q.device), need
-        at = workspace.data_ptr()
-    h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, batch, max_kv,
-                       dim ** -0.5 if scale is None else scale, causal, window, at, have, _raw_stream(stream, q))
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if not need:
+        return 0, 0, None
+    workspace = _empty(stream, need, dtype=torch.uint8, device=like.device)
+    return workspace.data_ptr(), need, workspace
+
+
+class SharedPrefix:
+    """Prefixes that groups of a call's sequences share: keys 0 .. kv_len[g] - 1 of row g of ``page_table``, seen by every
+    query of rows cu_tokens[g] .. cu_tokens[g+1] - 1 (device int32, as for ``kv_attention``); max_tokens is the most rows
+    of a group, max_kv the longest prefix."""
+
+    __slots__ = ("_page_table", "_kv_len", "_cu_tokens", "_max_tokens", "_max_kv", "_device", "_struct")
+    page_table, kv_len, cu_tokens = _fixed("page_table", "kv_len", "cu_tokens")
+    max_tokens, max_kv, device = _fixed("max_tokens", "max_kv", "device")
+
+    def __init__(self, page_table, kv_len, cu_tokens, max_tokens, max_kv):
+        device = page_table.get_device()
+        if kv_len is None:
+            raise ValueError("kv_len: lengths are wanted")
+        if not -1 <= (max_tokens | max_kv) >> 31 <= 0:
+            raise _too_large("h3fp4_kv_attention_shared")
+        self._struct = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
+        self._page_table, self._kv_len, self._cu_tokens, self._device = page_table, kv_len, cu_tokens, device
+        self._max_tokens, self._max_kv = max_tokens, max_kv
+
+
+@functools.lru_cache(maxsize=256)          # a function of the sizes and the device's SMs
+def _shared_workspace(device, *sizes):
+    return h3fp4_kv_attention_shared_workspace(*sizes)
+
+
+def kv_attention_shared(q, cache: KVCache, prefix: SharedPrefix, page_table, kv_len, cu_tokens, max_tokens, max_kv, *,
+                        scale=None, causal=False, out=None, lse=None, return_lse=False, workspace=None, stream=None):
+    """``kv_attention`` of sequences that share prefixes: each query sees all of its group's prefix, and of its sequence's
+    own keys what it sees in ``kv_attention``, under one softmax.  page_table and kv_len are those of the own keys alone,
+    which begin on pages of their own.  The prefixes' pages are read once for a group, not once for a sequence.  Returns
+    (out, lse)."""
+    device, shape, qs, out, lse, lse_at = _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream)
+    _need_device(prefix, "prefix", device)
+    tokens, heads, dim = shape
+    batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
+    need = _shared_workspace(device, tokens, heads, cache._heads, dim, prefix._page_table.shape[0], prefix._max_tokens,
+                             prefix._max_kv, page_table.shape[0], max_tokens, max_kv)
+    at, have, workspace = _workspace(workspace, need, device, stream, q)
+    h3fp4_kv_attention_shared(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, prefix._struct,
+                              prefix._max_kv, batch, max_kv, dim ** -0.5 if scale is None else scale, causal, at, have,
+                              _raw_stream(stream, q))
     return out, lse
+
+
+class KVTables(typing.NamedTuple):
+    """What ``kv_tables`` makes of a batch's lengths."""
+    cu_tokens: object      # int32 [batch + 1]
+    kv_len: object         # int32 [batch]
+    slots: object          # int64 [tokens]
+    positions: object      # float32 [tokens]
+    free_at: object        # int32 [1]
+
+
+def kv_tables(held, count, page_table, free_pages, free_at, page_size, num_pages, tokens, max_tokens, *, cu_tokens=None,
+              kv_len=None, slots=None, positions=None, free_at_out=None, stream=None) -> KVTables:
+    """The tables of a batch whose sequence b holds held[b] tokens and gets count[b] new ones (device int32 [batch], as are
+    all lengths here): cu_tokens and kv_len for the cache and attention calls, pages for the new tokens, taken from
+    free_pages[free_at[0]:] in the order of the sequences and written into page_table [batch, pages] where it has none
+    yet, and of each new token its slot (page * page_size + its place in the page, int64) and its position (float32, as a
+    Rope of one axis takes it).  slots and positions have ``tokens`` rows, of which those past the last token hold -1.
+    The returned free_at counts what has been taken; the one given stays as it was."""
+    import torch
+    device = held.get_device()
+    at = {"held": _need_array(held, "held", "i32", 1, device), "count": _need_array(count, "count", "i32", 1, device),
+          "page_table": _need_array(page_table, "page_table", "i32", 2, device),
+          "free_pages": _need_array(free_pages, "free_pages", "i32", 1, device),
+          "free_at": _need_array(free_at, "free_at", "i32", 1, device)}
+    batch, room = page_table.shape
+    if held.shape[0] != batch or count.shape[0] != batch or free_at.shape[0] != 1:
+        raise ValueError(f"page_table has {batch} sequences: held and count of {batch} and one free_at are wanted, got "
+                         f"{held.shape[0]}, {count.shape[0]} and {free_at.shape[0]}")
+    if not 0 <= tokens < 1 << 31 or not -1 <= (page_size | num_pages | max_tokens | batch | free_pages.shape[0]) >> 31 <= 0:
+        raise _too_large("h3fp4_kv_tables")
+    outs = []
+    for t, name, kind, n in ((cu_tokens, "cu_tokens", "i32", batch + 1), (kv_len, "kv_len", "i32", batch), (slots, "slots", "i64", tokens),
+                             (positions, "positions", "f32", tokens), (free_at_out, "free_at_out", "i32", 1)):
+        if t is None:
+            t = _empty(stream, n, dtype=_dtypes()[kind], device=held.device)
+        at[name] = _need_array(t, name, kind, 1, device)
+        if t.shape[0] != n:
+            _refuse(t, name, f"a contiguous [{n}] tensor", device)
+        outs.append(t)
+    h3fp4_kv_tables(_KV_REQUESTS.pack(at["held"], at["count"], at["page_table"], room, at["free_pages"], at["free_at"],
+                                      at["free_at_out"], at["cu_tokens"], at["kv_len"], at["slots"], at["positions"], tokens,
+                                      batch, max_tokens, free_pages.shape[0], num_pages, page_size), _raw_stream(stream, held))
+    return KVTables(*outs)

@@ -9,7 +9,9 @@
 #include <optional>
 
 #include "h3fp4.h"
+#include "kvtables.cuh"
 #include "launch.h"
+#include "norm_rope.cuh"
 
 #ifndef H3FP4_VERSION
 #define H3FP4_VERSION "0.1.0"
@@ -310,6 +312,39 @@ bool rows_overlap(const Strided &a, const Strided &b, int64_t tokens, int64_t he
     return false;
 }
 
+// Whether an output (check_strided_out) has an element in common with another array, of other heads perhaps (queries and keys
+// in the rows of a QKV projection): exactly, where strides and rows are alike; else whether their ranges do.
+bool heads_overlap(const Strided &a, int64_t a_heads, const Strided &b, int64_t b_heads, int64_t tokens, int64_t dim)
+{
+    const auto bytes = [&](const Strided &x, int64_t heads) { return 2 * ((tokens - 1) * x.token + (heads - 1) * x.head + dim); };
+    const char *pa = static_cast<const char *>(a.p), *pb = static_cast<const char *>(b.p);
+    if (pa >= pb + bytes(b, b_heads) || pb >= pa + bytes(a, a_heads))
+        return false;
+    if ((tokens > 1 && a.token != b.token) || (a_heads > 1 && b_heads > 1 && a.head != b.head))
+        return true;
+    const int64_t head = a_heads > 1 ? a.head : b.head, token = a.token, most = a_heads > b_heads ? a_heads : b_heads;
+    const int64_t d = (pb - pa) / 2;   // 16-byte aligned, both
+    // Rows i token + j head apart, i and j between the two: none within dim of -d?  Of the wider stride those nearest to it
+    // will do, for all of the other's multiples lie within one of its steps.
+    const auto meet = [&](int64_t outer, int64_t i_lo, int64_t i_hi, int64_t inner, int64_t j_lo, int64_t j_hi) {
+        const int64_t i0 = i_hi > i_lo ? -d / outer : 0;
+        for (int64_t i = i0 - 2; i <= i0 + 2; ++i) {
+            if (i < i_lo || i > i_hi)
+                continue;
+            const int64_t rest = d + i * outer, j0 = j_hi > j_lo ? -rest / inner : 0;
+            for (int64_t j = j0 - 1; j <= j0 + 1; ++j)
+                if (j >= j_lo && j <= j_hi && rest + j * inner < dim && rest + j * inner > -dim)
+                    return true;
+        }
+        return false;
+    };
+    if ((most == 1 || head >= dim) && (tokens == 1 || token >= (most - 1) * head + dim))
+        return meet(token, 1 - tokens, tokens - 1, head, 1 - a_heads, b_heads - 1);
+    if ((tokens == 1 || token >= dim) && (most == 1 || head >= (tokens - 1) * token + dim))
+        return meet(head, 1 - a_heads, b_heads - 1, token, 1 - tokens, tokens - 1);
+    return true;
+}
+
 h3fp4_status make_rope(const h3fp4_rope *r, int64_t dim, int64_t tokens, h3fp4::RopeArgs *out)
 {
     if (r == nullptr)
@@ -405,6 +440,144 @@ h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_stride, int64_t
     return from_cuda(h3fp4::launch_rope(static_cast<const uint16_t *>(x_bf16), x.token, x.head,
                                         static_cast<uint16_t *>(out_bf16), out.token, out.head, tokens, heads, head_dim,
                                         r, as_stream(stream)));
+}
+
+namespace {
+
+bool norm_sizes_ok(int64_t tokens, int32_t head_dim, float eps)
+{
+    return tokens >= 0 && tokens <= INT32_MAX && head_dim >= 8 && head_dim <= 256 && head_dim % 8 == 0 && eps >= 0x1p-100f &&
+           eps <= 0x1p20f;
+}
+
+// A rotation that may be absent; the norms know no inverse.
+h3fp4_status make_norm_rope(const h3fp4_rope *r, int64_t dim, int64_t tokens, h3fp4::RopeArgs *out)
+{
+    if (r == nullptr)
+        return H3FP4_OK;
+    const h3fp4_status s = make_rope(r, dim, tokens, out);
+    return s != H3FP4_OK ? s : out->inverse != 0 ? H3FP4_ERR_SHAPE : H3FP4_OK;
+}
+
+h3fp4_status check_weight(const void *weight, int32_t wide)
+{
+    if (wide != 0 && wide != 1)
+        return H3FP4_ERR_SHAPE;
+    return (reinterpret_cast<uintptr_t>(weight) & (wide ? 3u : 1u)) != 0 ? H3FP4_ERR_ALIGN : H3FP4_OK;
+}
+
+bool same_array(const Strided &a, const Strided &b) { return a.p == b.p && a.token == b.token && a.head == b.head; }
+
+}  // namespace
+
+h3fp4_status h3fp4_norm_rope(const h3fp4_norm_heads *q, const h3fp4_norm_heads *k, int64_t tokens, int32_t head_dim, float eps,
+                             const h3fp4_rope *rope, void *stream)
+{
+    if (!norm_sizes_ok(tokens, head_dim, eps))
+        return H3FP4_ERR_SHAPE;
+    h3fp4::RopeArgs r{};
+    h3fp4_status s = make_norm_rope(rope, head_dim, tokens, &r);
+    if (s != H3FP4_OK)
+        return s;
+    h3fp4::NormSide side[2] = {};
+    Strided in[2], out[2];
+    const h3fp4_norm_heads *given[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        const h3fp4_norm_heads *g = given[i];
+        if (g == nullptr)
+            continue;
+        if (g->heads < 0 || g->heads > 65535)
+            return H3FP4_ERR_SHAPE;
+        if ((s = check_weight(g->weight, g->weight_f32)) != H3FP4_OK)
+            return s;
+        if (g->heads == 0 || tokens == 0)
+            continue;
+        in[i] = {g->x, g->x_token_stride, g->x_head_stride};
+        out[i] = {g->out, g->out_token_stride, g->out_head_stride};
+        if ((s = check_strided(in[i])) != H3FP4_OK || (s = check_strided_out(out[i], tokens, g->heads, head_dim)) != H3FP4_OK)
+            return s;
+        side[i] = {static_cast<const uint16_t *>(g->x), in[i].token, in[i].head, static_cast<uint16_t *>(g->out), out[i].token,
+                   out[i].head, g->weight, g->heads, g->weight_f32};
+    }
+    if (side[0].heads + side[1].heads == 0)
+        return H3FP4_OK;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; side[i].heads > 0 && j < 2; ++j) {
+            if (side[j].heads == 0)
+                continue;
+            if (!(i == j && same_array(out[i], in[j])) && heads_overlap(out[i], side[i].heads, in[j], side[j].heads, tokens, head_dim))
+                return H3FP4_ERR_UNSUPPORTED;
+            if (i < j && heads_overlap(out[i], side[i].heads, out[j], side[j].heads, tokens, head_dim))
+                return H3FP4_ERR_UNSUPPORTED;
+        }
+    return from_cuda(h3fp4::launch_norm_rope(side[0], side[1], tokens, head_dim, eps, r, as_stream(stream)));
+}
+
+int64_t h3fp4_norm_rope_backward_workspace(int32_t head_dim)
+{
+    return head_dim < 8 || head_dim > 256 || head_dim % 8 != 0 ? -1 : h3fp4::norm_grad_workspace(head_dim);
+}
+
+h3fp4_status h3fp4_norm_rope_backward(const h3fp4_norm_grads *q, const h3fp4_norm_grads *k, int64_t tokens, int32_t head_dim,
+                                      float eps, const h3fp4_rope *rope, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (!norm_sizes_ok(tokens, head_dim, eps))
+        return H3FP4_ERR_SHAPE;
+    h3fp4::RopeArgs r{};
+    h3fp4_status s = make_norm_rope(rope, head_dim, tokens, &r);
+    if (s != H3FP4_OK)
+        return s;
+    h3fp4::NormGradSide side[2] = {};
+    Strided dy[2], x[2], dx[2];
+    const h3fp4_norm_grads *given[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        const h3fp4_norm_grads *g = given[i];
+        if (g == nullptr)
+            continue;
+        if (g->heads < 0 || g->heads > 65535)
+            return H3FP4_ERR_SHAPE;
+        if ((s = check_weight(g->weight, g->weight_f32)) != H3FP4_OK)
+            return s;
+        if ((reinterpret_cast<uintptr_t>(g->dweight) & 3u) != 0)
+            return H3FP4_ERR_ALIGN;
+        side[i].dweight = g->dweight;
+        if (g->heads == 0 || tokens == 0)
+            continue;
+        dy[i] = {g->dy, g->dy_token_stride, g->dy_head_stride};
+        x[i] = {g->x, g->x_token_stride, g->x_head_stride};
+        dx[i] = {g->dx, g->dx_token_stride, g->dx_head_stride};
+        if ((s = check_strided(dy[i])) != H3FP4_OK || (s = check_strided(x[i])) != H3FP4_OK ||
+            (s = check_strided_out(dx[i], tokens, g->heads, head_dim)) != H3FP4_OK)
+            return s;
+        side[i] = {static_cast<const uint16_t *>(g->dy), dy[i].token, dy[i].head, static_cast<const uint16_t *>(g->x), x[i].token,
+                   x[i].head, static_cast<uint16_t *>(g->dx), dx[i].token, dx[i].head, g->weight, g->dweight, g->heads,
+                   g->weight_f32};
+    }
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; side[i].heads > 0 && j < 2; ++j) {
+            if (side[j].heads == 0)
+                continue;
+            for (const Strided *in : {&dy[j], &x[j]})
+                if (!(i == j && same_array(dx[i], *in)) && heads_overlap(dx[i], side[i].heads, *in, side[j].heads, tokens, head_dim))
+                    return H3FP4_ERR_UNSUPPORTED;
+            if (i < j && heads_overlap(dx[i], side[i].heads, dx[j], side[j].heads, tokens, head_dim))
+                return H3FP4_ERR_UNSUPPORTED;
+        }
+    const bool sums = side[0].dweight != nullptr || side[1].dweight != nullptr;
+    if (side[0].dweight != nullptr && side[1].dweight != nullptr &&
+        side[0].dweight < side[1].dweight + head_dim && side[1].dweight < side[0].dweight + head_dim)
+        return H3FP4_ERR_UNSUPPORTED;
+    if (sums) {
+        if (workspace == nullptr)
+            return H3FP4_ERR_NULL;
+        if (workspace_bytes < h3fp4::norm_grad_workspace(head_dim))
+            return H3FP4_ERR_SHAPE;
+        if (!aligned16(workspace))
+            return H3FP4_ERR_ALIGN;
+    }
+    if (side[0].heads + side[1].heads == 0 && !sums)
+        return H3FP4_OK;
+    return from_cuda(h3fp4::launch_norm_rope_grad(side[0], side[1], tokens, head_dim, eps, r, workspace, as_stream(stream)));
 }
 
 h3fp4_status h3fp4_kv_cache_write(const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch, const void *k_bf16,
@@ -509,6 +682,112 @@ h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_stride, int6
     return a ? from_cuda(h3fp4::launch_attention(*a, workspace, as_stream(stream))) : s;
 }
 
+h3fp4_status h3fp4_kv_attention_sinks(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, void *out_bf16,
+                                      int64_t out_token_stride, int64_t out_head_stride, float *lse, int64_t tokens,
+                                      int32_t heads, const h3fp4_kv_cache *cache, const h3fp4_kv_batch *batch,
+                                      int32_t max_kv, float softmax_scale, int32_t causal, int32_t window, int32_t sinks,
+                                      void *workspace, int64_t workspace_bytes, void *stream)
+{
+    std::optional<h3fp4::AttnArgs> a;
+    const h3fp4_status s = check_attention({q_bf16, q_token_stride, q_head_stride},
+                                           {out_bf16, out_token_stride, out_head_stride}, lse, tokens, heads, cache, batch,
+                                           max_kv, softmax_scale, causal, window, workspace, workspace_bytes, &a);
+    if (s != H3FP4_OK)
+        return s;
+    if (sinks < 0 || sinks > (1 << 30))
+        return H3FP4_ERR_SHAPE;
+    if (!a)
+        return H3FP4_OK;
+    a->sinks = a->window > 0 ? sinks : 0;   // (without a window nothing is hidden from them)
+    return from_cuda(h3fp4::launch_attention(*a, workspace, as_stream(stream)));
+}
+
+int64_t h3fp4_kv_attention_shared_workspace(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t groups,
+                                            int32_t max_group_tokens, int32_t max_prefix, int32_t batch, int32_t max_tokens,
+                                            int32_t max_kv)
+{
+    if (!attention_sizes_ok(tokens, heads, kv_heads, head_dim, groups, max_group_tokens, max_prefix) ||
+        !attention_sizes_ok(tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv))
+        return -1;
+    return h3fp4::attention_shared_workspace(
+        h3fp4::AttnShape{tokens, heads, kv_heads, head_dim, groups, max_group_tokens, max_prefix},
+        h3fp4::AttnShape{tokens, heads, kv_heads, head_dim, batch, max_tokens, max_kv});
+}
+
+h3fp4_status h3fp4_kv_attention_shared(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, void *out_bf16,
+                                       int64_t out_token_stride, int64_t out_head_stride, float *lse, int64_t tokens,
+                                       int32_t heads, const h3fp4_kv_cache *cache, const h3fp4_kv_batch *prefix,
+                                       int32_t max_prefix, const h3fp4_kv_batch *batch, int32_t max_kv,
+                                       float softmax_scale, int32_t causal, void *workspace, int64_t workspace_bytes,
+                                       void *stream)
+{
+    h3fp4_status s = check_cache(cache);
+    if (s != H3FP4_OK || (s = check_batch(prefix, true, tokens)) != H3FP4_OK)
+        return s;
+    if (!attention_sizes_ok(tokens, heads, cache->heads, cache->head_dim, prefix->batch, prefix->max_tokens, max_prefix))
+        return H3FP4_ERR_SHAPE;
+    std::optional<h3fp4::AttnArgs> own;
+    const Strided q{q_bf16, q_token_stride, q_head_stride}, out{out_bf16, out_token_stride, out_head_stride};
+    s = check_attention(q, out, lse, tokens, heads, cache, batch, max_kv, softmax_scale, causal, 0, workspace, workspace_bytes, &own);
+    if (s != H3FP4_OK || !own)
+        return s;
+    const int64_t need = h3fp4_kv_attention_shared_workspace(tokens, heads, cache->heads, cache->head_dim, prefix->batch,
+                                                             prefix->max_tokens, max_prefix, batch->batch, batch->max_tokens, max_kv);
+    if (need > 0 && workspace == nullptr)
+        return H3FP4_ERR_NULL;
+    if (need < 0 || workspace_bytes < need)
+        return H3FP4_ERR_SHAPE;
+    h3fp4::AttnArgs first = *own;
+    first.batch = *prefix;
+    first.max_kv = max_prefix;
+    first.causal = 0;
+    return from_cuda(h3fp4::launch_attention_shared(first, *own, workspace, as_stream(stream)));
+}
+
+h3fp4_status h3fp4_kv_tables(const h3fp4_kv_requests *q, void *stream)
+{
+    if (q == nullptr || q->cu_tokens == nullptr || q->free_at == nullptr || q->free_at_out == nullptr)
+        return H3FP4_ERR_NULL;
+    if (q->batch < 0 || q->batch > 65535 || q->max_tokens < 0 || q->max_tokens > 1000000 || q->ld_table < 0 ||
+        q->ld_table > INT32_MAX || q->tokens < 0 || q->tokens > INT32_MAX || q->num_free < 0 || q->num_pages < 0)
+        return H3FP4_ERR_SHAPE;
+    if (q->page_size != 16 && q->page_size != 32 && q->page_size != 64 && q->page_size != 128)
+        return H3FP4_ERR_UNSUPPORTED;
+    if ((q->batch > 0 && (q->held == nullptr || q->count == nullptr || q->kv_len == nullptr ||
+                          (q->page_table == nullptr && q->ld_table > 0))) ||
+        (q->free_pages == nullptr && q->num_free > 0))
+        return H3FP4_ERR_NULL;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(q->held) | reinterpret_cast<uintptr_t>(q->count) |
+                            reinterpret_cast<uintptr_t>(q->page_table) | reinterpret_cast<uintptr_t>(q->free_pages) |
+                            reinterpret_cast<uintptr_t>(q->free_at) | reinterpret_cast<uintptr_t>(q->free_at_out) |
+                            reinterpret_cast<uintptr_t>(q->cu_tokens) | reinterpret_cast<uintptr_t>(q->kv_len) |
+                            reinterpret_cast<uintptr_t>(q->positions);
+    if ((words & 3u) != 0 || (reinterpret_cast<uintptr_t>(q->slots) & 7u) != 0)
+        return H3FP4_ERR_ALIGN;
+    // CTAs read every input while others write: no output may lie in one, nor in another output.
+    struct Range {
+        const void *p;
+        int64_t bytes;
+    };
+    const int64_t b = q->batch;
+    const Range in[] = {{q->held, 4 * b}, {q->count, 4 * b}, {q->free_pages, 4 * int64_t(q->num_free)}, {q->free_at, 4}};
+    const Range out[] = {{q->page_table, 4 * b * q->ld_table}, {q->free_at_out, 4}, {q->cu_tokens, 4 * (b + 1)}, {q->kv_len, 4 * b},
+                         {q->slots, 8 * q->tokens}, {q->positions, 4 * q->tokens}};
+    const auto meet = [](const Range &x, const Range &y) {
+        const char *px = static_cast<const char *>(x.p), *py = static_cast<const char *>(y.p);
+        return px != nullptr && py != nullptr && x.bytes > 0 && y.bytes > 0 && px < py + y.bytes && py < px + x.bytes;
+    };
+    for (int i = 0; i < 6; ++i) {
+        for (const Range &r : in)
+            if (meet(out[i], r))
+                return H3FP4_ERR_UNSUPPORTED;
+        for (int j = i + 1; j < 6; ++j)
+            if (meet(out[i], out[j]))
+                return H3FP4_ERR_UNSUPPORTED;
+    }
+    return from_cuda(h3fp4::launch_kv_tables(*q, as_stream(stream)));
+}
+
 h3fp4_status h3fp4_swizzle_scales(const uint8_t *sf_logical, int64_t rows, int64_t cols, int64_t ld,
                                   uint8_t *sf_out, void *stream)
 {
@@ -581,13 +860,14 @@ h3fp4_status h3fp4_device_error(uint32_t *code)
 {
     if (code == nullptr)
         return H3FP4_ERR_NULL;
-    uint32_t kv = 0, attn = 0;
+    uint32_t kv = 0, attn = 0, tables = 0;
     const h3fp4_status s = h3fp4::read_device_error(code);
     if (s != H3FP4_OK)
         return s;
-    if (h3fp4::read_kvcache_error(&kv) != cudaSuccess || h3fp4::read_attention_error(&attn) != cudaSuccess)
+    if (h3fp4::read_kvcache_error(&kv) != cudaSuccess || h3fp4::read_attention_error(&attn) != cudaSuccess ||
+        h3fp4::read_kv_tables_error(&tables) != cudaSuccess)
         return H3FP4_ERR_CUDA;
-    *code |= kv | attn;
+    *code |= kv | attn | tables;
     return H3FP4_OK;
 }
 

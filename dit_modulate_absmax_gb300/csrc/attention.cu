@@ -18,7 +18,7 @@ bool few_rows(const AttnShape &s) { return static_cast<int64_t>(s.max_tokens) * 
 AttnShape shape_of(const AttnArgs &a)
 {
     return AttnShape{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv,
-                     a.causal ? a.window : 0};
+                     a.causal || a.sinks > 0 ? a.window : 0, a.sinks, a.causal};
 }
 
 SplitPlan plan_of(const AttnShape &s) { return few_rows(s) ? plan_rows(s) : plan_tile(s); }
@@ -31,14 +31,50 @@ int64_t attention_workspace(const AttnShape &s)
     return rows > (int64_t(1) << 50) ? -1 : rows * (4 * s.head_dim + 8);   // a mean, and its sum's logarithm (or the sum and what it is kept against)
 }
 
-cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st)
+static cudaError_t launch_form(const AttnArgs &a, Form form, void *workspace, cudaStream_t st)
 {
     const AttnShape s = shape_of(a);   // (the parts are no more than without the reach: the workspace does for both)
     const SplitPlan plan = plan_of(s);
     float *part = static_cast<float *>(workspace);
     float *stat = part + plan.part_rows * s.head_dim;
-    return few_rows(s) ? launch_attention_rows(a, plan, stat, part, st)
-                       : launch_attention_tile(a, plan, reinterpret_cast<float2 *>(stat), part, st);
+    return few_rows(s) ? launch_attention_rows(a, form, plan, stat, part, st)
+                       : launch_attention_tile(a, form, plan, reinterpret_cast<float2 *>(stat), part, st);
+}
+
+cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st)
+{
+    return launch_form(a, a.sinks > 0 ? kSinks : kWhole, workspace, st);
+}
+
+// Of the workspace: the rows' prefix halves, then the parts of each call (the second may write its own while the first one's
+// are joined).
+static int64_t halves_bytes(const AttnShape &s) { return (s.tokens * s.heads * (4 * int64_t(s.head_dim) + 4) + 15) & ~int64_t(15); }
+
+int64_t attention_shared_workspace(const AttnShape &prefix, const AttnShape &own)
+{
+    const int64_t a = attention_workspace(prefix), b = attention_workspace(own);
+    if (a < 0 || b < 0 || own.tokens > (int64_t(1) << 50) / own.heads)
+        return -1;
+    if (prefix.batch == 0 || prefix.max_tokens == 0)
+        return b;   // no groups: the sequences' own keys are all
+    return halves_bytes(own) + ((a + 15) & ~int64_t(15)) + b;
+}
+
+cudaError_t launch_attention_shared(const AttnArgs &prefix, const AttnArgs &own, void *workspace, cudaStream_t st)
+{
+    if (prefix.batch.batch == 0 || prefix.batch.max_tokens == 0)
+        return launch_form(own, kWhole, workspace, st);
+    const AttnShape s = shape_of(own);
+    AttnArgs first = prefix, second = own;
+    first.half_mean = second.half_mean = static_cast<float *>(workspace);
+    first.half_log = second.half_log = first.half_mean + s.tokens * s.heads * s.head_dim;
+    second.prefix_cu = prefix.batch.cu_tokens;
+    second.prefix_groups = prefix.batch.batch;
+    uint8_t *parts = static_cast<uint8_t *>(workspace) + halves_bytes(s);
+    const cudaError_t e = launch_form(first, kPrefix, parts, st);
+    if (e != cudaSuccess)
+        return e;
+    return launch_form(second, kOwn, parts + ((attention_workspace(shape_of(prefix)) + 15) & ~int64_t(15)), st);
 }
 
 bool attention_timeout_ok(const AttnArgs &a)

@@ -62,7 +62,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
     return r;
 }
 
-// Positions [lo, hi) that query i of a sequence sees.
+// Forms of the kernels: all that a query sees in one call; the same with first positions that stay visible under a window;
+// the half over shared prefixes, and the half over a sequence's own keys that is joined to it.
+enum Form { kWhole, kSinks, kPrefix, kOwn };
+
+// Positions [lo, hi) that query i of a sequence sees.  With kSinks also those below a.sinks, as far as they lie below hi.
 struct Span {
     int lo, hi;
 };
@@ -78,6 +82,60 @@ __device__ __forceinline__ Span seen_by(const AttnArgs &a, const KvSequence &s, 
     if (r.hi <= r.lo)
         r.hi = r.lo = max(0, min(r.lo, s.len));   // empty
     return r;
+}
+
+template <int kForm>
+__device__ __forceinline__ bool seen(const AttnArgs &a, const Span &s, int tok)
+{
+    return tok < s.hi && (tok >= s.lo || (kForm == kSinks && tok < a.sinks));
+}
+
+// Whether [tok, tok + n) is seen as a whole by those that all see [lo, hi).
+template <int kForm>
+__device__ __forceinline__ bool all_seen(const AttnArgs &a, int lo, int hi, int tok, int n)
+{
+    return tok + n <= hi && (tok >= lo || (kForm == kSinks && tok + n <= a.sinks));
+}
+
+// The keys that some rows see, [lo, hi) and the sinks, as one run of places: place v below `keep` is position v, one from
+// there on position v + gap.  Both are multiples of `align` (a page and a kernel's step at least), so that neither a page nor
+// a step lies on both sides.  Sinks that reach to lo's step leave no gap.
+struct Fold {
+    int keep, gap;
+};
+
+template <int kForm>
+__device__ __forceinline__ Fold fold(const AttnArgs &a, int lo, int hi, int align)
+{
+    Fold f{0, 0};
+    if (kForm == kSinks) {
+        const int keep = (min(a.sinks, hi) + align - 1) & -align, from = lo & -align;
+        if (from > keep)
+            f = Fold{keep, from - keep};
+    }
+    return f;
+}
+
+template <int kForm>
+__device__ __forceinline__ int position(const Fold &f, int v)
+{
+    return kForm == kSinks && v >= f.keep ? v + f.gap : v;
+}
+
+// Waits, where this kernel was launched to overlap with it, for the one before, whose half of a row is read from here on.
+// Every thread of the kernel comes by here before it ends: what follows takes this grid's end for that of both.
+template <int kForm>
+__device__ __forceinline__ void after_prefix()
+{
+    if (kForm == kOwn)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <int kForm>
+__device__ __forceinline__ void let_next_start()
+{
+    if (kForm == kPrefix)
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Power of two that brings a row whose largest magnitude is amax (a bf16
@@ -137,6 +195,56 @@ __device__ __forceinline__ void add_log(float &top, float &sum, float log, float
     top = next;
 }
 
+// The shares of a row's two halves whose sums have these logarithms: each mean counts half^2 inv.
+struct Shares {
+    float own, prefix, inv, log;   // square roots of the shares before inv; log2 of the whole sum
+};
+
+__device__ __forceinline__ Shares shares_of(float own_log, float prefix_log)
+{
+    const float top = fmaxf(own_log, prefix_log), total = of_top(own_log, top) + of_top(prefix_log, top);
+    return Shares{half_of_top(own_log, top), half_of_top(prefix_log, top), reciprocal_sum(total), log_of_sum(top, total)};
+}
+
+// log2 of the sum of a row's prefix half; minus infinity for a row of no group.
+__device__ __forceinline__ float prefix_log(const AttnArgs &a, int64_t row, int head)
+{
+    const bool covered = row >= a.prefix_cu[0] && row < a.prefix_cu[a.prefix_groups];
+    return covered ? a.half_log[row * a.heads + head] : -INFINITY;
+}
+
+__device__ __forceinline__ float join_share(float own, float prefix, const Shares &s)
+{
+    return fmaf(prefix * s.prefix, s.prefix * s.inv, own * s.own * (s.own * s.inv));
+}
+
+// Writes four channels of a row: its output, its prefix half, or its output from both halves.
+template <int kForm>
+__device__ __forceinline__ void finish_row(const AttnArgs &a, int64_t row, int head, int c, float log, float4 mean)
+{
+    const int64_t at = row * a.heads + head;
+    if (kForm == kPrefix) {
+        *reinterpret_cast<float4 *>(a.half_mean + at * a.cache.head_dim + c) = mean;
+        if (c == 0)
+            a.half_log[at] = log;
+        return;
+    }
+    if (kForm == kOwn) {
+        const float other = prefix_log(a, row, head);
+        const Shares s = shares_of(log, other);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (other != -INFINITY)
+            v = *reinterpret_cast<const float4 *>(a.half_mean + at * a.cache.head_dim + c);
+        mean = make_float4(join_share(mean.x, v.x, s), join_share(mean.y, v.y, s), join_share(mean.z, v.z, s), join_share(mean.w, v.w, s));
+        log = s.log;
+    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(mean.x, mean.y), y = __floats2bfloat162_rn(mean.z, mean.w);
+    *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    if (a.lse != nullptr && c == 0)
+        a.lse[at] = log * kLn2;
+}
+
 // A page's table entry as the kernels keep it: id (< 0: none), the keys'
 // scale, log2 of the values' scale and its inverse: that of the logarithm as
 // it was rounded, so that the two cancel in the sum.
@@ -161,12 +269,28 @@ struct SplitPlan {
     bool cluster;
 };
 
+// For a launch that may begin while the one before it ends (it waits for that end itself).
+inline cudaLaunchAttribute overlap_with_last()
+{
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
+// Most keys that a window of s.reach and s.sinks leave to rows of `tokens` neighbouring queries, folded in steps of up to 128.
+inline int64_t folded_keys(const AttnShape &s, int64_t tokens)
+{
+    const int64_t kv = s.max_kv < 1 ? 1 : s.max_kv, most = int64_t(s.sinks) + s.reach + tokens + 256;
+    return s.sinks > 0 && s.reach > 0 && most < kv ? most : kv;
+}
+
 SplitPlan plan_rows(const AttnShape &s);
-cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st);
+cudaError_t launch_attention_rows(const AttnArgs &a, Form form, const SplitPlan &plan, float *logs, float *part, cudaStream_t st);
 cudaError_t launch_attention_rows_timeout(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, uint64_t wait_ns,
                                           cudaStream_t st);   // 128 channels, 8 rows at most
 SplitPlan plan_tile(const AttnShape &s);
-cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
+cudaError_t launch_attention_tile(const AttnArgs &a, Form form, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st);
 cudaError_t read_attention_tile_error(uint32_t *code);
 cudaError_t read_attention_rows_error(uint32_t *code);
 

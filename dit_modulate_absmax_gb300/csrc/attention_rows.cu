@@ -87,20 +87,23 @@ constexpr int resident()
 // Units of 128 tokens, one for each warp's 32, that a sequence's rows take: its
 // share of the work for each cache head and row tile.  0: nothing to do.
 struct Units {
-    int begin, count, tiles;   // first token (a multiple of 32), units, row tiles
+    int begin, count, tiles;   // first token's place (a multiple of 32), units, row tiles
+    Fold fold;
 };
 
-template <int kRows>
+template <int kRows, int kForm>
 __device__ __forceinline__ Units units_of(const AttnArgs &a, const KvSequence &s)
 {
     if (!s.ok || s.n == 0 || s.len > a.max_kv ||
         (s.len > 0 && ((s.len - 1) / a.cache.page_size >= a.batch.ld_table || a.cache.num_pages == 0)))
-        return Units{0, 0, 0};   // (a cache without pages has no arrays either: nothing of it may be read)
+        return Units{0, 0, 0, {0, 0}};   // (a cache without pages has no arrays either: nothing of it may be read)
     const Span first = seen_by(a, s, 0), last = seen_by(a, s, s.n - 1);
-    const int begin = min(first.lo, last.lo) & ~(kUnit - 1), end = max(first.hi, last.hi);
+    const int lo = min(first.lo, last.lo), hi = max(first.hi, last.hi);
+    const Fold f = fold<kForm>(a, lo, hi, max(kUnit, a.cache.page_size));
+    const int begin = kForm == kSinks ? 0 : lo & ~(kUnit - 1), end = hi - f.gap;
     constexpr int kTokens = kWarps * kUnit;
     return Units{begin, max(1, (end - begin + kTokens - 1) / kTokens),   // rows that see nothing are written all the same
-                 (s.n * (a.heads / a.cache.heads) + kRows - 1) / kRows};
+                 (s.n * (a.heads / a.cache.heads) + kRows - 1) / kRows, f};
 }
 
 // a / b of numbers that mostly fit 32 bits, where a division is several times shorter.
@@ -117,7 +120,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
 __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) { return divide((x + 1) * g - 1, total); }
 
 // kWithhold: for a check that waits end.  Each copy is announced larger than it is, so that none completes.
-template <int kDim, int kRows, bool kWithhold = false>
+template <int kDim, int kRows, int kForm, bool kWithhold = false>
 __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     rows_kernel(AttnArgs a, SplitPlan plan, float *ws_log, float *ws_out, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map, uint64_t wait_ns)
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         int64_t mine = 0;
         for (int b = threadIdx.x * share; b < min(a.batch.batch, (static_cast<int>(threadIdx.x) + 1) * share); ++b) {
             const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-            const Units u = units_of<kRows>(a, s);
+            const Units u = units_of<kRows, kForm>(a, s);
             mine += static_cast<int64_t>(u.count) * u.tiles * heads;
             if (u.count == 0 && s.n != 0 && blockIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
@@ -195,18 +198,21 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     bool whole = true;
     int64_t next = x_end;
     KvSequence s;
+    Fold places;
     if (plan.cluster) {   // one unit a CTA, a cluster for the rows of a sequence and cache head
         b = blockIdx.y;
         tile = 0;
         kh = blockIdx.x / plan.splits;
         s = kv_sequence(a.batch, b, a.tokens);
-        const Units u = units_of<kRows>(a, s);
+        const Units u = units_of<kRows, kForm>(a, s);
         if (u.count == 0) {   // the same in the whole cluster
             if (s.n != 0 && threadIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
+            after_prefix<kForm>();
             return;
         }
         __syncthreads();      // barriers initialised
+        places = u.fold;
         seg_begin = u.begin + blockIdx.x % plan.splits * kTokens;
         seg_end = seg_begin + kTokens;
     } else {
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             int at = threadIdx.x * share;
             if (share > 1)
                 for (;; ++at) {
-                    const Units v = units_of<kRows>(a, kv_sequence(a.batch, at, a.tokens));
+                    const Units v = units_of<kRows, kForm>(a, kv_sequence(a.batch, at, a.tokens));
                     const int64_t n = static_cast<int64_t>(v.count) * v.tiles * heads;
                     if (rest < n)
                         break;
@@ -228,11 +234,12 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         b = found_b;
         const int64_t rest = found_rest;
         s = kv_sequence(a.batch, b, a.tokens);
-        const Units u = units_of<kRows>(a, s);
+        const Units u = units_of<kRows, kForm>(a, s);
         const int item = static_cast<int>(divide(rest, u.count)), u0 = static_cast<int>(rest - static_cast<int64_t>(item) * u.count);
         const int u1 = static_cast<int>(min(static_cast<int64_t>(u.count), u0 + (x_end - x)));
         kh = item % heads;
         tile = item / heads;
+        places = u.fold;
         seg_begin = u.begin + u0 * kTokens;
         seg_end = u.begin + u1 * kTokens;
         whole = u0 == 0 && u1 == u.count;
@@ -243,12 +250,14 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, min(rows - 1, row0 + kRows - 1) / group);
     const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);   // seen by every row
     const int out_lo = min(first.lo, last.lo), out_hi = max(first.hi, last.hi); // seen by any
-    seg_begin = max(seg_begin, out_lo & ~(kUnit - 1));
-    seg_end = min(seg_end, out_hi);
+    if (kForm != kSinks)
+        seg_begin = max(seg_begin, out_lo & ~(kUnit - 1));
+    seg_end = min(seg_end, out_hi - places.gap);
+    const auto page_of = [&](int v) { return kForm == kSinks && v >= places.keep >> shift ? v + (places.gap >> shift) : v; };
     // The first pages' numbers are on their way while the queries are read.
     const int first_page = (seg_begin >> shift) + threadIdx.x;
     const int32_t first_id = seg_begin < seg_end && first_page <= (seg_end - 1) >> shift
-                                 ? a.batch.page_table[b * a.batch.ld_table + first_page] : 0;
+                                 ? a.batch.page_table[b * a.batch.ld_table + page_of(first_page)] : 0;
 
     // Q: rows g and g + 8; this lane's channels kDim/4 * t ...
     uint32_t q[kSteps][4];
@@ -307,10 +316,11 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     if (__syncthreads_or(!ok))   // the last part's readers are done
         break;
     for (int i = threadIdx.x; i < pages; i += kThreads) {
-        int32_t id = begin == seg_begin && i < kThreads ? first_id : a.batch.page_table[b * a.batch.ld_table + page0 + i];
-        // Units begin at multiples of 32 tokens, so that a page of 16 may lie before all that the rows see: whatever the
-        // table holds for it (it may be given up under a window), it is not copied.
-        if ((page0 + i + 1) << shift <= out_lo) {
+        const int at = page_of(page0 + i);
+        int32_t id = begin == seg_begin && i < kThreads ? first_id : a.batch.page_table[b * a.batch.ld_table + at];
+        // Units begin at multiples of 32 tokens, so that a page of 16 may lie before all that the rows see (or past the
+        // sinks): whatever the table holds for it (it may be given up under a window), it is not copied.
+        if ((at + 1) << shift <= out_lo && !(kForm == kSinks && at << shift < a.sinks)) {
             id = -1;
         } else if (id < 0 || id >= a.cache.num_pages) {
             atomicOr(&g_error, ERR_KV_RANGE);
@@ -391,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             }
         }
 
-        const bool edge = unit < in_lo || unit + kUnit > in_hi;
+        const int tok0 = position<kForm>(places, unit);
+        const bool edge = !all_seen<kForm>(a, in_lo, in_hi, tok0, kUnit);
         float top[kHalf];
 #pragma unroll
         for (int hf = 0; hf < kHalf; ++hf)
@@ -407,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                     float &v = sc[n][2 * hf + e];
                     v = fmaf(v, c_row[hf] * pe[n >> 1].ks, pe[n >> 1].lv);
                     if (edge) {
-                        const int tok = unit + 8 * n + 2 * t + e;
-                        if (tok < see[hf].lo || tok >= see[hf].hi)
+                        if (!seen<kForm>(a, see[hf], tok0 + 8 * n + 2 * t + e))
                             v = -INFINITY;
                     }
                     top[hf] = fmaxf(top[hf], v);
@@ -494,8 +504,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                     w[i][0] = v.x; w[i][1] = v.y;
                 }
                 if (edge) {   // codes that no row sees may be anything: zeros
-                    const int tok = unit + r;
-                    const uint32_t mask = tok >= out_lo && tok < out_hi ? 0xFFFFFFFFu : 0u;
+                    const uint32_t mask = seen<kForm>(a, Span{out_lo, out_hi}, tok0 + r) ? 0xFFFFFFFFu : 0u;
 #pragma unroll
                     for (int x = 0; x < kW; ++x) {
                         w[i][x] &= mask;
@@ -528,9 +537,8 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
                             uint32_t vis[2];
 #pragma unroll
                             for (int n = 0; n < 2; ++n) {
-                                const int tok = unit + 16 * hh + 8 * n + 2 * t;
-                                vis[n] = (tok >= see[hf].lo && tok < see[hf].hi ? 0x3C00u : 0u) |
-                                         (tok + 1 >= see[hf].lo && tok + 1 < see[hf].hi ? 0x3C000000u : 0u);
+                                const int tok = tok0 + 16 * hh + 8 * n + 2 * t;
+                                vis[n] = (seen<kForm>(a, see[hf], tok) ? 0x3C00u : 0u) | (seen<kForm>(a, see[hf], tok + 1) ? 0x3C000000u : 0u);
                             }
                             float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                             mma_f16(cnt, na, vis[0], vis[1]);
@@ -581,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             cluster_sync();
             cluster_sync();
         }
+        after_prefix<kForm>();
         return;
     }
     float *part = reinterpret_cast<float *>(dyn);   // [warp][row][kDim]
@@ -596,14 +605,9 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     float *joined = part + kWarps * kRows * kDim;                                 // [row][kDim], with a cluster
     float *joined_log = joined + kRows * kDim;                                    // [row]
     const auto finish = [&](int r, int c, float log, float4 mean) {
-        const int64_t row = s.row + (row0 + r) / group;
-        const int head = kh * group + (row0 + r) % group;
-        const __nv_bfloat162 x = __floats2bfloat162_rn(mean.x, mean.y), y = __floats2bfloat162_rn(mean.z, mean.w);
-        *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-        if (a.lse != nullptr && c == 0)
-            a.lse[row * a.heads + head] = log * kLn2;
+        finish_row<kForm>(a, s.row + (row0 + r) / group, kh * group + (row0 + r) % group, c, log, mean);
     };
+    after_prefix<kForm>();
     for (int i = threadIdx.x; i < kRows * (kDim / 4); i += kThreads) {
         const int r = i / (kDim / 4), c = (i % (kDim / 4)) * 4;
         if (row0 + r >= rows)
@@ -658,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     fence_proxy_async_smem();   // the join's plain accesses come before the next segment's copies to the same place
     __syncthreads();
     }
+    after_prefix<kForm>();   // (a CTA without a unit)
 }
 
 constexpr int kJoinThreads = 1024;
@@ -666,19 +671,20 @@ constexpr int kJoinThreads = 1024;
 // sequence, row tile and cache head, a thread for 4 channels of a row and every
 // kGroups-th part (one long request has as many parts as there are CTAs for a
 // cache head, 57 at 8 of them: one warp a row took 15 us over those).
-template <int kDim, int kRows>
+template <int kDim, int kRows, int kForm>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas, const float *ws_log, const float *ws_out)
 {
     constexpr int kPieces = kRows * kDim / 4;
     constexpr int kGroups = kJoinThreads / kPieces;
     __shared__ float4 means[kGroups][kPieces];
+    let_next_start<kForm>();
     const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
     const int kh = blockIdx.x % a.cache.heads, tile = blockIdx.x / a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
-    const Units u = units_of<kRows>(a, s);
+    const Units u = units_of<kRows, kForm>(a, s);
     int64_t ahead = 0, total = 0;   // units of the sequences before this one, and of all
     for (int i = lane; i < a.batch.batch; i += 32) {
-        const Units v = units_of<kRows>(a, kv_sequence(a.batch, i, a.tokens));
+        const Units v = units_of<kRows, kForm>(a, kv_sequence(a.batch, i, a.tokens));
         const int64_t n = static_cast<int64_t>(v.count) * v.tiles * a.cache.heads;
         total += n;
         ahead += i < b ? n : 0;
@@ -735,13 +741,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     }
     if (!live)
         return;
-    const int64_t row = s.row + row_in / group;
-    const int head = kh * group + row_in % group;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(mean.x, mean.y), y = __floats2bfloat162_rn(mean.z, mean.w);
-    *reinterpret_cast<uint2 *>(a.out + row * a.ot + head * a.oh + c) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    if (a.lse != nullptr && c == 0)
-        a.lse[row * a.heads + head] = log_of_sum(top, sum) * kLn2;
+    finish_row<kForm>(a, s.row + row_in / group, kh * group + row_in % group, c, log_of_sum(top, sum), mean);
 }
 
 }  // namespace
@@ -761,7 +761,7 @@ SplitPlan plan_rows(const AttnShape &s)
     const int64_t tile = rows <= 8 ? 8 : 16;
     const int64_t fit = sm_count() * (s.head_dim == 128 ? (tile == 8 ? resident<128, 8>() : resident<128, 16>())
                                                         : (tile == 8 ? resident<64, 8>() : resident<64, 16>()));
-    const int64_t per_row = s.max_kv < 1 ? 1 : (s.max_kv + kWarps * kUnit - 1) / (kWarps * kUnit);
+    const int64_t per_row = (folded_keys(s, s.max_tokens) + kWarps * kUnit - 1) / (kWarps * kUnit);
     if (per_row <= 8 && rows <= 16 && per_row * s.batch * s.kv_heads <= fit)
         return SplitPlan{static_cast<int32_t>(per_row), 0, 0, true};
     return SplitPlan{static_cast<int32_t>(fit), 0, fit * 2 * tile, false};
@@ -793,12 +793,12 @@ bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kDim, int kRows, bool kWithhold = false>
+template <int kDim, int kRows, int kForm, bool kWithhold = false>
 cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st, uint64_t wait_ns = kWaitNs)
 {
     constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = (kWarps + 1) * kRows * kDim * 4 + kRows * 4;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-    cudaError_t e = allow_shared<rows_kernel<kDim, kRows, kWithhold>>(kSmem);
+    cudaError_t e = allow_shared<rows_kernel<kDim, kRows, kForm, kWithhold>>(kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap k_map, v_map;
@@ -816,45 +816,59 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
     if (x > INT32_MAX || joins > INT32_MAX)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = plan.cluster ? dim3(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch))
                                : dim3(static_cast<unsigned>(plan.splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(plan.splits);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.numAttrs = plan.cluster ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows, kWithhold>, a, plan, logs, part, k_map, v_map, wait_ns);
+    cfg.attrs = attr;
+    if (plan.cluster) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(plan.splits);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    if (kForm == kOwn)
+        attr[cfg.numAttrs++] = overlap_with_last();
+    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows, kForm, kWithhold>, a, plan, logs, part, k_map, v_map, wait_ns);
     if (e != cudaSuccess || plan.cluster || kWithhold)
         return e;
     // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
     cfg.gridDim = dim3(static_cast<unsigned>(joins), static_cast<unsigned>(a.batch.batch));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    attr[0] = overlap_with_last();
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows>, a, static_cast<int>(plan.splits), static_cast<const float *>(logs),
+    return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows, kForm>, a, static_cast<int>(plan.splits), static_cast<const float *>(logs),
                               static_cast<const float *>(part));
 }
 
 }  // namespace
 
-cudaError_t launch_attention_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
+template <int kForm>
+static cudaError_t run_rows_form(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
 {
     const bool small = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads) <= 8;
     if (a.cache.head_dim == 64)
-        return small ? run_rows<64, 8>(a, plan, logs, part, st) : run_rows<64, 16>(a, plan, logs, part, st);
-    return small ? run_rows<128, 8>(a, plan, logs, part, st) : run_rows<128, 16>(a, plan, logs, part, st);
+        return small ? run_rows<64, 8, kForm>(a, plan, logs, part, st) : run_rows<64, 16, kForm>(a, plan, logs, part, st);
+    return small ? run_rows<128, 8, kForm>(a, plan, logs, part, st) : run_rows<128, 16, kForm>(a, plan, logs, part, st);
+}
+
+cudaError_t launch_attention_rows(const AttnArgs &a, Form form, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
+{
+    switch (form) {
+    case kSinks: return run_rows_form<kSinks>(a, plan, logs, part, st);
+    case kPrefix: return run_rows_form<kPrefix>(a, plan, logs, part, st);
+    case kOwn: return run_rows_form<kOwn>(a, plan, logs, part, st);
+    default: return run_rows_form<kWhole>(a, plan, logs, part, st);
+    }
 }
 
 cudaError_t launch_attention_rows_timeout(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, uint64_t wait_ns,
                                           cudaStream_t st)
 {
-    return run_rows<128, 8, true>(a, plan, logs, part, st, wait_ns);
+    return run_rows<128, 8, kWhole, true>(a, plan, logs, part, st, wait_ns);
 }
 
 cudaError_t read_attention_rows_error(uint32_t *code)

@@ -135,7 +135,7 @@ __device__ __forceinline__ void shrink_registers()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <int kDim, int kGroup>
+template <int kDim, int kGroup, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(AttnArgs a, SplitPlan plan, int row_tiles, bool longest_first, float2 *ws_stat, float *ws_out)
 {
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem<kDim> &sm = *reinterpret_cast<Smem<kDim> *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int page = a.cache.page_size, group = a.heads / a.cache.heads;
+    let_next_start<kForm>();
     int tile, rest;   // the order of the grid, see by_length()
     if (longest_first) {
         const int others = a.cache.heads * plan.splits * a.batch.batch;
@@ -154,23 +155,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int kh = rest % a.cache.heads, split = rest / a.cache.heads % plan.splits, b = rest / a.cache.heads / plan.splits;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-    if (s.n == 0)
+    if (s.n == 0) {
+        after_prefix<kForm>();
         return;   // without queries its length and pages are not looked at
+    }
     if (!s.ok || s.len > a.max_kv || (s.len > 0 && ((s.len - 1) / page >= a.batch.ld_table || a.cache.num_pages == 0))) {
         if (threadIdx.x == 0)
             atomicOr(&g_error, ERR_KV_RANGE);
+        after_prefix<kForm>();
         return;
     }
     const int rows = s.n * group;   // below 2^31 (run_tile checks max_tokens)
     const int row0 = tile * (kTiles * 128);
-    if (row0 >= rows || (split > 0 && split * plan.chunk >= s.len))
+    if (row0 >= rows || (split > 0 && split * plan.chunk >= s.len)) {
+        after_prefix<kForm>();
         return;
+    }
     const int row_end = min(rows, row0 + kTiles * 128);
     const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, (row_end - 1) / group);
     const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);     // seen by every row
     const int out_lo = min(first.lo, last.lo);                                    // seen by any
-    const int begin = max(split * plan.chunk, out_lo & ~(kKeys - 1));
-    const int end = min(min((split + 1) * plan.chunk, s.len), max(first.hi, last.hi));
+    // Places (of positions, folded where sinks and window lie apart) of this CTA's keys.
+    const int out_hi = max(first.hi, last.hi);
+    const Fold places = fold<kForm>(a, out_lo, out_hi, kKeys);
+    const int begin = kForm == kSinks ? split * plan.chunk : max(split * plan.chunk, out_lo & ~(kKeys - 1));
+    const int end = kForm == kSinks ? min((split + 1) * plan.chunk, out_hi - places.gap) : min(min((split + 1) * plan.chunk, s.len), out_hi);
     const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
     const int tiles = row_end - row0 > 128 ? 2 : 1;
 
@@ -211,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         if (warp == kMmaWarp)
             tmem_dealloc(sm.tmem, 512);
+        after_prefix<kForm>();
         return;
     }
 
@@ -256,27 +266,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             // inside of one loop 5,420 and 104).
             const auto step = [&](auto far_scales, int j) -> bool {
                 constexpr bool kFar = decltype(far_scales)::value;
-                const int k0 = begin + j * kKeys;
-                const bool edge = k0 < t_lo || k0 + kKeys > t_hi;
+                const int k0 = position<kForm>(places, begin + j * kKeys);
+                const bool edge = !all_seen<kForm>(a, t_lo, t_hi, k0, kKeys);
                 if (!wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) || (!kFar && j >= sm.far_from) ||
                     !wait_for(sm.s_full[t], j & 1))
                     return false;
                 tc_fence_after();
                 const PageEntry *pe = sm.entry[j % kEntrySlots];
                 const int lo = see.lo - k0, hi = see.hi - k0;
+                const auto visible = [&](int col) { return seen<kForm>(a, see, k0 + col); };
                 // A step in which some rows do not see some keys: minus infinity goes over those scores in TMEM, so that
                 // the straight code below is the same for all steps (masking its registers there, under a branch, made
                 // every step 13 % slower).
                 if (edge) {
 #pragma unroll 1
                     for (int n = 0; n < kKeys / 16; ++n) {
-                        if (__all_sync(0xFFFFFFFFu, lo <= 16 * n && hi >= 16 * n + 16))
+                        if (__all_sync(0xFFFFFFFFu, all_seen<kForm>(a, see.lo, see.hi, k0 + 16 * n, 16)))
                             continue;
                         uint32_t x[16];
                         tmem_ld_32x32b_x16_wait(sc + 16 * n, x);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            x[i] = 16 * n + i >= lo && 16 * n + i < hi ? x[i] : 0xFF800000u;
+                            x[i] = visible(16 * n + i) ? x[i] : 0xFF800000u;
                         tmem_st_32x32b_x16(sc + 16 * n, x);
                     }
                     tmem_st_wait();
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int y = 0; y < 2; ++y) {
                                 const int col = 16 * n + i + y;
                                 const float z = __uint_as_float(x[i + y]);
-                                w[y] = col >= lo && col < hi ? ex2(far ? fmaf(z, ck, e.lv) - at : fmaf(z, ck, off)) : 0.0f;
+                                w[y] = visible(col) ? ex2(far ? fmaf(z, ck, e.lv) - at : fmaf(z, ck, off)) : 0.0f;
                             }
                             p[i / 2] = pack_half2(w[0], w[1]);
                             float2 &sum = (i & 2) == 0 ? s0 : s1;
@@ -408,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                if (k0 < in_lo || k0 + kKeys > in_hi) {   // the conversion warps keep NaN out of such a step's values
+                if (!all_seen<kForm>(a, in_lo, in_hi, k0, kKeys)) {   // the conversion warps keep NaN out of such a step's values
                     if (!wait_for(sm.v_full[j % kStages], (j / kStages) & 1))
                         return false;
                     constexpr int kRowsPerWarp = 32 / (kDim / 16);   // of a conversion warp, among kConvertWarps * that
@@ -418,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint16_t *mine = sm.row_nan[128 * t + in_tile];
                         for (int c = 0; c < kDim / 16; ++c) {
                             uint32_t m = met_nan ? mine[c] : 0u;
-                            for (int x = max(lo, 0); x < min(hi, kKeys); ++x)
-                                if (x / kRowsPerWarp % kConvertWarps == w)
+                            for (int x = kForm == kSinks ? 0 : max(lo, 0); x < min(hi, kKeys); ++x)
+                                if ((kForm != kSinks || visible(x)) && x / kRowsPerWarp % kConvertWarps == w)
                                     m |= sm.nan_mask[j % kStages][x][c];
                             mine[c] = static_cast<uint16_t>(m);
                         }
@@ -465,7 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool final = plan.splits == 1;
                 const float inv = reciprocal_sum(l) * o_factor;
                 uint16_t *out = a.out + row * a.ot + head * a.oh;
-                float *part = ws_out + (at * plan.splits + split) * kDim;
+                float *part = kForm == kPrefix && final ? a.half_mean + at * kDim : ws_out + (at * plan.splits + split) * kDim;
+                Shares share{};
+                bool other_half = false;
+                if (kForm == kOwn && final) {
+                    after_prefix<kForm>();
+                    const float other = live ? prefix_log(a, row, head) : -INFINITY;
+                    other_half = other != -INFINITY;   // (else its mean may be anything)
+                    share = shares_of(log_of_sum(ref, l), other);
+                }
 #pragma unroll 1
                 for (int c = 0; c < kDim / 32; ++c) {
                     uint32_t v[32];
@@ -487,7 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             o[i] = m >> i & 1 ? __uint_as_float(0x7FC00000u) : o[i];
                     }
-                    if (live && final) {
+                    if (kForm == kOwn && final) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 p = other_half ? *reinterpret_cast<const float4 *>(a.half_mean + at * kDim + 32 * c + i)
+                                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            o[i] = join_share(o[i], p.x, share);
+                            o[i + 1] = join_share(o[i + 1], p.y, share);
+                            o[i + 2] = join_share(o[i + 2], p.z, share);
+                            o[i + 3] = join_share(o[i + 3], p.w, share);
+                        }
+                    }
+                    if (live && final && kForm != kPrefix) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
                             uint32_t w[4];
@@ -506,8 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live && !final)
                     ws_stat[at * plan.splits + split] = make_float2(ref, l);
+                else if (live && kForm == kPrefix)
+                    a.half_log[at] = log_of_sum(ref, l);
                 else if (live && a.lse != nullptr)
-                    a.lse[at] = log_of_sum(ref, l) * kLn2;
+                    a.lse[at] = (kForm == kOwn ? share.log : log_of_sum(ref, l)) * kLn2;
                 tc_fence_before();
             }
         }
@@ -526,8 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // only when its codes are loaded.
         const int shift = 31 - __clz(page);
         const auto page_ids = [&](int j) -> int32_t {
-            const int64_t tok = begin + static_cast<int64_t>(j) * kKeys + lane * page;
-            return lane < kKeys / page && tok < end && tok + page > out_lo ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift)] : -2;
+            const int64_t v = begin + static_cast<int64_t>(j) * kKeys + lane * page;
+            const int64_t tok = kForm == kSinks && v >= places.keep ? v + places.gap : v;
+            return lane < kKeys / page && v < end && (tok + page > out_lo || (kForm == kSinks && tok < a.sinks))
+                       ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift)] : -2;
         };
         const auto checked = [&](int32_t id) -> int32_t {        // -2: no page; out of range: reported, page 0 instead
             if (id == -2 || (id >= 0 && id < a.cache.num_pages))
@@ -544,9 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A piece's group of kRowStep tokens lies in one page (dim 128: 16 tokens) or in two (dim 64: 32).
         const int64_t page_bytes = static_cast<int64_t>(a.cache.heads) * page * kDim;
         const int64_t mine = static_cast<int64_t>(kh) * page * kDim + 16 * c;
-        const auto load = [&](const uint8_t *codes, int k0, uint4 (&w)[kPer]) {
+        const auto load = [&](const uint8_t *codes, int v0, uint4 (&w)[kPer]) {   // v0: the first key's place
             const uint8_t *base = codes + mine;
-            if (k0 >= out_lo && k0 + kKeys <= end) {
+            const int k0 = position<kForm>(places, v0);
+            if ((k0 >= out_lo || (kForm == kSinks && k0 + kKeys <= a.sinks)) && v0 + kKeys <= end) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
                     w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + ((r0 + i * kRowStep) & (page - 1)) * kDim);
@@ -555,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kPer; ++i) {
                     const int tok = k0 + r0 + i * kRowStep;
                     w[i] = make_uint4(0, 0, 0, 0);
-                    if (tok >= out_lo && tok < end)
+                    if ((tok >= out_lo || (kForm == kSinks && tok < a.sinks)) && v0 + r0 + i * kRowStep < end)
                         w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + (tok & (page - 1)) * kDim);
                 }
             }
@@ -584,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(a.cache.k_codes, begin, kw);
         load(a.cache.v_codes, begin, vw);
         for (int j = 0; j < steps; ++j) {
-            const int k0 = begin + j * kKeys, st = j % kStages;
-            const bool edge = k0 < in_lo || k0 + kKeys > in_hi;
+            const int v0 = begin + j * kKeys, st = j % kStages;
+            const bool edge = !all_seen<kForm>(a, in_lo, in_hi, position<kForm>(places, v0), kKeys);
             if (!wait_for(sm.k_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
@@ -605,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             next_id = page_ids(j + 2);
             scales();
             ids(lane_id);
-            load(a.cache.k_codes, k0 + kKeys, kw);   // zeros past the end
+            load(a.cache.k_codes, v0 + kKeys, kw);   // zeros past the end
 
             if (!wait_for(sm.v_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
@@ -636,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store(smem_u32(sm.v[st]), vw[i], i);
             fence_proxy_async_smem();
             warp_arrive(sm.v_full[st]);
-            load(a.cache.v_codes, k0 + kKeys, vw);
+            load(a.cache.v_codes, v0 + kKeys, vw);
         }
     } else {
         // ------------------------------------------------------------------ MMA issue
@@ -703,14 +738,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(0, 512);
     }
+    after_prefix<kForm>();
 }
 
 constexpr int kJoinThreads = 128;
 
 // Joins the parts of each row: one warp per query token and head.
-template <int kDim>
+template <int kDim, int kForm>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPlan plan, const float2 *ws_stat, const float *ws_out)
 {
+    let_next_start<kForm>();
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
@@ -719,7 +756,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
     const int64_t row = s.row + w / a.heads;
     const int head = static_cast<int>(w % a.heads);
     const int64_t at = row * a.heads + head;
-    const int parts = max(1, (s.len + plan.chunk - 1) / plan.chunk);
+    const int parts = min(plan.splits, max(1, (s.len + plan.chunk - 1) / plan.chunk));   // (folded: fewer than the length has)
     const float2 *stat = ws_stat + at * plan.splits;
     const auto log_of = [&](int i) { return log_of_sum(stat[i].x, stat[i].y); };
     float top = -INFINITY, sum = 0.0f;
@@ -747,6 +784,24 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
             mean[c + 1] = fmaf(v.y * half, rest, mean[c + 1]);
         }
     }
+    float log = log_of_sum(top, sum);
+    if (kForm == kOwn) {
+        const float other = prefix_log(a, row, head);
+        const Shares share = shares_of(log, other);
+        const float *half = a.half_mean + at * kDim + lane * kPer;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+            mean[c] = join_share(mean[c], other != -INFINITY ? half[c] : 0.0f, share);
+        log = share.log;
+    }
+    if (kForm == kPrefix) {
+#pragma unroll
+        for (int c = 0; c < kPer; c += 2)
+            *reinterpret_cast<float2 *>(a.half_mean + at * kDim + lane * kPer + c) = make_float2(mean[c], mean[c + 1]);
+        if (lane == 0)
+            a.half_log[at] = log;
+        return;
+    }
     uint16_t *dst = a.out + row * a.ot + head * a.oh + lane * kPer;
 #pragma unroll
     for (int c = 0; c < kPer; c += 2) {
@@ -754,7 +809,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
         *reinterpret_cast<uint32_t *>(dst + c) = *reinterpret_cast<const uint32_t *>(&v);
     }
     if (a.lse != nullptr && lane == 0)
-        a.lse[at] = log_of_sum(top, sum) * kLn2;
+        a.lse[at] = log * kLn2;
 }
 
 // kGroup: scores in a row that are sure to lie in one page.
@@ -769,18 +824,18 @@ bool by_length(const AttnArgs &a)
     return a.causal && 2.0 * a.batch.batch * a.cache.heads * a.max_kv * a.cache.head_dim <= 128.0 * 1048576;
 }
 
-template <int kDim, int kGroup>
+template <int kDim, int kGroup, int kForm>
 cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
 {
     // More than half of an SM's shared memory even at dim 64: a second CTA on the SM would wait for the first one's TMEM.
     constexpr int kNeed = sizeof(Smem<kDim>) + 1024, kSmem = kNeed > 120 * 1024 ? kNeed : 120 * 1024;
     static_assert(kSmem <= 227 * 1024, "fits an SM");
-    cudaError_t e = allow_shared<tile_kernel<kDim, kGroup>>(kSmem);
+    cudaError_t e = allow_shared<tile_kernel<kDim, kGroup, kForm>>(kSmem);
     if (e != cudaSuccess)
         return e;
     static const bool registers_fit = [] {   // a property of the build
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, tile_kernel<kDim, kGroup>) == cudaSuccess && 4 * f.numRegs >= kSplitRegs && f.numRegs >= kConvertRegs;
+        return cudaFuncGetAttributes(&f, tile_kernel<kDim, kGroup, kForm>) == cudaSuccess && 4 * f.numRegs >= kSplitRegs && f.numRegs >= kConvertRegs;
     }();
     if (!registers_fit)
         return cudaErrorLaunchOutOfResources;
@@ -788,9 +843,15 @@ cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     const int64_t tiles = (most * (a.heads / a.cache.heads) + kTiles * 128 - 1) / (kTiles * 128), x = tiles * a.cache.heads * plan.splits * a.batch.batch;
     if (x > INT32_MAX || tiles * (kTiles * 128) > INT32_MAX)
         return cudaErrorInvalidValue;
-    tile_kernel<kDim, kGroup><<<static_cast<unsigned>(x), kThreads, kSmem, st>>>(a, plan, static_cast<int>(tiles), by_length(a), stat,
-                                                                             part);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr = overlap_with_last();
+    cfg.gridDim = dim3(static_cast<unsigned>(x));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = kForm == kOwn ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, tile_kernel<kDim, kGroup, kForm>, a, plan, static_cast<int>(tiles), by_length(a), stat, part);
 }
 
 }  // namespace
@@ -802,7 +863,7 @@ SplitPlan plan_tile(const AttnShape &s)
 {
     const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);
     const int64_t ctas = static_cast<int64_t>(s.batch) * s.kv_heads * ((rows + kTiles * 128 - 1) / (kTiles * 128));
-    const int64_t kv = s.max_kv < 1 ? 1 : s.max_kv;
+    const int64_t group = s.heads / s.kv_heads, kv = s.max_kv < 1 ? 1 : s.max_kv;
     int64_t splits = ctas > 0 ? sm_count() / ctas : 1;
     const int64_t most = (kv + 255) / 256;
     splits = splits > most ? most : splits < 1 ? 1 : splits;
@@ -810,21 +871,26 @@ SplitPlan plan_tile(const AttnShape &s)
     splits = (kv + chunk - 1) / chunk;
     // Under a window that lies within a part most parts have nothing to do but to write that down (4,674 tokens of 2 heads,
     // window 5: 24.2 us in one part, 32.4 in four).
-    const int64_t tokens = kTiles * 128 / (s.heads / s.kv_heads) + 1;   // of a CTA's rows
-    if (s.reach > 0 && s.reach + tokens <= chunk) {
+    const int64_t tokens = kTiles * 128 / group + 1;   // of a CTA's rows
+    if (s.sinks > 0) {   // parts of what is left of the keys, no more than above
+        const int64_t left = folded_keys(s, s.causal ? tokens : s.max_tokens), parts = std::min(splits, (left + 255) / 256);
+        chunk = ((left + parts - 1) / parts + kKeys - 1) / kKeys * kKeys;
+        splits = (left + chunk - 1) / chunk;
+    } else if (s.reach > 0 && s.reach + tokens <= chunk) {
         splits = 1;
         chunk = (kv + kKeys - 1) / kKeys * kKeys;
     }
     return SplitPlan{static_cast<int32_t>(splits), static_cast<int32_t>(chunk), splits > 1 ? s.tokens * s.heads * splits : 0, false};
 }
 
-cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+template <int kForm>
+static cudaError_t run_tile_form(const AttnArgs &a, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
 {
     cudaError_t e;
     if (a.cache.page_size == 16)
-        e = a.cache.head_dim == 64 ? run_tile<64, 16>(a, plan, stat, part, st) : run_tile<128, 16>(a, plan, stat, part, st);
+        e = a.cache.head_dim == 64 ? run_tile<64, 16, kForm>(a, plan, stat, part, st) : run_tile<128, 16, kForm>(a, plan, stat, part, st);
     else
-        e = a.cache.head_dim == 64 ? run_tile<64, 32>(a, plan, stat, part, st) : run_tile<128, 32>(a, plan, stat, part, st);
+        e = a.cache.head_dim == 64 ? run_tile<64, 32, kForm>(a, plan, stat, part, st) : run_tile<128, 32, kForm>(a, plan, stat, part, st);
     if (e != cudaSuccess || plan.splits == 1)
         return e;
     constexpr int kJoinWarps = kJoinThreads / 32;
@@ -833,10 +899,20 @@ cudaError_t launch_attention_tile(const AttnArgs &a, const SplitPlan &plan, floa
         return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch));
     if (a.cache.head_dim == 64)
-        join_kernel<64><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
+        join_kernel<64, kForm><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
     else
-        join_kernel<128><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
+        join_kernel<128, kForm><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
     return cudaGetLastError();
+}
+
+cudaError_t launch_attention_tile(const AttnArgs &a, Form form, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)
+{
+    switch (form) {
+    case kSinks: return run_tile_form<kSinks>(a, plan, stat, part, st);
+    case kPrefix: return run_tile_form<kPrefix>(a, plan, stat, part, st);
+    case kOwn: return run_tile_form<kOwn>(a, plan, stat, part, st);
+    default: return run_tile_form<kWhole>(a, plan, stat, part, st);
+    }
 }
 
 cudaError_t read_attention_tile_error(uint32_t *code)

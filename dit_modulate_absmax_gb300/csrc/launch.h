@@ -127,16 +127,29 @@ struct AttnArgs {
     int32_t max_kv;
     float scale;
     int32_t causal, window;
+    int32_t sinks = 0;                // first positions that a window does not hide
+    // One half of a softmax over two sets of keys, per row and head: the mean [tokens, heads, dim] and log2 of the sum
+    // [tokens, heads].  The call over the prefixes writes them instead of out and lse; the other joins them to its own
+    // for the rows that prefix_cu (of prefix_groups groups) covers.
+    float *half_mean = nullptr, *half_log = nullptr;
+    const int32_t *prefix_cu = nullptr;
+    int32_t prefix_groups = 0;
 };
 
 struct AttnShape {
     int64_t tokens;
     int32_t heads, kv_heads, head_dim, batch, max_tokens, max_kv;
     int32_t reach = 0;   // most keys that a query sees under a causal window; 0: all
+    int32_t sinks = 0;   // with those first ones (the reach is then that of any window)
+    int32_t causal = 0;
 };
 
 int64_t attention_workspace(const AttnShape &s);
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st);
+
+// Attention over prefixes that groups of sequences share, then over the sequences' own keys, joined.
+int64_t attention_shared_workspace(const AttnShape &prefix, const AttnShape &own);
+cudaError_t launch_attention_shared(const AttnArgs &prefix, const AttnArgs &own, void *workspace, cudaStream_t st);
 
 // Failure detection: few queries with copies that never complete.
 bool attention_timeout_ok(const AttnArgs &a);

@@ -309,6 +309,76 @@ H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_strid
                                        void *stream);
 
 /*
+ * h3fp4_norm_rope -- per-head RMS norm of queries and keys, and their rotation,
+ * in one pass over each.
+ *
+ * For every token and head, with w the side's weight:
+ *     r = 1 / sqrt(mean(x^2) + eps),  z = x r w,  out = RN_bf16(z turned as by h3fp4_rope_axes)
+ * in FP32 before the one rounding.  Rows of any finite size are in range; a row
+ * with an infinity gives 0 for its finite channels (NaN for the others), one
+ * with a NaN gives NaN.
+ *
+ *   q, k       the two sides; either may be NULL (or have no heads).  x and out are [tokens, heads, head_dim]
+ *              bf16, strides as for h3fp4_rope_axes.  out either is its own x (same pointer and strides: in place)
+ *              or has no element in common with either side's x or the other out (else H3FP4_ERR_UNSUPPORTED): of
+ *              the same strides they may be interleaved, as queries and keys in a QKV projection's rows are, of
+ *              others their ranges are apart
+ *   weight     device [head_dim], shared by the side's heads; bf16 (weight_f32 0) or float (1).  NULL: ones
+ *   head_dim   multiple of 8, 8 .. 256
+ *   eps        2^-100 .. 2^20
+ *   rope       NULL: no rotation.  inverse must be 0
+ */
+typedef struct h3fp4_norm_heads {
+    const void *x;
+    int64_t x_token_stride, x_head_stride;
+    void *out;
+    int64_t out_token_stride, out_head_stride;
+    const void *weight;
+    int32_t heads;              /* 0 .. 65535 */
+    int32_t weight_f32;         /* 0 or 1 */
+} h3fp4_norm_heads;
+
+H3FP4_API h3fp4_status h3fp4_norm_rope(const h3fp4_norm_heads *q, const h3fp4_norm_heads *k, int64_t tokens,
+                                       int32_t head_dim, float eps, const h3fp4_rope *rope, void *stream);
+
+/*
+ * h3fp4_norm_rope_backward -- gradients of h3fp4_norm_rope from those of its
+ * outputs, dy; nothing of the forward pass is kept but its inputs.
+ *
+ * With g = dy turned back and r as above:
+ *     dx = RN_bf16(r (w g - x r^2 mean(w g x))),  dweight[c] = sum of g[c] x[c] r over the side's tokens and heads
+ * dweight is written, not added to, in FP32 sums of a fixed order (the same
+ * bits every time on a device); zeros where there are no tokens or heads.
+ *
+ *   dy, x, dx  [tokens, heads, head_dim] bf16, strides as for h3fp4_rope_axes.  dx either is its side's dy or x
+ *              (same pointer and strides) or has no element in common with any of the call's arrays, as above
+ *   weight     as in the forward call
+ *   dweight    device float [head_dim], 4-byte aligned; NULL: not wanted
+ *   workspace  h3fp4_norm_rope_backward_workspace bytes of device scratch, 16-byte aligned (contents on entry are
+ *              ignored; two calls that overlap on the GPU must not share it); may be NULL where no dweight is wanted
+ *   other arguments as for h3fp4_norm_rope
+ */
+typedef struct h3fp4_norm_grads {
+    const void *dy;
+    int64_t dy_token_stride, dy_head_stride;
+    const void *x;
+    int64_t x_token_stride, x_head_stride;
+    void *dx;
+    int64_t dx_token_stride, dx_head_stride;
+    const void *weight;
+    float *dweight;
+    int32_t heads;
+    int32_t weight_f32;
+} h3fp4_norm_grads;
+
+H3FP4_API h3fp4_status h3fp4_norm_rope_backward(const h3fp4_norm_grads *q, const h3fp4_norm_grads *k, int64_t tokens,
+                                                int32_t head_dim, float eps, const h3fp4_rope *rope, void *workspace,
+                                                int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that h3fp4_norm_rope_backward wants on the current device (-1 for a head_dim it refuses). */
+H3FP4_API int64_t h3fp4_norm_rope_backward_workspace(int32_t head_dim);
+
+/*
  * h3fp4_kv_cache -- keys and values in E4M3 (bias 7, max 448), in pages of
  * page_size tokens, with one FP32 scale per page and head for the keys and
  * one for the values: a value is code * scale.
@@ -431,6 +501,108 @@ H3FP4_API h3fp4_status h3fp4_kv_attention(const void *q_bf16, int64_t q_token_st
 /* Bytes of workspace that h3fp4_kv_attention wants for these sizes (host only; -1 for sizes it refuses). */
 H3FP4_API int64_t h3fp4_kv_attention_workspace(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                                int32_t batch, int32_t max_tokens, int32_t max_kv);
+
+/*
+ * h3fp4_kv_attention_sinks -- h3fp4_kv_attention whose first tokens stay visible
+ * under a sliding window: a query sees the positions j < len[b] with
+ *     j <= its own position                            if causal, and
+ *     j > its own position - window, or j < sinks      if window > 0.
+ * Pages that lie wholly between the two are not looked at, whatever the table
+ * holds for them, so that a bounded number of pages serves an endless
+ * sequence.
+ *
+ *   sinks      0 .. 2^30 (0, or no window: h3fp4_kv_attention)
+ *   workspace  as for h3fp4_kv_attention
+ */
+H3FP4_API h3fp4_status h3fp4_kv_attention_sinks(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                                                void *out_bf16, int64_t out_token_stride, int64_t out_head_stride,
+                                                float *lse, int64_t tokens, int32_t heads, const h3fp4_kv_cache *cache,
+                                                const h3fp4_kv_batch *batch, int32_t max_kv, float softmax_scale,
+                                                int32_t causal, int32_t window, int32_t sinks, void *workspace,
+                                                int64_t workspace_bytes, void *stream);
+
+/*
+ * h3fp4_kv_attention_shared -- attention of sequences that share prefixes,
+ * whose codes are read once for all of a group's queries.
+ *
+ * `prefix` holds a row of the page table for each group of sequences: len[g]
+ * keys, all of which every query of tokens prefix.cu_tokens[g] ..
+ * prefix.cu_tokens[g+1] - 1 sees (a group's tokens follow one another, and the
+ * groups).  `batch` holds the sequences' own keys, as for h3fp4_kv_attention:
+ * positions, lengths and pages count from the prefix's end, so that a prefix
+ * may end inside a page.  A token's output is the softmax over its prefix and
+ * what it sees of its own keys, out and lse as for h3fp4_kv_attention; tokens
+ * of no group have no prefix, groups may be empty, and prefixes too.  The two
+ * halves are joined from FP32 means and logarithms.  Rows outside the
+ * sequences are left as they were.
+ *
+ *   prefix      batch: the groups; max_tokens: the most tokens of a group
+ *   max_prefix  the most keys of a prefix; at most 2^30
+ *   workspace   h3fp4_kv_attention_shared_workspace bytes of device scratch, 16-byte aligned (contents on entry
+ *               are ignored; two calls that overlap on the GPU must not share it)
+ *   other arguments as for h3fp4_kv_attention
+ */
+H3FP4_API h3fp4_status h3fp4_kv_attention_shared(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                                                 void *out_bf16, int64_t out_token_stride, int64_t out_head_stride,
+                                                 float *lse, int64_t tokens, int32_t heads, const h3fp4_kv_cache *cache,
+                                                 const h3fp4_kv_batch *prefix, int32_t max_prefix,
+                                                 const h3fp4_kv_batch *batch, int32_t max_kv, float softmax_scale,
+                                                 int32_t causal, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that h3fp4_kv_attention_shared wants for these sizes (host only; -1 for sizes it refuses). */
+H3FP4_API int64_t h3fp4_kv_attention_shared_workspace(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                                      int32_t groups, int32_t max_group_tokens, int32_t max_prefix,
+                                                      int32_t batch, int32_t max_tokens, int32_t max_kv);
+
+/*
+ * h3fp4_kv_tables -- what the cache and attention calls want to know of a
+ * batch, from its requests' lengths, without the host: offsets and lengths,
+ * pages for the new tokens from a list of free ones, and each token's place.
+ *
+ * Sequence b holds held[b] tokens and gets count[b] new ones.  In the order of
+ * the sequences:
+ *     cu_tokens[b + 1] = count[0] + ... + count[b],   kv_len[b] = held[b] + count[b],
+ *     page_table[b, p] = the next of free_pages, for ceil(held[b] / page_size) <= p < ceil(kv_len[b] / page_size),
+ * the first taken being free_pages[*free_at] and *free_at_out = *free_at + those
+ * taken.  New token i of sequence b, at position held[b] + i, is row
+ * cu_tokens[b] + i of
+ *     slots     page_table[b, position / page_size] * page_size + position % page_size
+ *     positions the position (float, as h3fp4_rope takes them)
+ * and rows past the last token hold -1 in both.  Other entries of the table
+ * stay as they were.  (cu_tokens, kv_len) are an h3fp4_kv_batch's cu_tokens
+ * and len for attention, (cu_tokens, held) for h3fp4_kv_cache_write.
+ *
+ * Reported as bit 512 of h3fp4_device_error: a sequence whose held or count is
+ * negative, whose count is more than max_tokens or whose pages are more than
+ * ld_table (it gets nothing: no tokens, kv_len 0); a free list that runs out,
+ * or a page number outside [0, num_pages) in it or in the entry of a page that
+ * the sequence has begun (the table gets -1 for it, unless it was there; the
+ * tokens' slots are -1); more tokens than the rows of slots (those are not
+ * written; cu_tokens stops at 2^31 - 1).
+ *
+ *   held, count   device [batch]
+ *   page_table    device [batch, ld_table], read and written
+ *   free_pages    device [num_free]; free_at, free_at_out: one each, not the same (a call never changes what it reads,
+ *                 but for the table's entries past the tokens held)
+ *   cu_tokens     device [batch + 1]; kv_len device [batch]; slots device int64 [tokens]; positions device [tokens];
+ *                 slots and positions may be NULL.  No output overlaps an input or another output
+ *   batch         0 .. 65535; max_tokens 0 .. 1,000,000; tokens 0 .. 2^31 - 1; page_size 16, 32, 64 or 128
+ */
+typedef struct h3fp4_kv_requests {
+    const int32_t *held, *count;
+    int32_t *page_table;
+    int64_t ld_table;
+    const int32_t *free_pages;
+    const int32_t *free_at;
+    int32_t *free_at_out;
+    int32_t *cu_tokens, *kv_len;
+    int64_t *slots;
+    float *positions;
+    int64_t tokens;             /* rows of slots and positions */
+    int32_t batch, max_tokens, num_free, num_pages, page_size;
+} h3fp4_kv_requests;
+
+H3FP4_API h3fp4_status h3fp4_kv_tables(const h3fp4_kv_requests *requests, void *stream);
 
 /*
  * h3fp4_swizzle_scales -- helper for preparing weights: copies a LOGICAL

@@ -113,20 +113,22 @@ def gather(values, table, length):
     return values[np.asarray(table)[pos // page], :, pos % page]
 
 
-def attention(q, k, v, scale, causal=False, window=0):
-    """One sequence: q [n, heads, dim], k, v [L, kv_heads, dim] float64.  Returns out, lse and, for error
-    bounds, the weighted mean of |v|, the largest |s| product sum, and the largest single contribution's share."""
+def attention(q, k, v, scale, causal=False, window=0, sinks=0, before=0):
+    """One sequence: q [n, heads, dim], k, v [L, kv_heads, dim] float64.  The first `sinks` positions stay visible under a
+    window; the first `before` keys are a prefix that every query sees, positions counting from its end.  Returns out, lse
+    and, for error bounds, the weighted mean of |v|, the largest |s| product sum, and the largest single contribution's share."""
     n, heads, dim = q.shape
     L, kv_heads = k.shape[:2]
     out, mean_abs = np.zeros((n, heads, dim)), np.zeros((n, heads, dim))
     lse = np.full((n, heads), -np.inf)
     prod, top = np.zeros((n, heads)), np.zeros((n, heads))
-    pos, j = np.arange(L - n, L)[:, None], np.arange(L)[None]
+    pos, j = np.arange(L - before - n, L - before)[:, None], np.arange(-before, L - before)[None]
     see = np.ones((n, L), dtype=bool)
     if causal:
         see &= j <= pos
     if window > 0:
-        see &= j > pos - window
+        see &= (j > pos - window) | (j < sinks)
+    see |= j < 0
     for h in range(heads):
         kk, vv = k[:, h // (heads // kv_heads)], v[:, h // (heads // kv_heads)]
         for i in range(n):
@@ -143,3 +145,48 @@ def attention(q, k, v, scale, causal=False, window=0):
                 prod[i, h] = abs(scale) * (np.abs(kk[at]) @ np.abs(q[i, h])).max()
                 top[i, h] = np.nanmax(p[:, None] * np.abs(vv[at])) / p.sum() if np.isfinite(m) else np.nan
     return out, lse, mean_abs, prod, top
+
+
+def norm_rope(x, weight, eps, turn):
+    """x [tokens, heads, dim] float64 normed over its channels, times weight, turned by `turn` (a function of rows that
+    returns them and a bound on the pairs' sizes).  Unrounded."""
+    z = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * weight
+    return turn(z)
+
+
+def norm_rope_backward(dy, x, weight, eps, turn_back):
+    """Gradients (dx, dweight), and for error bounds the sums of magnitudes that each is made of."""
+    g, mag = turn_back(dy)
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    hat = x * r
+    dx = r * (weight * g - hat * (weight * g * hat).mean(-1, keepdims=True))
+    size = r * (np.abs(weight) * mag + np.abs(hat) * (np.abs(weight) * mag * np.abs(hat)).mean(-1, keepdims=True))
+    return dx, (g * hat).sum((0, 1)), size, (mag * np.abs(hat)).sum((0, 1))
+
+
+def kv_tables(held, count, table, free, free_at, page, pages, tokens, most):
+    """The batch's tables one token after another.  Returns cu, kv_len, slots, positions, table, free_at, whether anything
+    is out of range."""
+    table, cu, kv, slots, positions, bad = table.copy(), [0], [], [], [], False
+    room, at = table.shape[1], int(free_at)
+    for b in range(len(held)):
+        h, n = int(held[b]), int(count[b])
+        if h < 0 or n < 0 or n > most or h + n >= 2 ** 31 or -(-(h + n) // page) > room:
+            h, n, bad = 0, 0, True
+        for p in range(-(-h // page), -(-(h + n) // page)):
+            ok = 0 <= at < len(free)
+            table[b, p] = free[at] if ok and 0 <= free[at] < pages else -1
+            at += 1
+            bad |= table[b, p] < 0
+        for pos in range(h, h + n):
+            page_id = int(table[b, pos // page])
+            ok = 0 <= page_id < pages
+            bad |= not ok
+            slots.append(page_id * page + pos % page if ok else -1)
+            positions.append(float(pos))
+        cu.append(min(cu[-1] + n, 2 ** 31 - 1))
+        kv.append(h + n)
+    bad |= len(slots) > tokens
+    behind = [-1] * (tokens - len(slots))
+    taken = min(at - int(free_at), max(0, len(free) - max(int(free_at), 0)))
+    return cu, kv, (slots + behind)[:tokens], (positions + behind)[:tokens], table, int(free_at) + taken, bad

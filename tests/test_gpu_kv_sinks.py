@@ -1,0 +1,152 @@
+"""Attention under a window whose first tokens stay visible, against the 64-bit
+definition.  Bounds as for the attention without them."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as O
+from test_gpu_kv_attention import _filled
+from test_gpu_kv_cache import _dev, _patterns, _tables
+
+pytestmark = pytest.mark.gpu
+
+
+def check_rows(q, k, v, out, lse, scale, L, **seen):
+    """One sequence's rows against the definition: the bounds of test_gpu_kv_attention."""
+    ref, rl, A, P, T = O.attention(q, k, v, scale, **seen)
+    e = 2.0 ** -17 * P
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + 4 * e[..., None]) * A + L * 2.0 ** -22 * T[..., None] + 1e-38
+    nan = np.isnan(ref)
+    assert np.array_equal(np.isnan(out), nan), (int(np.isnan(out).sum()), int(nan.sum()))
+    bad = ~(np.abs(out - ref) <= tol) & ~nan
+    assert not bad.any(), (int(bad.sum()), float((np.abs(out - ref) / tol)[~nan].max()))
+    empty, fine = rl == -np.inf, np.isfinite(rl)
+    assert np.array_equal(lse == -np.inf, empty) and (out[empty] == 0).all()
+    assert (np.abs(lse[fine] - rl[fine]) <= e[fine] + 2.0 ** -20 * (1 + np.abs(rl[fine]))).all()
+
+
+def _check(c, q, table, lengths, cu, out, lse, **seen):
+    kv, vv = [O.cache_values(t.cpu().numpy(), s.cpu().numpy()) for t, s in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale))]
+    qv, got, gl = O.bf16_values(_patterns(q)), O.bf16_values(_patterns(out)), lse.cpu().numpy()
+    for b, L in enumerate(lengths):
+        at = slice(int(cu[b]), int(cu[b + 1]))
+        check_rows(qv[at], O.gather(kv, table[b], L), O.gather(vv, table[b], L), got[at], gl[at], q.shape[2] ** -0.5, L, **seen)
+
+
+def _run(h3, q, c, table, lengths, cu, most, **kw):
+    return h3.kv_attention(q, c, _dev(table), _dev(lengths), _dev(cu), most, max(list(lengths) + [0]), return_lse=True, **kw)
+
+
+def _give_up(table, page, seqs, window, sinks):
+    """Entries of pages of which no query sees anything, out of range."""
+    t = table.copy()
+    for b, (n, L) in enumerate(seqs):
+        for p in range(-(-L // page)):
+            if p * page >= sinks and (p + 1) * page <= max(0, L - n - window + 1):
+                t[b, p] = 10 ** 6 if p % 2 else -5
+    return t
+
+
+CASES = [   # (new, keys) of each sequence, heads, kv_heads, dim, page, causal, window, sinks
+    ([(1, 1)], 1, 1, 128, 16, 1, 5, 3),
+    ([(1, 777)], 7, 7, 128, 16, 1, 100, 1),
+    ([(1, 777)], 7, 7, 128, 128, 1, 1, 40),
+    ([(1, 3000), (1, 40), (1, 900)], 16, 2, 128, 64, 1, 130, 70),
+    ([(1, 300), (1, 16), (1, 0)], 8, 1, 64, 16, 1, 20, 4),
+    ([(1, 300), (1, 16), (1, 33)], 8, 1, 64, 16, 0, 20, 24),
+    ([(3, 500), (0, 50), (2, 2)], 6, 2, 128, 32, 1, 33, 17),
+    ([(16, 1029)], 5, 1, 64, 32, 1, 7, 64),
+    ([(20, 2140), (33, 33)], 12, 3, 128, 64, 0, 77, 129),
+    ([(5, 3), (4, 0), (1, 4)], 4, 4, 64, 16, 1, 2, 1),       # more queries than keys
+    ([(70, 70), (129, 1400)], 4, 2, 128, 16, 1, 60, 300),
+    ([(257, 1259)], 2, 2, 64, 128, 1, 50, 5),
+    ([(130, 1513), (1, 90)], 3, 1, 128, 64, 0, 130, 128),
+    ([(300, 200)], 2, 1, 128, 64, 1, 9, 2),
+    ([(200, 650)], 3, 3, 64, 16, 1, 1, 1),
+    ([(200, 2650)], 3, 3, 128, 32, 1, 400, 900),             # sinks reach past several steps
+    ([(140, 700)], 2, 2, 128, 64, 1, 100, 100_000),          # sinks past the end: the window hides nothing
+    ([(9, 700)], 2, 2, 128, 64, 1, 100, 690),
+]
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads,dim,page,causal,window,sinks", CASES)
+def test_against_64_bits(h3, seqs, heads, kv_heads, dim, page, causal, window, sinks):
+    """Hidden tokens hold NaN, hidden pages are none."""
+    rng = np.random.default_rng(len(seqs) * 100 + heads)
+    new, lengths = [a for a, _ in seqs], [b for _, b in seqs]
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, kv_heads, page, dim)
+    for b, (n, L) in enumerate(seqs):
+        for pos in range(min(sinks, L), max(0, L - n - window + 1)):
+            for codes in (c.k_codes, c.v_codes):
+                codes[int(table[b, pos // page]), :, pos % page] = 0x7F
+    cu = np.cumsum([0] + new)
+    wide = torch.randn(cu[-1], heads + 2, dim, generator=torch.Generator().manual_seed(heads)).mul(2).bfloat16().cuda()
+    q = wide[:, 1:1 + heads]
+    out, lse = _run(h3, q, c, _give_up(table, page, seqs, window, sinks), lengths, cu, max(new), causal=bool(causal), window=window,
+                    sinks=sinks)
+    assert h3.h3fp4_device_error() == 0
+    _check(c, q, table, lengths, cu, out, lse, causal=bool(causal), window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("new,length,window,sinks", [(1, 40_011, 9_000, 100), (1, 20_000, 50, 8_000), (9, 9_000, 3_000, 5),
+                                                     (150, 9_003, 2_000, 700), (700, 5_000, 100, 1_000)])
+def test_long_caches(h3, new, length, window, sinks):
+    rng = np.random.default_rng(new)
+    table, pages = _tables(rng, [length], 64)
+    c = _filled(h3, rng, table, [length], pages, 2, 64, 128, spread=5)
+    q = torch.randn(new, 4, 128, generator=torch.Generator().manual_seed(new)).mul(3).bfloat16().cuda()
+    for causal in (False, True):
+        out, lse = _run(h3, q, c, table, [length], [0, new], new, causal=causal, window=window, sinks=sinks)
+        _check(c, q, table, [length], [0, new], out, lse, causal=causal, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("new", [1, 7, 200])
+def test_nan_reaches_only_those_that_see_it(h3, new):
+    rng = np.random.default_rng(4)
+    L, page, window, sinks = 700, 16, 150, 40
+    table, pages = _tables(rng, [L], page)
+    c = _filled(h3, rng, table, [L], pages, 2, page, 128)
+    for pos, head, kv, chan in ((L - 1, 0, 1, 5), (3, 0, 1, 77), (39, 1, 1, 9), (40, 1, 1, 10), (L - 160, 0, 1, 6), (L - 200, 0, 0, 127)):
+        codes = c.k_codes if kv == 0 else c.v_codes
+        codes[int(table[0, pos // page]), head, pos % page, chan] = 0x7F
+    q = torch.randn(new, 4, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    out, lse = _run(h3, q, c, table, [L], [0, new], new, causal=True, window=window, sinks=sinks)
+    _check(c, q, table, [L], [0, new], out, lse, causal=True, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("new", [1, 5, 140])
+def test_values_scales_far_apart(h3, new):
+    """Sinks whose values' scale is 2^100 times the window's, and the other way round."""
+    rng = np.random.default_rng(6)
+    L, page = 900, 32
+    table, pages = _tables(rng, [L], page)
+    q = torch.randn(new, 2, 128, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    for first, rest in ((60, -40), (-40, 60)):
+        c = _filled(h3, rng, table, [L], pages, 1, page, 128)
+        c.v_scale.fill_(2.0 ** rest)
+        c.v_scale[int(table[0, 0])] = 2.0 ** first
+        kw = dict(causal=True, window=200, sinks=20)
+        out, lse = _run(h3, q, c, table, [L], [0, new], new, **kw)
+        _check(c, q, table, [L], [0, new], out, lse, **kw)
+
+
+@pytest.mark.parametrize("new", [1, 6, 140])
+def test_without_a_window_or_sinks_it_is_the_attention_without(h3, new):
+    rng = np.random.default_rng(9)
+    L, page = 1_000, 64
+    table, pages = _tables(rng, [L], page)
+    c = _filled(h3, rng, table, [L], pages, 2, page, 128)
+    q = torch.randn(new, 8, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    plain = _run(h3, q, c, table, [L], [0, new], new, causal=True)
+    assert all(torch.equal(a, b) for a, b in zip(plain, _run(h3, q, c, table, [L], [0, new], new, causal=True, sinks=9)))
+    under = _run(h3, q, c, table, [L], [0, new], new, causal=True, window=77)
+    wide = torch.full((new, 10, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    need = h3.h3fp4_kv_attention_workspace(new, 8, 2, 128, 1, new, L)
+    ws = torch.empty(max(16, need), dtype=torch.uint8, device="cuda")
+    lse = torch.empty(new, 8, device="cuda")
+    h3.h3fp4_kv_attention_sinks(q.data_ptr(), 1024, 128, wide[:, 1:].data_ptr(), 1280, 128, lse.data_ptr(), new, 8, c.struct(),
+                                h3._kv_batch(t := _dev(table), n := _dev([L]), cu := _dev([0, new]), new, 0), L, 128 ** -0.5, 1, 77, 0,
+                                ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(wide[:, 1:9], under[0]) and torch.equal(lse, under[1])
+    assert (wide[:, 0] == 7).all() and (wide[:, 9] == 7).all()
