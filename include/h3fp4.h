@@ -315,8 +315,8 @@ H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_strid
  * For every token and head, with w the side's weight:
  *     r = 1 / sqrt(mean(x^2) + eps),  z = x r w,  out = RN_bf16(z turned as by h3fp4_rope_axes)
  * in FP32 before the one rounding.  Rows of any finite size are in range; a row
- * with an infinity gives 0 for its finite channels (NaN for the others), one
- * with a NaN gives NaN.
+ * with an infinity gives 0, and NaN in the infinity's pair; one with a NaN
+ * gives NaN.
  *
  *   q, k       the two sides; either may be NULL (or have no heads).  x and out are [tokens, heads, head_dim]
  *              bf16, strides as for h3fp4_rope_axes.  out either is its own x (same pointer and strides: in place)

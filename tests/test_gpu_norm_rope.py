@@ -86,6 +86,17 @@ CASES = [   # tokens, query heads, key heads, dim, rotated channels, layout, wei
     (1_003, 3, 1, 96, (96,), "interleaved", 1, 1),
     (50, 6, 2, 128, None, "interleaved", 0, 0),              # no rotation
     (2_001, 2, 1, 128, (44, 42, 42), "halves", 0, 0),
+    (33, 6, 3, 256, (256,), "halves", 1, 0),
+    (33, 6, 3, 80, (80,), "halves", 0, 0),                   # halves that face each other across lanes that idle
+    (33, 6, 3, 72, (72,), "halves", 0, 0),                   # an odd number of chunks
+    (70, 9, 2, 64, (64,), "halves", 0, 0),
+    (65, 3, 2, 16, (16,), "halves", 0, 0),
+    (1_999, 7, 3, 256, (120, 100), "interleaved", 1, 0),
+    (301, 11, 5, 40, (16, 8, 8, 8), "halves", 1, 0),
+    (33, 6, 3, 128, (32, 48, 48), "halves", 0, 0),           # sections of whole chunks
+    (33, 6, 3, 72, (32, 16), "halves", 1, 0),                # and channels that do not turn, an odd number of chunks
+    (33, 6, 3, 256, (64, 0, 96, 16), "halves", 0, 0),
+    (5, 3, 1, 8, (8,), "halves", 0, 0),
 ]
 
 
@@ -174,6 +185,23 @@ def test_rows_of_any_size(h3):
     keep = torch.ones(3, 8, dtype=torch.bool, device="cuda")
     keep[1, 0] = keep[1, 7] = False
     assert torch.equal(y[keep].view(torch.int16), clean[keep].view(torch.int16))
+
+
+@pytest.mark.parametrize("layout,dims,still,turned,pair", [("interleaved", (10, 16), 27, 5, 4), ("halves", (10, 16), 27, 5, 0),
+                                                           ("halves", (16, 16), 45, 21, 29)])
+def test_an_infinity_stays_in_its_pair_beside_channels_that_do_not_turn(h3, layout, dims, still, turned, pair):
+    x = _normal((2, 2, 64), 7)
+    x[0, 0, still], x[1, 1, turned] = float("inf"), float("-inf")
+    rope = _rope(h3, 2, dims, layout, 2)
+    y = h3.norm_rope(x, rope=rope)[0]
+    assert y[0, 0, still].isnan() and y[1, 1, turned].isnan() and y[1, 1, pair].isnan()
+    assert int(y[0, 0].isnan().sum()) == 1 and int(y[1, 1].isnan().sum()) == 2
+    assert (y[0, 0][~y[0, 0].isnan()] == 0).all() and y[0, 1].isfinite().all()
+    g = _normal(x.shape, 8)
+    g[0, 1, 47] = float("inf")
+    one = torch.ones(64, device="cuda")
+    _, _, dw, _ = h3.norm_rope_backward(g, None, _normal(x.shape, 9), q_weight=one, rope=rope)
+    assert not dw[47].isfinite() and int((~dw.isfinite()).sum()) == 1
 
 
 @pytest.mark.parametrize("layout", ["interleaved", "halves"])
