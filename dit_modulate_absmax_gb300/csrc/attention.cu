@@ -15,10 +15,10 @@ constexpr int64_t kMostRows = 32;
 
 bool few_rows(const AttnShape &s) { return static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads) <= kMostRows; }
 
-AttnShape shape_of(const AttnArgs &a)
+AttnShape shape_of(const AttnArgs &a, Form form = kWhole)
 {
     return AttnShape{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv,
-                     a.causal || a.sinks > 0 ? a.window : 0, a.sinks, a.causal};
+                     a.causal || a.sinks > 0 ? a.window : 0, a.sinks, a.causal, form};
 }
 
 SplitPlan plan_of(const AttnShape &s) { return few_rows(s) ? plan_rows(s) : plan_tile(s); }
@@ -33,7 +33,7 @@ int64_t attention_workspace(const AttnShape &s)
 
 static cudaError_t launch_form(const AttnArgs &a, Form form, void *workspace, cudaStream_t st)
 {
-    const AttnShape s = shape_of(a);   // (the parts are no more than without the reach: the workspace does for both)
+    const AttnShape s = shape_of(a, form);   // (the parts are no more than without the reach: the workspace does for both)
     const SplitPlan plan = plan_of(s);
     float *part = static_cast<float *>(workspace);
     float *stat = part + plan.part_rows * s.head_dim;

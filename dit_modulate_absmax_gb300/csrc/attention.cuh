@@ -99,7 +99,8 @@ __device__ __forceinline__ bool all_seen(const AttnArgs &a, int lo, int hi, int 
 
 // The keys that some rows see, [lo, hi) and the sinks, as one run of places: place v below `keep` is position v, one from
 // there on position v + gap.  Both are multiples of `align` (a page and a kernel's step at least), so that neither a page nor
-// a step lies on both sides.  Sinks that reach to lo's step leave no gap.
+// a step lies on both sides.  Sinks that reach to lo's step leave no gap.  Where there is one, lo lies past keep for all rows,
+// so that a row sees place v if that is a sink or in [lo - gap, hi - gap): seen() holds of places too, with that span.
 struct Fold {
     int keep, gap;
 };

@@ -27,6 +27,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstring>
 #include <mutex>
 
@@ -199,22 +200,22 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
     int64_t next = x_end;
     KvSequence s;
     Fold places;
-    if (plan.cluster) {   // one unit a CTA, a cluster for the rows of a sequence and cache head
+    if (plan.cluster) {   // plan.chunk units a CTA, a cluster for a row tile of a sequence and cache head
         b = blockIdx.y;
-        tile = 0;
-        kh = blockIdx.x / plan.splits;
+        kh = blockIdx.x / plan.splits % heads;
+        tile = blockIdx.x / plan.splits / heads;
         s = kv_sequence(a.batch, b, a.tokens);
         const Units u = units_of<kRows, kForm>(a, s);
-        if (u.count == 0) {   // the same in the whole cluster
-            if (s.n != 0 && threadIdx.x == 0)
+        if (u.count == 0 || tile >= u.tiles) {   // the same in the whole cluster
+            if (u.count == 0 && s.n != 0 && threadIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
             after_prefix<kForm>();
             return;
         }
         __syncthreads();      // barriers initialised
         places = u.fold;
-        seg_begin = u.begin + blockIdx.x % plan.splits * kTokens;
-        seg_end = seg_begin + kTokens;
+        seg_begin = u.begin + blockIdx.x % plan.splits * plan.chunk * kTokens;
+        seg_end = seg_begin + plan.chunk * kTokens;
     } else {
         if (mine_lo <= x && x < mine_hi) {   // one thread: in its share, which sequence
             int64_t rest = x - mine_lo;
@@ -763,7 +764,16 @@ SplitPlan plan_rows(const AttnShape &s)
                                                         : (tile == 8 ? resident<64, 8>() : resident<64, 16>()));
     const int64_t per_row = (folded_keys(s, s.max_tokens) + kWarps * kUnit - 1) / (kWarps * kUnit);
     if (per_row <= 8 && rows <= 16 && per_row * s.batch * s.kv_heads <= fit)
-        return SplitPlan{static_cast<int32_t>(per_row), 0, 0, true};
+        return SplitPlan{static_cast<int32_t>(per_row), 1, 0, true};
+    if (s.form != kWhole) {
+        const int64_t items = s.batch * s.kv_heads * ((rows + tile - 1) / tile);
+        int64_t ctas = 1;
+        while (ctas < 8 && 2 * ctas <= per_row && 2 * ctas * items <= fit)
+            ctas *= 2;
+        const int64_t chunk = (per_row + ctas - 1) / ctas, even = items * per_row / fit;
+        if (items >= 2 * fit || std::max(chunk, even + chunk / 2) <= even + (tile == 8 ? 10 : 4))
+            return SplitPlan{static_cast<int32_t>(ctas), static_cast<int32_t>(chunk), 0, true};
+    }
     return SplitPlan{static_cast<int32_t>(fit), 0, fit * 2 * tile, false};
 }
 
@@ -812,12 +822,12 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
         return cudaErrorInvalidValue;
     }
     const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
-    const int64_t joins = (rows + kRows - 1) / kRows * a.cache.heads, x = static_cast<int64_t>(plan.splits) * a.cache.heads;
-    if (x > INT32_MAX || joins > INT32_MAX)
+    const int64_t joins = (rows + kRows - 1) / kRows * a.cache.heads;
+    if (plan.splits * joins > INT32_MAX)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = plan.cluster ? dim3(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch))
+    cfg.gridDim = plan.cluster ? dim3(static_cast<unsigned>(plan.splits * joins), static_cast<unsigned>(a.batch.batch))
                                : dim3(static_cast<unsigned>(plan.splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;

@@ -50,8 +50,9 @@ constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 4);  // whole warpgroups, for the register split; two warps idle
 // Registers per thread of the three kinds of warpgroup, out of the 128 that 512 threads launch with (run_tile checks):
-// a softmax thread holds its row's 128 scores.
-constexpr int kSoftmaxRegs = 184, kConvertRegs = 112, kMmaRegs = 32;
+// a softmax thread holds its row's 128 scores.  (184, 112 and 32 left the conversion with sinks short: 5.21 ms where all is
+// seen, 5.09 now; without sinks 5.12 and 5.10.  176, 128 and 32: 5.00 with sinks, 5.59 without.)
+constexpr int kSoftmaxRegs = 184, kConvertRegs = 120, kMmaRegs = 24;
 constexpr int kSplitRegs = 2 * kSoftmaxRegs + kConvertRegs + kMmaRegs;
 static_assert(kSplitRegs <= 4 * 128 && kConvertRegs <= 128 && kMmaRegs <= 128, "the launch's registers cover the split");
 constexpr int kStages = 2;
@@ -143,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem<kDim> &sm = *reinterpret_cast<Smem<kDim> *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int page = a.cache.page_size, group = a.heads / a.cache.heads;
-    let_next_start<kForm>();
+    if (kForm != kWhole)   // what follows waits for this grid's end itself: the join, or the half over the sequences' own keys
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int tile, rest;   // the order of the grid, see by_length()
     if (longest_first) {
         const int others = a.cache.heads * plan.splits * a.batch.batch;
@@ -173,13 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int row_end = min(rows, row0 + kTiles * 128);
     const Span first = seen_by(a, s, row0 / group), last = seen_by(a, s, (row_end - 1) / group);
-    const int in_lo = max(first.lo, last.lo), in_hi = min(first.hi, last.hi);     // seen by every row
-    const int out_lo = min(first.lo, last.lo);                                    // seen by any
-    // Places (of positions, folded where sinks and window lie apart) of this CTA's keys.
-    const int out_hi = max(first.hi, last.hi);
-    const Fold places = fold<kForm>(a, out_lo, out_hi, kKeys);
+    // With sinks everything below is in places (see Fold): what a row sees, less the gap, and the sinks, which end before it.
+    const Fold places = fold<kForm>(a, min(first.lo, last.lo), max(first.hi, last.hi), kKeys);
+    const int in_lo = max(first.lo, last.lo) - places.gap, in_hi = min(first.hi, last.hi) - places.gap;   // seen by every row
+    const int out_lo = min(first.lo, last.lo) - places.gap, out_hi = max(first.hi, last.hi) - places.gap; // seen by any
     const int begin = kForm == kSinks ? split * plan.chunk : max(split * plan.chunk, out_lo & ~(kKeys - 1));
-    const int end = kForm == kSinks ? min((split + 1) * plan.chunk, out_hi - places.gap) : min(min((split + 1) * plan.chunk, s.len), out_hi);
+    const int end = min(min((split + 1) * plan.chunk, s.len), out_hi);
     const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
     const int tiles = row_end - row0 > 128 ? 2 : 1;
 
@@ -232,10 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = r < rows;
         if (t < tiles) {
             const int tok = live ? r / group : 0, head = kh * group + (live ? r % group : 0);
-            const Span see = live ? seen_by(a, s, tok) : Span{0, 0};
+            Span see = live ? seen_by(a, s, tok) : Span{0, 0};
+            if (kForm == kSinks)
+                see = Span{see.lo - places.gap, see.hi - places.gap};
             // what the tile's rows all see
             const Span tf = seen_by(a, s, (row0 + 128 * t) / group), tl = seen_by(a, s, (min(rows, row0 + 128 * t + 128) - 1) / group);
-            const int t_lo = max(tf.lo, tl.lo), t_hi = min(tf.hi, tl.hi);
+            const int t_lo = max(tf.lo, tl.lo) - places.gap, t_hi = min(tf.hi, tl.hi) - places.gap;
             float c_row;
             {
                 const uint16_t *src = a.q + (s.row + tok) * a.qt + head * a.qh;
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // inside of one loop 5,420 and 104).
             const auto step = [&](auto far_scales, int j) -> bool {
                 constexpr bool kFar = decltype(far_scales)::value;
-                const int k0 = position<kForm>(places, begin + j * kKeys);
+                const int k0 = begin + j * kKeys;
                 const bool edge = !all_seen<kForm>(a, t_lo, t_hi, k0, kKeys);
                 if (!wait_for(sm.entry_full[j % kEntrySlots], (j / kEntrySlots) & 1) || (!kFar && j >= sm.far_from) ||
                     !wait_for(sm.s_full[t], j & 1))
@@ -558,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // only when its codes are loaded.
         const int shift = 31 - __clz(page);
         const auto page_ids = [&](int j) -> int32_t {
-            const int64_t v = begin + static_cast<int64_t>(j) * kKeys + lane * page;
-            const int64_t tok = kForm == kSinks && v >= places.keep ? v + places.gap : v;
-            return lane < kKeys / page && v < end && (tok + page > out_lo || (kForm == kSinks && tok < a.sinks))
-                       ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift)] : -2;
+            const int64_t tok = begin + static_cast<int64_t>(j) * kKeys + lane * page;
+            const int gap = kForm == kSinks && tok >= places.keep ? places.gap >> shift : 0;
+            return lane < kKeys / page && tok < end && (tok + page > out_lo || (kForm == kSinks && tok < a.sinks))
+                       ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift) + gap] : -2;
         };
         const auto checked = [&](int32_t id) -> int32_t {        // -2: no page; out of range: reported, page 0 instead
             if (id == -2 || (id >= 0 && id < a.cache.num_pages))
@@ -573,15 +576,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto ids = [&](int32_t of_lane) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                id[i] = __shfl_sync(0xFFFFFFFFu, of_lane, (r0 + i * kRowStep) >> shift);
+                id[i] = __shfl_sync(0xFFFFFFFFu, kForm == kSinks ? max(of_lane, 0) : of_lane, (r0 + i * kRowStep) >> shift);
         };
         // A piece's group of kRowStep tokens lies in one page (dim 128: 16 tokens) or in two (dim 64: 32).
         const int64_t page_bytes = static_cast<int64_t>(a.cache.heads) * page * kDim;
         const int64_t mine = static_cast<int64_t>(kh) * page * kDim + 16 * c;
-        const auto load = [&](const uint8_t *codes, int v0, uint4 (&w)[kPer]) {   // v0: the first key's place
+        const auto load = [&](const uint8_t *codes, int k0, uint4 (&w)[kPer]) {
             const uint8_t *base = codes + mine;
-            const int k0 = position<kForm>(places, v0);
-            if ((k0 >= out_lo || (kForm == kSinks && k0 + kKeys <= a.sinks)) && v0 + kKeys <= end) {
+            if constexpr (kForm == kSinks) {
+                // Whole steps, whoever sees them, and page 0 in place of pages that nobody sees (or past the end): such a step
+                // is at an edge for every row, where scores are masked and NaN is kept out of the values.  (A test here of
+                // which of the step's keys are seen cost every step: 5.42 ms for a call that takes 5.09 with it gone and 5.10
+                // without sinks.)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + ((r0 + i * kRowStep) & (page - 1)) * kDim);
+            } else if (k0 >= out_lo && k0 + kKeys <= end) {
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
                     w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + ((r0 + i * kRowStep) & (page - 1)) * kDim);
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kPer; ++i) {
                     const int tok = k0 + r0 + i * kRowStep;
                     w[i] = make_uint4(0, 0, 0, 0);
-                    if ((tok >= out_lo || (kForm == kSinks && tok < a.sinks)) && v0 + r0 + i * kRowStep < end)
+                    if (tok >= out_lo && tok < end)
                         w[i] = *reinterpret_cast<const uint4 *>(base + id[i] * page_bytes + (tok & (page - 1)) * kDim);
                 }
             }
@@ -616,11 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         scales();
         ids(lane_id);
-        load(a.cache.k_codes, begin, kw);
-        load(a.cache.v_codes, begin, vw);
+        if (kForm != kSinks || steps > 0) {   // (without keys there may be no pages)
+            load(a.cache.k_codes, begin, kw);
+            load(a.cache.v_codes, begin, vw);
+        }
         for (int j = 0; j < steps; ++j) {
-            const int v0 = begin + j * kKeys, st = j % kStages;
-            const bool edge = !all_seen<kForm>(a, in_lo, in_hi, position<kForm>(places, v0), kKeys);
+            const int k0 = begin + j * kKeys, st = j % kStages;
+            const bool edge = !all_seen<kForm>(a, in_lo, in_hi, k0, kKeys);
             if (!wait_for(sm.k_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
             if (warp == kSoftmaxWarps) {   // the step's page entries, 8 at most
@@ -640,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             next_id = page_ids(j + 2);
             scales();
             ids(lane_id);
-            load(a.cache.k_codes, v0 + kKeys, kw);   // zeros past the end
+            load(a.cache.k_codes, k0 + kKeys, kw);   // zeros past the end
 
             if (!wait_for(sm.v_empty[st], ((j / kStages) & 1) ^ 1))
                 break;
@@ -671,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store(smem_u32(sm.v[st]), vw[i], i);
             fence_proxy_async_smem();
             warp_arrive(sm.v_full[st]);
-            load(a.cache.v_codes, v0 + kKeys, vw);
+            load(a.cache.v_codes, k0 + kKeys, vw);
         }
     } else {
         // ------------------------------------------------------------------ MMA issue
@@ -748,6 +760,8 @@ template <int kDim, int kForm>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPlan plan, const float2 *ws_stat, const float *ws_out)
 {
     let_next_start<kForm>();
+    if (kForm != kWhole)   // launched to overlap with the kernel before
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
@@ -897,12 +911,17 @@ static cudaError_t run_tile_form(const AttnArgs &a, const SplitPlan &plan, float
     const int64_t x = (std::min<int64_t>(a.batch.max_tokens, a.tokens) * a.heads + kJoinWarps - 1) / kJoinWarps;
     if (x > INT32_MAX)
         return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch));
-    if (a.cache.head_dim == 64)
-        join_kernel<64, kForm><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
-    else
-        join_kernel<128, kForm><<<grid, kJoinThreads, 0, st>>>(a, plan, stat, part);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr = overlap_with_last();
+    cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(a.batch.batch));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = kForm != kWhole ? 1 : 0;
+    const float2 *const stats = stat;
+    const float *const parts = part;
+    return a.cache.head_dim == 64 ? cudaLaunchKernelEx(&cfg, join_kernel<64, kForm>, a, plan, stats, parts)
+                                  : cudaLaunchKernelEx(&cfg, join_kernel<128, kForm>, a, plan, stats, parts);
 }
 
 cudaError_t launch_attention_tile(const AttnArgs &a, Form form, const SplitPlan &plan, float2 *stat, float *part, cudaStream_t st)

@@ -142,6 +142,7 @@ struct AttnShape {
     int32_t reach = 0;   // most keys that a query sees under a causal window; 0: all
     int32_t sinks = 0;   // with those first ones (the reach is then that of any window)
     int32_t causal = 0;
+    int32_t form = 0;    // of the kernel, see attention.cuh
 };
 
 int64_t attention_workspace(const AttnShape &s);

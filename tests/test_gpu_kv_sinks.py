@@ -150,3 +150,16 @@ def test_without_a_window_or_sinks_it_is_the_attention_without(h3, new):
                                 ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(wide[:, 1:9], under[0]) and torch.equal(lse, under[1])
     assert (wide[:, 0] == 7).all() and (wide[:, 9] == 7).all()
+
+
+@pytest.mark.parametrize("new", [1, 140])
+@pytest.mark.parametrize("pages", [0, 3])
+def test_sequences_without_keys(h3, new, pages):
+    """No keys, of a cache with and without pages: zeros and minus infinity, nothing reported."""
+    c = h3.KVCache.empty(pages, 32, 2, 128)
+    q = torch.ones(new, 4, 128, dtype=torch.bfloat16, device="cuda")
+    for most in (0, 90):
+        out, lse = h3.kv_attention(q, c, torch.empty(1, 0, dtype=torch.int32, device="cuda"), _dev([0]), _dev([0, new]), new, most,
+                                   causal=True, window=4, sinks=2, return_lse=True)
+        assert (out == 0).all() and (lse == -np.inf).all()
+    assert h3.h3fp4_device_error() == 0
