@@ -124,6 +124,26 @@ __device__ __forceinline__ void warp_arrive(const uint64_t &bar)
         mbar_arrive(smem_u32(&bar));
 }
 
+// Every by-th row of a sequence and cache head: its token and the query head among the cache head's, with one division.
+struct RowWalk {
+    int row, token, head, by, by_tokens, by_heads, group;
+
+    __device__ __forceinline__ RowWalk(int first, int by, int group)
+        : row(first), token(first / group), head(first % group), by(by), by_tokens(by / group), by_heads(by % group), group(group)
+    {
+    }
+    __device__ __forceinline__ void step()
+    {
+        row += by;
+        token += by_tokens;
+        head += by_heads;
+        if (head >= group) {
+            head -= group;
+            ++token;
+        }
+    }
+};
+
 template <int kRegs>
 __device__ __forceinline__ void grow_registers()
 {
@@ -184,6 +204,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int steps = end > begin ? (end - begin + kKeys - 1) / kKeys : 0;
     const int tiles = row_end - row0 > 128 ? 2 : 1;
 
+    constexpr int kRowLanes = kDim / 8, kRowsAtOnce = 32 / kRowLanes;
+    const int shift = 31 - __clz(page);
+    const auto page_ids = [&](int j) -> int32_t {
+        const int64_t tok = begin + static_cast<int64_t>(j) * kKeys + lane * page;
+        const int gap = kForm == kSinks && tok >= places.keep ? places.gap >> shift : 0;
+        return lane < kKeys / page && tok < end && (tok + page > out_lo || (kForm == kSinks && tok < a.sinks))
+                   ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift) + gap] : -2;
+    };
+
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTiles; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 4);
@@ -239,29 +268,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             // what the tile's rows all see
             const Span tf = seen_by(a, s, (row0 + 128 * t) / group), tl = seen_by(a, s, (min(rows, row0 + 128 * t + 128) - 1) / group);
             const int t_lo = max(tf.lo, tl.lo) - places.gap, t_hi = min(tf.hi, tl.hi) - places.gap;
+            // The warp's 32 rows, kDim / 8 lanes a row: whole rows are read at a time.
+            uint4 query[kRowLanes];
+            RowWalk at(row0 + 32 * warp + lane / kRowLanes, kRowsAtOnce, group);
+            const uint16_t *first_head = a.q + s.row * a.qt + kh * group * a.qh + 8 * (lane % kRowLanes);
+#pragma unroll
+            for (int y = 0; y < kRowLanes; ++y) {
+                query[y] = at.row < rows ? *reinterpret_cast<const uint4 *>(first_head + at.token * a.qt + at.head * a.qh) : make_uint4(0, 0, 0, 0);
+                at.step();
+            }
+            // Each row's largest channel: the lanes of a row give away half of their rows' maxima at each exchange, until lane
+            // y of them holds that of row y.
             float c_row;
             {
-                const uint16_t *src = a.q + (s.row + tok) * a.qt + head * a.qh;
-                uint4 w[kDim / 8];
-                uint32_t m2 = 0;
+                uint32_t top[kRowLanes];
 #pragma unroll
-                for (int i = 0; i < kDim / 8; ++i) {
-                    w[i] = live ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-                    m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m2, w[i].x), w[i].y), w[i].z), w[i].w);
+                for (int y = 0; y < kRowLanes; ++y) {
+                    const uint32_t m2 =
+                        bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(0, query[y].x), query[y].y), query[y].z), query[y].w);
+                    top[y] = max(m2 & 0xFFFFu, m2 >> 16);
                 }
-                const float2 p = row_power(max(m2 & 0xFFFFu, m2 >> 16));
-                const float f = a.scale < 0.0f ? -p.x : p.x;
-                c_row = fabsf(a.scale) * kLog2e * p.y;
 #pragma unroll
-                for (int i = 0; i < kDim / 8; ++i)
-                    st_shared_v4(smem_u32(sm.q[t]) + operand_at(in_tile, i), bf16x2_to_half2(w[i].x, f), bf16x2_to_half2(w[i].y, f),
-                                 bf16x2_to_half2(w[i].z, f), bf16x2_to_half2(w[i].w, f));
+                for (int x = kRowLanes / 2; x > 0; x >>= 1) {
+                    const bool upper = (lane & x) != 0;
+#pragma unroll
+                    for (int y = 0; y < x; ++y)
+                        top[y] = max(upper ? top[y + x] : top[y], __shfl_xor_sync(0xFFFFFFFFu, upper ? top[y] : top[y + x], x));
+                }
+                const float2 p = row_power(top[0]);
+                c_row = fabsf(a.scale) * kLog2e * __shfl_sync(0xFFFFFFFFu, p.y, lane % kRowsAtOnce * kRowLanes + lane / kRowsAtOnce);
+                const float mine = a.scale < 0.0f ? -p.x : p.x;
+#pragma unroll
+                for (int y = 0; y < kRowLanes; ++y) {
+                    const float f = __shfl_sync(0xFFFFFFFFu, mine, (lane & -kRowLanes) + y);
+                    st_shared_v4(smem_u32(sm.q[t]) + operand_at((warp & 3) * 32 + y * kRowsAtOnce + lane / kRowLanes, lane % kRowLanes),
+                                 bf16x2_to_half2(query[y].x, f), bf16x2_to_half2(query[y].y, f), bf16x2_to_half2(query[y].z, f),
+                                 bf16x2_to_half2(query[y].w, f));
+                }
                 fence_proxy_async_smem();
                 warp_arrive(sm.q_full[t]);
             }
             float ref = -INFINITY, l = 0.0f;
             bool met_nan = false;
-            const int shift = 31 - __clz(page);
             const uint32_t sc = 128u * t + lanes, oc = 256u + static_cast<uint32_t>(kDim) * t + lanes;
             float apart_ref = -INFINITY, apart_l = 0.0f;   // with far scales: a sum against a reference of its own
             // One step; false: a wait gave up, or (kFar false) the first step with a far scale has come.  Those that follow are a
@@ -478,8 +526,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = s.row + tok, at = row * a.heads + head;
                 const bool final = plan.splits == 1;
                 const float inv = reciprocal_sum(l) * o_factor;
-                uint16_t *out = a.out + row * a.ot + head * a.oh;
-                float *part = kForm == kPrefix && final ? a.half_mean + at * kDim : ws_out + (at * plan.splits + split) * kDim;
                 Shares share{};
                 bool other_half = false;
                 if (kForm == kOwn && final) {
@@ -487,6 +533,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float other = live ? prefix_log(a, row, head) : -INFINITY;
                     other_half = other != -INFINITY;   // (else its mean may be anything)
                     share = shares_of(log_of_sum(ref, l), other);
+                }
+                // Rows are written through shared memory in whole sectors, or, where that gains nothing, straight from the
+                // threads that hold them (128 channels: 1,560 tokens over as many keys 5,700 cycles a CTA, 7,000 straight; 64
+                // channels, ragged prompts: 99.2 us, 97.5 straight; with sinks, a chunk: 3,105 us, 3,055).
+                constexpr bool kStaged = kDim == 128 && kForm != kSinks;
+                const bool narrow = final && kForm != kPrefix;   // bf16 to the output, else FP32 for a join
+                const int pieces = narrow ? 4 : 8;
+                const auto place_of = [&](int64_t to_row, int64_t to_head) -> uint8_t * {
+                    const int64_t to = to_row * a.heads + to_head;
+                    return narrow ? reinterpret_cast<uint8_t *>(a.out + to_row * a.ot + to_head * a.oh)
+                                  : reinterpret_cast<uint8_t *>(kForm == kPrefix && final ? a.half_mean + to * kDim
+                                                                                          : ws_out + (to * plan.splits + split) * kDim);
+                };
+                uint8_t *to[8];
+                if constexpr (kStaged) {   // of this lane's pieces
+                    RowWalk at_row(row0 + 32 * warp + lane / pieces, 32 / pieces, group);
+                    const int last_row = min(rows, row0 + 32 * warp + 32);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        to[i] = at_row.row < last_row ? place_of(s.row + at_row.token, kh * group + at_row.head) + 16 * (lane & (pieces - 1))
+                                                      : nullptr;
+                        at_row.step();
+                    }
+                } else {
+                    to[0] = live ? place_of(row, head) : nullptr;
                 }
 #pragma unroll 1
                 for (int c = 0; c < kDim / 32; ++c) {
@@ -520,21 +591,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[i + 3] = join_share(o[i + 3], p.w, share);
                         }
                     }
-                    if (live && final && kForm != kPrefix) {
+                    const auto bf16_piece = [&](int i) {   // 8 channels
+                        uint32_t x[4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const __nv_bfloat162 y = __floats2bfloat162_rn(o[i + 2 * x], o[i + 2 * x + 1]);
-                                w[x] = *reinterpret_cast<const uint32_t *>(&y);
-                            }
-                            *reinterpret_cast<uint4 *>(out + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int y = 0; y < 4; ++y) {
+                            const __nv_bfloat162 z = __floats2bfloat162_rn(o[8 * i + 2 * y], o[8 * i + 2 * y + 1]);
+                            x[y] = *reinterpret_cast<const uint32_t *>(&z);
                         }
+                        return make_uint4(x[0], x[1], x[2], x[3]);
+                    };
+                    const auto float_piece = [&](int i) {   // 4 channels
+                        return make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                                          __float_as_uint(o[4 * i + 3]));
+                    };
+                    if constexpr (kStaged) {
+                        // The queries' place is free (all that read them is done): 4 KB a warp, pieces moved by the row's number.
+                        const uint32_t stage = smem_u32(sm.q[t]) + (warp & 3) * 4096;
+                        const auto at_piece = [&](int in, int x) { return stage + in * 128 + ((x ^ (in & 7)) << 4); };
+                        const auto put = [&](int x, const uint4 &p) { st_shared_v4(at_piece(lane, x), p.x, p.y, p.z, p.w); };
+                        __syncwarp();
+                        if (narrow) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                put(i, bf16_piece(i));
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                put(i, float_piece(i));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (to[i] != nullptr)
+                                *reinterpret_cast<uint4 *>(to[i] + c * (16 * pieces)) =
+                                    ld_shared_v4(at_piece(lane / pieces + i * (32 / pieces), lane & (pieces - 1)));
+                    } else if (live && narrow) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4 *>(to[0] + 64 * c + 16 * i) = bf16_piece(i);
                     } else if (live) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(part + 32 * c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(to[0] + 128 * c + 16 * i) = float_piece(i);
                     }
                 }
                 if (live && !final)
@@ -557,15 +655,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int w0 = warp - kSoftmaxWarps;
         const int r0 = kDim == 128 ? 4 * w0 + ((lane >> 2) & 1) + ((lane >> 4) << 1) : 8 * w0 + (lane >> 2);
         const int c = kDim == 128 ? (lane & 3) | ((lane >> 3) & 1) << 2 : lane & 3;
-        // Lane p of each warp holds the number of page p of a step (8 at most), loaded two steps ahead and looked at
-        // only when its codes are loaded.
-        const int shift = 31 - __clz(page);
-        const auto page_ids = [&](int j) -> int32_t {
-            const int64_t tok = begin + static_cast<int64_t>(j) * kKeys + lane * page;
-            const int gap = kForm == kSinks && tok >= places.keep ? places.gap >> shift : 0;
-            return lane < kKeys / page && tok < end && (tok + page > out_lo || (kForm == kSinks && tok < a.sinks))
-                       ? a.batch.page_table[b * a.batch.ld_table + (tok >> shift) + gap] : -2;
-        };
         const auto checked = [&](int32_t id) -> int32_t {        // -2: no page; out of range: reported, page 0 instead
             if (id == -2 || (id >= 0 && id < a.cache.num_pages))
                 return id;
