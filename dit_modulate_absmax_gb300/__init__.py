@@ -584,7 +584,10 @@ def rope_axes(x, rope: Rope, *, inverse=False, out=None, stream=None):
 
 def _norm_side(x, name, weight, shape, device):
     """A side's array, weight and what the structures say of the weight."""
-    at = _need_tokens(x, name, (shape[0], x.shape[1] if x.dim() == 3 else -1, shape[2]), device)
+    its = x.shape
+    if len(its) != 3 or its[0] != shape[0] or its[2] != shape[2]:
+        _refuse(x, name, f"a [{shape[0]}, heads, {shape[2]}] tensor", device)
+    at = _need_tokens(x, name, None, device)
     if weight is None:
         return at, 0, 0
     wide = weight.dtype is _dtypes()["f32"]
@@ -592,6 +595,15 @@ def _norm_side(x, name, weight, shape, device):
             and (wide or weight.dtype in _dtypes()["bf16"])):
         _refuse(weight, f"{name}_weight", f"a contiguous [{shape[2]}] tensor of bf16 values or float32", device)
     return at, weight.data_ptr(), int(wide)
+
+
+def _out_like(x, out, name, device, stream):
+    """The output given for x, or a new contiguous one; its address and strides."""
+    if out is not None:
+        return out, _need_tokens(out, name, x.shape, device)
+    shape = x.shape
+    out = _empty(stream, shape, dtype=x.dtype, device=x.device)
+    return out, (out.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope: Rope | None = None, eps=1e-6, q_out=None, k_out=None,
@@ -610,9 +622,8 @@ def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope: Rope | None = No
             outs.append(None)
             continue
         at, w, wide = _norm_side(x, name, weight, shape, device)
-        if out is None:
-            out = x.new_empty(x.shape) if stream is None else _empty(stream, x.shape, dtype=x.dtype, device=x.device)
-        sides.append(_NORM_HEADS.pack(*at, *_need_tokens(out, f"{name}_out", x.shape, device), w, x.shape[1], wide))
+        out, to = _out_like(x, out, name + "_out", device, stream)
+        sides.append(_NORM_HEADS.pack(*at, *to, w, x.shape[1], wide))
         outs.append(out)
     if rope is not None:
         _positions_for(rope, shape[0], device)
@@ -640,19 +651,18 @@ def norm_rope_backward(q_grad, k_grad, q, k=None, *, q_weight=None, k_weight=Non
             continue
         at, w, wide = _norm_side(x, name, weight, shape, device)
         gt = _need_tokens(g, f"{name}_grad", x.shape, device)
-        if out is None:
-            out = x.new_empty(x.shape) if stream is None else _empty(stream, x.shape, dtype=x.dtype, device=x.device)
-        if weight is None:
-            if dw is not None:
-                raise ValueError(f"{name}_weight_grad: there is no {name}_weight")
-        elif dw is None:
-            dw = _empty(stream, shape[2], dtype=torch.float32, device=x.device)
+        out, to = _out_like(x, out, name + "_out", device, stream)
         dw_at = 0
         if dw is not None:
+            if weight is None:
+                raise ValueError(f"{name}_weight_grad: there is no {name}_weight")
             dw_at = _need_array(dw, f"{name}_weight_grad", "f32", 1, device)
             if dw.shape != shape[2:]:
                 _refuse(dw, f"{name}_weight_grad", f"a contiguous [{shape[2]}] tensor", device)
-        sides.append(_NORM_GRADS.pack(*gt, *at, *_need_tokens(out, f"{name}_out", x.shape, device), w, dw_at, x.shape[1], wide))
+        elif weight is not None:
+            dw = _empty(stream, shape[2], dtype=torch.float32, device=x.device)
+            dw_at = dw.data_ptr()
+        sides.append(_NORM_GRADS.pack(*gt, *at, *to, w, dw_at, x.shape[1], wide))
         outs.append(out)
         sums.append(dw)
     if rope is not None:
@@ -761,17 +771,17 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
     before it (window > 0), unless they are among the first ``sinks``.  scale defaults to
     head_dim ** -0.5.  Returns (out, lse); lse [tokens, heads] float32 is None unless asked
     for."""
-    device, shape, qs, out, lse, lse_at = _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream)
+    device, shape, qs, out, to, lse, lse_at = _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream)
     tokens, heads, dim = shape
     batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
     need = _attention_workspace(device, tokens, heads, cache._heads, dim, page_table.shape[0], max_tokens, max_kv)
     at, have, workspace = _workspace(workspace, need, device, stream, q)
     if sinks:
-        h3fp4_kv_attention_sinks(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, batch,
+        h3fp4_kv_attention_sinks(*qs, *to, lse_at, tokens, heads, cache._struct, batch,
                                  max_kv, dim ** -0.5 if scale is None else scale, causal, window, sinks, at, have,
                                  _raw_stream(stream, q))
     else:
-        h3fp4_kv_attention(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, batch, max_kv,
+        h3fp4_kv_attention(*qs, *to, lse_at, tokens, heads, cache._struct, batch, max_kv,
                            dim ** -0.5 if scale is None else scale, causal, window, at, have, _raw_stream(stream, q))
     return out, lse
 
@@ -786,16 +796,17 @@ def _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream):
     if dim != cache._head_dim or heads % cache._heads or kv_len is None:
         raise ValueError(f"q: {heads} heads of {dim} for a cache of {cache.heads} heads of {cache.head_dim}"
                          if kv_len is not None else "kv_len: lengths are wanted")
-    if out is None:
-        out = q.new_empty(shape) if stream is None else _empty(stream, shape, dtype=q.dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = _empty(stream, tokens, heads, dtype=torch.float32, device=q.device)
+    out, to = _out_like(q, out, "out", device, stream)
     lse_at = None
-    if lse is not None:
+    if lse is None:
+        if return_lse:
+            lse = _empty(stream, tokens, heads, dtype=torch.float32, device=q.device)
+            lse_at = lse.data_ptr()
+    else:
         lse_at = _need_array(lse, "lse", "f32", 2, device)
         if lse.shape != (tokens, heads):
             _refuse(lse, "lse", f"a contiguous {(tokens, heads)} tensor", device)
-    return device, shape, qs, out, lse, lse_at
+    return device, shape, qs, out, to, lse, lse_at
 
 
 def _workspace(workspace, need, device, stream, like):
@@ -842,14 +853,14 @@ def kv_attention_shared(q, cache: KVCache, prefix: SharedPrefix, page_table, kv_
     own keys what it sees in ``kv_attention``, under one softmax.  page_table and kv_len are those of the own keys alone,
     which begin on pages of their own.  The prefixes' pages are read once for a group, not once for a sequence.  Returns
     (out, lse)."""
-    device, shape, qs, out, lse, lse_at = _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream)
+    device, shape, qs, out, to, lse, lse_at = _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream)
     _need_device(prefix, "prefix", device)
     tokens, heads, dim = shape
     batch = _kv_batch(page_table, kv_len, cu_tokens, max_tokens, device)
     need = _shared_workspace(device, tokens, heads, cache._heads, dim, prefix._page_table.shape[0], prefix._max_tokens,
                              prefix._max_kv, page_table.shape[0], max_tokens, max_kv)
     at, have, workspace = _workspace(workspace, need, device, stream, q)
-    h3fp4_kv_attention_shared(*qs, *_need_tokens(out, "out", shape, device), lse_at, tokens, heads, cache._struct, prefix._struct,
+    h3fp4_kv_attention_shared(*qs, *to, lse_at, tokens, heads, cache._struct, prefix._struct,
                               prefix._max_kv, batch, max_kv, dim ** -0.5 if scale is None else scale, causal, at, have,
                               _raw_stream(stream, q))
     return out, lse
@@ -889,9 +900,11 @@ def kv_tables(held, count, page_table, free_pages, free_at, page_size, num_pages
                              (positions, "positions", "f32", tokens), (free_at_out, "free_at_out", "i32", 1)):
         if t is None:
             t = _empty(stream, n, dtype=_dtypes()[kind], device=held.device)
-        at[name] = _need_array(t, name, kind, 1, device)
-        if t.shape[0] != n:
-            _refuse(t, name, f"a contiguous [{n}] tensor", device)
+            at[name] = t.data_ptr()
+        else:
+            at[name] = _need_array(t, name, kind, 1, device)
+            if t.shape[0] != n:
+                _refuse(t, name, f"a contiguous [{n}] tensor", device)
         outs.append(t)
     h3fp4_kv_tables(_KV_REQUESTS.pack(at["held"], at["count"], at["page_table"], room, at["free_pages"], at["free_at"],
                                       at["free_at_out"], at["cu_tokens"], at["kv_len"], at["slots"], at["positions"], tokens,

@@ -5,7 +5,9 @@
 // one, each scanning the tile's tokens and pages in shared memory and writing
 // its share of the rows, whose sequence a binary search finds.  What lies
 // before the tile and the batch's total each CTA sums up for itself (8 bytes a
-// sequence out of L2), which costs less than a second launch or a wait.
+// sequence out of L2), which costs less than a second launch or a wait.  Bound
+// by a launch and a chain of dependent loads: lengths, the table's entry or the
+// free list's, the stores (64 requests of one token 5.0 us in a graph).
 #include <algorithm>
 
 #include "kvcache.cuh"
@@ -16,8 +18,10 @@ namespace {
 
 __device__ uint32_t g_error;
 
-constexpr int kThreads = 256;
-constexpr int kEach = 4;                    // sequences a thread
+// 512 threads and two sequences each: 64 requests 5.0 us, 1,000 prompts (320,000 tokens) 7.0; 256 and four 5.3 and 7.9, 1,024
+// and one 6.4 and 8.4, 128 and eight 6.1 and 10.9.
+constexpr int kThreads = 512;
+constexpr int kEach = 2;                    // sequences a thread
 constexpr int kTile = kThreads * kEach;
 constexpr int kRows = 4;                    // rows of slots a thread takes at a time
 
@@ -51,12 +55,11 @@ __device__ __forceinline__ T warp_sum_up_to(T v, int lane)
 }
 
 // Sequence of element x among those that begin at at[0 .. n - 1], of which x is at or past the first: the last that begins at
-// or before it.
-__device__ __forceinline__ int owner(const int *at, int n, int x)
+// or before it.  first_step: the largest power of two below n (or 0).
+__device__ __forceinline__ int owner(const int *at, int n, int first_step, int x)
 {
     int lo = 0;
-#pragma unroll
-    for (int step = kTile / 2; step > 0; step >>= 1)
+    for (int step = first_step; step > 0; step >>= 1)
         if (lo + step < n && at[lo + step] <= x)
             lo += step;
     return lo;
@@ -70,14 +73,21 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(h3fp4_kv_requests q, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b0 = blockIdx.y * kTile, n = min(kTile, q.batch - b0);
     uint32_t error = 0;
+    const int free_at = *q.free_at;
 
     // The tile: tokens and pages of each thread's sequences, summed up.
     Request mine[kEach];
-    int t = 0, p = 0;
+    int t = 0, p = 0, page_begun[kEach];
+    bool begins[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int at = threadIdx.x * kEach + i;
         mine[i] = at < n ? request(q, b0 + at, shift) : Request{0, 0, 0, 0, true};
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        begins[i] = mine[i].count > 0 && (mine[i].held & ((1 << shift) - 1)) != 0;   // within a page
+        page_begun[i] = begins[i] ? q.page_table[(b0 + threadIdx.x * kEach + i) * q.ld_table + (mine[i].held >> shift)] : -1;
         error |= mine[i].ok ? 0u : ERR_KV_RANGE;
         t += mine[i].count;   // below 2^30 in a tile
         p += mine[i].pages;
@@ -105,13 +115,9 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(h3fp4_kv_requests q, i
         pages_at[at] = pages_to;
         held[at] = mine[i].held;
         first[at] = mine[i].first;
-        begun[at] = -1;
-        if (mine[i].count > 0 && (mine[i].held & ((1 << shift) - 1)) != 0) {   // the page that the sequence has begun
-            const int id = q.page_table[(b0 + at) * q.ld_table + (mine[i].held >> shift)];
-            const bool in = id >= 0 && id < q.num_pages;
-            begun[at] = in ? id : -1;
-            error |= in ? 0u : ERR_KV_RANGE;
-        }
+        const bool in = page_begun[i] >= 0 && page_begun[i] < q.num_pages;
+        begun[at] = in ? page_begun[i] : -1;
+        error |= begins[i] && !in ? ERR_KV_RANGE : 0u;
         tokens_to += mine[i].count;
         pages_to += mine[i].pages;
     }
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(h3fp4_kv_requests q, i
     __syncthreads();
     const int64_t tokens0 = ahead[0], pages0 = ahead[1];
     const int64_t tokens_all = tokens0 + tile_tokens + total[0], pages_all = pages0 + tile_pages + total[1];
-    const int free_at = *q.free_at;
+    const int first_step = n > 1 ? 1 << (31 - __clz(n - 1)) : 0;
     const auto page_of = [&](int64_t k) {   // number of the k-th page taken; -1 where there is none
         const int64_t at = free_at + k;
         const int id = at >= 0 && at < q.num_free ? q.free_pages[at] : -1;
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(h3fp4_kv_requests q, i
     }
     const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, threads = static_cast<int64_t>(gridDim.x) * kThreads;
     for (int64_t i = thread; i < tile_pages; i += threads) {
-        const int s = owner(pages_at, n, static_cast<int>(i));
+        const int s = owner(pages_at, n, first_step, static_cast<int>(i));
         const int id = page_of(pages0 + i);
         error |= id < 0 ? ERR_KV_RANGE : 0u;
         q.page_table[(b0 + s) * q.ld_table + first[s] + (i - pages_at[s])] = id;
@@ -174,23 +180,51 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(h3fp4_kv_requests q, i
     if (error != 0)
         atomicOr(&g_error, error);
 
-    // Rows of slots and positions, kRows at a time.
+    // Rows of slots and positions, kRows at a time, in wide stores where the arrays allow it.
     const int64_t row_end = min(tokens0 + tile_tokens, q.tokens);
+    const bool wide_stores = ((reinterpret_cast<uintptr_t>(q.slots) | reinterpret_cast<uintptr_t>(q.positions)) & 15u) == 0;
     for (int64_t row0 = tokens0 / kRows * kRows + thread * kRows; row0 < row_end; row0 += threads * kRows) {
-        const int64_t from = max(row0, tokens0), to = min(row0 + kRows, row_end);
-        int s = owner(tokens_at, n, static_cast<int>(from - tokens0));
-        for (int64_t row = from; row < to; ++row) {
+        const int64_t from = max(row0, tokens0);
+        int s = owner(tokens_at, n, first_step, static_cast<int>(from - tokens0)), page = -1, id = -1;
+        long long slot[kRows];
+        float position[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int64_t row = row0 + i;
+            slot[i] = -1;
+            position[i] = -1.0f;
+            if (row < from || row >= row_end)
+                continue;
             const int x = static_cast<int>(row - tokens0);
-            while (s + 1 < n && tokens_at[s + 1] <= x)
+            while (s + 1 < n && tokens_at[s + 1] <= x) {
                 ++s;
-            const int pos = held[s] + (x - tokens_at[s]), page = pos >> shift;
+                page = -1;
+            }
+            const int pos = held[s] + (x - tokens_at[s]);
+            if (pos >> shift != page) {
+                page = pos >> shift;
+                id = page < first[s] ? begun[s] : page_of(pages0 + pages_at[s] + (page - first[s]));
+            }
+            slot[i] = id < 0 ? -1 : (static_cast<int64_t>(id) << shift) + (pos & ((1 << shift) - 1));
+            position[i] = static_cast<float>(pos);
+        }
+        if (wide_stores && row0 >= tokens0 && row0 + kRows <= row_end) {
             if (q.slots != nullptr) {
-                const int id = page < first[s] ? begun[s] : page_of(pages0 + pages_at[s] + (page - first[s]));
-                q.slots[row] = id < 0 ? -1 : (static_cast<int64_t>(id) << shift) + (pos & ((1 << shift) - 1));
+                *reinterpret_cast<longlong2 *>(q.slots + row0) = make_longlong2(slot[0], slot[1]);
+                *reinterpret_cast<longlong2 *>(q.slots + row0 + 2) = make_longlong2(slot[2], slot[3]);
             }
             if (q.positions != nullptr)
-                q.positions[row] = static_cast<float>(pos);
+                *reinterpret_cast<float4 *>(q.positions + row0) = make_float4(position[0], position[1], position[2], position[3]);
+            continue;
         }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (row0 + i >= from && row0 + i < row_end) {
+                if (q.slots != nullptr)
+                    q.slots[row0 + i] = slot[i];
+                if (q.positions != nullptr)
+                    q.positions[row0 + i] = position[i];
+            }
     }
     // Rows past the last token, by all.
     const int64_t wide = threads * gridDim.y;
