@@ -121,7 +121,7 @@ def _status_text(status: int) -> str:
 
 
 def _call(name: str, *args) -> None:
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != 0:
         raise H3FP4Error(name, st)
 
@@ -333,11 +333,12 @@ def _empty(stream, *shape, dtype, device):
     """Uninitialised memory that belongs to the stream the call's kernels run on (None: torch's current one).  torch's
     allocator hands a block out again in the order of its own stream: a block of another stream may still be in use
     there, or come into use again before these kernels have finished with it."""
-    import torch
+    empty = (_types or _dtypes())["empty"]
     if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
+        return empty(*shape, dtype=dtype, device=device)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=device)
+        return empty(*shape, dtype=dtype, device=device)
 
 
 def _need_cuda(*ts):
@@ -491,7 +492,7 @@ def _dtypes():
     if _types is None:
         import torch
         _types = {"bf16": (torch.bfloat16, torch.int16), "i32": torch.int32, "i64": torch.int64, "f32": torch.float32,
-                  "f64": torch.float64, "u8": torch.uint8}
+                  "f64": torch.float64, "u8": torch.uint8, "empty": torch.empty}
     return _types
 
 
@@ -599,9 +600,9 @@ def _norm_side(x, name, weight, shape, device):
 
 def _out_like(x, out, name, device, stream):
     """The output given for x, or a new contiguous one; its address and strides."""
-    if out is not None:
-        return out, _need_tokens(out, name, x.shape, device)
     shape = x.shape
+    if out is not None:
+        return out, _need_tokens(out, name, shape, device)
     out = _empty(stream, shape, dtype=x.dtype, device=x.device)
     return out, (out.data_ptr(), shape[1] * shape[2], shape[2])
 
@@ -612,23 +613,22 @@ def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope: Rope | None = No
     [head_dim] (bf16 or float32; None: ones), then turned by ``rope`` (None: not), rounded once.  q and k may have
     different numbers of heads; q_out=q works in place.  Returns (q_out, k_out); k_out is None without k."""
     device, shape = q.get_device(), q.shape
-    _need_tokens(q, "q")
-    sides, outs = [], []
-    for x, name, weight, out in ((q, "q", q_weight, q_out), (k, "k", k_weight, k_out)):
-        if x is None:
-            if weight is not None or out is not None:
-                raise ValueError(f"{name}: a weight or an output without {name}")
-            sides.append(None)
-            outs.append(None)
-            continue
-        at, w, wide = _norm_side(x, name, weight, shape, device)
-        out, to = _out_like(x, out, name + "_out", device, stream)
-        sides.append(_NORM_HEADS.pack(*at, *to, w, x.shape[1], wide))
-        outs.append(out)
+    _need_tokens(q, "q")                   # (three dimensions and a device: what the rest goes by)
+    at, w, wide = _norm_side(q, "q", q_weight, shape, device)
+    q_out, to = _out_like(q, q_out, "q_out", device, stream)
+    q_side, k_side = _NORM_HEADS.pack(*at, *to, w, shape[1], wide), None
+    if k is not None:
+        at, w, wide = _norm_side(k, "k", k_weight, shape, device)
+        k_out, to = _out_like(k, k_out, "k_out", device, stream)
+        k_side = _NORM_HEADS.pack(*at, *to, w, k.shape[1], wide)
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k: a weight or an output without k")
+    rope_at = None
     if rope is not None:
         _positions_for(rope, shape[0], device)
-    h3fp4_norm_rope(*sides, shape[0], shape[2], eps, rope._struct if rope is not None else None, _raw_stream(stream, q))
-    return tuple(outs)
+        rope_at = rope._struct
+    h3fp4_norm_rope(q_side, k_side, shape[0], shape[2], eps, rope_at, _raw_stream(stream, q))
+    return q_out, k_out
 
 
 def norm_rope_backward(q_grad, k_grad, q, k=None, *, q_weight=None, k_weight=None, rope: Rope | None = None, eps=1e-6,
@@ -636,42 +636,40 @@ def norm_rope_backward(q_grad, k_grad, q, k=None, *, q_weight=None, k_weight=Non
     """Gradients of ``norm_rope`` from those of its outputs and its inputs (nothing else is kept of the forward pass).
     Returns (dq, dk, dq_weight, dk_weight): dq and dk like q and k (q_out=q_grad works in place), the weights' float32
     [head_dim], None where there is no weight."""
-    import torch
     device, shape = q.get_device(), q.shape
     _need_tokens(q, "q")
-    sides, outs, sums = [], [], []
-    for g, x, name, weight, out, dw in ((q_grad, q, "q", q_weight, q_out, q_weight_grad),
-                                        (k_grad, k, "k", k_weight, k_out, k_weight_grad)):
-        if x is None:
-            if g is not None or weight is not None or out is not None or dw is not None:
-                raise ValueError(f"{name}: gradients, a weight or an output without {name}")
-            sides.append(None)
-            outs.append(None)
-            sums.append(None)
-            continue
-        at, w, wide = _norm_side(x, name, weight, shape, device)
-        gt = _need_tokens(g, f"{name}_grad", x.shape, device)
-        out, to = _out_like(x, out, name + "_out", device, stream)
-        dw_at = 0
-        if dw is not None:
-            if weight is None:
-                raise ValueError(f"{name}_weight_grad: there is no {name}_weight")
-            dw_at = _need_array(dw, f"{name}_weight_grad", "f32", 1, device)
-            if dw.shape != shape[2:]:
-                _refuse(dw, f"{name}_weight_grad", f"a contiguous [{shape[2]}] tensor", device)
-        elif weight is not None:
-            dw = _empty(stream, shape[2], dtype=torch.float32, device=x.device)
-            dw_at = dw.data_ptr()
-        sides.append(_NORM_GRADS.pack(*gt, *at, *to, w, dw_at, x.shape[1], wide))
-        outs.append(out)
-        sums.append(dw)
+    q_side, q_out, q_weight_grad = _norm_grad_side(q_grad, q, "q", q_weight, q_out, q_weight_grad, shape, device, stream)
+    k_side = None
+    if k is not None:
+        k_side, k_out, k_weight_grad = _norm_grad_side(k_grad, k, "k", k_weight, k_out, k_weight_grad, shape, device, stream)
+    elif any(t is not None for t in (k_grad, k_weight, k_out, k_weight_grad)):
+        raise ValueError("k: gradients, a weight or an output without k")
+    rope_at = None
     if rope is not None:
         _positions_for(rope, shape[0], device)
-    at, have, workspace = _workspace(workspace, _norm_workspace(device, shape[2]) if any(t is not None for t in sums) else 0,
-                                     device, stream, q)
-    h3fp4_norm_rope_backward(*sides, shape[0], shape[2], eps, rope._struct if rope is not None else None, at, have,
-                             _raw_stream(stream, q))
-    return (*outs, *sums)
+        rope_at = rope._struct
+    sums = q_weight_grad is not None or k_weight_grad is not None
+    at, have, workspace = _workspace(workspace, _norm_workspace(device, shape[2]) if sums else 0, device, stream, q)
+    h3fp4_norm_rope_backward(q_side, k_side, shape[0], shape[2], eps, rope_at, at, have, _raw_stream(stream, q))
+    return q_out, k_out, q_weight_grad, k_weight_grad
+
+
+def _norm_grad_side(g, x, name, weight, out, dw, shape, device, stream):
+    """A side's structure, and its gradients."""
+    at, w, wide = _norm_side(x, name, weight, shape, device)
+    gt = _need_tokens(g, name + "_grad", x.shape, device)
+    out, to = _out_like(x, out, name + "_out", device, stream)
+    dw_at = 0
+    if dw is not None:
+        if weight is None:
+            raise ValueError(f"{name}_weight_grad: there is no {name}_weight")
+        dw_at = _need_array(dw, name + "_weight_grad", "f32", 1, device)
+        if dw.shape != shape[2:]:
+            _refuse(dw, name + "_weight_grad", f"a contiguous [{shape[2]}] tensor", device)
+    elif weight is not None:
+        dw = _empty(stream, shape[2:], dtype=_dtypes()["f32"], device=x.device)
+        dw_at = dw.data_ptr()
+    return _NORM_GRADS.pack(*gt, *at, *to, w, dw_at, x.shape[1], wide), out, dw
 
 
 @functools.lru_cache(maxsize=64)           # a function of the head's channels and the device's SMs
@@ -788,7 +786,6 @@ def kv_attention(q, cache: KVCache, page_table, kv_len, cu_tokens, max_tokens, m
 
 def _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream):
     """Checks of what every attention call takes, and its outputs."""
-    import torch
     device, shape = q.get_device(), q.shape
     qs = _need_tokens(q, "q")
     _need_device(cache, "cache", device)
@@ -800,7 +797,7 @@ def _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream):
     lse_at = None
     if lse is None:
         if return_lse:
-            lse = _empty(stream, tokens, heads, dtype=torch.float32, device=q.device)
+            lse = _empty(stream, (tokens, heads), dtype=_dtypes()["f32"], device=q.device)
             lse_at = lse.data_ptr()
     else:
         lse_at = _need_array(lse, "lse", "f32", 2, device)
@@ -811,14 +808,13 @@ def _attention_arrays(q, cache, kv_len, out, lse, return_lse, stream):
 
 def _workspace(workspace, need, device, stream, like):
     """Address and bytes of the caller's workspace, or of one made for the call (which the third result keeps)."""
-    import torch
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():   # (its bytes are written as they lie)
             _refuse(workspace, "workspace", "a contiguous tensor", device)
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if not need:
         return 0, 0, None
-    workspace = _empty(stream, need, dtype=torch.uint8, device=like.device)
+    workspace = _empty(stream, need, dtype=_dtypes()["u8"], device=like.device)
     return workspace.data_ptr(), need, workspace
 
 
@@ -883,30 +879,30 @@ def kv_tables(held, count, page_table, free_pages, free_at, page_size, num_pages
     yet, and of each new token its slot (page * page_size + its place in the page, int64) and its position (float32, as a
     Rope of one axis takes it).  slots and positions have ``tokens`` rows, of which those past the last token hold -1.
     The returned free_at counts what has been taken; the one given stays as it was."""
-    import torch
-    device = held.get_device()
-    at = {"held": _need_array(held, "held", "i32", 1, device), "count": _need_array(count, "count", "i32", 1, device),
-          "page_table": _need_array(page_table, "page_table", "i32", 2, device),
-          "free_pages": _need_array(free_pages, "free_pages", "i32", 1, device),
-          "free_at": _need_array(free_at, "free_at", "i32", 1, device)}
-    batch, room = page_table.shape
+    device, batch, room, free = held.get_device(), *page_table.shape, free_pages.shape[0]
+    at = (_need_array(held, "held", "i32", 1, device), _need_array(count, "count", "i32", 1, device),
+          _need_array(page_table, "page_table", "i32", 2, device), room, _need_array(free_pages, "free_pages", "i32", 1, device),
+          _need_array(free_at, "free_at", "i32", 1, device))
     if held.shape[0] != batch or count.shape[0] != batch or free_at.shape[0] != 1:
         raise ValueError(f"page_table has {batch} sequences: held and count of {batch} and one free_at are wanted, got "
                          f"{held.shape[0]}, {count.shape[0]} and {free_at.shape[0]}")
-    if not 0 <= tokens < 1 << 31 or not -1 <= (page_size | num_pages | max_tokens | batch | free_pages.shape[0]) >> 31 <= 0:
+    if not 0 <= tokens < 1 << 31 or not -1 <= (page_size | num_pages | max_tokens | batch | free) >> 31 <= 0:
         raise _too_large("h3fp4_kv_tables")
-    outs = []
-    for t, name, kind, n in ((cu_tokens, "cu_tokens", "i32", batch + 1), (kv_len, "kv_len", "i32", batch), (slots, "slots", "i64", tokens),
-                             (positions, "positions", "f32", tokens), (free_at_out, "free_at_out", "i32", 1)):
+
+    def out(t, name, kind, n):
         if t is None:
             t = _empty(stream, n, dtype=_dtypes()[kind], device=held.device)
-            at[name] = t.data_ptr()
-        else:
-            at[name] = _need_array(t, name, kind, 1, device)
-            if t.shape[0] != n:
-                _refuse(t, name, f"a contiguous [{n}] tensor", device)
-        outs.append(t)
-    h3fp4_kv_tables(_KV_REQUESTS.pack(at["held"], at["count"], at["page_table"], room, at["free_pages"], at["free_at"],
-                                      at["free_at_out"], at["cu_tokens"], at["kv_len"], at["slots"], at["positions"], tokens,
-                                      batch, max_tokens, free_pages.shape[0], num_pages, page_size), _raw_stream(stream, held))
-    return KVTables(*outs)
+            return t, t.data_ptr()
+        to = _need_array(t, name, kind, 1, device)
+        if t.shape[0] != n:
+            _refuse(t, name, f"a contiguous [{n}] tensor", device)
+        return t, to
+
+    cu_tokens, cu_at = out(cu_tokens, "cu_tokens", "i32", batch + 1)
+    kv_len, len_at = out(kv_len, "kv_len", "i32", batch)
+    slots, slots_at = out(slots, "slots", "i64", tokens)
+    positions, positions_at = out(positions, "positions", "f32", tokens)
+    free_at_out, next_at = out(free_at_out, "free_at_out", "i32", 1)
+    h3fp4_kv_tables(_KV_REQUESTS.pack(*at, next_at, cu_at, len_at, slots_at, positions_at, tokens, batch, max_tokens, free, num_pages,
+                                      page_size), _raw_stream(stream, held))
+    return KVTables(cu_tokens, kv_len, slots, positions, free_at_out)
