@@ -756,6 +756,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
 // whatever the lengths of the batch (equal parts per sequence, sized for the
 // longest, left SMs idle: 32 ragged requests took 87 us, then 73); rows that
 // lie with several CTAs are joined by a second kernel.
+// With sinks, and in the halves over shared prefixes and own keys, a row tile
+// of a sequence and cache head (an item) may also have a cluster (or one CTA)
+// to itself that takes several units each: no parts to join, and no CTA that
+// goes from one sequence to the next with its copies run dry.  That is taken
+// where there are two items or more for each place, or where what the longest
+// item's CTA has to do is no more than an equal share and 10 units (4 where a
+// CTA has 16 rows, whose units take longer).  In units of 128 keys, an item's
+// and an equal share, 128 channels: 32 sequences of 19 and 10.7: 37.5 us,
+// equal shares 42.5; 5 and 2.8: 17 and 26.7; 8 of 5 and 2.7: 17.3 and 21; 200
+// of 5 and 17.5 (four waves): 62 and 149; but 32 of 34 and 19: 64.5 and 59; of
+// 66 and 37: 110 and 74; 4 requests of 32 rows, 16 and 6.7: 48 and 35.
 SplitPlan plan_rows(const AttnShape &s)
 {
     const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);
@@ -833,7 +844,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
-    if (plan.cluster) {
+    if (plan.cluster && plan.splits > 1) {   // (without the attribute each CTA is a cluster of its own)
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = static_cast<unsigned>(plan.splits);
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;

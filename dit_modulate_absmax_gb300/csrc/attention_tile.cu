@@ -20,14 +20,18 @@
 // Shared memory at dim 128: queries 64 KB, two stages of keys and of values 32
 // KB each.
 //
-// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.13
-// ms, 1.07 PFLOP/s, about 4,100 cycles a step.  No pipe is full (tensor 43 to
-// 50 %, exponentials 21 %, issue 45 %, shared memory 32 %), and leaving out any
+// Measured: 5,042 tokens of 56 heads of 128 channels against 37,810 keys 5.01
+// ms, 1.09 PFLOP/s, about 4,100 cycles a step; with a window of 16,384 and 3,600
+// sinks 3.06 ms, 1.06 PFLOP/s.  No pipe is full (tensor 43 to 50 %,
+// exponentials 21 %, issue 45 %, shared memory 32 %), and leaving out any
 // one part of the arithmetic but the exponentials changes nothing.  What is
 // left is the length of a tile's chain -- scores, softmax, weights, product,
 // the next scores, of which some 500 cycles lie between a product's end and the
 // issue of the next scores -- with two tiles in turn, and the last wave: 1,120
-// CTAs of equal length on 152 SMs are 7.4 waves run as 8.
+// CTAs of equal length on 152 SMs are 7.4 waves run as 8.  Short CTAs (13
+// steps: 1,560 tokens over as many) lose more: of 80,000 cycles 15,000 go by
+// until the first step is done (set-up 2,600, the queries' way through DRAM and
+// into shared memory 8,000), and 5,000 after the last.
 // Tried and slower: half steps of 64 keys with two score buffers (5.65 ms), the
 // next scores' first half issued while the softmax works (4 %), two threads a
 // row (8.2 ms), a quarter of the exponentials as polynomials (16 %).

@@ -18,7 +18,7 @@ namespace {
 
 __device__ uint32_t g_error;
 
-// 512 threads and two sequences each: 64 requests 5.0 us, 1,000 prompts (320,000 tokens) 7.0; 256 and four 5.3 and 7.9, 1,024
+// 512 threads and two sequences each: 64 requests 5.0 us, 1,000 prompts (314,388 tokens) 7.0; 256 and four 5.3 and 7.9, 1,024
 // and one 6.4 and 8.4, 128 and eight 6.1 and 10.9.
 constexpr int kThreads = 512;
 constexpr int kEach = 2;                    // sequences a thread

@@ -14,7 +14,17 @@
 // interleaved lie within a chunk; of halves whose sections are whole chunks
 // the lane's second chunk is the partner of its first; other halves are
 // exchanged through shared memory.  FP32 pairs go through the packed
-// instructions.
+// instructions.  (With 8 channels a lane and single FP32 instructions the
+// forward kernel issued 147 for each 512 bytes read, and that bound it: 452 us
+// where it takes 320 now.)
+//
+// Reads and writes each value once, so HBM bounds both: 37,810 tokens of 56 +
+// 56 heads of 128 channels forward 320 us, 6.8 TB/s (the copy rate); 5,042
+// tokens' gradients 77 us, 5.6 TB/s, 20,000 tokens' 279 us, 6.2 TB/s.  What is
+// left of the gradient's is a launch, the first loads and the join of dw, about
+// 10 us; of small calls a launch and a chain of dependent loads (32 tokens of
+// 72 heads 4.1 us).  Exchanged halves cost the shared-memory pipe: 20,000
+// tokens 212 us, the other two ways 176.  All in a graph of 10 passes.
 #include <cuda_bf16.h>
 
 #include "norm_rope.cuh"
@@ -25,9 +35,15 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kForwardStages = 8, kBackwardStages = 4;   // units of a warp that are loaded or on their way
-constexpr int kForwardCtas = 2, kBackwardCtas = 1;       // of an SM
-constexpr int kForwardWaves = 16, kBackwardWaves = 1, kWaveUnits = 28;
+// Units of a warp that are loaded or on their way: 1 KB each forward, 2 KB for the gradients, half of the ring in a burst (a
+// unit at a time 371 us, 357 in bursts, both in one wave: longer runs of addresses).  Half and twice as many: within 3 %.
+constexpr int kForwardStages = 8, kBackwardStages = 4;
+// CTAs of an SM: three forward 424 us against 360 (more streams of addresses at a time), two for the gradients 79 against 78.
+constexpr int kForwardCtas = 2, kBackwardCtas = 1;
+// Forward calls come in waves of short CTAs, which even out what SMs get of the memory and read it in order (one wave 357 us, 8
+// waves 342, 16 and 32 326), as long as a warp has kWaveUnits units in each (14 and 56: the same).  Gradients take one wave
+// (two: 89 us against 80): each CTA leaves its part of dw.
+constexpr int kForwardWaves = 16, kWaveUnits = 28;
 static_assert((kForwardStages & (kForwardStages - 1)) == 0 && (kBackwardStages & (kBackwardStages - 1)) == 0, "stages wrap by a mask");
 
 // Where a channel's partner is: beside it, anywhere (exchanged), or at its place in the lane's other chunk (axes of 16 n
@@ -236,8 +252,7 @@ __device__ __forceinline__ int2 facing_place(const RopeArgs &r, int c)
 }
 
 // Word of a channel in the warp's exchange buffer: heads one after another, moved so that the lanes' words, four apart, fall
-// into different banks (a lane's eight words side by side put those of two lanes' partners into one bank: 264 us for 20,000
-// tokens of 112 heads of 128 channels, 54 conflicts for 24 accesses).
+// into different banks.
 template <int kLanes>
 __device__ __forceinline__ int exchange_at(int sub, int channel)
 {
@@ -723,13 +738,13 @@ cudaError_t run(const NormSide &q, const NormSide &k, int64_t tokens, int dim, f
     return cudaGetLastError();
 }
 
-int grad_ctas() { return kBackwardCtas * kBackwardWaves * sm_count(); }
+int grad_ctas() { return kBackwardCtas * sm_count(); }
 
 template <int kMode, int kLanes>
 cudaError_t run_grad(const NormGradSide &q, const NormGradSide &k, int64_t tokens, int dim, float eps, const RopeArgs &r, float *parts,
                      cudaStream_t st)
 {
-    const Split p = split_of(tokens, q.heads, k.heads, 32 / kLanes, kBackwardCtas * sm_count(), kBackwardWaves);
+    const Split p = split_of(tokens, q.heads, k.heads, 32 / kLanes, grad_ctas(), 1);
     if (p.ctas > 0) {
         constexpr int kSmem = sizeof(GradShared<kMode, kLanes>);
         cudaError_t e = allow_shared<norm_rope_grad_kernel<kMode, kLanes>>(kSmem);
