@@ -158,3 +158,26 @@ def test_out_of_range_entries_are_reported(h3, new):
     prefix = h3.SharedPrefix(_dev(table), _dev([32]), _dev([0, new]), new, 32)
     h3.kv_attention_shared(q, c, prefix, _dev(table), _dev([32]), _dev([0, new]), new, 32)
     assert h3.h3fp4_device_error() == 0
+
+
+@pytest.mark.parametrize("groups,seqs", [
+    ([(2_000, 1)], [(1, 300), (90, 400), (64, 64)]),        # few queries over the prefix, many over own keys
+    ([(300, 1), (900, 1)], [(2, 40), (1, 700), (150, 151)]),
+    ([(3_000, 2)], [(150, 150), (1, 1), (3, 5_000)]),
+])
+def test_groups_that_cover_some_of_the_sequences(h3, groups, seqs):
+    c, q, own, shared, cu, p_cu, first = _setup(h3, 21, groups, seqs, 8, 4, 128, 64)
+    out, lse = _call(h3, c, q, own, shared, groups, seqs, cu, p_cu, causal=True)
+    assert h3.h3fp4_device_error() == 0
+    _check(c, q, own, shared, groups, seqs, cu, first, out, lse, True)
+
+
+@pytest.mark.parametrize("new,batch", [(1, 3), (1, 40), (90, 2)])
+def test_nothing_before_or_nothing_own(h3, new, batch):
+    """Prefixes without keys, own keys without any, and both, with the largest lengths given as 0."""
+    for P, L in ((0, new + 30), (200, 0), (0, 0)):
+        seqs, groups = [(new, L)] * batch, [(P, batch)]
+        c, q, own, shared, cu, p_cu, first = _setup(h3, 22, groups, seqs, 4, 2, 64, 16)
+        out, lse = _call(h3, c, q, own, shared, groups, seqs, cu, p_cu)
+        assert h3.h3fp4_device_error() == 0
+        _check(c, q, own, shared, groups, seqs, cu, first, out, lse, False)

@@ -163,3 +163,46 @@ def test_sequences_without_keys(h3, new, pages):
                                    causal=True, window=4, sinks=2, return_lse=True)
         assert (out == 0).all() and (lse == -np.inf).all()
     assert h3.h3fp4_device_error() == 0
+
+
+@pytest.mark.parametrize("new", [1, 7, 140])
+def test_what_stands_in_for_hidden_pages_has_no_effect(h3, new):
+    """Page 0, and everything past the end, holds NaN: a sequence that does not use it, with a gap of whole pages, pages that
+    end inside a step, and a last step that is not full."""
+    rng = np.random.default_rng(11)
+    L, page = 1_111, 16
+    table, pages = _tables(rng, [L], page)
+    table = np.where(table == 0, pages, table)                      # page 0 goes unused
+    c = _filled(h3, rng, table, [L], pages + 1, 2, page, 128)
+    for codes in (c.k_codes, c.v_codes):
+        codes[0] = 0x7F
+    q = torch.randn(new, 4, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    for window, sinks in ((100, 10), (3, 200), (500, 129)):
+        given = _give_up(table, page, [(new, L)], window, sinks)
+        out, lse = _run(h3, q, c, given, [L], [0, new], new, causal=True, window=window, sinks=sinks)
+        assert h3.h3fp4_device_error() == 0
+        _check(c, q, table, [L], [0, new], out, lse, causal=True, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("new", [1, 140])
+def test_codes_past_32_bits(h3, new):
+    """The last pages of a cache of 5.2 GB of keys against the same pages in a small one, with sinks and behind a prefix."""
+    rng = np.random.default_rng(12)
+    L, page, heads = 700, 128, 8
+    small = h3.KVCache.empty(6, page, heads, 128)
+    for t in (small.k_codes, small.v_codes):
+        t.copy_(_dev(O.e4m3_encode(rng.standard_normal(t.shape) * 40), torch.uint8))
+    many = 40_000
+    big = h3.KVCache.empty(many, page, heads, 128)
+    for a, b in ((big.k_codes, small.k_codes), (big.v_codes, small.v_codes)):
+        a[-6:].copy_(b)
+    table = np.arange(6)[None]
+    q = torch.randn(new, heads, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    got = []
+    for c, first in ((small, 0), (big, many - 6)):
+        t = _dev(table + first)
+        got.append(h3.kv_attention(q, c, t, _dev([L]), _dev([0, new]), new, L, causal=True, window=100, sinks=200, return_lse=True))
+        prefix = h3.SharedPrefix(t[:, :2].contiguous(), _dev([200]), _dev([0, new]), new, 200)
+        got.append(h3.kv_attention_shared(q, c, prefix, t[:, 2:].contiguous(), _dev([300]), _dev([0, new]), new, 300, return_lse=True))
+    for a, b in zip(got[:2], got[2:]):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
