@@ -20,10 +20,10 @@
 //
 // Reads and writes each value once, so HBM bounds both: 37,810 tokens of 56 +
 // 56 heads of 128 channels forward 320 us, 6.8 TB/s (the copy rate); 5,042
-// tokens' gradients 77 us, 5.6 TB/s, 20,000 tokens' 279 us, 6.2 TB/s.  What is
-// left of the gradient's is a launch, the first loads and the join of dw, about
-// 10 us; of small calls a launch and a chain of dependent loads (32 tokens of
-// 72 heads 4.1 us).  Exchanged halves cost the shared-memory pipe: 20,000
+// tokens' gradients 72 us, 6.0 TB/s, 20,000 tokens' 259 us, 6.6 TB/s.  What is
+// left of the gradient's is a launch, the first loads and the join of dw (3
+// us); of small calls a launch and a chain of dependent loads (32 tokens of 72
+// heads 4.1 us).  Exchanged halves cost the shared-memory pipe: 20,000
 // tokens 212 us, the other two ways 176.  All in a graph of 10 passes.
 #include <cuda_bf16.h>
 
@@ -36,12 +36,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // Units of a warp that are loaded or on their way: 1 KB each forward, 2 KB for the gradients, half of the ring in a burst (a
-// unit at a time 371 us, 357 in bursts, both in one wave: longer runs of addresses).  Half and twice as many: within 3 %.
-constexpr int kForwardStages = 8, kBackwardStages = 4;
+// unit at a time 371 us, 357 in bursts, both in one wave: longer runs of addresses).  Forward with half as many 338 us (326);
+// 5,042 tokens' gradients with half as many 77 us (72).
+constexpr int kForwardStages = 8, kBackwardStages = 8;
 // CTAs of an SM: three forward 424 us against 360 (more streams of addresses at a time), two for the gradients 79 against 78.
 constexpr int kForwardCtas = 2, kBackwardCtas = 1;
 // Forward calls come in waves of short CTAs, which even out what SMs get of the memory and read it in order (one wave 357 us, 8
-// waves 342, 16 and 32 326), as long as a warp has kWaveUnits units in each (14 and 56: the same).  Gradients take one wave
+// waves 342, 16 and 32 326), as long as a warp has kWaveUnits units in each (20,000 tokens 177 us; with 14 units 184).  Gradients take one wave
 // (two: 89 us against 80): each CTA leaves its part of dw.
 constexpr int kForwardWaves = 16, kWaveUnits = 28;
 static_assert((kForwardStages & (kForwardStages - 1)) == 0 && (kBackwardStages & (kBackwardStages - 1)) == 0, "stages wrap by a mask");
