@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas)
     const Walk at(tokens, units);
     // Some units ahead: those of one side of a token lie a step apart.
     int to_copy = at.left, copy_t = at.t, copy_unit = at.unit, run = 0, head = 0, heads = 0;
-    const uint16_t *xp = nullptr;
+    const uint16_t *xp = nullptr, *const some = qs.heads > 0 ? qs.x : ks.x;   // (an address for copies of nothing)
     int64_t x_step = 0;
     const auto fetch = [&](int first) {   // half of the ring; past the last unit, nothing
 #pragma unroll
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kForwardCtas)
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                copy_ahead(&s.ring[stage][j][threadIdx.x], xp + place.c[j], head < heads && place.live[j]);
+                copy_ahead(&s.ring[stage][j][threadIdx.x], (head < heads ? xp : some) + place.c[j], head < heads && place.live[j]);
             xp += x_step;
             head += kPerWarp;
             --run;
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
     const Walk at(tokens, units);
     // Some units ahead, as above.
     int to_copy = at.left, copy_t = at.t, copy_unit = at.unit, run = 0, head = 0, heads = 0;
-    const uint16_t *xp = nullptr, *gp = nullptr;
+    const uint16_t *xp = nullptr, *gp = nullptr, *const some = qs.heads > 0 ? qs.x : ks.x;
     int64_t x_step = 0, g_step = 0;
     const auto fetch = [&](int first) {
 #pragma unroll
@@ -572,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardCtas)
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                copy_ahead(&s.ring[stage][j][threadIdx.x], xp + place.c[j], head < heads && place.live[j]);
-                copy_ahead(&s.ring[stage][2 + j][threadIdx.x], gp + place.c[j], head < heads && place.live[j]);
+                copy_ahead(&s.ring[stage][j][threadIdx.x], (head < heads ? xp : some) + place.c[j], head < heads && place.live[j]);
+                copy_ahead(&s.ring[stage][2 + j][threadIdx.x], (head < heads ? gp : some) + place.c[j], head < heads && place.live[j]);
             }
             xp += x_step;
             gp += g_step;
