@@ -268,6 +268,7 @@ struct SplitPlan {
     int32_t splits, chunk;
     int64_t part_rows;
     bool cluster;
+    int32_t warps = 0;   // rows: of a CTA
 };
 
 // For a launch that may begin while the one before it ends (it waits for that end itself).

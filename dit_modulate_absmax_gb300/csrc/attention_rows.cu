@@ -4,8 +4,8 @@
 //
 // Reads every visible code once (2 * dim bytes a token and cache head) for each
 // 16 rows, of which there are 32 at most, so it is bound by HBM.  What it takes to stay there:
-//  - The keys are spread evenly over as many CTAs as fit; each of a CTA's 4
-//    warps runs its own online softmax over units of 32 tokens, fed by its own
+//  - The keys are spread evenly over as many CTAs as fit; each of a CTA's 4 or
+//    6 warps runs its own online softmax over units of 32 tokens, fed by its own
 //    ring of TMA copies (one lane issues two a unit), with no barrier between
 //    warps in the loop.
 //  - Codes go from shared memory to registers as they lie and are converted to
@@ -39,8 +39,7 @@ namespace {
 
 __device__ uint32_t g_error;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kFew = 4, kMany = 6;        // warps of a CTA, see plan_rows
 constexpr int kUnit = 32;                 // tokens a warp takes at a time
 constexpr int kStages = 2;
 constexpr int kMaxEntries = 512;          // pages of one part
@@ -79,20 +78,20 @@ __device__ __forceinline__ void join(float4 &mean, const float4 &v, float half, 
 }
 
 // CTAs that fit an SM: shared memory at 128 channels, registers at 64.
-template <int kDim, int kRows>
+template <int kDim, int kRows, int kWarps = kFew>
 constexpr int resident()
 {
-    return kDim == 128 ? (kRows == 8 ? 3 : 2) : (kRows == 8 ? 4 : 3);
+    return kWarps == kMany ? 2 : kDim == 128 ? (kRows == 8 ? 3 : 2) : (kRows == 8 ? 4 : 3);
 }
 
-// Units of 128 tokens, one for each warp's 32, that a sequence's rows take: its
+// Units of 128 or 192 tokens, one for each warp's 32, that a sequence's rows take: its
 // share of the work for each cache head and row tile.  0: nothing to do.
 struct Units {
     int begin, count, tiles;   // first token's place (a multiple of 32), units, row tiles
     Fold fold;
 };
 
-template <int kRows, int kForm>
+template <int kRows, int kForm, int kWarps>
 __device__ __forceinline__ Units units_of(const AttnArgs &a, const KvSequence &s)
 {
     if (!s.ok || s.n == 0 || s.len > a.max_kv ||
@@ -121,15 +120,15 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
 __device__ __forceinline__ int64_t cta_of(int64_t x, int64_t g, int64_t total) { return divide((x + 1) * g - 1, total); }
 
 // kWithhold: for a check that waits end.  Each copy is announced larger than it is, so that none completes.
-template <int kDim, int kRows, int kForm, bool kWithhold = false>
-__global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
+template <int kDim, int kRows, int kForm, int kWarps, bool kWithhold = false>
+__global__ void __launch_bounds__(kWarps * 32, resident<kDim, kRows, kWarps>())
     rows_kernel(AttnArgs a, SplitPlan plan, float *ws_log, float *ws_out, const __grid_constant__ CUtensorMap k_map,
                 const __grid_constant__ CUtensorMap v_map, uint64_t wait_ns)
 {
     constexpr int kSteps = kDim / 16;            // k16 steps of Q K^T = 16-channel tiles of O^T
     constexpr int kHalf = kRows / 8;             // groups of 8 rows
     constexpr int kTile = kUnit * kDim;          // bytes of a unit's keys
-    constexpr int kTokens = kWarps * kUnit;
+    constexpr int kThreads = kWarps * 32, kTokens = kWarps * kUnit;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ PageEntry entry[kMaxEntries];
     __shared__ uint64_t full[kWarps][kStages];
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         int64_t mine = 0;
         for (int b = threadIdx.x * share; b < min(a.batch.batch, (static_cast<int>(threadIdx.x) + 1) * share); ++b) {
             const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-            const Units u = units_of<kRows, kForm>(a, s);
+            const Units u = units_of<kRows, kForm, kWarps>(a, s);
             mine += static_cast<int64_t>(u.count) * u.tiles * heads;
             if (u.count == 0 && s.n != 0 && blockIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         kh = blockIdx.x / plan.splits % heads;
         tile = blockIdx.x / plan.splits / heads;
         s = kv_sequence(a.batch, b, a.tokens);
-        const Units u = units_of<kRows, kForm>(a, s);
+        const Units u = units_of<kRows, kForm, kWarps>(a, s);
         if (u.count == 0 || tile >= u.tiles) {   // the same in the whole cluster
             if (u.count == 0 && s.n != 0 && threadIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
@@ -222,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
             int at = threadIdx.x * share;
             if (share > 1)
                 for (;; ++at) {
-                    const Units v = units_of<kRows, kForm>(a, kv_sequence(a.batch, at, a.tokens));
+                    const Units v = units_of<kRows, kForm, kWarps>(a, kv_sequence(a.batch, at, a.tokens));
                     const int64_t n = static_cast<int64_t>(v.count) * v.tiles * heads;
                     if (rest < n)
                         break;
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, resident<kDim, kRows>())
         b = found_b;
         const int64_t rest = found_rest;
         s = kv_sequence(a.batch, b, a.tokens);
-        const Units u = units_of<kRows, kForm>(a, s);
+        const Units u = units_of<kRows, kForm, kWarps>(a, s);
         const int item = static_cast<int>(divide(rest, u.count)), u0 = static_cast<int>(rest - static_cast<int64_t>(item) * u.count);
         const int u1 = static_cast<int>(min(static_cast<int64_t>(u.count), u0 + (x_end - x)));
         kh = item % heads;
@@ -682,10 +681,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
     const int kh = blockIdx.x % a.cache.heads, tile = blockIdx.x / a.cache.heads;
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
-    const Units u = units_of<kRows, kForm>(a, s);
+    const Units u = units_of<kRows, kForm, kFew>(a, s);
     int64_t ahead = 0, total = 0;   // units of the sequences before this one, and of all
     for (int i = lane; i < a.batch.batch; i += 32) {
-        const Units v = units_of<kRows, kForm>(a, kv_sequence(a.batch, i, a.tokens));
+        const Units v = units_of<kRows, kForm, kFew>(a, kv_sequence(a.batch, i, a.tokens));
         const int64_t n = static_cast<int64_t>(v.count) * v.tiles * a.cache.heads;
         total += n;
         ahead += i < b ? n : 0;
@@ -767,25 +766,37 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
 // equal shares 42.5; 5 and 2.8: 17 and 26.7; 8 of 5 and 2.7: 17.3 and 21; 200
 // of 5 and 17.5 (four waves): 62 and 149; but 32 of 34 and 19: 64.5 and 59; of
 // 66 and 37: 110 and 74; 4 requests of 32 rows, 16 and 6.7: 48 and 35.
+// Items that are more than one and a half for each SM and no more than two get
+// CTAs of six warps, two an SM, which take units of 192 keys: at one to two
+// CTAs an SM a warp's own chain through a unit is what counts (32 sequences of
+// 19 units of 128 keys 33.1 us, 37.4 with four warps; of 34: 54.6, equal shares
+// 59; of 66: 90 and 74; 64 channels, 6 units 11.6 and 14.3; 12 units of own keys
+// behind a prefix 23.9 and 27.3, but 4: 48.9 and 44.5; 24 sequences, which four
+// warps take in clusters of two, 31.6 and 30.0).
 SplitPlan plan_rows(const AttnShape &s)
 {
     const int64_t rows = static_cast<int64_t>(s.max_tokens) * (s.heads / s.kv_heads);
     const int64_t tile = rows <= 8 ? 8 : 16;
     const int64_t fit = sm_count() * (s.head_dim == 128 ? (tile == 8 ? resident<128, 8>() : resident<128, 16>())
                                                         : (tile == 8 ? resident<64, 8>() : resident<64, 16>()));
-    const int64_t per_row = (folded_keys(s, s.max_tokens) + kWarps * kUnit - 1) / (kWarps * kUnit);
+    const int64_t keys = folded_keys(s, s.max_tokens), per_row = (keys + kFew * kUnit - 1) / (kFew * kUnit);
     if (per_row <= 8 && rows <= 16 && per_row * s.batch * s.kv_heads <= fit)
-        return SplitPlan{static_cast<int32_t>(per_row), 1, 0, true};
+        return SplitPlan{static_cast<int32_t>(per_row), 1, 0, true, kFew};
     if (s.form != kWhole) {
         const int64_t items = s.batch * s.kv_heads * ((rows + tile - 1) / tile);
         int64_t ctas = 1;
         while (ctas < 8 && 2 * ctas <= per_row && 2 * ctas * items <= fit)
             ctas *= 2;
         const int64_t chunk = (per_row + ctas - 1) / ctas, even = items * per_row / fit;
+        if (tile == 8 && 2 * items > 3 * sm_count() && items <= 2 * sm_count() && per_row >= 6) {
+            const int64_t units = (keys + kMany * kUnit - 1) / (kMany * kUnit);
+            if (std::max(units, even + units / 2) <= even + 11)
+                return SplitPlan{1, static_cast<int32_t>(units), 0, true, kMany};
+        }
         if (items >= 2 * fit || std::max(chunk, even + chunk / 2) <= even + (tile == 8 ? 10 : 4))
-            return SplitPlan{static_cast<int32_t>(ctas), static_cast<int32_t>(chunk), 0, true};
+            return SplitPlan{static_cast<int32_t>(ctas), static_cast<int32_t>(chunk), 0, true, kFew};
     }
-    return SplitPlan{static_cast<int32_t>(fit), 0, fit * 2 * tile, false};
+    return SplitPlan{static_cast<int32_t>(fit), 0, fit * 2 * tile, false, kFew};
 }
 
 namespace {
@@ -814,12 +825,12 @@ bool encode_cache_map(CUtensorMap *tm, const void *codes, int head_dim, int page
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kDim, int kRows, int kForm, bool kWithhold = false>
+template <int kDim, int kRows, int kForm, int kWarps = kFew, bool kWithhold = false>
 cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st, uint64_t wait_ns = kWaitNs)
 {
     constexpr int kRing = kWarps * kStages * 2 * kUnit * kDim, kJoin = (kWarps + 1) * kRows * kDim * 4 + kRows * 4;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-    cudaError_t e = allow_shared<rows_kernel<kDim, kRows, kForm, kWithhold>>(kSmem);
+    cudaError_t e = allow_shared<rows_kernel<kDim, kRows, kForm, kWarps, kWithhold>>(kSmem);
     if (e != cudaSuccess)
         return e;
     CUtensorMap k_map, v_map;
@@ -840,7 +851,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
     cudaLaunchAttribute attr[2];
     cfg.gridDim = plan.cluster ? dim3(static_cast<unsigned>(plan.splits * joins), static_cast<unsigned>(a.batch.batch))
                                : dim3(static_cast<unsigned>(plan.splits));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -852,7 +863,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
     }
     if (kForm == kOwn)
         attr[cfg.numAttrs++] = overlap_with_last();
-    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows, kForm, kWithhold>, a, plan, logs, part, k_map, v_map, wait_ns);
+    e = cudaLaunchKernelEx(&cfg, rows_kernel<kDim, kRows, kForm, kWarps, kWithhold>, a, plan, logs, part, k_map, v_map, wait_ns);
     if (e != cudaSuccess || plan.cluster || kWithhold)
         return e;
     // The join may be scheduled while the last CTAs run; it waits for them before it reads what they wrote.
@@ -871,6 +882,10 @@ template <int kForm>
 static cudaError_t run_rows_form(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
 {
     const bool small = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads) <= 8;
+    if constexpr (kForm != kWhole)
+        if (plan.warps == kMany)
+            return a.cache.head_dim == 64 ? run_rows<64, 8, kForm, kMany>(a, plan, logs, part, st)
+                                          : run_rows<128, 8, kForm, kMany>(a, plan, logs, part, st);
     if (a.cache.head_dim == 64)
         return small ? run_rows<64, 8, kForm>(a, plan, logs, part, st) : run_rows<64, 16, kForm>(a, plan, logs, part, st);
     return small ? run_rows<128, 8, kForm>(a, plan, logs, part, st) : run_rows<128, 16, kForm>(a, plan, logs, part, st);
@@ -889,7 +904,7 @@ cudaError_t launch_attention_rows(const AttnArgs &a, Form form, const SplitPlan 
 cudaError_t launch_attention_rows_timeout(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, uint64_t wait_ns,
                                           cudaStream_t st)
 {
-    return run_rows<128, 8, kWhole, true>(a, plan, logs, part, st, wait_ns);
+    return run_rows<128, 8, kWhole, kFew, true>(a, plan, logs, part, st, wait_ns);
 }
 
 cudaError_t read_attention_rows_error(uint32_t *code)

@@ -206,3 +206,31 @@ def test_codes_past_32_bits(h3, new):
         got.append(h3.kv_attention_shared(q, c, prefix, t[:, 2:].contiguous(), _dev([300]), _dev([0, new]), new, 300, return_lse=True))
     for a, b in zip(got[:2], got[2:]):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("batch,kv_heads,dim,window,sinks", [(36, 8, 128, 900, 70), (29, 8, 64, 700, 33), (300, 1, 128, 40, 4_000), (150, 1, 128, 600, 9),
+                                                             (700, 1, 64, 300, 5), (12, 20, 128, 1_500, 1)])
+def test_batches_whose_rows_have_ctas_to_themselves(h3, batch, kv_heads, dim, window, sinks):
+    """Ragged batches of every size about the number of SMs, whose rows go to one CTA each (of four or six warps) or a few:
+    sampled sequences against the definition, all against calls of few sequences."""
+    rng = np.random.default_rng(batch)
+    lengths = [int(n) for n in rng.integers(1, 2_600, batch)]
+    lengths[0], lengths[1] = 2_600, 1
+    page, heads = 32, 2 * kv_heads
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, kv_heads, page, dim)
+    q = torch.randn(batch, heads, dim, generator=torch.Generator().manual_seed(batch)).mul(2).bfloat16().cuda()
+    given = _give_up(table, page, [(1, L) for L in lengths], window, sinks)
+    kw = dict(causal=True, window=window, sinks=sinks)
+    out, lse = _run(h3, q, c, given, lengths, np.arange(batch + 1), 1, **kw)
+    assert h3.h3fp4_device_error() == 0
+    for b in (0, 1, 2, batch // 2, batch - 1):
+        one = _run(h3, q[b:b + 1], c, given[b:b + 1], lengths[b:b + 1], [0, 1], 1, **kw)
+        _check(c, q[b:b + 1], table[b:b + 1], lengths[b:b + 1], [0, 1], out[b:b + 1], lse[b:b + 1], **kw)
+        _check(c, q[b:b + 1], table[b:b + 1], lengths[b:b + 1], [0, 1], *one, **kw)
+    for b in range(0, batch, 5):                       # the rest: two spreads of the same sums, each rounded to bf16 (2^-8)
+        n = min(5, batch - b)
+        few, few_lse = _run(h3, q[b:b + n], c, given[b:b + n], lengths[b:b + n], np.arange(n + 1), 1, **kw)
+        scale = out[b:b + n].float().abs().amax(-1, keepdim=True)
+        assert ((few.float() - out[b:b + n].float()).abs() <= 2.0 ** -7 * scale).all()
+        assert torch.allclose(few_lse, lse[b:b + n], rtol=0, atol=1e-3)
