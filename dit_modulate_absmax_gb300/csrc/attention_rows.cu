@@ -668,18 +668,19 @@ __global__ void __launch_bounds__(kWarps * 32, resident<kDim, kRows, kWarps>())
 constexpr int kJoinThreads = 1024;
 
 // Joins the parts of the rows whose units lie with several CTAs: a CTA for each
-// sequence, row tile and cache head, a thread for 4 channels of a row and every
+// sequence, cache head and kTake rows of a tile, a thread for 4 channels of a row and every
 // kGroups-th part (one long request has as many parts as there are CTAs for a
 // cache head, 57 at 8 of them: one warp a row took 15 us over those).
-template <int kDim, int kRows, int kForm>
+template <int kDim, int kRows, int kForm, int kTake = kRows>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas, const float *ws_log, const float *ws_out)
 {
-    constexpr int kPieces = kRows * kDim / 4;
+    constexpr int kPieces = kTake * kDim / 4;
     constexpr int kGroups = kJoinThreads / kPieces;
     __shared__ float4 means[kGroups][kPieces];
     let_next_start<kForm>();
     const int lane = threadIdx.x & 31, b = blockIdx.y, group = a.heads / a.cache.heads;
     const int kh = blockIdx.x % a.cache.heads, tile = blockIdx.x / a.cache.heads;
+    const int r0 = kTake == kRows ? 0 : blockIdx.z * kTake;   // its first row of the tile
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);   // (not written by the kernel before)
     const Units u = units_of<kRows, kForm, kFew>(a, s);
     int64_t ahead = 0, total = 0;   // units of the sequences before this one, and of all
@@ -707,7 +708,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c0 == c1)
         return;   // nothing, or one CTA had them all and has written the output
-    const int part0 = threadIdx.x / kPieces, piece = threadIdx.x % kPieces, r = piece / (kDim / 4), c = piece % (kDim / 4) * 4;
+    const int part0 = threadIdx.x / kPieces, piece = threadIdx.x % kPieces, r = r0 + piece / (kDim / 4), c = piece % (kDim / 4) * 4;
     const int row_in = tile * kRows + r;
     const bool live = row_in < s.n * group;
     const auto place = [&](int64_t p) { return (p == c0 ? slot0 : p * 2) * kRows + r; };
@@ -744,6 +745,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
     finish_row<kForm>(a, s.row + row_in / group, kh * group + row_in % group, c, log_of_sum(top, sum), mean);
 }
 
+// Rows of a tile that a CTA of the join takes: one or two where those CTAs are
+// half the SMs at most, for one SM is slow to read all parts of a tile (one
+// request, a window of 65,536, 8 cache heads of 4 rows: a CTA a row 33.0 us, a
+// tile 36.1; one cache head of 4 rows 21.5 and 45.5; 8 of 8 rows behind a
+// prefix 22.7, 26.7; 8 of 16 rows, two a CTA 27.9, a tile 32.8, but one a CTA,
+// 128 CTAs, 32.0; 16 tiles of 16, 128 CTAs of two, 40.4 and 38.7).
+int join_rows(int64_t rows, int tile, int64_t items)
+{
+    for (int take = 1; take <= 2; ++take)
+        if (2 * items * ((std::min<int64_t>(rows, tile) + take - 1) / take) <= sm_count())
+            return take;
+    return tile;
+}
+
 }  // namespace
 
 // Two ways to spread the keys.
@@ -761,11 +776,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas
 // goes from one sequence to the next with its copies run dry.  That is taken
 // where there are two items or more for each place, or where what the longest
 // item's CTA has to do is no more than an equal share and 10 units (4 where a
-// CTA has 16 rows, whose units take longer).  In units of 128 keys, an item's
+// CTA has 16 rows, whose units take longer, and 3 with sinks where the join has
+// a CTA for each row).  In units of 128 keys, an item's
 // and an equal share, 128 channels: 32 sequences of 19 and 10.7: 37.5 us,
 // equal shares 42.5; 5 and 2.8: 17 and 26.7; 8 of 5 and 2.7: 17.3 and 21; 200
 // of 5 and 17.5 (four waves): 62 and 149; but 32 of 34 and 19: 64.5 and 59; of
-// 66 and 37: 110 and 74; 4 requests of 32 rows, 16 and 6.7: 48 and 35.
+// 66 and 37: 110 and 74; 4 requests of 32 rows, 16 and 6.7: 48 and 35.  One
+// request, whose rows are joined a row a CTA: an item's 8 and 1.1: 21 and 15;
+// 5 and 0.7: 16.4 and 14.3; 4 and 0.5: 13.4 and 11.9; 2: 10.8 both; but 4
+// requests, 9 and 4.6: 24.1 and 25.5.
 // Items that are more than one and a half for each SM and no more than two get
 // CTAs of six warps, two an SM, which take units of 192 keys: at one to two
 // CTAs an SM a warp's own chain through a unit is what counts (32 sequences of
@@ -788,12 +807,13 @@ SplitPlan plan_rows(const AttnShape &s)
         while (ctas < 8 && 2 * ctas <= per_row && 2 * ctas * items <= fit)
             ctas *= 2;
         const int64_t chunk = (per_row + ctas - 1) / ctas, even = items * per_row / fit;
+        const int64_t margin = tile == 16 ? 4 : s.form == kSinks && join_rows(rows, tile, items) == 1 ? 3 : 10;
         if (tile == 8 && 2 * items > 3 * sm_count() && items <= 2 * sm_count() && per_row >= 6) {
             const int64_t units = (keys + kMany * kUnit - 1) / (kMany * kUnit);
             if (std::max(units, even + units / 2) <= even + 11)
                 return SplitPlan{1, static_cast<int32_t>(units), 0, true, kMany};
         }
-        if (items >= 2 * fit || std::max(chunk, even + chunk / 2) <= even + (tile == 8 ? 10 : 4))
+        if (items >= 2 * fit || std::max(chunk, even + chunk / 2) <= even + margin)
             return SplitPlan{static_cast<int32_t>(ctas), static_cast<int32_t>(chunk), 0, true, kFew};
     }
     return SplitPlan{static_cast<int32_t>(fit), 0, fit * 2 * tile, false, kFew};
@@ -872,7 +892,15 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
     cfg.dynamicSmemBytes = 0;
     attr[0] = overlap_with_last();
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<kDim, kRows, kForm>, a, static_cast<int>(plan.splits), static_cast<const float *>(logs),
+    auto join = join_kernel<kDim, kRows, kForm>;
+    if constexpr (kForm != kWhole) {
+        const int take = join_rows(rows, kRows, joins * a.batch.batch);
+        if (take < kRows) {
+            cfg.gridDim.z = static_cast<unsigned>((std::min<int64_t>(rows, kRows) + take - 1) / take);
+            join = take == 1 ? join_kernel<kDim, kRows, kForm, 1> : join_kernel<kDim, kRows, kForm, 2>;
+        }
+    }
+    return cudaLaunchKernelEx(&cfg, join, a, static_cast<int>(plan.splits), static_cast<const float *>(logs),
                               static_cast<const float *>(part));
 }
 

@@ -234,3 +234,22 @@ def test_batches_whose_rows_have_ctas_to_themselves(h3, batch, kv_heads, dim, wi
         scale = out[b:b + n].float().abs().amax(-1, keepdim=True)
         assert ((few.float() - out[b:b + n].float()).abs() <= 2.0 ** -7 * scale).all()
         assert torch.allclose(few_lse, lse[b:b + n], rtol=0, atol=1e-3)
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,dim,n", [(1, 4, 1, 128, 1), (2, 8, 4, 128, 2), (1, 16, 2, 64, 1), (1, 96, 6, 128, 1), (1, 6, 2, 64, 4),
+                                                        (3, 40, 8, 128, 2)])
+def test_few_rows_over_many_keys_are_joined_from_many_parts(h3, batch, heads, kv_heads, dim, n):
+    """Rows whose parts lie with hundreds of CTAs, joined a row, two rows or a whole tile at a time."""
+    rng = np.random.default_rng(heads)
+    lengths = [int(x) for x in rng.integers(14_000, 17_000, batch)]
+    page = 64
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, kv_heads, page, dim)
+    q = torch.randn(batch * n, heads, dim, generator=torch.Generator().manual_seed(heads)).mul(2).bfloat16().cuda()
+    window, sinks = 9_000, 130
+    given = _give_up(table, page, [(n, L) for L in lengths], window, sinks)
+    kw = dict(causal=True, window=window, sinks=sinks)
+    cu = np.arange(batch + 1) * n
+    out, lse = _run(h3, q, c, given, lengths, cu, n, **kw)
+    assert h3.h3fp4_device_error() == 0
+    _check(c, q, table, lengths, cu, out, lse, **kw)
