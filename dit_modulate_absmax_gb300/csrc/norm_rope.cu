@@ -27,6 +27,7 @@
 // tokens 212 us, the other two ways 176.  All in a graph of 10 passes.
 #include <cuda_bf16.h>
 
+#include "norm_exchange.h"
 #include "norm_rope.cuh"
 #include "rope.cuh"
 
@@ -154,7 +155,7 @@ struct __align__(16) Tables {
     float2 cs[kWarps][(kEach ? 16 : 8) * kLanes];
     float weight[kEach ? 4 : 2][16 * kLanes];   // of queries and keys, then those of each channel's partner
     float2 turns[8 * kLanes];                   // FP64 is slow here: once a pair, not once a pair and token
-    uint32_t swap[kEach ? kWarps : 1][kEach ? 280 : 4];
+    uint32_t swap[kEach ? kWarps : 1][kEach ? kExchangeWords : 4];
     ushort2 members[kEach ? 8 * kLanes : 1];    // a pair's channels
     uint16_t partner[kEach ? 16 * kLanes : 2];  // a channel's (itself where it does not turn)
 };
@@ -250,15 +251,6 @@ __device__ __forceinline__ int2 facing_place(const RopeArgs &r, int c)
         return make_int2((r.pairs >> 3) + ((c - 2 * r.pairs) >> 4), (c - 2 * r.pairs) >> 3 & 1);
     const RopeChannel ch = rope_channel(r, c);
     return make_int2(ch.pair >> 3, ch.first ? 0 : 1);
-}
-
-// Word of a channel in the warp's exchange buffer: heads one after another, moved so that the lanes' words, four apart, fall
-// into different banks.
-template <int kLanes>
-__device__ __forceinline__ int exchange_at(int sub, int channel)
-{
-    const int w = channel >> 1;
-    return sub * (8 * kLanes) + w + (kLanes == 16 ? 2 * (w >> 5) : 0) + (sub & 3) + (kLanes == 4 ? 16 * (sub >> 2) : 0);
 }
 
 // A lane's place: its two chunks (either may be none), and with kExchanged where each channel's partner stands in the warp's

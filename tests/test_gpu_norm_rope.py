@@ -282,3 +282,37 @@ def test_offsets_past_32_bits(h3):
     h3.norm_rope(wide[:, :1], q_weight=w, rope=h3.Rope(pos, freqs, (128,)), q_out=wide[:, :1])
     want = h3.norm_rope(tail[:, :1], q_weight=w, rope=h3.Rope(pos[-5:], freqs, (128,)))[0]
     assert torch.equal(wide[-5:, :1], want) and torch.equal(wide[-5:, 1:], tail[:, 1:])
+
+
+@pytest.mark.parametrize("tokens,hq,hk,dim,dims,wide", [
+    (5, 4, 3, 256, (88, 84, 84), 0),            # sections that are not whole chunks, over all of the widest head
+    (7, 5, 2, 256, (10, 246), 1),
+    (6, 7, 4, 256, (10, 30, 208), 0),
+    (9, 3, 0, 256, (120,), 0),                  # and over a part of it
+    (8, 9, 5, 256, (254,), None),
+    (4, 6, 3, 248, (248,), 1),
+    (5, 3, 4, 248, (82, 82, 84), 0),
+    (61, 11, 7, 240, (120, 120), 0),
+    (5, 5, 3, 136, (12, 124), 1),
+    (9, 13, 5, 128, (10, 118), 0),              # the widest of eight lanes, and of four
+    (9, 17, 9, 64, (10, 54), 1),
+    (700, 8, 3, 256, (88, 84, 84), 1),
+])
+def test_widest_heads_in_halves_of_uneven_sections(h3, tokens, hq, hk, dim, dims, wide):
+    """Forward and backward, then in place in a projection's rows: each head of a warp keeps its own words while they are
+    exchanged."""
+    rows, rope = _normal((tokens, hq + hk + 1, dim), tokens + hq, 1.5), _rope(h3, tokens, dims, "halves", 3)
+    q, k = rows[:, :hq], rows[:, hq:hq + hk] if hk else None
+    wq, wk = [None if wide is None else _weight(dim, wide, i) for i in (1, 2)]
+    wk = wk if hk else None
+    gq, gk = _normal(q.shape, 5, 0.1), _normal(k.shape, 6, 0.1) if hk else None
+    kw = dict(q_weight=wq, k_weight=wk, rope=rope, eps=EPS)
+    out, back = h3.norm_rope(q, k, **kw), h3.norm_rope_backward(gq, gk, q, k, **kw)
+    for x, w, y, g, dx, dw in ((q, wq, out[0], gq, back[0], back[2]), (k, wk, out[1], gk, back[1], back[3])):
+        if x is not None:
+            _check_forward(x, w, rope, y)
+            _check_backward(g, x, w, rope, dx, dw)
+    over = h3.norm_rope_backward(gq, gk, q, k, q_out=gq, k_out=gk, **kw)
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(over, back))
+    h3.norm_rope(q, k, q_out=q, k_out=k, **kw)
+    assert torch.equal(q, out[0]) and (k is None or torch.equal(k, out[1]))
