@@ -84,6 +84,13 @@ __device__ __forceinline__ Span seen_by(const AttnArgs &a, const KvSequence &s, 
     return r;
 }
 
+// Whether a sequence's rows, length and pages are within the arrays.  (A cache without pages has no arrays either: nothing of
+// it may be read.)
+__device__ __forceinline__ bool in_range(const AttnArgs &a, const KvSequence &s)
+{
+    return s.ok && s.len <= a.max_kv && (s.len <= 0 || ((s.len - 1) / a.cache.page_size < a.batch.ld_table && a.cache.num_pages != 0));
+}
+
 template <int kForm>
 __device__ __forceinline__ bool seen(const AttnArgs &a, const Span &s, int tok)
 {
@@ -207,6 +214,23 @@ __device__ __forceinline__ Shares shares_of(float own_log, float prefix_log)
     return Shares{half_of_top(own_log, top), half_of_top(prefix_log, top), reciprocal_sum(total), log_of_sum(top, total)};
 }
 
+// In place of the logarithm of a row whose group is out of range: a NaN that arithmetic does not make.  Such rows are left as
+// they were, as those of a sequence that is.
+constexpr uint32_t kRefusedLog = 0x7FBADBADu;
+
+__device__ __forceinline__ bool refused(float log) { return __float_as_uint(log) == kRefusedLog; }
+
+// Says so of a group's rows, as far as they lie in the arrays.  All threads of a CTA.
+template <int kForm>
+__device__ __forceinline__ void refuse_rows(const AttnArgs &a, const KvSequence &s)
+{
+    if (kForm != kPrefix)
+        return;
+    const int64_t first = s.row > 0 ? s.row : 0, end = min(s.row + s.n, a.tokens) * a.heads;
+    for (int64_t i = first * a.heads + threadIdx.x; i < end; i += blockDim.x)
+        a.half_log[i] = __uint_as_float(kRefusedLog);
+}
+
 // log2 of the sum of a row's prefix half; minus infinity for a row of no group.
 __device__ __forceinline__ float prefix_log(const AttnArgs &a, int64_t row, int head)
 {
@@ -232,6 +256,8 @@ __device__ __forceinline__ void finish_row(const AttnArgs &a, int64_t row, int h
     }
     if (kForm == kOwn) {
         const float other = prefix_log(a, row, head);
+        if (refused(other))
+            return;
         const Shares s = shares_of(log, other);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (other != -INFINITY)

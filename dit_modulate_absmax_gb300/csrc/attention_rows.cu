@@ -94,9 +94,8 @@ struct Units {
 template <int kRows, int kForm, int kWarps>
 __device__ __forceinline__ Units units_of(const AttnArgs &a, const KvSequence &s)
 {
-    if (!s.ok || s.n == 0 || s.len > a.max_kv ||
-        (s.len > 0 && ((s.len - 1) / a.cache.page_size >= a.batch.ld_table || a.cache.num_pages == 0)))
-        return Units{0, 0, 0, {0, 0}};   // (a cache without pages has no arrays either: nothing of it may be read)
+    if (s.n == 0 || !in_range(a, s))
+        return Units{0, 0, 0, {0, 0}};
     const Span first = seen_by(a, s, 0), last = seen_by(a, s, s.n - 1);
     const int lo = min(first.lo, last.lo), hi = max(first.hi, last.hi);
     const Fold f = fold<kForm>(a, lo, hi, max(kUnit, a.cache.page_size));
@@ -158,12 +157,15 @@ __global__ void __launch_bounds__(kWarps * 32, resident<kDim, kRows, kWarps>())
     int64_t mine_lo = 0, mine_hi = 0;
     if (!plan.cluster) {
         int64_t mine = 0;
+        bool bad = false;
         for (int b = threadIdx.x * share; b < min(a.batch.batch, (static_cast<int>(threadIdx.x) + 1) * share); ++b) {
             const KvSequence s = kv_sequence(a.batch, b, a.tokens);
             const Units u = units_of<kRows, kForm, kWarps>(a, s);
             mine += static_cast<int64_t>(u.count) * u.tiles * heads;
-            if (u.count == 0 && s.n != 0 && blockIdx.x == 0)
+            if (u.count == 0 && s.n != 0 && blockIdx.x == 0) {
+                bad = true;
                 atomicOr(&g_error, ERR_KV_RANGE);
+            }
         }
         mine_hi = mine;
 #pragma unroll
@@ -173,7 +175,15 @@ __global__ void __launch_bounds__(kWarps * 32, resident<kDim, kRows, kWarps>())
         }
         if (lane == 31)
             warp_units[warp] = mine_hi;
-        __syncthreads();
+        if constexpr (kForm != kPrefix) {
+            __syncthreads();
+        } else if (__syncthreads_or(bad)) {   // in the first CTA
+            for (int b = 0; b < a.batch.batch; ++b) {
+                const KvSequence s = kv_sequence(a.batch, b, a.tokens);
+                if (s.n != 0 && units_of<kRows, kForm, kWarps>(a, s).count == 0)
+                    refuse_rows<kForm>(a, s);
+            }
+        }
         int64_t total = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -208,6 +218,8 @@ __global__ void __launch_bounds__(kWarps * 32, resident<kDim, kRows, kWarps>())
         if (u.count == 0 || tile >= u.tiles) {   // the same in the whole cluster
             if (u.count == 0 && s.n != 0 && threadIdx.x == 0)
                 atomicOr(&g_error, ERR_KV_RANGE);
+            if (u.count == 0 && blockIdx.x == 0)
+                refuse_rows<kForm>(a, s);
             after_prefix<kForm>();
             return;
         }

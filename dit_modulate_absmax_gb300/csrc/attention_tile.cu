@@ -185,9 +185,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         after_prefix<kForm>();
         return;   // without queries its length and pages are not looked at
     }
-    if (!s.ok || s.len > a.max_kv || (s.len > 0 && ((s.len - 1) / page >= a.batch.ld_table || a.cache.num_pages == 0))) {
+    if (!in_range(a, s)) {
         if (threadIdx.x == 0)
             atomicOr(&g_error, ERR_KV_RANGE);
+        if (tile == 0 && kh == 0 && split == 0)
+            refuse_rows<kForm>(a, s);
         after_prefix<kForm>();
         return;
     }
@@ -531,13 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool final = plan.splits == 1;
                 const float inv = reciprocal_sum(l) * o_factor;
                 Shares share{};
-                bool other_half = false;
+                bool other_half = false, written = live;
                 if (kForm == kOwn && final) {
                     after_prefix<kForm>();
                     const float other = live ? prefix_log(a, row, head) : -INFINITY;
                     other_half = other != -INFINITY;   // (else its mean may be anything)
                     share = shares_of(log_of_sum(ref, l), other);
+                    written = live && !refused(other);
                 }
+                const uint32_t rows_written = kForm == kOwn ? __ballot_sync(0xFFFFFFFFu, written) : 0;
                 // Rows are written through shared memory in whole sectors, or, where that gains nothing, straight from the
                 // threads that hold them (128 channels: 1,560 tokens over as many keys 5,700 cycles a CTA, 7,000 straight; 64
                 // channels, ragged prompts: 99.2 us, 97.5 straight; with sinks, a chunk: 3,105 us, 3,055).
@@ -553,15 +557,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *to[8];
                 if constexpr (kStaged) {   // of this lane's pieces
                     RowWalk at_row(row0 + 32 * warp + lane / pieces, 32 / pieces, group);
-                    const int last_row = min(rows, row0 + 32 * warp + 32);
+                    const int first_row = row0 + 32 * warp, last_row = min(rows, first_row + 32);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        to[i] = at_row.row < last_row ? place_of(s.row + at_row.token, kh * group + at_row.head) + 16 * (lane & (pieces - 1))
-                                                      : nullptr;
+                        bool mine = at_row.row < last_row;
+                        if (kForm == kOwn)
+                            mine = mine && (rows_written >> (at_row.row - first_row) & 1) != 0;
+                        to[i] = mine ? place_of(s.row + at_row.token, kh * group + at_row.head) + 16 * (lane & (pieces - 1)) : nullptr;
                         at_row.step();
                     }
                 } else {
-                    to[0] = live ? place_of(row, head) : nullptr;
+                    to[0] = written ? place_of(row, head) : nullptr;
                 }
 #pragma unroll 1
                 for (int c = 0; c < kDim / 32; ++c) {
@@ -629,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (to[i] != nullptr)
                                 *reinterpret_cast<uint4 *>(to[i] + c * (16 * pieces)) =
                                     ld_shared_v4(at_piece(lane / pieces + i * (32 / pieces), lane & (pieces - 1)));
-                    } else if (live && narrow) {
+                    } else if (written && narrow) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             *reinterpret_cast<uint4 *>(to[0] + 64 * c + 16 * i) = bf16_piece(i);
-                    } else if (live) {
+                    } else if (written) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             *reinterpret_cast<uint4 *>(to[0] + 128 * c + 16 * i) = float_piece(i);
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ws_stat[at * plan.splits + split] = make_float2(ref, l);
                 else if (live && kForm == kPrefix)
                     a.half_log[at] = log_of_sum(ref, l);
-                else if (live && a.lse != nullptr)
+                else if (written && a.lse != nullptr)
                     a.lse[at] = (kForm == kOwn ? share.log : log_of_sum(ref, l)) * kLn2;
                 tc_fence_before();
             }
@@ -858,7 +864,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int64_t w = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
     const KvSequence s = kv_sequence(a.batch, b, a.tokens);
-    if (!s.ok || s.len > a.max_kv || w >= static_cast<int64_t>(s.n) * a.heads)
+    if (!in_range(a, s) || w >= static_cast<int64_t>(s.n) * a.heads)
         return;
     const int64_t row = s.row + w / a.heads;
     const int head = static_cast<int>(w % a.heads);
@@ -894,6 +900,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, SplitPla
     float log = log_of_sum(top, sum);
     if (kForm == kOwn) {
         const float other = prefix_log(a, row, head);
+        if (refused(other))
+            return;
         const Shares share = shares_of(log, other);
         const float *half = a.half_mean + at * kDim + lane * kPer;
 #pragma unroll

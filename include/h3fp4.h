@@ -534,7 +534,8 @@ H3FP4_API h3fp4_status h3fp4_kv_attention_sinks(const void *q_bf16, int64_t q_to
  * what it sees of its own keys, out and lse as for h3fp4_kv_attention; tokens
  * of no group have no prefix, groups may be empty, and prefixes too.  The two
  * halves are joined from FP32 means and logarithms.  Rows outside the
- * sequences are left as they were.
+ * sequences are left as they were, and so are those of a group whose length or
+ * rows are out of range (or of a sequence's): reported, joined to nothing.
  *
  *   prefix      batch: the groups; max_tokens: the most tokens of a group
  *   max_prefix  the most keys of a prefix; at most 2^30

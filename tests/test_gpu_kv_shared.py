@@ -181,3 +181,43 @@ def test_nothing_before_or_nothing_own(h3, new, batch):
         out, lse = _call(h3, c, q, own, shared, groups, seqs, cu, p_cu)
         assert h3.h3fp4_device_error() == 0
         _check(c, q, own, shared, groups, seqs, cu, first, out, lse, False)
+
+
+@pytest.mark.parametrize("new,batch,own,dim", [(1, 6, 40, 128), (1, 70, 90, 128), (1, 6, 3_000, 64), (1, 30, 2_000, 128), (90, 6, 120, 128),
+                                               (90, 6, 120, 64), (300, 4, 700, 128), (3, 12, 50, 64)])
+def test_rows_of_a_refused_group_stay_as_they_were(h3, new, batch, own, dim):
+    """One group of three is out of range, in each way that its lengths and rows can be: its rows are neither written nor
+    joined to anything, and the others' are right."""
+    few = max(1, batch // 6)
+    sizes = [few, batch - 2 * few, few]
+    groups, seqs = [(200, n) for n in sizes], [(new, own + b) for b in range(batch)]
+    heads = 4
+    c, q, table, shared, cu, p_cu, first = _setup(h3, batch + own, groups, seqs, heads, 2, dim, 16)
+    kv, vv = [O.cache_values(t.cpu().numpy(), s.cpu().numpy()) for t, s in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale))]
+    qv, most = O.bf16_values(_patterns(q)), int(np.diff(p_cu).max())
+    args = _dev(table), _dev([L for _, L in seqs]), _dev(cu), new, own + batch - 1
+    past = p_cu.copy()
+    past[-1] = q.shape[0] + 1
+    for refused, lens, rows, most_rows, most_keys in (
+            (None, [200] * 3, p_cu, most, 10_000),
+            (0, [-1, 200, 200], p_cu, most, 200),
+            (1, [200, 201, 200], p_cu, most, 200),
+            (2, [200, 200, 16 * shared.shape[1] + 1], p_cu, most, 10_000),      # past the table
+            (1, [200] * 3, p_cu, most - 1, 200),                # more rows than said
+            (2, [200] * 3, past, most + 9, 200)):               # rows past the arrays
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(q.shape[:2], 5.0, device="cuda")
+        prefix = h3.SharedPrefix(_dev(shared), _dev(lens), _dev(rows), most_rows, most_keys)
+        need = h3.h3fp4_kv_attention_shared_workspace(q.shape[0], heads, 2, dim, 3, most_rows, most_keys, batch, new, own + batch - 1)
+        ws = torch.full((need,), 0x40, dtype=torch.uint8, device="cuda")        # (what scratch held: 3.0 in every place)
+        h3.kv_attention_shared(q, c, prefix, *args, causal=True, out=out, lse=lse, workspace=ws)
+        assert h3.h3fp4_device_error() == (0 if refused is None else 512)
+        got, gl = O.bf16_values(_patterns(out)), lse.cpu().numpy()
+        for b in range(batch):
+            g, at = int(np.searchsorted(first, b, side="right")) - 1, slice(int(cu[b]), int(cu[b + 1]))
+            if g == refused:
+                assert (got[at] == 7).all() and (gl[at] == 5).all(), (refused, b)
+            elif b % max(1, batch // 6) == 0:
+                k, v = [np.concatenate([O.gather(x, shared[g], 200), O.gather(x, table[b], own + b)]) for x in (kv, vv)]
+                check_rows(qv[at], k, v, got[at], gl[at], dim ** -0.5, 200 + own + b, causal=True, before=200)
+        assert (out[cu[-1]:] == 7).all() and (lse[cu[-1]:] == 5).all()

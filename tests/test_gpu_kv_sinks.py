@@ -253,3 +253,26 @@ def test_few_rows_over_many_keys_are_joined_from_many_parts(h3, batch, heads, kv
     out, lse = _run(h3, q, c, given, lengths, cu, n, **kw)
     assert h3.h3fp4_device_error() == 0
     _check(c, q, table, lengths, cu, out, lse, **kw)
+
+
+@pytest.mark.parametrize("new,heads", [(1, 4), (1, 32), (20, 4), (140, 4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (2_000, 0), (1_500, 70)])
+def test_rows_of_a_refused_sequence_stay_as_they_were(h3, new, heads, window, sinks):
+    """The middle one of three, whose pages or keys are past what was said, also where the parts of its keys would be joined."""
+    rng = np.random.default_rng(new)
+    page, lengths = 32, [2_900, 2_800, 2_700]
+    table, pages = _tables(rng, lengths, page)
+    c = _filled(h3, rng, table, lengths, pages, 2, page, 128)
+    q = torch.randn(3 * new, heads, 128, generator=torch.Generator().manual_seed(new)).mul(2).bfloat16().cuda()
+    cu, kw = np.arange(4) * new, dict(causal=True, window=window, sinks=sinks)
+    for keys, most in ((page * table.shape[1] + 1, 20_000), (20_001, 20_000), (-1, 20_000)):
+        out, lse = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda"), torch.full(q.shape[:2], 5.0, device="cuda")
+        need = h3.h3fp4_kv_attention_workspace(3 * new, heads, 2, 128, 3, new, most)
+        ws = torch.full((max(16, need),), 0x40, dtype=torch.uint8, device="cuda")
+        given = [lengths[0], keys, lengths[2]]
+        h3.kv_attention(q, c, _dev(table), _dev(given), _dev(cu), new, most, out=out, lse=lse, workspace=ws, **kw)
+        assert h3.h3fp4_device_error() == 512
+        assert (out[new:2 * new] == 7).all() and (lse[new:2 * new] == 5).all()
+        for b in (0, 2) if keys < 0 else ():
+            at = slice(b * new, b * new + new)
+            _check(c, q[at], table[b:b + 1], lengths[b:b + 1], [0, new], out[at], lse[at], **kw)
