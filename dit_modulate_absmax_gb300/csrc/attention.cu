@@ -2,6 +2,8 @@
 // workspace.
 #include "attention.cuh"
 
+#include <algorithm>
+
 namespace h3fp4 {
 namespace {
 
@@ -17,7 +19,7 @@ bool few_rows(const AttnShape &s) { return static_cast<int64_t>(s.max_tokens) * 
 
 AttnShape shape_of(const AttnArgs &a, Form form = kWhole)
 {
-    return AttnShape{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, a.batch.max_tokens, a.max_kv,
+    return AttnShape{a.tokens, a.heads, a.cache.heads, a.cache.head_dim, a.batch.batch, most_rows(a.batch), a.max_kv,
                      a.causal || a.sinks > 0 ? a.window : 0, a.sinks, a.causal, form};
 }
 
@@ -50,19 +52,21 @@ cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st
 // are joined).
 static int64_t halves_bytes(const AttnShape &s) { return (s.tokens * s.heads * (4 * int64_t(s.head_dim) + 4) + 15) & ~int64_t(15); }
 
-int64_t attention_shared_workspace(const AttnShape &prefix, const AttnShape &own)
+int64_t attention_shared_workspace(const AttnShape &groups, const AttnShape &own)
 {
+    AttnShape prefix = groups;
+    prefix.max_tokens = std::max(1, groups.max_tokens);   // as most_rows has it
     const int64_t a = attention_workspace(prefix), b = attention_workspace(own);
     if (a < 0 || b < 0 || own.tokens > (int64_t(1) << 50) / own.heads)
         return -1;
-    if (prefix.batch == 0 || prefix.max_tokens == 0)
+    if (prefix.batch == 0)
         return b;   // no groups: the sequences' own keys are all
     return halves_bytes(own) + ((a + 15) & ~int64_t(15)) + b;
 }
 
 cudaError_t launch_attention_shared(const AttnArgs &prefix, const AttnArgs &own, void *workspace, cudaStream_t st)
 {
-    if (prefix.batch.batch == 0 || prefix.batch.max_tokens == 0)
+    if (prefix.batch.batch == 0)
         return launch_form(own, kWhole, workspace, st);
     const AttnShape s = shape_of(own);
     AttnArgs first = prefix, second = own;

@@ -306,6 +306,10 @@ inline cudaLaunchAttribute overlap_with_last()
     return a;
 }
 
+// Most tokens of a sequence for which a call is launched: groups that are all to be empty are looked at all the same, for one
+// that is not is out of range.
+inline int32_t most_rows(const KvBatch &b) { return b.max_tokens > 1 ? b.max_tokens : 1; }
+
 // Most keys that a window of s.reach and s.sinks leave to rows of `tokens` neighbouring queries, folded in steps of up to 128.
 inline int64_t folded_keys(const AttnShape &s, int64_t tokens)
 {

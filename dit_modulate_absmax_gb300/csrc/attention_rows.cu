@@ -875,7 +875,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
                !encode_cache_map(&v_map, a.cache.v_codes, kDim, a.cache.page_size, blocks, box)) {
         return cudaErrorInvalidValue;
     }
-    const int64_t rows = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads);
+    const int64_t rows = static_cast<int64_t>(most_rows(a.batch)) * (a.heads / a.cache.heads);
     const int64_t joins = (rows + kRows - 1) / kRows * a.cache.heads;
     if (plan.splits * joins > INT32_MAX)
         return cudaErrorInvalidValue;
@@ -921,7 +921,7 @@ cudaError_t run_rows(const AttnArgs &a, const SplitPlan &plan, float *logs, floa
 template <int kForm>
 static cudaError_t run_rows_form(const AttnArgs &a, const SplitPlan &plan, float *logs, float *part, cudaStream_t st)
 {
-    const bool small = static_cast<int64_t>(a.batch.max_tokens) * (a.heads / a.cache.heads) <= 8;
+    const bool small = static_cast<int64_t>(most_rows(a.batch)) * (a.heads / a.cache.heads) <= 8;
     if constexpr (kForm != kWhole)
         if (plan.warps == kMany)
             return a.cache.head_dim == 64 ? run_rows<64, 8, kForm, kMany>(a, plan, logs, part, st)

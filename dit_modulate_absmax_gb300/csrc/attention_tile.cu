@@ -954,7 +954,7 @@ cudaError_t run_tile(const AttnArgs &a, const SplitPlan &plan, float2 *stat, flo
     }();
     if (!registers_fit)
         return cudaErrorLaunchOutOfResources;
-    const int64_t most = std::min<int64_t>(a.batch.max_tokens, a.tokens);   // of a sequence
+    const int64_t most = std::min<int64_t>(most_rows(a.batch), a.tokens);   // of a sequence
     const int64_t tiles = (most * (a.heads / a.cache.heads) + kTiles * 128 - 1) / (kTiles * 128), x = tiles * a.cache.heads * plan.splits * a.batch.batch;
     if (x > INT32_MAX || tiles * (kTiles * 128) > INT32_MAX)
         return cudaErrorInvalidValue;
@@ -1009,7 +1009,7 @@ static cudaError_t run_tile_form(const AttnArgs &a, const SplitPlan &plan, float
     if (e != cudaSuccess || plan.splits == 1)
         return e;
     constexpr int kJoinWarps = kJoinThreads / 32;
-    const int64_t x = (std::min<int64_t>(a.batch.max_tokens, a.tokens) * a.heads + kJoinWarps - 1) / kJoinWarps;
+    const int64_t x = (std::min<int64_t>(most_rows(a.batch), a.tokens) * a.heads + kJoinWarps - 1) / kJoinWarps;
     if (x > INT32_MAX)
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg{};

@@ -149,7 +149,7 @@ int64_t attention_workspace(const AttnShape &s);
 cudaError_t launch_attention(const AttnArgs &a, void *workspace, cudaStream_t st);
 
 // Attention over prefixes that groups of sequences share, then over the sequences' own keys, joined.
-int64_t attention_shared_workspace(const AttnShape &prefix, const AttnShape &own);
+int64_t attention_shared_workspace(const AttnShape &groups, const AttnShape &own);
 cudaError_t launch_attention_shared(const AttnArgs &prefix, const AttnArgs &own, void *workspace, cudaStream_t st);
 
 // Failure detection: few queries with copies that never complete.

@@ -221,3 +221,29 @@ def test_rows_of_a_refused_group_stay_as_they_were(h3, new, batch, own, dim):
                 k, v = [np.concatenate([O.gather(x, shared[g], 200), O.gather(x, table[b], own + b)]) for x in (kv, vv)]
                 check_rows(qv[at], k, v, got[at], gl[at], dim ** -0.5, 200 + own + b, causal=True, before=200)
         assert (out[cu[-1]:] == 7).all() and (lse[cu[-1]:] == 5).all()
+
+
+@pytest.mark.parametrize("new,heads", [(1, 4), (40, 4), (3, 64)])
+def test_groups_said_to_be_empty(h3, new, heads):
+    """The most rows of a group given as 0: right where all groups are empty, and where one is not its rows are out of range."""
+    groups, seqs = [(200, 1)] * 3, [(new, 50 + b) for b in range(3)]
+    c, q, own, shared, cu, p_cu, first = _setup(h3, new, groups, seqs, heads, 2, 128, 32)
+    args = _dev(own), _dev([L for _, L in seqs]), _dev(cu), new, 52
+    want = h3.kv_attention(q, c, *args, causal=True, return_lse=True)
+    n = int(cu[-1])
+    for rows, refused in (([0, 0, 0, 0], None), ([n, n, n, n], None), ([0, 0, new, new], 0), (p_cu, slice(None))):
+        out, lse = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda"), torch.full(q.shape[:2], 5.0, device="cuda")
+        prefix = h3.SharedPrefix(_dev(shared), _dev([200] * 3), _dev(rows), 0, 200)
+        h3.kv_attention_shared(q, c, prefix, *args, causal=True, out=out, lse=lse)
+        assert h3.h3fp4_device_error() == (0 if refused is None else 512)
+        gone = torch.zeros(3, dtype=torch.bool)
+        if refused is not None:
+            gone[refused] = True
+        for b in range(3):
+            at = slice(b * new, b * new + new)
+            if gone[b]:
+                assert (out[at] == 7).all() and (lse[at] == 5).all()
+            else:
+                check = [[(0, 0)] * 3, [seqs[b]], cu[b:b + 2] - cu[b], [0, 0, 0, 0]]
+                _check(c, q[at], own[b:b + 1], shared, *check, out[at], lse[at], True)
+                assert (out[at].float() - want[0][at].float()).abs().max() <= 2.0 ** -7 * want[0][at].float().abs().max()
