@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(h3fp4_kv_requests q, i
         }
         if (blockIdx.y == 0 && threadIdx.x == 0) {
             q.cu_tokens[0] = 0;
-            const int64_t left = max(0, q.num_free - max(free_at, 0));
+            const int64_t left = max(static_cast<int64_t>(q.num_free) - free_at, static_cast<int64_t>(0));   // (places before the list too)
             *q.free_at_out = static_cast<int>(free_at + min(pages_all, left));
             if (tokens_all > INT32_MAX || (q.slots != nullptr || q.positions != nullptr ? tokens_all > q.tokens : false))
                 error |= ERR_KV_RANGE;

@@ -575,8 +575,9 @@ H3FP4_API int64_t h3fp4_kv_attention_shared_workspace(int64_t tokens, int32_t he
  *
  * Reported as bit 512 of h3fp4_device_error: a sequence whose held or count is
  * negative, whose count is more than max_tokens or whose pages are more than
- * ld_table (it gets nothing: no tokens, kv_len 0); a free list that runs out,
- * or a page number outside [0, num_pages) in it or in the entry of a page that
+ * ld_table (it gets nothing: no tokens, kv_len 0); a free list that runs out
+ * or whose place is negative (what lies outside it counts as taken up to its
+ * end, so that no page is taken twice), or a page number outside [0, num_pages) in it or in the entry of a page that
  * the sequence has begun (the table gets -1 for it, unless it was there; the
  * tokens' slots are -1); more tokens than the rows of slots (those are not
  * written; cu_tokens stops at 2^31 - 1).

@@ -188,5 +188,5 @@ def kv_tables(held, count, table, free, free_at, page, pages, tokens, most):
         kv.append(h + n)
     bad |= len(slots) > tokens
     behind = [-1] * (tokens - len(slots))
-    taken = min(at - int(free_at), max(0, len(free) - max(int(free_at), 0)))
+    taken = min(at - int(free_at), max(0, len(free) - int(free_at)))     # a place before the list is passed like any other
     return cu, kv, (slots + behind)[:tokens], (positions + behind)[:tokens], table, int(free_at) + taken, bad

@@ -140,3 +140,21 @@ def test_streams_outputs_given_and_graphs(h3):
         assert got.cu_tokens.tolist() == want[0] and got.kv_len.tolist() == want[1] and got.slots.tolist() == want[2]
         assert got.positions.tolist() == want[3] and np.array_equal(dev[2].cpu().numpy(), want[4]) and out_at.item() == want[5]
     assert h3.h3fp4_device_error() == 0
+
+
+@pytest.mark.parametrize("free_at,wanted", [(-2, 10), (-2, 6), (-2, 2), (-2 ** 31, 10), (3, 10), (5, 1), (7, 2), (2 ** 31 - 1, 2)])
+def test_no_page_is_taken_twice_whatever_the_place_in_the_list(h3, free_at, wanted):
+    """A list of five pages taken from twice in a row, from before its beginning, past its end, and to its end."""
+    free, page, at = np.array([5, 6, 7, 8, 9]), 16, free_at
+    given = []
+    for _ in range(2):
+        table = np.full((1, wanted), -9)
+        want = O.kv_tables([0], [wanted * page], table, free, at, page, 20, wanted * page, wanted * page)
+        tab = _dev(table)
+        got = h3.kv_tables(_dev([0]), _dev([wanted * page]), tab, _dev(free), _dev([at]), page, 20, wanted * page, wanted * page)
+        assert np.array_equal(tab.cpu().numpy(), want[4]) and got.slots.tolist() == want[2]
+        at = got.free_at.item()
+        assert at == want[5] and free_at <= at <= max(5, free_at)
+        assert h3.h3fp4_device_error() == (512 if want[6] else 0)
+        given += [int(p) for p in tab.cpu().numpy()[0] if p >= 0]
+    assert len(set(given)) == len(given)
