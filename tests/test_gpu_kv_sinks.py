@@ -276,3 +276,53 @@ def test_rows_of_a_refused_sequence_stay_as_they_were(h3, new, heads, window, si
         for b in (0, 2) if keys < 0 else ():
             at = slice(b * new, b * new + new)
             _check(c, q[at], table[b:b + 1], lengths[b:b + 1], [0, new], out[at], lse[at], **kw)
+
+
+def _filled_on_gpu(h3, table, lengths, pages, heads, page, dim, seed):
+    """As _filled: NaN wherever no sequence has a token."""
+    c, gen = h3.KVCache.empty(pages, page, heads, dim), torch.Generator(device="cuda").manual_seed(seed)
+    used = np.zeros((pages, page), dtype=bool)
+    for b, n in enumerate(lengths):
+        used[table[b, np.arange(n) // page], np.arange(n) % page] = True
+    for codes, scale in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale)):
+        x = torch.randn(codes.shape, generator=gen, device="cuda").mul(40).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        codes.copy_(torch.where(torch.from_numpy(used).cuda()[:, None, :, None], x, torch.full_like(x, 0x7F)))
+        scale.copy_(torch.exp2(torch.randint(-6, -4, scale.shape, generator=gen, device="cuda").float()))
+    return c
+
+
+def _all_within_bounds(c, q, table, lengths, out, lse, window, sinks):
+    """check_rows' bounds for every sequence of one token each, the definition evaluated on the GPU in 64 bits."""
+    heads, dim = q.shape[1:]
+    group, page = heads // c.heads, c.page_size
+    for b, L in enumerate(lengths):
+        pos = torch.arange(L, device="cuda")
+        pos = pos[(pos > L - 1 - window) | (pos < sinks)]
+        ids = _dev(table[b], torch.int64)[pos // page]
+        k, v = [(x[ids, :, pos % page].view(torch.float8_e4m3fn).double() * s[ids][..., None].double()).repeat_interleave(group, 1)
+                for x, s in ((c.k_codes, c.k_scale), (c.v_codes, c.v_scale))]
+        mine = q[b].double()
+        score = (mine * k).sum(2) * dim ** -0.5
+        size = (mine * k).abs().sum(2).amax(0) * dim ** -0.5
+        log, p = torch.logsumexp(score, 0), torch.softmax(score, 0)
+        e = 2.0 ** -17 * size
+        assert ((lse[b].double() - log).abs() <= e + 2.0 ** -20 * (1 + log.abs())).all(), b
+        part = p[:, :, None] * v
+        ref, near, top = part.sum(0), part.abs().sum(0), part.abs().amax(0)
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 4 * e[:, None]) * near + L * 2.0 ** -22 * top + 1e-38
+        assert ((out[b].double() - ref).abs() <= tol).all(), b
+
+
+@pytest.mark.parametrize("batch,kv_heads,dim,window,sinks", [(36, 8, 128, 900, 70), (29, 8, 64, 700, 33), (300, 1, 128, 40, 4_000), (150, 1, 128, 600, 9),
+                                                             (700, 1, 64, 300, 5), (12, 20, 128, 1_500, 1)])
+def test_every_sequence_of_batches_whose_rows_have_ctas_to_themselves(h3, batch, kv_heads, dim, window, sinks):
+    rng = np.random.default_rng(batch + 1)
+    lengths = [int(n) for n in rng.integers(1, 2_600, batch)]
+    lengths[0], lengths[-1] = 2_600, 1
+    table, pages = _tables(rng, lengths, 32)
+    c = _filled_on_gpu(h3, table, lengths, pages, kv_heads, 32, dim, batch)
+    q = torch.randn(batch, 2 * kv_heads, dim, generator=torch.Generator().manual_seed(batch)).mul(2).bfloat16().cuda()
+    given = _give_up(table, 32, [(1, L) for L in lengths], window, sinks)
+    out, lse = _run(h3, q, c, given, lengths, np.arange(batch + 1), 1, causal=True, window=window, sinks=sinks)
+    assert h3.h3fp4_device_error() == 0
+    _all_within_bounds(c, q, table, lengths, out, lse, window, sinks)
