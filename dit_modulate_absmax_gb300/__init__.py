@@ -902,6 +902,8 @@ def kv_tables(held, count, page_table, free_pages, free_at, page_size, num_pages
     kv_len, len_at = out(kv_len, "kv_len", "i32", batch)
     slots, slots_at = out(slots, "slots", "i64", tokens)
     positions, positions_at = out(positions, "positions", "f32", tokens)
+    if not tokens:
+        slots_at = positions_at = 16    # no rows have no address, but are not unwanted: tokens without a row are reported
     free_at_out, next_at = out(free_at_out, "free_at_out", "i32", 1)
     h3fp4_kv_tables(_KV_REQUESTS.pack(*at, next_at, cu_at, len_at, slots_at, positions_at, tokens, batch, max_tokens, free, num_pages,
                                       page_size), _raw_stream(stream, held))

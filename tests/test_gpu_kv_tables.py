@@ -158,3 +158,13 @@ def test_no_page_is_taken_twice_whatever_the_place_in_the_list(h3, free_at, want
         assert h3.h3fp4_device_error() == (512 if want[6] else 0)
         given += [int(p) for p in tab.cpu().numpy()[0] if p >= 0]
     assert len(set(given)) == len(given)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_tokens_without_any_row_are_reported(h3, given):
+    kw = dict(slots=torch.empty(0, dtype=torch.int64, device="cuda"), positions=torch.empty(0, device="cuda")) if given else {}
+    for count, bad in ((3, True), (0, False)):
+        table = _dev([[-1]])
+        t = h3.kv_tables(_dev([0]), _dev([count]), table, _dev([4, 5]), _dev([0]), 16, 9, 0, 3, **kw)
+        assert t.cu_tokens.tolist() == [0, count] and t.free_at.item() == (1 if bad else 0) and t.slots.numel() == t.positions.numel() == 0
+        assert table.item() == (4 if bad else -1) and h3.h3fp4_device_error() == (512 if bad else 0)
