@@ -242,7 +242,7 @@ cudaError_t launch_kv_tables(const h3fp4_kv_requests &q, cudaStream_t st)
 {
     const int shift = q.page_size == 16 ? 4 : q.page_size == 32 ? 5 : q.page_size == 64 ? 6 : 7;
     const int tiles = std::max(1, (q.batch + kTile - 1) / kTile);
-    // CTAs of a tile: one for each 1,024 rows, until the SMs have two each.
+    // CTAs of a tile: one for each kThreads * kRows = 2,048 of its rows, until the SMs have two each.
     const int64_t rows = q.slots != nullptr || q.positions != nullptr ? q.tokens : 0;
     const int64_t wanted = (rows / tiles + kThreads * kRows - 1) / (kThreads * kRows), most = std::max(1, 2 * sm_count() / tiles);
     const dim3 grid(static_cast<unsigned>(std::clamp<int64_t>(wanted, 1, most)), static_cast<unsigned>(tiles));

@@ -24,7 +24,11 @@
 // left of the gradient's is a launch, the first loads and the join of dw (3
 // us); of small calls a launch and a chain of dependent loads (32 tokens of 72
 // heads 4.1 us).  Exchanged halves cost the shared-memory pipe: 20,000
-// tokens 212 us, the other two ways 176.  All in a graph of 10 passes.
+// tokens 213 us (gradients 277), interleaved pairs 175 (259).  Halves that face
+// each other take 174 (260) as one section; in several a lane's chunks lie in
+// shorter runs: (32, 32, 64) 189 (311), (32, 48, 48) 221 (359).  Heads of 256
+// channels, half as many: exchanged 217 (290), else 181 (279).  All in a graph of
+// 10 passes.
 #include <cuda_bf16.h>
 
 #include "norm_exchange.h"

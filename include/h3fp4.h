@@ -314,9 +314,9 @@ H3FP4_API h3fp4_status h3fp4_rope_axes(const void *x_bf16, int64_t x_token_strid
  *
  * For every token and head, with w the side's weight:
  *     r = 1 / sqrt(mean(x^2) + eps),  z = x r w,  out = RN_bf16(z turned as by h3fp4_rope_axes)
- * in FP32 before the one rounding.  Rows of any finite size are in range; a row
- * with an infinity gives 0, and NaN in the infinity's pair; one with a NaN
- * gives NaN.
+ * in FP32 before the one rounding.  Rows of any finite size are in range, and
+ * weights of up to 2^77 (x meets w before r); a row with an infinity gives 0,
+ * and NaN in the infinity's pair; one with a NaN gives NaN.
  *
  *   q, k       the two sides; either may be NULL (or have no heads).  x and out are [tokens, heads, head_dim]
  *              bf16, strides as for h3fp4_rope_axes.  out either is its own x (same pointer and strides: in place)
@@ -347,8 +347,9 @@ H3FP4_API h3fp4_status h3fp4_norm_rope(const h3fp4_norm_heads *q, const h3fp4_no
  *
  * With g = dy turned back and r as above:
  *     dx = RN_bf16(r (w g - x r^2 mean(w g x))),  dweight[c] = sum of g[c] x[c] r over the side's tokens and heads
- * dweight is written, not added to, in FP32 sums of a fixed order (the same
- * bits every time on a device); zeros where there are no tokens or heads.
+ * Products w g are in range up to 2^115.  dweight is written, not added to, in
+ * FP32 sums of a fixed order (the same bits every time on a device); zeros where
+ * there are no tokens or heads.
  *
  *   dy, x, dx  [tokens, heads, head_dim] bf16, strides as for h3fp4_rope_axes.  dx either is its side's dy or x
  *              (same pointer and strides) or has no element in common with any of the call's arrays, as above
@@ -508,8 +509,9 @@ H3FP4_API int64_t h3fp4_kv_attention_workspace(int64_t tokens, int32_t heads, in
  *     j <= its own position                            if causal, and
  *     j > its own position - window, or j < sinks      if window > 0.
  * Pages that lie wholly between the two are not looked at, whatever the table
- * holds for them, so that a bounded number of pages serves an endless
- * sequence.
+ * holds for them, so that they may serve other sequences: a bounded number is
+ * in use however long the sequence is.  Positions, and the table's row, go on
+ * counting from its beginning.
  *
  *   sinks      0 .. 2^30 (0, or no window: h3fp4_kv_attention)
  *   workspace  as for h3fp4_kv_attention
@@ -565,7 +567,9 @@ H3FP4_API int64_t h3fp4_kv_attention_shared_workspace(int64_t tokens, int32_t he
  *     cu_tokens[b + 1] = count[0] + ... + count[b],   kv_len[b] = held[b] + count[b],
  *     page_table[b, p] = the next of free_pages, for ceil(held[b] / page_size) <= p < ceil(kv_len[b] / page_size),
  * the first taken being free_pages[*free_at] and *free_at_out = *free_at + those
- * taken.  New token i of sequence b, at position held[b] + i, is row
+ * taken.  (The list is read forwards only: pages that are given up come back
+ * by a new list, or a new place in one.)
+ * New token i of sequence b, at position held[b] + i, is row
  * cu_tokens[b] + i of
  *     slots     page_table[b, position / page_size] * page_size + position % page_size
  *     positions the position (float, as h3fp4_rope takes them)

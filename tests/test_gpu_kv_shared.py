@@ -247,3 +247,18 @@ def test_groups_said_to_be_empty(h3, new, heads):
                 check = [[(0, 0)] * 3, [seqs[b]], cu[b:b + 2] - cu[b], [0, 0, 0, 0]]
                 _check(c, q[at], own[b:b + 1], shared, *check, out[at], lse[at], True)
                 assert (out[at].float() - want[0][at].float()).abs().max() <= 2.0 ** -7 * want[0][at].float().abs().max()
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_halves_past_32_bits(h3, new):
+    """The last rows of a call whose prefix halves take 10 GB, against the same rows in a small call."""
+    groups, seqs, many = [(200, 1)], [(new, 150)], 300_000
+    c, q, own, shared, cu, p_cu, first = _setup(h3, 31, groups, seqs, 64, 8, 128, 64)
+    want = _call(h3, c, q[:new], own, shared, groups, seqs, cu, p_cu, causal=True)
+    wide = torch.empty(many, 64, 128, dtype=torch.bfloat16, device="cuda")
+    wide[-new:] = q[:new]
+    at = _dev([many - new, many])
+    prefix = h3.SharedPrefix(_dev(shared), _dev([200]), at, new, 200)
+    out, lse = h3.kv_attention_shared(wide, c, prefix, _dev(own), _dev([150]), at, new, 150, causal=True, return_lse=True)
+    assert h3.h3fp4_device_error() == 0
+    assert torch.equal(out[-new:], want[0]) and torch.equal(lse[-new:], want[1])
